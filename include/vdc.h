@@ -1,9 +1,11 @@
 /*
  * vdc.h - packed variable-length width-4 depthwise causal convolution
  * followed by SiLU, training forward and backward, on AMD Instinct MI355X
- * (gfx950).  C ABI of libvdc.so.
+ * (gfx950), and the operators of the state space layer around it: the
+ * convolution with a carried state, the selective scan and the gated group
+ * norm (second half of this file).  C ABI of libvdc.so.
  *
- * The operation is the one documented on the pages of
+ * The convolution is the one documented on the pages of
  * flashinfer.cake_causal_conv1d_train:
  *   [F] cake_causal_conv1d_train_forward  (Parameters, Returns)
  *   [B] cake_causal_conv1d_train_backward (Description, Parameters, Returns)
@@ -240,6 +242,165 @@ int conv1d_plan(int direction, int64_t S, int64_t C, int policy, int64_t out[11]
  * library so far (a diagnostic counter, e.g. to check that S == 0
  * launches nothing). */
 uint64_t conv1d_launch_count(void);
+
+/* ------------------------------------------------------------------------
+ * The state space layer around the convolution.
+ *
+ * The general rules above hold here too, with these differences: activation
+ * inputs may have a row stride (elements between rows, at least the row's
+ * length; a row itself is dense), outputs are dense, and the alignment is
+ * each entry point's own.  A cache of per-sequence states is updated in
+ * place.  Its slots are chosen by `state_index` (int32, one per sequence;
+ * NULL: sequence i has slot i); a sequence whose index lies outside
+ * [0, slots) has no slot, and two sequences of one call must not share one
+ * (unspecified results).
+ * ------------------------------------------------------------------------ */
+
+/*
+ * conv1d_prefill - the forward over packed prompts with carried state.
+ *
+ * x, weight, w_dtype, bias, b_dtype, cu_seqlens, num_docs, S, C, y: as for
+ *             conv1d_fwd.
+ * state       bf16 [slots][3][C], 16-byte aligned: each sequence's last
+ *             three inputs, row 0 the oldest.  Every document leaves its
+ *             last three inputs (zeros where it has had fewer) in its slot.
+ * resume      uint8 [num_docs] or NULL.  Where non-zero, the document goes
+ *             on from its slot: the rows of its slot are the inputs before
+ *             its first token.  Elsewhere, and without a slot, its history
+ *             is zero and y is bitwise that of conv1d_fwd.
+ *
+ * Two launches: the packed forward, then a pass over the documents' first
+ * and last three tokens (alone when S == 0; none when num_docs == 0).
+ */
+int conv1d_prefill(const void *x, const void *weight, int w_dtype,
+                   const void *bias, int b_dtype,
+                   const int32_t *cu_seqlens, int64_t num_docs,
+                   int64_t S, int64_t C,
+                   void *state, int64_t slots, const int32_t *state_index,
+                   const uint8_t *resume, void *y, hipStream_t stream);
+
+/*
+ * conv1d_update - one token of each of `rows` sequences.
+ *
+ * x           bf16 [rows][C], x_stride a multiple of 8, 16-byte aligned.
+ * y           bf16 [rows][C], 16-byte aligned.
+ * state       as for conv1d_prefill: read, and moved up by the token.
+ *
+ * A row without a slot is padding: its y is zero, nothing else is touched.
+ * One launch; none when rows == 0.
+ */
+int conv1d_update(const void *x, int64_t x_stride, const void *weight, int w_dtype,
+                  const void *bias, int b_dtype, int64_t rows, int64_t C,
+                  void *state, int64_t slots, const int32_t *state_index,
+                  void *y, hipStream_t stream);
+
+/*
+ * The selective scan.  For token t, channel c of group c / (C / groups),
+ * state n, with d = softplus(dt + dt_bias), or dt + dt_bias without
+ * dt_softplus:
+ *
+ *   h[t,c,n] = exp(d[t,c] A[c,n]) h[t-1,c,n] + d[t,c] x[t,c] B[t,group,n]
+ *   y[t,c]   = (sum_n Cm[t,group,n] h[t,c,n] + D[c] x[t,c]) silu(z[t,c])
+ *
+ * in FP32, y rounded to bf16 once.  h before a document's first token is
+ * zero, or its slot's state where the document resumes.
+ */
+typedef struct vdc_scan {
+    int64_t S;        /* tokens; for selective_update rows, one token each   */
+    int64_t C;        /* channels, 1 .. 2^20                                 */
+    int64_t N;        /* states of a channel, 1 .. 64                        */
+    int64_t groups;   /* groups of B and Cm; divides C                       */
+    const void *x;    /* bf16 [S][C]                                         */
+    const void *dt;   /* bf16 [S][C]                                         */
+    const void *z;    /* bf16 [S][C], or NULL: no gate                       */
+    const void *B;    /* bf16 [S][groups][N], a row dense                    */
+    const void *Cm;   /* bf16 [S][groups][N], a row dense                    */
+    int64_t x_stride, dt_stride, z_stride, B_stride, C_stride;
+    const void *A;       /* [C][N]; a decay has A < 0                        */
+    const void *D;       /* [C] or NULL                                      */
+    const void *dt_bias; /* [C] or NULL                                      */
+    int A_dtype, D_dtype, dt_bias_dtype;
+    int dt_softplus;     /* non-zero: step sizes are softplus(dt + dt_bias)  */
+    const int32_t *cu_seqlens; /* int32 [num_docs + 1]; unused by selective_update */
+    int64_t num_docs;
+    float *state;        /* FP32 [slots][C][N], in place; forward: or NULL   */
+    int64_t slots;
+    const int32_t *state_index; /* one per document (row), or NULL           */
+    const uint8_t *resume;      /* per document, or NULL: none resumes       */
+} vdc_scan;
+
+/* selective_scan_workspace_bytes - workspace of selective_scan_fwd
+ * (VDC_FWD) or selective_scan_bwd (VDC_BWD); 0 for invalid sizes.  Its
+ * contents need not start at zero. */
+size_t selective_scan_workspace_bytes(int direction, int64_t S, int64_t C, int64_t N,
+                                      int64_t groups);
+
+/*
+ * selective_scan_fwd - prompts, and the training forward.
+ *
+ * y bf16 [S][C].  With a state, every document leaves the state after its
+ * last token in its slot; an empty one leaves zeros, or its slot as it is
+ * where it resumes.  Activations are 2-byte aligned, A, D, dt_bias by their
+ * dtypes, the state 4-byte, the workspace 16-byte.
+ */
+int selective_scan_fwd(const vdc_scan *args, void *y, void *workspace, size_t ws_bytes,
+                       hipStream_t stream);
+
+/*
+ * selective_scan_bwd - gradients of the training forward (every document
+ * from zero history; args->state must be NULL) from x, dt, z, B, Cm alone.
+ *
+ * dy            bf16 [S][C], dy_stride elements between rows.
+ * dx, ddt, dz   bf16 [S][C] outputs; dz NULL exactly where z is.
+ * dB, dC        bf16 [S][groups][N] outputs.
+ * dA, dD, ddt_bias outputs of the parameters' dtypes; dD and ddt_bias NULL
+ *               exactly where the parameter is.
+ * Sums over tokens and channels are taken in an order that depends on the
+ * sizes only: results are bitwise reproducible.  S == 0 sets dA, dD and
+ * ddt_bias to zero.
+ */
+int selective_scan_bwd(const vdc_scan *args, const void *dy, int64_t dy_stride,
+                       void *dx, void *ddt, void *dz, void *dB, void *dC,
+                       void *dA, void *dD, void *ddt_bias,
+                       void *workspace, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * selective_update - one token of each of args->S sequences: the state of
+ * its slot is read and replaced.  A row without a slot is padding: its y is
+ * zero, nothing else is touched.  args->state is required.
+ */
+int selective_update(const vdc_scan *args, void *y, hipStream_t stream);
+
+/*
+ * group_norm_silu_fwd - group norm over each token's channels with a SiLU.
+ *
+ * Per token and group of C / groups channels (at most 16384 of them):
+ *   v = weight (x - mean) / sqrt(var + eps) + bias,  var the biased variance,
+ *   y = silu(v), or v silu(z) where a gate z is given.
+ *
+ * x, z   bf16 [S][C] with row strides; y bf16 [S][C]; 2-byte aligned.
+ * weight, bias [C] of their dtypes; bias or z may be NULL.  eps >= 0.
+ */
+int group_norm_silu_fwd(const void *x, int64_t x_stride, const void *weight, int w_dtype,
+                        const void *bias, int b_dtype, const void *z, int64_t z_stride,
+                        int64_t S, int64_t C, int64_t groups, float eps,
+                        void *y, hipStream_t stream);
+
+/* group_norm_silu_workspace_bytes - workspace of group_norm_silu_bwd. */
+size_t group_norm_silu_workspace_bytes(int64_t S, int64_t C, int64_t groups);
+
+/*
+ * group_norm_silu_bwd - its gradients, from the forward's inputs alone.
+ * dx, dz bf16 [S][C]; dweight, dbias [C] of the parameters' dtypes; dz and
+ * dbias NULL exactly where z and bias are.  Reproducible as above; S == 0
+ * sets dweight and dbias to zero.
+ */
+int group_norm_silu_bwd(const void *x, int64_t x_stride, const void *weight, int w_dtype,
+                        const void *bias, int b_dtype, const void *z, int64_t z_stride,
+                        const void *dy, int64_t dy_stride,
+                        int64_t S, int64_t C, int64_t groups, float eps,
+                        void *dx, void *dweight, void *dbias, void *dz,
+                        void *workspace, size_t ws_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -20,6 +20,9 @@ DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
                 "-ffp-contract=off"]
 COMMON = ["-O3", "-std=c++17", "-fPIC", "--offload-arch=" + ARCH, "-I", INCLUDE, "-I", CSRC]
 
+SOURCES = ("vdc_kernels.hip", "vdc_conv_state.hip", "vdc_scan.hip", "vdc_norm.hip", "vdc_api.cpp",
+           "vdc_ssm_api.cpp")
+
 
 def hipcc() -> str:
     path = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
@@ -32,14 +35,18 @@ def build(verbose: bool = False) -> str:
     """Compile csrc/*.hip + csrc/*.cpp into libvdc.so (always rebuilds)."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     cc = hipcc()
-    objs = []
-    for src, extra in (("vdc_kernels.hip", DEVICE_FLAGS), ("vdc_api.cpp", [])):
+    objs, running = [], []
+    for src in SOURCES:
         obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
+        extra = DEVICE_FLAGS if src.endswith(".hip") else []
         cmd = [cc, *COMMON, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
-        subprocess.run(cmd, check=True)
+        running.append((cmd, subprocess.Popen(cmd)))
         objs.append(obj)
+    for cmd, p in running:
+        if p.wait():
+            raise subprocess.CalledProcessError(p.returncode, cmd)
     tmp = LIBRARY + ".tmp%d" % os.getpid()
     cmd = [cc, "-shared", "-fPIC", "--offload-arch=" + ARCH, "-o", tmp, *objs]
     if verbose:

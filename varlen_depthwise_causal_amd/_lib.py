@@ -16,6 +16,22 @@ STATUS = {VDC_OK: "VDC_OK", VDC_EINVAL: "VDC_EINVAL", VDC_EDTYPE: "VDC_EDTYPE",
           VDC_EALIGN: "VDC_EALIGN", VDC_EWORKSPACE: "VDC_EWORKSPACE",
           VDC_ENOBIAS: "VDC_ENOBIAS", VDC_EHIP: "VDC_EHIP", VDC_ESCRATCH: "VDC_ESCRATCH"}
 
+
+
+class VdcScan(ctypes.Structure):
+    """struct vdc_scan of include/vdc.h."""
+
+    _fields_ = ([(n, ctypes.c_int64) for n in ("S", "C", "N", "groups")]
+                + [(n, ctypes.c_void_p) for n in ("x", "dt", "z", "B", "Cm")]
+                + [(n, ctypes.c_int64) for n in ("x_stride", "dt_stride", "z_stride", "B_stride",
+                                                 "C_stride")]
+                + [(n, ctypes.c_void_p) for n in ("A", "D", "dt_bias")]
+                + [(n, ctypes.c_int) for n in ("A_dtype", "D_dtype", "dt_bias_dtype", "dt_softplus")]
+                + [("cu_seqlens", ctypes.c_void_p), ("num_docs", ctypes.c_int64),
+                   ("state", ctypes.c_void_p), ("slots", ctypes.c_int64),
+                   ("state_index", ctypes.c_void_p), ("resume", ctypes.c_void_p)])
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -59,6 +75,22 @@ def load(path: str | None = None):
         lib.conv1d_status_string.restype = ctypes.c_char_p
         lib.conv1d_plan.argtypes = [i32, i64, i64, i32, ctypes.POINTER(i64)]
         lib.conv1d_plan.restype = i32
+        scan, size_t, f32 = ctypes.POINTER(VdcScan), ctypes.c_size_t, ctypes.c_float
+        for name, restype, argtypes in (
+                ("conv1d_prefill", i32, [vp, vp, i32, vp, i32, vp, i64, i64, i64, vp, i64, vp, vp, vp,
+                                         vp]),
+                ("conv1d_update", i32, [vp, i64, vp, i32, vp, i32, i64, i64, vp, i64, vp, vp, vp]),
+                ("selective_scan_workspace_bytes", size_t, [i32, i64, i64, i64, i64]),
+                ("selective_scan_fwd", i32, [scan, vp, vp, size_t, vp]),
+                ("selective_scan_bwd", i32, [scan, vp, i64] + [vp] * 8 + [vp, size_t, vp]),
+                ("selective_update", i32, [scan, vp, vp]),
+                ("group_norm_silu_fwd", i32, [vp, i64, vp, i32, vp, i32, vp, i64, i64, i64, i64, f32,
+                                              vp, vp]),
+                ("group_norm_silu_workspace_bytes", size_t, [i64, i64, i64]),
+                ("group_norm_silu_bwd", i32, [vp, i64, vp, i32, vp, i32, vp, i64, vp, i64, i64, i64,
+                                              i64, f32, vp, vp, vp, vp, vp, size_t, vp])):
+            fn = getattr(lib, name)
+            fn.restype, fn.argtypes = restype, argtypes
         lib.conv1d_launch_count.argtypes = []
         lib.conv1d_launch_count.restype = ctypes.c_uint64
         if path is None:

@@ -133,6 +133,9 @@ int check_sizes(int64_t S, int64_t C, int64_t num_docs) {
 }
 
 }  // namespace
+
+void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
+
 }  // namespace vdc
 
 using namespace vdc;

@@ -152,6 +152,9 @@ constexpr size_t kScratchBytes = size_t(16) << 20;
 // with the device current, then cached).
 hipError_t scratch_pointer(int device, void** out);
 
+// Adds a kernel launch to the process's count (conv1d_launch_count).
+void count_launch();
+
 // Launchers (return the hipError_t of the launch).
 hipError_t launch_fwd(const Plan& plan, const FwdArgs& a, bool has_bias, hipStream_t s);
 hipError_t launch_bwd_main(const Plan& plan, const BwdArgs& a, bool has_bias, bool fp32_policy,

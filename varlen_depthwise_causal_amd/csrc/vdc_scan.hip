@@ -1,0 +1,724 @@
+// The selective state space scan over packed documents: forward for prompts
+// and training, backward, and the form for single tokens.
+//
+// For token t, channel c, state n, with d = softplus(dt + bias):
+//
+//   h[t,c,n] = exp(d[t,c] A[c,n]) h[t-1,c,n] + d[t,c] x[t,c] B[t,n]
+//   y[t,c]   = (sum_n C[t,n] h[t,c,n] + D[c] x[t,c]) silu(z[t,c])
+//
+// The decay differs for every (token, channel, state), so the sum over time
+// is no matrix product: an element costs one exponential and four FP32
+// instructions, and the kernels are bound by VALU issue, not by HBM.
+//
+// Time is cut into chunks that run in parallel.  The states after each chunk
+// are found first with zero history (scan_local), joined in order
+// (scan_join; the decay over a whole chunk is exp(A sum d), one exponential),
+// and the outputs follow with the right state at each chunk's start.
+// Everything between documents is assigned, never multiplied by zero, so
+// that an infinity or a NaN stays in its document.
+
+#include "vdc_search.h"
+#include "vdc_ssm.h"
+#include "vdc_ssm_math.h"
+
+namespace vdc {
+namespace {
+
+// First index i in [0, n) with cu[i] >= v (n if none), by a whole wave.
+__device__ __forceinline__ int32_t first_at_least(const int32_t* cu, int32_t n, int32_t v) {
+  const int lane = (int)(threadIdx.x & 63);
+  int64_t lo = 0, hi = n;
+  while (lo < hi) {
+    const int64_t step = search_step(lo, hi);
+    const int64_t idx = search_probe(lo, hi, step, lane);
+    const uint64_t ball = __ballot(idx >= 0 && cu[idx] < v);
+    search_narrow(lo, hi, step, ~ball == 0 ? 64 : (int)__builtin_ctzll(~ball));
+  }
+  return __builtin_amdgcn_readfirstlane((int32_t)lo);
+}
+
+__device__ __forceinline__ float step_size(const ScanArgs& a, float raw) {
+  return a.softplus ? softplus_f32(raw) : raw;
+}
+
+// ---------------------------------------------- forward, lane = channel --
+
+// A lane's channel: column of the workspace rows, channel, and whether the
+// channel exists (a group's last wave may have lanes past it; they run on
+// its first channel's addresses and store nothing).
+struct Column {
+  int32_t group, col;
+  int64_t c;
+  bool active;
+};
+
+__device__ __forceinline__ Column column_of(const ScanArgs& a, int32_t wave) {
+  Column o;
+  o.group = wave / a.wpg;
+  const int32_t i = (wave - o.group * a.wpg) * 64 + (int32_t)(threadIdx.x & 63);
+  o.col = wave * 64 + (int32_t)(threadIdx.x & 63);
+  o.active = i < a.per;
+  o.c = (int64_t)o.group * a.per + (o.active ? i : 0);
+  return o;
+}
+
+template <int NT>
+__device__ __forceinline__ void load_decay(const ScanArgs& a, const Column& l, float (&A2)[NT]) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+    A2[n] = n < a.N ? param_at(a.A, a.A_bf16, l.c * a.N + n) * kLog2E : 0.0f;
+}
+
+// One pass over a chunk.  kOut = false: the state after the chunk from zero
+// history (or a document's own start), the sum of the step sizes, and what a
+// resumed document that runs past the chunk began with.  kOut = true: the
+// outputs, from the joined states.
+template <int NT, bool kOut>
+__global__ __launch_bounds__(64) void scan_fwd_kernel(ScanArgs a) {
+  const int32_t waves = a.G * a.wpg;
+  const int32_t k = blockIdx.x / waves, w = blockIdx.x - k * waves;
+  const Column l = column_of(a, w);
+  const int32_t t0 = k * a.chunk;
+  const int32_t t1 = (int32_t)min((int64_t)a.S, (int64_t)t0 + a.chunk);
+  const int64_t ws = ((int64_t)k * a.N) * a.cols + l.col;  // this chunk's rows of the workspace
+  float A2[NT], h[NT];
+  load_decay<NT>(a, l, A2);
+  const float Dc = a.D ? param_at(a.D, a.D_bf16, l.c) : 0.0f;
+  const float bias = a.bias ? param_at(a.bias, a.bias_bf16, l.c) : 0.0f;
+  float sum = 0.0f;
+  int32_t flags = 0;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) h[n] = 0.0f;
+
+  int32_t doc, next;  // the document of token t, and where it ends
+  int32_t t = t0;
+  // Document `d` is the first that may start at t: passes the empty ones
+  // (whose slots hold an empty sequence's state, zero, unless they resume)
+  // and begins the next.
+  auto open = [&](int32_t d) {
+    while (d < a.num_docs && a.cu[d + 1] <= t) {
+      if (kOut && a.state && l.active) {
+        const int64_t slot = slot_of(a.index, d, a.slots);
+        if (slot >= 0 && !(a.resume && a.resume[d]))
+          for (int n = 0; n < a.N; ++n) a.state[(slot * a.C + l.c) * a.N + n] = 0.0f;
+      }
+      ++d;
+    }
+    doc = d;
+    next = d < a.num_docs ? a.cu[d + 1] : INT32_MAX;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) h[n] = 0.0f;
+    flags |= t == t0 ? 1 : 2;
+    if (a.state && d < a.num_docs && a.resume && a.resume[d]) {
+      const int64_t slot = slot_of(a.index, d, a.slots);
+      if (slot >= 0) {
+        // The chunk that ends a document writes its slot while others may
+        // still have to read it: a document that runs past its first chunk
+        // has its start copied by the first pass and read from there.
+        const bool past = next > t1;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          if (n < a.N) {
+            if (kOut && past) h[n] = a.snap[ws + (int64_t)n * a.cols];
+            else if (l.active) h[n] = a.state[(slot * a.C + l.c) * a.N + n];
+            if (!kOut && past) a.snap[ws + (int64_t)n * a.cols] = h[n];
+          }
+      }
+    }
+  };
+
+  const int32_t i = first_at_least(a.cu, a.num_docs + 1, t0);
+  if (i <= a.num_docs && a.cu[i] == t0) {
+    open(i);
+  } else {
+    doc = i - 1;
+    next = doc >= 0 && doc < a.num_docs ? a.cu[doc + 1] : INT32_MAX;
+    if (kOut && k > 0) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        if (n < a.N) h[n] = a.hend[ws + ((int64_t)n - a.N) * a.cols];
+    }
+  }
+
+  while (t < t1) {
+    const int32_t end = next > t && next < t1 ? next : t1;
+    for (; t < end; ++t) {
+      const float x = l.active ? bf16_f32(a.x[t * a.xs + l.c]) : 0.0f;
+      const float raw = bf16_f32(a.dt[t * a.dts + l.c]) + bias;
+      const float d = l.active ? step_size(a, raw) : 0.0f;
+      const float dx = d * x;
+      const uint16_t* B = a.B + t * a.Bs + l.group * a.N;
+      const uint16_t* Cm = a.Cm + t * a.Cs + l.group * a.N;
+      float y = Dc * x;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float b = n < a.N ? bf16_f32(B[n]) : 0.0f;
+        const float e = __builtin_amdgcn_exp2f(d * A2[n]);
+        h[n] = __builtin_fmaf(e, h[n], dx * b);
+        if (kOut) y = __builtin_fmaf(n < a.N ? bf16_f32(Cm[n]) : 0.0f, h[n], y);
+      }
+      if (kOut) {
+        if (a.z) {
+          const float z = bf16_f32(a.z[t * a.zs + l.c]);
+          y *= z * sigmoid_f32(z);
+        }
+        if (l.active) a.y[(int64_t)t * a.C + l.c] = bf16_of(y);
+      } else {
+        sum += d;
+      }
+    }
+    if (t == next && doc >= 0 && doc < a.num_docs) {
+      if (kOut && a.state && l.active) {
+        const int64_t slot = slot_of(a.index, doc, a.slots);
+        if (slot >= 0) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            if (n < a.N) a.state[(slot * a.C + l.c) * a.N + n] = h[n];
+        }
+      }
+      if (t < t1 || t == a.S) open(doc + 1);
+    }
+  }
+  if (!kOut) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      if (n < a.N) a.hend[ws + (int64_t)n * a.cols] = h[n];
+    a.sum[(int64_t)k * a.cols + l.col] = sum;
+    if (w == 0 && threadIdx.x == 0) a.flags[k] = flags;
+  }
+}
+
+// Joins the chunks: forward in time the states after each chunk, and for the
+// backward (blockIdx.z = 1) against it the gradients that leave each chunk.
+__global__ __launch_bounds__(256) void scan_join_kernel(ScanArgs a) {
+  const int32_t col = blockIdx.x * 256 + threadIdx.x, n = blockIdx.y;
+  if (col >= a.cols) return;
+  const int32_t g = col / (a.wpg * 64), i = col - g * a.wpg * 64;
+  if (i >= a.per) return;
+  const float A2 = param_at(a.A, a.A_bf16, ((int64_t)g * a.per + i) * a.N + n) * kLog2E;
+  const bool back = blockIdx.z == 1;
+  float* v = (back ? a.mu : a.hend) + (int64_t)n * a.cols + col;
+  const int64_t row = (int64_t)a.N * a.cols;
+  float carry = 0.0f;
+  for (int32_t s = 0; s < a.chunks - 1; ++s) {
+    const int32_t k = back ? a.chunks - 1 - s : s;
+    const int32_t f = a.flags[k];
+    const float own = v[k * row];
+    if (back && (f & 1)) {
+      carry = 0.0f;  // a document starts with the chunk: nothing leaves it
+    } else if (f == 0 && carry != 0.0f) {
+      carry = __builtin_fmaf(__builtin_amdgcn_exp2f(A2 * a.sum[(int64_t)k * a.cols + col]), carry, own);
+    } else {
+      carry = own;
+    }
+    v[k * row] = carry;
+  }
+}
+
+// ------------------------------------------------------------- backward --
+//
+// With g = dy silu(z) and lambda[t] the gradient at h[t]:
+//
+//   lambda[t] = C[t] g[t] + exp(d[t+1] A) lambda[t+1]
+//   v[t]      = lambda[t] exp(d[t] A) h[t-1]
+//   dx = D g + d sum_n lambda B      dd  = x sum_n lambda B + sum_n v A
+//   dB = sum_c lambda d x            dC  = sum_c g h
+//   dA = sum_t v d                   dD  = sum_t g x
+//
+// Document starts of a chunk are a bitmask in LDS: bit i for token t0 + i,
+// the token after the chunk's last included.
+
+struct Starts {
+  uint32_t bits[kScanMaxChunk / 32 + 2];
+};
+
+__device__ __forceinline__ void find_starts(const ScanArgs& a, Starts& m, int32_t t0, int32_t t1) {
+  const int32_t lane = threadIdx.x & 63;
+  const int32_t words = (t1 - t0) / 32 + 2;
+  for (int32_t i = lane; i < words; i += 64) m.bits[i] = 0u;
+  __syncthreads();
+  for (int64_t i = (int64_t)first_at_least(a.cu, a.num_docs + 1, t0) + lane; i <= a.num_docs; i += 64) {
+    const int32_t v = a.cu[i];
+    if (v > t1) break;
+    if (v >= t0) atomicOr(&m.bits[(v - t0) >> 5], 1u << ((v - t0) & 31));
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ bool starts_at(const Starts& m, int32_t i) {
+  return (__builtin_amdgcn_readfirstlane(m.bits[i >> 5]) >> (i & 31)) & 1u;
+}
+
+// Forward over a chunk from zero history: the states every kScanKeep tokens,
+// the state after the chunk, and the gradient that the chunk's own tokens
+// send to its left: sum_t exp(A (d[t0] + .. + d[t])) C[t] g[t] over the
+// tokens of the first document in it.
+template <int NT>
+__global__ __launch_bounds__(64) void scan_bwd_local_kernel(ScanArgs a) {
+  __shared__ Starts m;
+  const int32_t waves = a.G * a.wpg;
+  const int32_t k = blockIdx.x / waves, w = blockIdx.x - k * waves;
+  const Column l = column_of(a, w);
+  const int32_t t0 = k * a.chunk;
+  const int32_t t1 = (int32_t)min((int64_t)a.S, (int64_t)t0 + a.chunk);
+  find_starts(a, m, t0, t1);
+  float A2[NT], h[NT], mu[NT], p[NT];
+  load_decay<NT>(a, l, A2);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) h[n] = 0.0f, mu[n] = 0.0f, p[n] = 1.0f;
+  const float bias = a.bias ? param_at(a.bias, a.bias_bf16, l.c) : 0.0f;
+  float sum = 0.0f;
+  int32_t flags = starts_at(m, 0) ? 1 : 0;
+  bool first = true;  // still in the chunk's first document
+  for (int32_t t = t0; t < t1; ++t) {
+    const int32_t i = t - t0;
+    if (i && i % kScanKeep == 0) {
+      float* r = a.keep + (int64_t)(t / kScanKeep) * (a.N + 1) * a.cols + l.col;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        if (n < a.N) r[(int64_t)n * a.cols] = h[n];
+      r[(int64_t)a.N * a.cols] = sum;
+    }
+    if (i && starts_at(m, i)) {
+      flags |= 2;
+      first = false;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) h[n] = 0.0f;
+    }
+    const float x = l.active ? bf16_f32(a.x[t * a.xs + l.c]) : 0.0f;
+    const float raw = bf16_f32(a.dt[t * a.dts + l.c]) + bias;
+    const float d = l.active ? step_size(a, raw) : 0.0f;
+    float g = l.active ? bf16_f32(a.dy[t * a.dys + l.c]) : 0.0f;
+    if (a.z && l.active) {
+      const float z = bf16_f32(a.z[t * a.zs + l.c]);
+      g *= z * sigmoid_f32(z);
+    }
+    const float dx = d * x;
+    const uint16_t* B = a.B + t * a.Bs + l.group * a.N;
+    const uint16_t* Cm = a.Cm + t * a.Cs + l.group * a.N;
+    sum += d;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float e = __builtin_amdgcn_exp2f(d * A2[n]);
+      h[n] = __builtin_fmaf(e, h[n], dx * (n < a.N ? bf16_f32(B[n]) : 0.0f));
+      if (first) {
+        p[n] *= e;
+        mu[n] = __builtin_fmaf(p[n], g * (n < a.N ? bf16_f32(Cm[n]) : 0.0f), mu[n]);
+      }
+    }
+  }
+  const int64_t ws = ((int64_t)k * a.N) * a.cols + l.col;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+    if (n < a.N) {
+      a.hend[ws + (int64_t)n * a.cols] = h[n];
+      a.mu[ws + (int64_t)n * a.cols] = mu[n];
+    }
+  a.sum[(int64_t)k * a.cols + l.col] = sum;
+  if (w == 0 && threadIdx.x == 0) a.flags[k] = flags;
+}
+
+// The main pass runs a chunk backwards in blocks of kScanKeep tokens.  A lane
+// holds RC channels x RN states: lane = 4 * quad + part, channels
+// RC * quad .., states RN * part .. , so that the sums over states take two
+// exchanges within a quad, those over channels RC terms in registers first,
+// and neither direction dominates.  A block's states are computed forward
+// from its kept start twice: once for the starts of its sub-blocks, then for
+// each sub-block, whose decays and decayed states stay in registers for the
+// way back.
+constexpr int kSub = 4;
+
+template <int R>
+__device__ __forceinline__ float quad_from(float v) {
+  return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), R * 0x55, 0xf, 0xf, true));
+}
+template <int RC>
+__device__ __forceinline__ void quad_spread(float v, float (&o)[RC]) {
+  o[0] = quad_from<0>(v);
+  if constexpr (RC > 1) o[1] = quad_from<1>(v);
+  if constexpr (RC > 2) o[2] = quad_from<2>(v), o[3] = quad_from<3>(v);
+}
+__device__ __forceinline__ float quad_sum(float v) {
+  v += __shfl_xor(v, 1);
+  return v + __shfl_xor(v, 2);
+}
+
+template <int NT>
+__global__ __launch_bounds__(64) void scan_bwd_main_kernel(ScanArgs a) {
+  constexpr int RN = NT / 4, RC = NT <= 16 ? 4 : NT == 32 ? 2 : 1, CB = 16 * RC;
+  __shared__ Starts m;
+  __shared__ float sub_h[kScanKeep / kSub][RC * RN][64];
+  const int32_t lane = threadIdx.x, part = lane & 3, quad = lane >> 2;
+  const int32_t bpg = (a.per + CB - 1) / CB, blocks = a.G * bpg;
+  const int32_t k = blockIdx.x / blocks, wb = blockIdx.x - k * blocks;
+  const int32_t g = wb / bpg, i0 = (wb - g * bpg) * CB;
+  const int32_t t0 = k * a.chunk;
+  const int32_t t1 = (int32_t)min((int64_t)a.S, (int64_t)t0 + a.chunk);
+  find_starts(a, m, t0, t1);
+  // The channel whose loads and per-channel terms are this lane's.
+  const int32_t mine = part % RC;
+  const bool active = i0 + RC * quad + mine < a.per, owner = active && part < RC;
+  const int64_t c = (int64_t)g * a.per + (active ? i0 + RC * quad + mine : 0);
+  const float Dc = a.D ? param_at(a.D, a.D_bf16, c) : 0.0f;
+  const float bias = a.bias ? param_at(a.bias, a.bias_bf16, c) : 0.0f;
+  const int64_t col = (int64_t)g * a.wpg * 64 + i0 + RC * quad;
+  const int32_t n0 = RN * part;
+
+  float A[RC][RN], mu[RC][RN], dA[RC][RN];
+#pragma unroll
+  for (int r = 0; r < RC; ++r) {
+    const int32_t i = i0 + RC * quad + r;
+#pragma unroll
+    for (int j = 0; j < RN; ++j) {
+      const bool there = i < a.per && n0 + j < a.N;
+      A[r][j] = there ? param_at(a.A, a.A_bf16, ((int64_t)g * a.per + i) * a.N + n0 + j) : 0.0f;
+      dA[r][j] = 0.0f;
+      // What the chunk to the right sends.
+      mu[r][j] = there && k + 1 < a.chunks
+                     ? a.mu[((int64_t)(k + 1) * a.N + n0 + j) * a.cols + col + r] : 0.0f;
+    }
+  }
+  if (starts_at(m, t1 - t0)) {
+#pragma unroll
+    for (int r = 0; r < RC; ++r)
+#pragma unroll
+      for (int j = 0; j < RN; ++j) mu[r][j] = 0.0f;
+  }
+  float dD = 0.0f, dbias = 0.0f;
+
+  struct Token {
+    float x, raw, d, dx;
+  };
+  auto token = [&](int32_t t) {
+    Token o;
+    const bool in = active && t < t1;
+    const int64_t tt = min(t, t1 - 1);
+    o.x = in ? bf16_f32(a.x[tt * a.xs + c]) : 0.0f;
+    o.raw = bf16_f32(a.dt[tt * a.dts + c]) + bias;
+    o.d = in ? step_size(a, o.raw) : 0.0f;
+    o.dx = o.d * o.x;
+    return o;
+  };
+  auto states = [&](const uint16_t* p, int64_t stride, int32_t t, float (&o)[RN]) {
+    const uint16_t* q = p + (int64_t)min(t, t1 - 1) * stride + g * a.N + n0;
+#pragma unroll
+    for (int j = 0; j < RN; ++j) o[j] = n0 + j < a.N ? bf16_f32(q[j]) : 0.0f;
+  };
+
+  for (int32_t ib = (t1 - t0 - 1) / kScanKeep; ib >= 0; --ib) {
+    const int32_t tb = t0 + ib * kScanKeep;
+    // The state before token tb: kept from zero history, plus what came into
+    // the chunk, decayed, if no document has started since.
+    bool carried = k > 0;
+    for (int32_t i = 0; carried && i < ib * kScanKeep; ++i) carried = !starts_at(m, i);
+    float h[RC][RN];
+    float csum[RC];
+    const float* kept = a.keep + (int64_t)(tb / kScanKeep) * (a.N + 1) * a.cols + col;
+#pragma unroll
+    for (int r = 0; r < RC; ++r) {
+      csum[r] = ib > 0 ? kept[(int64_t)a.N * a.cols + r] : 0.0f;
+#pragma unroll
+      for (int j = 0; j < RN; ++j) {
+        float v = 0.0f;
+        if (i0 + RC * quad + r < a.per && n0 + j < a.N) {
+          if (ib > 0) v = kept[(int64_t)(n0 + j) * a.cols + r];
+          if (carried) {
+            const float in = a.hend[((int64_t)(k - 1) * a.N + n0 + j) * a.cols + col + r];
+            if (in != 0.0f)
+              v = __builtin_fmaf(__builtin_amdgcn_exp2f(A[r][j] * kLog2E * csum[r]), in, v);
+          }
+        }
+        h[r][j] = v;
+      }
+    }
+    for (int32_t s = 0; s < kScanKeep / kSub; ++s) {
+#pragma unroll
+      for (int e = 0; e < RC * RN; ++e) sub_h[s][e][lane] = h[e / RN][e % RN];
+      if (s + 1 < kScanKeep / kSub) {
+        for (int i = 0; i < kSub; ++i) {
+          const int32_t t = tb + s * kSub + i;
+          if (t < t1 && starts_at(m, t - t0)) {
+#pragma unroll
+            for (int r = 0; r < RC; ++r)
+#pragma unroll
+              for (int j = 0; j < RN; ++j) h[r][j] = 0.0f;
+          }
+          const Token o = token(t);
+          float B[RN], d[RC], dx[RC];
+          states(a.B, a.Bs, t, B);
+          quad_spread<RC>(o.d, d);
+          quad_spread<RC>(o.dx, dx);
+#pragma unroll
+          for (int r = 0; r < RC; ++r)
+#pragma unroll
+            for (int j = 0; j < RN; ++j)
+              h[r][j] = __builtin_fmaf(__builtin_amdgcn_exp2f(d[r] * (A[r][j] * kLog2E)), h[r][j],
+                                       dx[r] * B[j]);
+        }
+      }
+    }
+    for (int32_t s = kScanKeep / kSub - 1; s >= 0; --s) {
+      const int32_t ts = tb + s * kSub;
+      if (ts >= t1) continue;
+      float aw[kSub][RC][RN], hw[kSub][RC][RN];
+      Token tok[kSub];
+#pragma unroll
+      for (int e = 0; e < RC * RN; ++e) h[e / RN][e % RN] = sub_h[s][e][lane];
+#pragma unroll
+      for (int i = 0; i < kSub; ++i) {
+        const int32_t t = ts + i;
+        if (t < t1 && starts_at(m, t - t0)) {
+#pragma unroll
+          for (int r = 0; r < RC; ++r)
+#pragma unroll
+            for (int j = 0; j < RN; ++j) h[r][j] = 0.0f;
+        }
+        tok[i] = token(t);
+        float B[RN], d[RC], dx[RC];
+        states(a.B, a.Bs, t, B);
+        quad_spread<RC>(tok[i].d, d);
+        quad_spread<RC>(tok[i].dx, dx);
+#pragma unroll
+        for (int r = 0; r < RC; ++r)
+#pragma unroll
+          for (int j = 0; j < RN; ++j) {
+            const float e = __builtin_amdgcn_exp2f(d[r] * (A[r][j] * kLog2E));
+            aw[i][r][j] = e;
+            hw[i][r][j] = e * h[r][j];  // the state of the token before, decayed
+            h[r][j] = __builtin_fmaf(dx[r], B[j], hw[i][r][j]);
+          }
+      }
+#pragma unroll
+      for (int i = kSub - 1; i >= 0; --i) {
+        const int32_t t = ts + i;
+        if (t < t1) {
+          const Token& o = tok[i];
+          const float dy = active ? bf16_f32(a.dy[t * a.dys + c]) : 0.0f;
+          float z = 0.0f, sz = 0.0f, gate = 1.0f;
+          if (a.z && active) {
+            z = bf16_f32(a.z[t * a.zs + c]);
+            sz = sigmoid_f32(z);
+            gate = z * sz;
+          }
+          const float gy = dy * gate;
+          float B[RN], Cm[RN], d[RC], dx[RC], gr[RC];
+          states(a.B, a.Bs, t, B);
+          states(a.Cm, a.Cs, t, Cm);
+          quad_spread<RC>(o.d, d);
+          quad_spread<RC>(o.dx, dx);
+          quad_spread<RC>(gy, gr);
+          float dB[RN], dC[RN], lb[RC], va[RC], y0[RC];
+#pragma unroll
+          for (int j = 0; j < RN; ++j) dB[j] = 0.0f, dC[j] = 0.0f;
+#pragma unroll
+          for (int r = 0; r < RC; ++r) {
+            lb[r] = va[r] = y0[r] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < RN; ++j) {
+              const float lam = __builtin_fmaf(gr[r], Cm[j], mu[r][j]);
+              const float ht = __builtin_fmaf(dx[r], B[j], hw[i][r][j]);
+              const float v = lam * hw[i][r][j];
+              y0[r] = __builtin_fmaf(Cm[j], ht, y0[r]);
+              lb[r] = __builtin_fmaf(lam, B[j], lb[r]);
+              va[r] = __builtin_fmaf(v, A[r][j], va[r]);
+              dA[r][j] = __builtin_fmaf(v, d[r], dA[r][j]);
+              dB[j] = __builtin_fmaf(lam, dx[r], dB[j]);
+              dC[j] = __builtin_fmaf(gr[r], ht, dC[j]);
+              mu[r][j] = aw[i][r][j] * lam;
+            }
+          }
+          if (starts_at(m, t - t0)) {
+#pragma unroll
+            for (int r = 0; r < RC; ++r)
+#pragma unroll
+              for (int j = 0; j < RN; ++j) mu[r][j] = 0.0f;
+          }
+          // Sums over the states, each lane keeping its own channel's.
+          float slb = 0.0f, sva = 0.0f, sy = 0.0f;
+#pragma unroll
+          for (int r = 0; r < RC; ++r) {
+            const float u = quad_sum(lb[r]), v = quad_sum(va[r]), y = quad_sum(y0[r]);
+            if (mine == r) slb = u, sva = v, sy = y;
+          }
+          const float ddt = __builtin_fmaf(o.x, slb, sva) * (a.softplus ? sigmoid_f32(o.raw) : 1.0f);
+          dD = __builtin_fmaf(gy, o.x, dD);
+          dbias += ddt;
+          if (owner) {
+            const int64_t at = (int64_t)t * a.C + c;
+            a.dx[at] = bf16_of(__builtin_fmaf(Dc, gy, o.d * slb));
+            a.ddt[at] = bf16_of(ddt);
+            if (a.z) a.dz[at] = bf16_of(dy * __builtin_fmaf(Dc, o.x, sy) * dsilu_f32(z, sz));
+          }
+          // Sums over the wave's channels.
+#pragma unroll
+          for (int j = 0; j < RN; ++j) {
+#pragma unroll
+            for (int x = 4; x < 64; x *= 2) dB[j] += __shfl_xor(dB[j], x), dC[j] += __shfl_xor(dC[j], x);
+          }
+          if (quad == 0) {
+            float* o2 = a.pbc + ((int64_t)wb * a.S + t) * (2 * NT) + n0;
+#pragma unroll
+            for (int j = 0; j < RN; ++j) o2[j] = dB[j], o2[NT + j] = dC[j];
+          }
+        }
+      }
+    }
+  }
+  float* pp = a.pparam + (int64_t)k * (a.N + 2) * a.cols;
+#pragma unroll
+  for (int r = 0; r < RC; ++r)
+#pragma unroll
+    for (int j = 0; j < RN; ++j)
+      if (n0 + j < a.N) pp[(int64_t)(n0 + j) * a.cols + col + r] = dA[r][j];
+  if (part < RC) {
+    pp[(int64_t)a.N * a.cols + col + mine] = dD;
+    pp[(int64_t)(a.N + 1) * a.cols + col + mine] = dbias;
+  }
+}
+
+// dA, dD and ddt_bias: the chunks' partial rows in order, summed in FP64.
+__global__ __launch_bounds__(256) void scan_param_sum_kernel(ScanArgs a) {
+  const int32_t col = blockIdx.x * 256 + threadIdx.x, n = blockIdx.y;
+  const int32_t g = col / (a.wpg * 64), i = col - g * a.wpg * 64;
+  if (col >= a.cols || i >= a.per) return;
+  const float* p = a.pparam + (int64_t)n * a.cols + col;
+  double sum = 0.0;
+  for (int32_t k = 0; k < a.chunks; ++k) sum += p[(int64_t)k * (a.N + 2) * a.cols];
+  const int64_t c = (int64_t)g * a.per + i;
+  if (n < a.N) param_put(a.dA, a.A_bf16, c * a.N + n, (float)sum);
+  else if (n == a.N) {
+    if (a.dD) param_put(a.dD, a.D_bf16, c, (float)sum);
+  } else if (a.dbias) {
+    param_put(a.dbias, a.bias_bf16, c, (float)sum);
+  }
+}
+
+// dB and dC: the partial rows of a group's channel blocks, in order.
+__global__ __launch_bounds__(256) void scan_bc_sum_kernel(ScanArgs a, int32_t bpg, int32_t NT) {
+  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t row = (int64_t)a.G * a.N;
+  if (e >= 2 * (int64_t)a.S * row) return;
+  const int64_t half = e / ((int64_t)a.S * row), q = e - half * a.S * row;
+  const int64_t t = q / row, gn = q - t * row, g = gn / a.N, n = gn - g * a.N;
+  const float* p = a.pbc + (g * bpg * a.S + t) * (2 * NT) + half * NT + n;
+  float sum = 0.0f;
+  for (int32_t b = 0; b < bpg; ++b) sum += p[(int64_t)b * a.S * 2 * NT];
+  (half ? a.dC : a.dB)[q] = bf16_of(sum);
+}
+
+// --------------------------------------------------------- single tokens --
+
+// One token a row: NL lanes hold a channel's states, four each.
+template <int NL>
+__global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs a) {
+  const int64_t e = (int64_t)blockIdx.x * (256 / NL) + threadIdx.x / NL;
+  const int32_t part = threadIdx.x % NL;
+  const bool there = e < (int64_t)a.S * a.C;
+  const int64_t row = there ? e / a.C : 0, c = there ? e - row * a.C : 0;
+  const int64_t slot = slot_of(a.index, row, a.slots);
+  float y = 0.0f, x = 0.0f;
+  if (there && slot >= 0) {
+    x = bf16_f32(a.x[row * a.xs + c]);
+    const float raw = bf16_f32(a.dt[row * a.dts + c]) +
+                      (a.bias ? param_at(a.bias, a.bias_bf16, c) : 0.0f);
+    const float d = step_size(a, raw);
+    const int64_t g = c / a.per;
+    float* h = a.state + (slot * a.C + c) * a.N;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int32_t n = 4 * part + j;
+      if (n < a.N) {
+        const float e2 = __builtin_amdgcn_exp2f(d * (param_at(a.A, a.A_bf16, c * a.N + n) * kLog2E));
+        const float v = __builtin_fmaf(e2, h[n], d * x * bf16_f32(a.B[row * a.Bs + g * a.N + n]));
+        h[n] = v;
+        y = __builtin_fmaf(bf16_f32(a.Cm[row * a.Cs + g * a.N + n]), v, y);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 1; o < NL; o *= 2) y += __shfl_xor(y, o);
+  if (there && part == 0) {
+    if (slot >= 0) {
+      if (a.D) y = __builtin_fmaf(param_at(a.D, a.D_bf16, c), x, y);
+      if (a.z) {
+        const float z = bf16_f32(a.z[row * a.zs + c]);
+        y *= z * sigmoid_f32(z);
+      }
+    }
+    a.y[row * a.C + c] = slot >= 0 ? bf16_of(y) : (uint16_t)0;
+  }
+}
+
+template <bool kOut>
+hipError_t fwd(const ScanArgs& a, int32_t chunks, hipStream_t s) {
+  const dim3 grid((uint32_t)((int64_t)a.G * a.wpg * chunks)), block(64);
+  switch (scan_states(a.N)) {
+    case 8: hipLaunchKernelGGL((scan_fwd_kernel<8, kOut>), grid, block, 0, s, a); break;
+    case 16: hipLaunchKernelGGL((scan_fwd_kernel<16, kOut>), grid, block, 0, s, a); break;
+    case 32: hipLaunchKernelGGL((scan_fwd_kernel<32, kOut>), grid, block, 0, s, a); break;
+    default: hipLaunchKernelGGL((scan_fwd_kernel<64, kOut>), grid, block, 0, s, a); break;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_scan_local(const ScanArgs& a, hipStream_t s) { return fwd<false>(a, a.chunks - 1, s); }
+hipError_t launch_scan_out(const ScanArgs& a, hipStream_t s) { return fwd<true>(a, a.chunks, s); }
+
+hipError_t launch_scan_join(const ScanArgs& a, bool backward, hipStream_t s) {
+  hipLaunchKernelGGL(scan_join_kernel, dim3((a.cols + 255) / 256, a.N, backward ? 2 : 1), dim3(256),
+                     0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_scan_bwd_local(const ScanArgs& a, hipStream_t s) {
+  const dim3 grid((uint32_t)((int64_t)a.G * a.wpg * a.chunks)), block(64);
+  switch (scan_states(a.N)) {
+    case 8: hipLaunchKernelGGL(scan_bwd_local_kernel<8>, grid, block, 0, s, a); break;
+    case 16: hipLaunchKernelGGL(scan_bwd_local_kernel<16>, grid, block, 0, s, a); break;
+    case 32: hipLaunchKernelGGL(scan_bwd_local_kernel<32>, grid, block, 0, s, a); break;
+    default: hipLaunchKernelGGL(scan_bwd_local_kernel<64>, grid, block, 0, s, a); break;
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_scan_bwd_main(const ScanArgs& a, hipStream_t s) {
+  const int32_t cb = scan_bwd_channels(a.N), bpg = (a.per + cb - 1) / cb;
+  const dim3 grid((uint32_t)((int64_t)a.G * bpg * a.chunks)), block(64);
+  switch (scan_states(a.N)) {
+    case 8: hipLaunchKernelGGL(scan_bwd_main_kernel<8>, grid, block, 0, s, a); break;
+    case 16: hipLaunchKernelGGL(scan_bwd_main_kernel<16>, grid, block, 0, s, a); break;
+    case 32: hipLaunchKernelGGL(scan_bwd_main_kernel<32>, grid, block, 0, s, a); break;
+    default: hipLaunchKernelGGL(scan_bwd_main_kernel<64>, grid, block, 0, s, a); break;
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_scan_bwd_sum(const ScanArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL(scan_param_sum_kernel, dim3((a.cols + 255) / 256, a.N + 2), dim3(256), 0, s, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int32_t cb = scan_bwd_channels(a.N), bpg = (a.per + cb - 1) / cb;
+  const int64_t n = 2 * (int64_t)a.S * a.G * a.N;
+  if (n == 0) return hipSuccess;
+  hipLaunchKernelGGL(scan_bc_sum_kernel, dim3((uint32_t)((n + 255) / 256)), dim3(256), 0, s, a, bpg,
+                     scan_states(a.N));
+  return hipGetLastError();
+}
+
+hipError_t launch_scan_step(const ScanArgs& a, hipStream_t s) {
+  const int64_t n = (int64_t)a.S * a.C;
+  const int nl = a.N <= 4 ? 1 : a.N <= 8 ? 2 : a.N <= 16 ? 4 : a.N <= 32 ? 8 : 16;
+  const dim3 grid((uint32_t)((n + 256 / nl - 1) / (256 / nl))), block(256);
+  switch (nl) {
+    case 1: hipLaunchKernelGGL(scan_step_kernel<1>, grid, block, 0, s, a); break;
+    case 2: hipLaunchKernelGGL(scan_step_kernel<2>, grid, block, 0, s, a); break;
+    case 4: hipLaunchKernelGGL(scan_step_kernel<4>, grid, block, 0, s, a); break;
+    case 8: hipLaunchKernelGGL(scan_step_kernel<8>, grid, block, 0, s, a); break;
+    default: hipLaunchKernelGGL(scan_step_kernel<16>, grid, block, 0, s, a); break;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace vdc

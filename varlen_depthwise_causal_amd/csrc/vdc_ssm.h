@@ -1,0 +1,117 @@
+// Internal interface between the host entry points (vdc_ssm_api.cpp) and the
+// kernels of the state space layer (vdc_conv_state.hip, vdc_scan.hip,
+// vdc_norm.hip).  Not installed; include/vdc.h is the ABI.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include <hip/hip_runtime_api.h>
+
+namespace vdc {
+
+// ------------------------------------------- convolution, carried state --
+
+struct ConvStateArgs {
+  const uint16_t* x;      // [rows][C], x_stride elements between rows
+  uint16_t* y;            // [rows][C] dense
+  const void* w;          // [C][4]
+  const void* b;          // [C] or null
+  uint16_t* state;        // [slots][3][C]
+  const int32_t* index;   // slot of each sequence, or null: its own number
+  const int32_t* cu;      // prompts: prefix sums
+  const uint8_t* resume;  // prompts: documents that go on from their slot
+  int64_t rows;
+  int64_t C;
+  int64_t x_stride;
+  int64_t slots;
+  int32_t w_bf16;
+  int32_t b_bf16;
+};
+
+hipError_t launch_conv_step(const ConvStateArgs& a, hipStream_t s);
+hipError_t launch_conv_edges(const ConvStateArgs& a, int64_t docs, hipStream_t s);
+
+// -------------------------------------------------------- selective scan --
+
+// Largest number of states a channel may have.
+constexpr int kMaxStates = 64;
+// Backward: tokens between two kept states, and the longest chunk (its
+// document starts are a bitmask in LDS).
+constexpr int kScanKeep = 16;
+constexpr int kScanMaxChunk = 2048;
+
+struct ScanArgs {
+  const uint16_t *x, *dt, *z, *B, *Cm, *dy;
+  int64_t xs, dts, zs, Bs, Cs, dys;  // elements between rows
+  const void *A, *D, *bias;          // [C][N], [C], [C]
+  int32_t A_bf16, D_bf16, bias_bf16;
+  int32_t softplus;
+  const int32_t* cu;
+  int32_t num_docs;
+  int32_t S, C, N, G;
+  // Channels by waves of 64 within a group: column (g, i) of the workspace
+  // rows is g * wpg * 64 + i, for channel g * per + i.
+  int32_t per;             // C / G
+  int32_t wpg;             // waves of 64 channels a group takes
+  int32_t cols;            // G * wpg * 64
+  int32_t chunk, chunks;   // tokens a chunk holds, chunks of the packed row
+  float* state;            // [slots][C][N]
+  const int32_t* index;
+  const uint8_t* resume;
+  int64_t slots;
+  uint16_t* y;
+  uint16_t *dx, *ddt, *dz, *dB, *dC;
+  void *dA, *dD, *dbias;
+  // workspace
+  float* hend;             // [chunks][N][cols] state after each chunk
+  float* mu;               // [chunks][N][cols] gradient that leaves each chunk to its left
+  float* sum;              // [chunks][cols] sum of the step sizes of each chunk
+  float* snap;             // [chunks][N][cols] state a resumed document began with
+  int32_t* flags;          // [chunks] bit 0: a document starts at the chunk's first token, 1: inside
+  float* keep;             // [chunks * chunk / kScanKeep][N + 1][cols]
+  float* pparam;           // [chunks][N + 2][cols] partial dA, dD, ddt_bias
+  float* pbc;              // [G * bpg][S][2][NT] partial dB, dC
+};
+
+// States rounded up to what the kernels are built for.
+inline int scan_states(int64_t N) { return N <= 8 ? 8 : N <= 16 ? 16 : N <= 32 ? 32 : 64; }
+// Channels one wave of the backward's main kernel covers.
+inline int scan_bwd_channels(int64_t N) {
+  const int nt = scan_states(N);
+  return nt <= 16 ? 64 : nt == 32 ? 32 : 16;
+}
+
+hipError_t launch_scan_local(const ScanArgs& a, hipStream_t s);
+hipError_t launch_scan_join(const ScanArgs& a, bool backward, hipStream_t s);
+hipError_t launch_scan_out(const ScanArgs& a, hipStream_t s);
+hipError_t launch_scan_bwd_local(const ScanArgs& a, hipStream_t s);
+hipError_t launch_scan_bwd_main(const ScanArgs& a, hipStream_t s);
+hipError_t launch_scan_bwd_sum(const ScanArgs& a, hipStream_t s);
+hipError_t launch_scan_step(const ScanArgs& a, hipStream_t s);
+
+// ------------------------------------------------------------ group norm --
+
+struct NormArgs {
+  const uint16_t *x, *z, *dy;
+  int64_t xs, zs, dys;
+  const void *w, *b;
+  int32_t w_bf16, b_bf16;
+  int32_t G, per;          // groups, channels of a group
+  int64_t S, C;
+  float eps;
+  uint16_t *y, *dx, *dz;
+  void *dw, *db;
+  float* part;             // [prows][2][C]
+  int32_t prows;
+};
+
+// Largest group, in channels.
+constexpr int kNormMaxGroup = 16384;
+
+hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t s);
+hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s);
+hipError_t launch_norm_bwd_sum(const NormArgs& a, hipStream_t s);
+int norm_bwd_rows(int64_t S, int64_t C, int64_t G);
+
+}  // namespace vdc
