@@ -41,14 +41,63 @@ __device__ __forceinline__ float step_size(const ScanArgs& a, float raw) {
   return a.softplus ? softplus_f32(raw) : raw;
 }
 
+// Neighbouring workgroups go to different XCDs; this hands each XCD a
+// contiguous range of the work instead, so that the cache lines two waves
+// share at their channels' border, and the rows of B and C that all waves of
+// a chunk read, meet in one L2.  The grid is a multiple of kXcds (padded);
+// -1: no work.
+constexpr uint32_t kXcds = 8;
+__device__ __forceinline__ int32_t place_of(int32_t work) {
+  const uint32_t p = (blockIdx.x % kXcds) * (gridDim.x / kXcds) + blockIdx.x / kXcds;
+  return p < (uint32_t)work ? (int32_t)p : -1;
+}
+
+// ------------------------------------------- B and C of one token, uniform --
+//
+// Every lane of a wave needs the same N values of B and of C, so they live in
+// scalar registers.  kWide: the states are exactly NT and a row's values start
+// at a multiple of 4 bytes: scalar loads of whole dwords, split into FP32 by
+// the scalar unit.  Otherwise lane n loads state n and the values are read
+// out of the lanes, two VALU instructions a state and token more.
+
+typedef const __attribute__((address_space(4))) uint32_t* scalar_ptr;
+
+template <int NT, bool kWide>
+struct Uniform;
+
+template <int NT>
+struct Uniform<NT, true> {
+  uint32_t v[NT / 2];
+  __device__ __forceinline__ void load(const uint16_t* row, int32_t) {
+    scalar_ptr p = (scalar_ptr)(uintptr_t)row;
+#pragma unroll
+    for (int i = 0; i < NT / 2; ++i) v[i] = p[i];
+  }
+  __device__ __forceinline__ float get(int n) const {
+    return n % 2 ? bf16_hi(v[n / 2]) : bf16_lo(v[n / 2]);
+  }
+};
+
+template <int NT>
+struct Uniform<NT, false> {
+  float v;
+  __device__ __forceinline__ void load(const uint16_t* row, int32_t N) {
+    const int32_t lane = (int32_t)(threadIdx.x & 63);
+    v = lane < N ? bf16_f32(row[lane]) : 0.0f;
+  }
+  __device__ __forceinline__ float get(int n) const {
+    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), n));
+  }
+};
+
 // ---------------------------------------------- forward, lane = channel --
 
 // A lane's channel: column of the workspace rows, channel, and whether the
 // channel exists (a group's last wave may have lanes past it; they run on
 // its first channel's addresses and store nothing).
 struct Column {
-  int32_t group, col;
-  int64_t c;
+  int32_t group;
+  uint32_t col, c;  // unsigned: 32-bit offsets from uniform addresses
   bool active;
 };
 
@@ -56,35 +105,65 @@ __device__ __forceinline__ Column column_of(const ScanArgs& a, int32_t wave) {
   Column o;
   o.group = wave / a.wpg;
   const int32_t i = (wave - o.group * a.wpg) * 64 + (int32_t)(threadIdx.x & 63);
-  o.col = wave * 64 + (int32_t)(threadIdx.x & 63);
+  o.col = (uint32_t)wave * 64u + (threadIdx.x & 63u);
   o.active = i < a.per;
-  o.c = (int64_t)o.group * a.per + (o.active ? i : 0);
+  o.c = (uint32_t)(o.group * a.per + (o.active ? i : 0));
   return o;
 }
 
+// A's row of a channel times log2(e); 0 past the last state.
 template <int NT>
 __device__ __forceinline__ void load_decay(const ScanArgs& a, const Column& l, float (&A2)[NT]) {
+  const int64_t at = (int64_t)l.c * a.N;
+  if (a.A_bf16) {
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
-    A2[n] = n < a.N ? param_at(a.A, a.A_bf16, l.c * a.N + n) * kLog2E : 0.0f;
+    for (int n = 0; n < NT; ++n)
+      A2[n] = bf16_f32(static_cast<const uint16_t*>(a.A)[at + min(n, a.N - 1)]);
+  } else {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) A2[n] = static_cast<const float*>(a.A)[at + min(n, a.N - 1)];
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n) A2[n] = n < a.N ? A2[n] * kLog2E : 0.0f;
 }
+
+// A value the compiler must not compute addresses from ahead of its use: the
+// rare paths' addresses would otherwise be held in registers over the loops.
+__device__ __forceinline__ uint32_t here(uint32_t v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+__device__ __forceinline__ int32_t here_uniform(int32_t v) {
+  asm volatile("" : "+s"(v));
+  return v;
+}
+
+// Tokens whose activations are requested together, a group ahead.
+constexpr int kAhead = 4;
 
 // One pass over a chunk.  kOut = false: the state after the chunk from zero
 // history (or a document's own start), the sum of the step sizes, and what a
 // resumed document that runs past the chunk began with.  kOut = true: the
 // outputs, from the joined states.
-template <int NT, bool kOut>
-__global__ __launch_bounds__(64) void scan_fwd_kernel(ScanArgs a) {
+template <int NT, bool kOut, bool kWide>
+__global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(NT <= 16 ? 4 : NT == 32 ? 2 : 1)))
+void scan_fwd_kernel(ScanArgs a, int32_t work) {
+  const int32_t place = place_of(work);
+  if (place < 0) return;
   const int32_t waves = a.G * a.wpg;
-  const int32_t k = blockIdx.x / waves, w = blockIdx.x - k * waves;
+  const int32_t k = place / waves, w = place - k * waves;
   const Column l = column_of(a, w);
   const int32_t t0 = k * a.chunk;
   const int32_t t1 = (int32_t)min((int64_t)a.S, (int64_t)t0 + a.chunk);
-  const int64_t ws = ((int64_t)k * a.N) * a.cols + l.col;  // this chunk's rows of the workspace
+  // Row n of a chunk's states in the workspace.
+  auto row = [&](float* base, int32_t chunk, int n) {
+    return base + ((int64_t)chunk * a.N + n) * a.cols;
+  };
   float A2[NT], h[NT];
   load_decay<NT>(a, l, A2);
   const float Dc = a.D ? param_at(a.D, a.D_bf16, l.c) : 0.0f;
   const float bias = a.bias ? param_at(a.bias, a.bias_bf16, l.c) : 0.0f;
+  const bool gated = kOut && a.z != nullptr;
   float sum = 0.0f;
   int32_t flags = 0;
 #pragma unroll
@@ -100,7 +179,7 @@ __global__ __launch_bounds__(64) void scan_fwd_kernel(ScanArgs a) {
       if (kOut && a.state && l.active) {
         const int64_t slot = slot_of(a.index, d, a.slots);
         if (slot >= 0 && !(a.resume && a.resume[d]))
-          for (int n = 0; n < a.N; ++n) a.state[(slot * a.C + l.c) * a.N + n] = 0.0f;
+          for (int n = 0; n < a.N; ++n) (a.state + slot * a.C * a.N)[here(l.c) * a.N + n] = 0.0f;
       }
       ++d;
     }
@@ -116,17 +195,116 @@ __global__ __launch_bounds__(64) void scan_fwd_kernel(ScanArgs a) {
         // still have to read it: a document that runs past its first chunk
         // has its start copied by the first pass and read from there.
         const bool past = next > t1;
+        const uint32_t col = here(l.col);
+        const int32_t kk = here_uniform(k), N = here_uniform(a.N);
+        if (kOut && past) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-          if (n < a.N) {
-            if (kOut && past) h[n] = a.snap[ws + (int64_t)n * a.cols];
-            else if (l.active) h[n] = a.state[(slot * a.C + l.c) * a.N + n];
-            if (!kOut && past) a.snap[ws + (int64_t)n * a.cols] = h[n];
+          for (int n = 0; n < NT; ++n)
+            if (n < N) h[n] = row(a.snap, kk, n)[col];
+        } else {
+          const float* s = a.state + slot * a.C * a.N + here(l.c) * (uint32_t)a.N;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            if (n < N) h[n] = s[n];
+          if (past) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              if (n < N) row(a.snap, kk, n)[col] = h[n];
           }
+        }
       }
     }
   };
+  auto close = [&]() {
+    if (kOut && a.state && l.active) {
+      const int64_t slot = slot_of(a.index, doc, a.slots);
+      if (slot >= 0) {
+        const int32_t N = here_uniform(a.N);
+        float* s = a.state + slot * a.C * N + here(l.c) * (uint32_t)N;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          if (n < N) s[n] = h[n];
+      }
+    }
+    if (t < t1 || t == a.S) open(doc + 1);
+  };
 
+  // Activations are requested kAhead tokens ahead, B and C one token ahead;
+  // past the chunk the last token's are requested again.
+  struct Raw {
+    uint16_t x, dt, z;
+  };
+  const uint16_t* px = a.x + t0 * a.xs;
+  const uint16_t* pd = a.dt + t0 * a.dts;
+  const uint16_t* pz = gated ? a.z + t0 * a.zs : nullptr;
+  const uint16_t* pB = a.B + t0 * a.Bs + l.group * a.N;
+  const uint16_t* pC = a.Cm + t0 * a.Cs + l.group * a.N;
+  uint16_t* py = kOut ? a.y + (int64_t)t0 * a.C : nullptr;
+  int32_t left = t1 - t0;  // tokens not requested yet, and as many of B and C
+  int32_t left_bc = left;
+  auto request = [&]() {
+    Raw r;
+    r.x = px[l.c];
+    r.dt = pd[l.c];
+    r.z = gated ? pz[l.c] : (uint16_t)0;
+    --left;
+    px += left > 0 ? a.xs : 0;
+    pd += left > 0 ? a.dts : 0;
+    if (gated) pz += left > 0 ? a.zs : 0;
+    return r;
+  };
+  struct Rows {
+    Uniform<NT, kWide> B, C;
+  };
+  auto request_bc = [&]() {
+    Rows r;
+    r.B.load(pB, a.N);
+    if (kOut) r.C.load(pC, a.N);
+    --left_bc;
+    pB += left_bc > 0 ? a.Bs : 0;
+    if (kOut) pC += left_bc > 0 ? a.Cs : 0;
+    return r;
+  };
+  // One token.  `now` has its B and C, `then` receives the next token's:
+  // scalar loads complete in no order, so the wait for `now` is placed before
+  // `then` is requested, and nothing waits for `then` until its own token.
+  auto token = [&](const Raw& r, const Rows& now, Rows& then) {
+    if (kWide) {
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+      then = request_bc();
+      __builtin_amdgcn_sched_barrier(0);
+    } else {
+      then = request_bc();
+    }
+    const float x = bf16_f32(r.x);
+    const float d = step_size(a, bf16_f32(r.dt) + bias);
+    const float dx = d * x;
+    float y = Dc * x;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      h[n] = __builtin_fmaf(__builtin_amdgcn_exp2f(d * A2[n]), h[n], dx * now.B.get(n));
+      if (kOut) y = __builtin_fmaf(now.C.get(n), h[n], y);
+    }
+    if (kOut) {
+      if (gated) {
+        const float z = bf16_f32(r.z);
+        y *= z * sigmoid_f32(z);
+      }
+      if (l.active) py[l.c] = bf16_of(y);
+      py += a.C;
+    } else {
+      sum += d;
+    }
+  };
+
+  Raw q[kAhead];
+  Rows bc[2];
+  if (t0 < t1) {
+    bc[0] = request_bc();
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) q[i] = request();
+  }
   const int32_t i = first_at_least(a.cu, a.num_docs + 1, t0);
   if (i <= a.num_docs && a.cu[i] == t0) {
     open(i);
@@ -136,54 +314,41 @@ __global__ __launch_bounds__(64) void scan_fwd_kernel(ScanArgs a) {
     if (kOut && k > 0) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
-        if (n < a.N) h[n] = a.hend[ws + ((int64_t)n - a.N) * a.cols];
+        if (n < a.N) h[n] = row(a.hend, k - 1, n)[l.col];
     }
   }
 
+#pragma unroll 1
   while (t < t1) {
     const int32_t end = next > t && next < t1 ? next : t1;
+    static_assert(kAhead % 2 == 0, "two rows of B and C in turn");
+#pragma unroll 1
+    for (; t + kAhead <= end; t += kAhead) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const Raw r = q[i];
+        q[i] = request();
+        token(r, bc[i % 2], bc[1 - i % 2]);
+      }
+    }
+#pragma unroll 1
     for (; t < end; ++t) {
-      const float x = l.active ? bf16_f32(a.x[t * a.xs + l.c]) : 0.0f;
-      const float raw = bf16_f32(a.dt[t * a.dts + l.c]) + bias;
-      const float d = l.active ? step_size(a, raw) : 0.0f;
-      const float dx = d * x;
-      const uint16_t* B = a.B + t * a.Bs + l.group * a.N;
-      const uint16_t* Cm = a.Cm + t * a.Cs + l.group * a.N;
-      float y = Dc * x;
+      const Raw r = q[0];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float b = n < a.N ? bf16_f32(B[n]) : 0.0f;
-        const float e = __builtin_amdgcn_exp2f(d * A2[n]);
-        h[n] = __builtin_fmaf(e, h[n], dx * b);
-        if (kOut) y = __builtin_fmaf(n < a.N ? bf16_f32(Cm[n]) : 0.0f, h[n], y);
-      }
-      if (kOut) {
-        if (a.z) {
-          const float z = bf16_f32(a.z[t * a.zs + l.c]);
-          y *= z * sigmoid_f32(z);
-        }
-        if (l.active) a.y[(int64_t)t * a.C + l.c] = bf16_of(y);
-      } else {
-        sum += d;
-      }
+      for (int i = 0; i + 1 < kAhead; ++i) q[i] = q[i + 1];
+      q[kAhead - 1] = request();
+      token(r, bc[0], bc[1]);
+      bc[0] = bc[1];
     }
-    if (t == next && doc >= 0 && doc < a.num_docs) {
-      if (kOut && a.state && l.active) {
-        const int64_t slot = slot_of(a.index, doc, a.slots);
-        if (slot >= 0) {
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-            if (n < a.N) a.state[(slot * a.C + l.c) * a.N + n] = h[n];
-        }
-      }
-      if (t < t1 || t == a.S) open(doc + 1);
-    }
+    if (t == next && doc >= 0 && doc < a.num_docs) close();
   }
   if (!kOut) {
+    const int32_t kk = here_uniform(k), N = here_uniform(a.N);
+    const uint32_t col = here(l.col);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
-      if (n < a.N) a.hend[ws + (int64_t)n * a.cols] = h[n];
-    a.sum[(int64_t)k * a.cols + l.col] = sum;
+      if (n < N) row(a.hend, kk, n)[col] = h[n];
+    (a.sum + (int64_t)k * a.cols)[l.col] = sum;
     if (w == 0 && threadIdx.x == 0) a.flags[k] = flags;
   }
 }
@@ -649,14 +814,29 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs a) {
   }
 }
 
+// Whether B's and C's rows can be read by whole dwords (see Uniform).
+bool wide_rows(const ScanArgs& a) {
+  const auto even = [](const uint16_t* p, int64_t stride) {
+    return reinterpret_cast<uintptr_t>(p) % 4 == 0 && stride % 2 == 0;
+  };
+  return a.N == scan_states(a.N) && even(a.B, a.Bs) && even(a.Cm, a.Cs);
+}
+
+template <int NT, bool kOut>
+void fwd_nt(const ScanArgs& a, int32_t work, hipStream_t s) {
+  const dim3 grid((uint32_t)((work + (int32_t)kXcds - 1) / (int32_t)kXcds * (int32_t)kXcds)), block(64);
+  if (wide_rows(a)) hipLaunchKernelGGL((scan_fwd_kernel<NT, kOut, true>), grid, block, 0, s, a, work);
+  else hipLaunchKernelGGL((scan_fwd_kernel<NT, kOut, false>), grid, block, 0, s, a, work);
+}
+
 template <bool kOut>
 hipError_t fwd(const ScanArgs& a, int32_t chunks, hipStream_t s) {
-  const dim3 grid((uint32_t)((int64_t)a.G * a.wpg * chunks)), block(64);
+  const int32_t work = a.G * a.wpg * chunks;
   switch (scan_states(a.N)) {
-    case 8: hipLaunchKernelGGL((scan_fwd_kernel<8, kOut>), grid, block, 0, s, a); break;
-    case 16: hipLaunchKernelGGL((scan_fwd_kernel<16, kOut>), grid, block, 0, s, a); break;
-    case 32: hipLaunchKernelGGL((scan_fwd_kernel<32, kOut>), grid, block, 0, s, a); break;
-    default: hipLaunchKernelGGL((scan_fwd_kernel<64, kOut>), grid, block, 0, s, a); break;
+    case 8: fwd_nt<8, kOut>(a, work, s); break;
+    case 16: fwd_nt<16, kOut>(a, work, s); break;
+    case 32: fwd_nt<32, kOut>(a, work, s); break;
+    default: fwd_nt<64, kOut>(a, work, s); break;
   }
   return hipGetLastError();
 }

@@ -178,7 +178,7 @@ bool scan_plan(int dir, int64_t S, int64_t C, int64_t N, int64_t G, ScanPlan* ou
   chunk = std::max(kScanMinChunk, ceil_div(chunk, kScanKeep) * kScanKeep);
   if (dir == VDC_BWD) chunk = std::min<int64_t>(chunk, kScanMaxChunk);
   const int64_t chunks = std::max<int64_t>(1, ceil_div(S, chunk));
-  if (chunk > INT32_MAX || chunks * std::max(blocks, waves) > kMaxGrid) return false;
+  if (chunk > INT32_MAX || chunks * std::max(blocks, waves) > kMaxGrid - 8) return false;
   out->wpg = (int32_t)wpg;
   out->cols = (int32_t)(waves * 64);
   out->chunk = (int32_t)chunk;
