@@ -315,6 +315,7 @@ typedef struct vdc_scan {
     const void *z;    /* bf16 [S][C], or NULL: no gate                       */
     const void *B;    /* bf16 [S][groups][N], a row dense                    */
     const void *Cm;   /* bf16 [S][groups][N], a row dense                    */
+    /* x_stride, dt_stride, z_stride: below 2^19, or 4 C where that is more. */
     int64_t x_stride, dt_stride, z_stride, B_stride, C_stride;
     const void *A;       /* [C][N]; a decay has A < 0                        */
     const void *D;       /* [C] or NULL                                      */

@@ -24,6 +24,31 @@
 namespace vdc {
 namespace {
 
+typedef const __attribute__((address_space(4))) uint32_t* scalar_ptr;
+
+// Entry i of an int32 array the whole wave asks for, in a scalar register.
+__device__ __forceinline__ int32_t uniform_at(const int32_t* p, int32_t i) {
+  return (int32_t)((scalar_ptr)(uintptr_t)p)[i];
+}
+// A value that is the same in all lanes, back in scalar registers: where
+// control flow joins the compiler may have moved it to vector registers.
+__device__ __forceinline__ const uint16_t* uniform(const uint16_t* p) {
+  const uint64_t v = (uint64_t)(uintptr_t)p;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return (const uint16_t*)(uintptr_t)(((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Whether document d resumes, and its slot (-1: none).
+__device__ __forceinline__ bool resumes(const ScanArgs& a, int32_t d) {
+  return a.resume && __builtin_amdgcn_readfirstlane((int32_t)a.resume[d]) != 0;
+}
+__device__ __forceinline__ int64_t doc_slot(const ScanArgs& a, int32_t d) {
+  const int64_t s = a.index ? (int64_t)uniform_at(a.index, d) : (int64_t)d;
+  return s >= 0 && s < a.slots ? s : -1;
+}
+
 // First index i in [0, n) with cu[i] >= v (n if none), by a whole wave.
 __device__ __forceinline__ int32_t first_at_least(const int32_t* cu, int32_t n, int32_t v) {
   const int lane = (int)(threadIdx.x & 63);
@@ -37,19 +62,54 @@ __device__ __forceinline__ int32_t first_at_least(const int32_t* cu, int32_t n, 
   return __builtin_amdgcn_readfirstlane((int32_t)lo);
 }
 
-__device__ __forceinline__ float step_size(const ScanArgs& a, float raw) {
-  return a.softplus ? softplus_f32(raw) : raw;
+// The bias of a channel's step size, and times log2(e).
+struct StepBias {
+  float b, b2;
+};
+__device__ __forceinline__ StepBias step_bias(const ScanArgs& a, int64_t c) {
+  const float b = a.bias ? param_at(a.bias, a.bias_bf16, c) : 0.0f;
+  return StepBias{b, b * kLog2E};
+}
+__device__ __forceinline__ float step_size(const ScanArgs& a, float dt, const StepBias& b) {
+  return a.softplus ? softplus_f32(dt, b.b, b.b2) : dt + b.b;
 }
 
-// Neighbouring workgroups go to different XCDs; this hands each XCD a
-// contiguous range of the work instead, so that the cache lines two waves
-// share at their channels' border, and the rows of B and C that all waves of
-// a chunk read, meet in one L2.  The grid is a multiple of kXcds (padded);
-// -1: no work.
-constexpr uint32_t kXcds = 8;
+// One BF16 row of activations after another, addressed by a buffer resource
+// at the first of them: the lane's byte and a scalar offset per row, no
+// address arithmetic in the lanes.  The host keeps every offset below 2^31.
+struct RowBuffer {
+  __amdgpu_buffer_rsrc_t r;
+  uint32_t row, stride;  // byte offset of the current row, bytes between rows
+  __device__ __forceinline__ void open(const uint16_t* base, int64_t first, int64_t stride_) {
+    const uint16_t* p = base + first * stride_;
+    r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p), (short)0, 0x7fffffff, 0x00020000);
+    row = 0;
+    stride = (uint32_t)stride_ * 2u;
+  }
+  __device__ __forceinline__ uint16_t get(uint32_t lane2) const {
+    return __builtin_amdgcn_raw_buffer_load_b16(r, (int)lane2, (int)row, 0);
+  }
+  __device__ __forceinline__ void put(uint32_t lane2, uint16_t v) const {
+    __builtin_amdgcn_raw_buffer_store_b16(v, r, (int)lane2, (int)row, 0);
+  }
+};
+
+// The piece of work of a wave, -1: none.  Neighbouring workgroups go to
+// different XCDs; this hands each XCD a contiguous range of the work instead,
+// so that the cache lines two waves share at their channels' border, and the
+// rows of B and C that all waves of a chunk read, meet in one L2.  The waves
+// are independent of each other, but come kWaves to a workgroup: those of one
+// workgroup go to the four SIMDs of a CU in turn, where single waves crowd
+// some SIMDs, which then finish last.  The grid is a multiple of kXcds.
+constexpr uint32_t kXcds = 8, kWaves = 4;
 __device__ __forceinline__ int32_t place_of(int32_t work) {
-  const uint32_t p = (blockIdx.x % kXcds) * (gridDim.x / kXcds) + blockIdx.x / kXcds;
+  const uint32_t p = ((blockIdx.x % kXcds) * (gridDim.x / kXcds) + blockIdx.x / kXcds) * kWaves +
+                     __builtin_amdgcn_readfirstlane(threadIdx.x / 64u);
   return p < (uint32_t)work ? (int32_t)p : -1;
+}
+inline uint32_t place_grid(int64_t work) {
+  const int64_t blocks = (work + kWaves - 1) / kWaves;
+  return (uint32_t)((blocks + kXcds - 1) / kXcds * kXcds);
 }
 
 // ------------------------------------------- B and C of one token, uniform --
@@ -59,8 +119,6 @@ __device__ __forceinline__ int32_t place_of(int32_t work) {
 // at a multiple of 4 bytes: scalar loads of whole dwords, split into FP32 by
 // the scalar unit.  Otherwise lane n loads state n and the values are read
 // out of the lanes, two VALU instructions a state and token more.
-
-typedef const __attribute__((address_space(4))) uint32_t* scalar_ptr;
 
 template <int NT, bool kWide>
 struct Uniform;
@@ -72,6 +130,11 @@ struct Uniform<NT, true> {
     scalar_ptr p = (scalar_ptr)(uintptr_t)row;
 #pragma unroll
     for (int i = 0; i < NT / 2; ++i) v[i] = p[i];
+  }
+  // Keeps the values in scalar registers where control flow joins.
+  __device__ __forceinline__ void pin() {
+#pragma unroll
+    for (int i = 0; i < NT / 2; ++i) v[i] = __builtin_amdgcn_readfirstlane(v[i]);
   }
   __device__ __forceinline__ float get(int n) const {
     return n % 2 ? bf16_hi(v[n / 2]) : bf16_lo(v[n / 2]);
@@ -85,6 +148,7 @@ struct Uniform<NT, false> {
     const int32_t lane = (int32_t)(threadIdx.x & 63);
     v = lane < N ? bf16_f32(row[lane]) : 0.0f;
   }
+  __device__ __forceinline__ void pin() {}
   __device__ __forceinline__ float get(int n) const {
     return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), n));
   }
@@ -138,16 +202,15 @@ __device__ __forceinline__ int32_t here_uniform(int32_t v) {
   return v;
 }
 
-// Tokens whose activations are requested together, a group ahead.
-constexpr int kAhead = 4;
-
 // One pass over a chunk.  kOut = false: the state after the chunk from zero
 // history (or a document's own start), the sum of the step sizes, and what a
 // resumed document that runs past the chunk began with.  kOut = true: the
 // outputs, from the joined states.
 template <int NT, bool kOut, bool kWide>
-__global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(NT <= 16 ? 4 : NT == 32 ? 2 : 1)))
+__global__ __launch_bounds__(64 * kWaves)
+__attribute__((amdgpu_waves_per_eu(NT <= 16 ? 4 : NT == 32 ? 2 : 1)))
 void scan_fwd_kernel(ScanArgs a, int32_t work) {
+  constexpr int kAhead = NT <= 16 ? 8 : 4;
   const int32_t place = place_of(work);
   if (place < 0) return;
   const int32_t waves = a.G * a.wpg;
@@ -162,7 +225,7 @@ void scan_fwd_kernel(ScanArgs a, int32_t work) {
   float A2[NT], h[NT];
   load_decay<NT>(a, l, A2);
   const float Dc = a.D ? param_at(a.D, a.D_bf16, l.c) : 0.0f;
-  const float bias = a.bias ? param_at(a.bias, a.bias_bf16, l.c) : 0.0f;
+  const StepBias bias = step_bias(a, l.c);
   const bool gated = kOut && a.z != nullptr;
   float sum = 0.0f;
   int32_t flags = 0;
@@ -175,21 +238,21 @@ void scan_fwd_kernel(ScanArgs a, int32_t work) {
   // (whose slots hold an empty sequence's state, zero, unless they resume)
   // and begins the next.
   auto open = [&](int32_t d) {
-    while (d < a.num_docs && a.cu[d + 1] <= t) {
+    while (d < a.num_docs && uniform_at(a.cu, d + 1) <= t) {
       if (kOut && a.state && l.active) {
-        const int64_t slot = slot_of(a.index, d, a.slots);
-        if (slot >= 0 && !(a.resume && a.resume[d]))
+        const int64_t slot = doc_slot(a, d);
+        if (slot >= 0 && !resumes(a, d))
           for (int n = 0; n < a.N; ++n) (a.state + slot * a.C * a.N)[here(l.c) * a.N + n] = 0.0f;
       }
       ++d;
     }
     doc = d;
-    next = d < a.num_docs ? a.cu[d + 1] : INT32_MAX;
+    next = d < a.num_docs ? uniform_at(a.cu, d + 1) : INT32_MAX;
 #pragma unroll
     for (int n = 0; n < NT; ++n) h[n] = 0.0f;
     flags |= t == t0 ? 1 : 2;
-    if (a.state && d < a.num_docs && a.resume && a.resume[d]) {
-      const int64_t slot = slot_of(a.index, d, a.slots);
+    if (a.state && d < a.num_docs && resumes(a, d)) {
+      const int64_t slot = doc_slot(a, d);
       if (slot >= 0) {
         // The chunk that ends a document writes its slot while others may
         // still have to read it: a document that runs past its first chunk
@@ -217,7 +280,7 @@ void scan_fwd_kernel(ScanArgs a, int32_t work) {
   };
   auto close = [&]() {
     if (kOut && a.state && l.active) {
-      const int64_t slot = slot_of(a.index, doc, a.slots);
+      const int64_t slot = doc_slot(a, doc);
       if (slot >= 0) {
         const int32_t N = here_uniform(a.N);
         float* s = a.state + slot * a.C * N + here(l.c) * (uint32_t)N;
@@ -229,28 +292,33 @@ void scan_fwd_kernel(ScanArgs a, int32_t work) {
     if (t < t1 || t == a.S) open(doc + 1);
   };
 
-  // Activations are requested kAhead tokens ahead, B and C one token ahead;
+  // Activations are requested kAhead tokens ahead (as many tokens as the loop
+  // below is unrolled by), B and C one token ahead;
   // past the chunk the last token's are requested again.
   struct Raw {
     uint16_t x, dt, z;
   };
-  const uint16_t* px = a.x + t0 * a.xs;
-  const uint16_t* pd = a.dt + t0 * a.dts;
-  const uint16_t* pz = gated ? a.z + t0 * a.zs : nullptr;
+  RowBuffer bx, bd, bz, by;
+  bx.open(a.x, t0, a.xs);
+  bd.open(a.dt, t0, a.dts);
+  bz.open(gated ? a.z : a.x, t0, gated ? a.zs : a.xs);  // without a gate nothing uses it
+  by.open(a.y, t0, a.C);
+  // Past a group's channels a lane's stores are out of the buffer's range,
+  // which drops them.
+  const uint32_t lane2 = l.c * 2u, put2 = l.active ? lane2 : 0x80000000u;
   const uint16_t* pB = a.B + t0 * a.Bs + l.group * a.N;
   const uint16_t* pC = a.Cm + t0 * a.Cs + l.group * a.N;
-  uint16_t* py = kOut ? a.y + (int64_t)t0 * a.C : nullptr;
   int32_t left = t1 - t0;  // tokens not requested yet, and as many of B and C
   int32_t left_bc = left;
   auto request = [&]() {
     Raw r;
-    r.x = px[l.c];
-    r.dt = pd[l.c];
-    r.z = gated ? pz[l.c] : (uint16_t)0;
+    r.x = bx.get(lane2);
+    r.dt = bd.get(lane2);
+    if (kOut) r.z = bz.get(lane2);
     --left;
-    px += left > 0 ? a.xs : 0;
-    pd += left > 0 ? a.dts : 0;
-    if (gated) pz += left > 0 ? a.zs : 0;
+    bx.row += left > 0 ? bx.stride : 0u;
+    bd.row += left > 0 ? bd.stride : 0u;
+    if (kOut) bz.row += left > 0 ? bz.stride : 0u;
     return r;
   };
   struct Rows {
@@ -278,7 +346,7 @@ void scan_fwd_kernel(ScanArgs a, int32_t work) {
       then = request_bc();
     }
     const float x = bf16_f32(r.x);
-    const float d = step_size(a, bf16_f32(r.dt) + bias);
+    const float d = step_size(a, bf16_f32(r.dt), bias);
     const float dx = d * x;
     float y = Dc * x;
 #pragma unroll
@@ -291,8 +359,8 @@ void scan_fwd_kernel(ScanArgs a, int32_t work) {
         const float z = bf16_f32(r.z);
         y *= z * sigmoid_f32(z);
       }
-      if (l.active) py[l.c] = bf16_of(y);
-      py += a.C;
+      by.put(put2, bf16_of(y));
+      by.row += by.stride;
     } else {
       sum += d;
     }
@@ -306,11 +374,11 @@ void scan_fwd_kernel(ScanArgs a, int32_t work) {
     for (int i = 0; i < kAhead; ++i) q[i] = request();
   }
   const int32_t i = first_at_least(a.cu, a.num_docs + 1, t0);
-  if (i <= a.num_docs && a.cu[i] == t0) {
+  if (i <= a.num_docs && uniform_at(a.cu, i) == t0) {
     open(i);
   } else {
     doc = i - 1;
-    next = doc >= 0 && doc < a.num_docs ? a.cu[doc + 1] : INT32_MAX;
+    next = doc >= 0 && doc < a.num_docs ? uniform_at(a.cu, doc + 1) : INT32_MAX;
     if (kOut && k > 0) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -324,6 +392,10 @@ void scan_fwd_kernel(ScanArgs a, int32_t work) {
     static_assert(kAhead % 2 == 0, "two rows of B and C in turn");
 #pragma unroll 1
     for (; t + kAhead <= end; t += kAhead) {
+      pB = uniform(pB);
+      pC = uniform(pC);
+      bc[0].B.pin();
+      if (kOut) bc[0].C.pin();
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         const Raw r = q[i];
@@ -349,34 +421,47 @@ void scan_fwd_kernel(ScanArgs a, int32_t work) {
     for (int n = 0; n < NT; ++n)
       if (n < N) row(a.hend, kk, n)[col] = h[n];
     (a.sum + (int64_t)k * a.cols)[l.col] = sum;
-    if (w == 0 && threadIdx.x == 0) a.flags[k] = flags;
+    if (w == 0 && (threadIdx.x & 63) == 0) a.flags[k] = flags;
   }
 }
 
 // Joins the chunks: forward in time the states after each chunk, and for the
 // backward (blockIdx.z = 1) against it the gradients that leave each chunk.
-__global__ __launch_bounds__(256) void scan_join_kernel(ScanArgs a) {
-  const int32_t col = blockIdx.x * 256 + threadIdx.x, n = blockIdx.y;
-  if (col >= a.cols) return;
+// A lane has one column and state; the chain is short, the loads are what
+// takes time, so those of kJoin chunks are requested at once.
+__global__ __launch_bounds__(64) void scan_join_kernel(ScanArgs a) {
+  constexpr int kJoin = 16;
+  const int32_t col = blockIdx.x * 64 + threadIdx.x, n = blockIdx.y;
   const int32_t g = col / (a.wpg * 64), i = col - g * a.wpg * 64;
   if (i >= a.per) return;
   const float A2 = param_at(a.A, a.A_bf16, ((int64_t)g * a.per + i) * a.N + n) * kLog2E;
   const bool back = blockIdx.z == 1;
   float* v = (back ? a.mu : a.hend) + (int64_t)n * a.cols + col;
   const int64_t row = (int64_t)a.N * a.cols;
+  const int32_t steps = a.chunks - 1;
   float carry = 0.0f;
-  for (int32_t s = 0; s < a.chunks - 1; ++s) {
-    const int32_t k = back ? a.chunks - 1 - s : s;
-    const int32_t f = a.flags[k];
-    const float own = v[k * row];
-    if (back && (f & 1)) {
-      carry = 0.0f;  // a document starts with the chunk: nothing leaves it
-    } else if (f == 0 && carry != 0.0f) {
-      carry = __builtin_fmaf(__builtin_amdgcn_exp2f(A2 * a.sum[(int64_t)k * a.cols + col]), carry, own);
-    } else {
-      carry = own;
+  for (int32_t s0 = 0; s0 < steps; s0 += kJoin) {
+    float own[kJoin], decay[kJoin];
+#pragma unroll
+    for (int j = 0; j < kJoin; ++j) {
+      const int32_t s = min(s0 + j, steps - 1), k = back ? a.chunks - 1 - s : s;
+      own[j] = v[k * row];
+      decay[j] = a.sum[(int64_t)k * a.cols + col];
     }
-    v[k * row] = carry;
+#pragma unroll
+    for (int j = 0; j < kJoin; ++j) {
+      if (s0 + j >= steps) break;
+      const int32_t k = back ? a.chunks - 1 - (s0 + j) : s0 + j;
+      const int32_t f = uniform_at(a.flags, k);
+      if (back && (f & 1)) {
+        carry = 0.0f;  // a document starts with the chunk: nothing leaves it
+      } else if (f == 0 && carry != 0.0f) {
+        carry = __builtin_fmaf(__builtin_amdgcn_exp2f(A2 * decay[j]), carry, own[j]);
+      } else {
+        carry = own[j];
+      }
+      v[k * row] = carry;
+    }
   }
 }
 
@@ -431,7 +516,7 @@ __global__ __launch_bounds__(64) void scan_bwd_local_kernel(ScanArgs a) {
   load_decay<NT>(a, l, A2);
 #pragma unroll
   for (int n = 0; n < NT; ++n) h[n] = 0.0f, mu[n] = 0.0f, p[n] = 1.0f;
-  const float bias = a.bias ? param_at(a.bias, a.bias_bf16, l.c) : 0.0f;
+  const StepBias bias = step_bias(a, l.c);
   float sum = 0.0f;
   int32_t flags = starts_at(m, 0) ? 1 : 0;
   bool first = true;  // still in the chunk's first document
@@ -451,8 +536,7 @@ __global__ __launch_bounds__(64) void scan_bwd_local_kernel(ScanArgs a) {
       for (int n = 0; n < NT; ++n) h[n] = 0.0f;
     }
     const float x = l.active ? bf16_f32(a.x[t * a.xs + l.c]) : 0.0f;
-    const float raw = bf16_f32(a.dt[t * a.dts + l.c]) + bias;
-    const float d = l.active ? step_size(a, raw) : 0.0f;
+    const float d = l.active ? step_size(a, bf16_f32(a.dt[t * a.dts + l.c]), bias) : 0.0f;
     float g = l.active ? bf16_f32(a.dy[t * a.dys + l.c]) : 0.0f;
     if (a.z && l.active) {
       const float z = bf16_f32(a.z[t * a.zs + l.c]);
@@ -525,7 +609,7 @@ __global__ __launch_bounds__(64) void scan_bwd_main_kernel(ScanArgs a) {
   const bool active = i0 + RC * quad + mine < a.per, owner = active && part < RC;
   const int64_t c = (int64_t)g * a.per + (active ? i0 + RC * quad + mine : 0);
   const float Dc = a.D ? param_at(a.D, a.D_bf16, c) : 0.0f;
-  const float bias = a.bias ? param_at(a.bias, a.bias_bf16, c) : 0.0f;
+  const StepBias bias = step_bias(a, c);
   const int64_t col = (int64_t)g * a.wpg * 64 + i0 + RC * quad;
   const int32_t n0 = RN * part;
 
@@ -559,8 +643,9 @@ __global__ __launch_bounds__(64) void scan_bwd_main_kernel(ScanArgs a) {
     const bool in = active && t < t1;
     const int64_t tt = min(t, t1 - 1);
     o.x = in ? bf16_f32(a.x[tt * a.xs + c]) : 0.0f;
-    o.raw = bf16_f32(a.dt[tt * a.dts + c]) + bias;
-    o.d = in ? step_size(a, o.raw) : 0.0f;
+    const float dt = bf16_f32(a.dt[tt * a.dts + c]);
+    o.raw = dt + bias.b;
+    o.d = in ? step_size(a, dt, bias) : 0.0f;
     o.dx = o.d * o.x;
     return o;
   };
@@ -784,9 +869,7 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs a) {
   float y = 0.0f, x = 0.0f;
   if (there && slot >= 0) {
     x = bf16_f32(a.x[row * a.xs + c]);
-    const float raw = bf16_f32(a.dt[row * a.dts + c]) +
-                      (a.bias ? param_at(a.bias, a.bias_bf16, c) : 0.0f);
-    const float d = step_size(a, raw);
+    const float d = step_size(a, bf16_f32(a.dt[row * a.dts + c]), step_bias(a, c));
     const int64_t g = c / a.per;
     float* h = a.state + (slot * a.C + c) * a.N;
 #pragma unroll
@@ -824,7 +907,7 @@ bool wide_rows(const ScanArgs& a) {
 
 template <int NT, bool kOut>
 void fwd_nt(const ScanArgs& a, int32_t work, hipStream_t s) {
-  const dim3 grid((uint32_t)((work + (int32_t)kXcds - 1) / (int32_t)kXcds * (int32_t)kXcds)), block(64);
+  const dim3 grid(place_grid(work)), block(64 * kWaves);
   if (wide_rows(a)) hipLaunchKernelGGL((scan_fwd_kernel<NT, kOut, true>), grid, block, 0, s, a, work);
   else hipLaunchKernelGGL((scan_fwd_kernel<NT, kOut, false>), grid, block, 0, s, a, work);
 }
@@ -847,8 +930,7 @@ hipError_t launch_scan_local(const ScanArgs& a, hipStream_t s) { return fwd<fals
 hipError_t launch_scan_out(const ScanArgs& a, hipStream_t s) { return fwd<true>(a, a.chunks, s); }
 
 hipError_t launch_scan_join(const ScanArgs& a, bool backward, hipStream_t s) {
-  hipLaunchKernelGGL(scan_join_kernel, dim3((a.cols + 255) / 256, a.N, backward ? 2 : 1), dim3(256),
-                     0, s, a);
+  hipLaunchKernelGGL(scan_join_kernel, dim3(a.cols / 64, a.N, backward ? 2 : 1), dim3(64), 0, s, a);
   return hipGetLastError();
 }
 

@@ -165,6 +165,9 @@ int scan_sizes(int64_t S, int64_t C, int64_t N, int64_t G) {
 constexpr int64_t kScanWaves = 4096;
 constexpr int64_t kScanMinChunk = 32;
 
+// Largest row stride of x, dt, z and dy: a chunk of it stays below 2^31 bytes.
+int64_t scan_stride_limit(int64_t C) { return std::max<int64_t>(int64_t(1) << 19, 4 * C) - 1; }
+
 struct ScanPlan {
   int32_t wpg, cols, chunk, chunks, blocks;  // blocks: channel blocks of the backward's main kernel
 };
@@ -176,9 +179,11 @@ bool scan_plan(int dir, int64_t S, int64_t C, int64_t N, int64_t G, ScanPlan* ou
   const int64_t want = std::max<int64_t>(1, kScanWaves / blocks);
   int64_t chunk = ceil_div(std::max<int64_t>(S, 1), want);
   chunk = std::max(kScanMinChunk, ceil_div(chunk, kScanKeep) * kScanKeep);
-  if (dir == VDC_BWD) chunk = std::min<int64_t>(chunk, kScanMaxChunk);
+  // A chunk's rows are addressed by 32-bit offsets from its first: with at
+  // most 2^28 / C tokens, row strides up to scan_stride_limit fit.
+  chunk = std::min<int64_t>(chunk, std::min<int64_t>(kScanMaxChunk, (int64_t(1) << 28) / C / 32 * 32));
   const int64_t chunks = std::max<int64_t>(1, ceil_div(S, chunk));
-  if (chunk > INT32_MAX || chunks * std::max(blocks, waves) > kMaxGrid - 8) return false;
+  if (chunk > INT32_MAX || chunks * std::max(blocks, waves) > kMaxGrid - 64) return false;
   out->wpg = (int32_t)wpg;
   out->cols = (int32_t)(waves * 64);
   out->chunk = (int32_t)chunk;
@@ -223,7 +228,8 @@ int scan_common(const vdc_scan* v, bool prompt, ScanArgs* a) {
   const int64_t strides[5] = {v->x_stride, v->dt_stride, v->z ? v->z_stride : v->C, v->B_stride,
                               v->C_stride};
   for (int i = 0; i < 5; ++i)
-    if (strides[i] < (i < 3 ? v->C : bc) || strides[i] > kMaxStride) return VDC_EINVAL;
+    if (strides[i] < (i < 3 ? v->C : bc) || strides[i] > (i < 3 ? scan_stride_limit(v->C) : kMaxStride))
+      return VDC_EINVAL;
   if (prompt) {
     if (v->num_docs < 0 || v->num_docs > kMaxS - 1 || (v->S > 0 && v->num_docs < 1)) return VDC_EINVAL;
     if (v->num_docs > 0 && !v->cu_seqlens) return VDC_EINVAL;
@@ -353,7 +359,7 @@ extern "C" int selective_scan_bwd(const vdc_scan* v, const void* dy, int64_t dy_
   if (rc) return rc;
   if (v->state) return VDC_EINVAL;
   if (!scan_plan(VDC_BWD, v->S, v->C, v->N, v->groups, &p)) return VDC_EINVAL;
-  if (dy_stride < v->C || dy_stride > kMaxStride) return VDC_EINVAL;
+  if (dy_stride < v->C || dy_stride > scan_stride_limit(v->C)) return VDC_EINVAL;
   if (!dA || (dD == nullptr) != (v->D == nullptr) || (ddt_bias == nullptr) != (v->dt_bias == nullptr))
     return VDC_EINVAL;
   if (v->S > 0 && (!dy || !dx || !ddt || !dB || !dC || (dz == nullptr) != (v->z == nullptr)))

@@ -13,9 +13,7 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
-constexpr float kLog2E = 1.4426950408889634f;       // log2(e) to binary32 ...
-constexpr float kLog2ELow = 1.925963033500e-8f;     // ... and what that leaves
-constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLog2E = 1.4426950408889634f;
 
 __device__ __forceinline__ float bf16_f32(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
@@ -49,29 +47,26 @@ __device__ __forceinline__ float dsilu_f32(float z, float s) {
   return s * __builtin_fmaf(z, 1.0f - s, 1.0f);
 }
 
-// log(1 + exp(v)) with a small relative error on all of its range: the
-// result is a step size, which may be many orders below 1.  With
-// e = exp(-|v|) <= 1 and s = e / (2 + e) <= 1/3, log1p(e) = 2 atanh(s), by
-// its series up to s^15 (what is left is below 2e-9 of it).  Above 20 the
-// result is v, half a unit in binary32's last place off at most.
-__device__ __forceinline__ float softplus_f32(float v) {
-  const float m = -__builtin_fabsf(v);
-  const float hi = m * kLog2E;
-  const float lo = __builtin_fmaf(m, kLog2ELow, __builtin_fmaf(m, kLog2E, -hi));
-  float e = __builtin_amdgcn_exp2f(hi);
-  e = __builtin_fmaf(e, lo * kLn2, e);
+// log(1 + exp(v)), v = (p + q) with q2 = q log2(e) at hand, with a small
+// relative error on all of its range: the result is a step size, which may be
+// many orders below 1.  With e = exp(-|v|) <= 1 and s = e / (2 + e) <= 1/3,
+//
+//   log1p(e) = 2 atanh(s) = s P(s^2),
+//
+// P the polynomial of degree 4 nearest to 2 atanh(s) / s in relative error
+// (8e-9).  The exponent v log2(e) is rounded once more than v itself, at most
+// |v| 2^-24 of e.  max(v, 0) is taken as (v + |v|) / 2, which keeps a NaN.
+__device__ __forceinline__ float softplus_f32(float p, float q, float q2) {
+  const float v = p + q;
+  const float e = __builtin_amdgcn_exp2f(-__builtin_fabsf(__builtin_fmaf(p, kLog2E, q2)));
   const float s = e * __builtin_amdgcn_rcpf(2.0f + e);
-  const float q = s * s;
-  float r = 1.0f / 15.0f;
-  r = __builtin_fmaf(r, q, 1.0f / 13.0f);
-  r = __builtin_fmaf(r, q, 1.0f / 11.0f);
-  r = __builtin_fmaf(r, q, 1.0f / 9.0f);
-  r = __builtin_fmaf(r, q, 1.0f / 7.0f);
-  r = __builtin_fmaf(r, q, 1.0f / 5.0f);
-  r = __builtin_fmaf(r, q, 1.0f / 3.0f);
-  r = __builtin_fmaf(r, q, 1.0f);
-  const float l = 2.0f * s * r + __builtin_fmaxf(v, 0.0f);
-  return v > 20.0f ? v : l;
+  const float u = s * s;
+  float r = 0.28178334f;
+  r = __builtin_fmaf(r, u, 0.27960604f);
+  r = __builtin_fmaf(r, u, 0.4002491f);
+  r = __builtin_fmaf(r, u, 0.66666317f);
+  r = __builtin_fmaf(r, u, 2.0f);
+  return __builtin_fmaf(0.5f, v + __builtin_fabsf(v), s * r);
 }
 
 // The slot of sequence `i` in a cache of `slots` sequences, or -1 where it
