@@ -17,6 +17,8 @@
 // Everything between documents is assigned, never multiplied by zero, so
 // that an infinity or a NaN stays in its document.
 
+#include <type_traits>
+
 #include "vdc_search.h"
 #include "vdc_ssm.h"
 #include "vdc_ssm_math.h"
@@ -71,7 +73,8 @@ __device__ __forceinline__ StepBias step_bias(const ScanArgs& a, int64_t c) {
   return StepBias{b, b * kLog2E};
 }
 __device__ __forceinline__ float step_size(const ScanArgs& a, float dt, const StepBias& b) {
-  return a.softplus ? softplus_f32(dt, b.b, b.b2) : dt + b.b;
+  const float s = softplus_f32(dt, b.b, b.b2);
+  return a.softplus ? s : dt + b.b;
 }
 
 // One BF16 row of activations after another, addressed by a buffer resource
@@ -475,343 +478,593 @@ __global__ __launch_bounds__(64) void scan_join_kernel(ScanArgs a) {
 //   dB = sum_c lambda d x            dC  = sum_c g h
 //   dA = sum_t v d                   dD  = sum_t g x
 //
-// Document starts of a chunk are a bitmask in LDS: bit i for token t0 + i,
-// the token after the chunk's last included.
+// A pass over the chunks first (scan_bwd_local) leaves each chunk's state from
+// zero history, the gradient its own tokens send to its left, and the state
+// every kScanKeep tokens; both are joined; the main pass then runs every
+// chunk backwards from what its neighbours send.
 
-struct Starts {
-  uint32_t bits[kScanMaxChunk / 32 + 2];
-};
-
-__device__ __forceinline__ void find_starts(const ScanArgs& a, Starts& m, int32_t t0, int32_t t1) {
-  const int32_t lane = threadIdx.x & 63;
-  const int32_t words = (t1 - t0) / 32 + 2;
-  for (int32_t i = lane; i < words; i += 64) m.bits[i] = 0u;
-  __syncthreads();
-  for (int64_t i = (int64_t)first_at_least(a.cu, a.num_docs + 1, t0) + lane; i <= a.num_docs; i += 64) {
-    const int32_t v = a.cu[i];
-    if (v > t1) break;
-    if (v >= t0) atomicOr(&m.bits[(v - t0) >> 5], 1u << ((v - t0) & 31));
-  }
-  __syncthreads();
-}
-
-__device__ __forceinline__ bool starts_at(const Starts& m, int32_t i) {
-  return (__builtin_amdgcn_readfirstlane(m.bits[i >> 5]) >> (i & 31)) & 1u;
-}
-
-// Forward over a chunk from zero history: the states every kScanKeep tokens,
-// the state after the chunk, and the gradient that the chunk's own tokens
-// send to its left: sum_t exp(A (d[t0] + .. + d[t])) C[t] g[t] over the
-// tokens of the first document in it.
-template <int NT>
-__global__ __launch_bounds__(64) void scan_bwd_local_kernel(ScanArgs a) {
-  __shared__ Starts m;
+// Forward over a chunk from zero history.  With p the decay since the chunk's
+// start, the gradient that leaves to the left is sum_t p[t] C[t] g[t] over the
+// tokens of the chunk's first document.
+template <int NT, bool kWide>
+__global__ __launch_bounds__(64 * kWaves)
+__attribute__((amdgpu_waves_per_eu(NT <= 16 ? 4 : NT == 32 ? 2 : 1)))
+void scan_bwd_local_kernel(ScanArgs a, int32_t work) {
+  constexpr int kAhead = 4;
+  static_assert(kScanKeep % kAhead == 0, "states are kept between groups of tokens");
+  const int32_t place = place_of(work);
+  if (place < 0) return;
   const int32_t waves = a.G * a.wpg;
-  const int32_t k = blockIdx.x / waves, w = blockIdx.x - k * waves;
+  const int32_t k = place / waves, w = place - k * waves;
   const Column l = column_of(a, w);
   const int32_t t0 = k * a.chunk;
   const int32_t t1 = (int32_t)min((int64_t)a.S, (int64_t)t0 + a.chunk);
-  find_starts(a, m, t0, t1);
   float A2[NT], h[NT], mu[NT], p[NT];
   load_decay<NT>(a, l, A2);
 #pragma unroll
   for (int n = 0; n < NT; ++n) h[n] = 0.0f, mu[n] = 0.0f, p[n] = 1.0f;
   const StepBias bias = step_bias(a, l.c);
+  const bool gated = a.z != nullptr;
   float sum = 0.0f;
-  int32_t flags = starts_at(m, 0) ? 1 : 0;
-  bool first = true;  // still in the chunk's first document
-  for (int32_t t = t0; t < t1; ++t) {
-    const int32_t i = t - t0;
-    if (i && i % kScanKeep == 0) {
-      float* r = a.keep + (int64_t)(t / kScanKeep) * (a.N + 1) * a.cols + l.col;
+
+  struct Raw {
+    uint16_t x, dt, dy, z;
+  };
+  RowBuffer bx, bd, bg, bz;
+  bx.open(a.x, t0, a.xs);
+  bd.open(a.dt, t0, a.dts);
+  bg.open(a.dy, t0, a.dys);
+  bz.open(gated ? a.z : a.x, t0, gated ? a.zs : a.xs);  // without a gate nothing uses it
+  const uint16_t* pB = a.B + t0 * a.Bs + l.group * a.N;
+  const uint16_t* pC = a.Cm + t0 * a.Cs + l.group * a.N;
+  const uint32_t lane2 = l.c * 2u;
+  int32_t left = t1 - t0, left_bc = left;
+  auto request = [&]() {
+    Raw r;
+    r.x = bx.get(lane2);
+    r.dt = bd.get(lane2);
+    r.dy = bg.get(lane2);
+    r.z = bz.get(lane2);
+    --left;
+    bx.row += left > 0 ? bx.stride : 0u;
+    bd.row += left > 0 ? bd.stride : 0u;
+    bg.row += left > 0 ? bg.stride : 0u;
+    bz.row += left > 0 ? bz.stride : 0u;
+    return r;
+  };
+  struct Rows {
+    Uniform<NT, kWide> B, C;
+  };
+  auto request_bc = [&]() {
+    Rows r;
+    r.B.load(pB, a.N);
+    r.C.load(pC, a.N);
+    --left_bc;
+    pB += left_bc > 0 ? a.Bs : 0;
+    pC += left_bc > 0 ? a.Cs : 0;
+    return r;
+  };
+  bool in_first = true;  // still in the chunk's first document
+  auto token = [&](auto first, const Raw& r, const Rows& now, Rows& then) {
+    if (kWide) {
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0), as in the forward
+      then = request_bc();
+      __builtin_amdgcn_sched_barrier(0);
+    } else {
+      then = request_bc();
+    }
+    const float d = step_size(a, bf16_f32(r.dt), bias);
+    const float dx = d * bf16_f32(r.x);
+    sum += d;
+    if (first.value) {
+      float g = bf16_f32(r.dy);
+      if (gated) {
+        const float z = bf16_f32(r.z);
+        g *= z * sigmoid_f32(z);
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float e = __builtin_amdgcn_exp2f(d * A2[n]);
+        h[n] = __builtin_fmaf(e, h[n], dx * now.B.get(n));
+        p[n] *= e;
+        mu[n] = __builtin_fmaf(p[n], g * now.C.get(n), mu[n]);
+      }
+    } else {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
-        if (n < a.N) r[(int64_t)n * a.cols] = h[n];
-      r[(int64_t)a.N * a.cols] = sum;
+        h[n] = __builtin_fmaf(__builtin_amdgcn_exp2f(d * A2[n]), h[n], dx * now.B.get(n));
     }
-    if (i && starts_at(m, i)) {
-      flags |= 2;
-      first = false;
+  };
+
+  Raw q[kAhead];
+  Rows bc[2];
+  bc[0] = request_bc();
 #pragma unroll
-      for (int n = 0; n < NT; ++n) h[n] = 0.0f;
-    }
-    const float x = l.active ? bf16_f32(a.x[t * a.xs + l.c]) : 0.0f;
-    const float d = l.active ? step_size(a, bf16_f32(a.dt[t * a.dts + l.c]), bias) : 0.0f;
-    float g = l.active ? bf16_f32(a.dy[t * a.dys + l.c]) : 0.0f;
-    if (a.z && l.active) {
-      const float z = bf16_f32(a.z[t * a.zs + l.c]);
-      g *= z * sigmoid_f32(z);
-    }
-    const float dx = d * x;
-    const uint16_t* B = a.B + t * a.Bs + l.group * a.N;
-    const uint16_t* Cm = a.Cm + t * a.Cs + l.group * a.N;
-    sum += d;
+  for (int i = 0; i < kAhead; ++i) q[i] = request();
+  // The next document start behind t0.
+  int32_t doc = first_at_least(a.cu, a.num_docs + 1, t0);
+  int32_t flags = doc <= a.num_docs && uniform_at(a.cu, doc) == t0 ? 1 : 0;
+  int32_t next = t0;
+  auto advance = [&](int32_t t) {
+    while (doc <= a.num_docs && uniform_at(a.cu, doc) <= t) ++doc;
+    next = doc <= a.num_docs ? uniform_at(a.cu, doc) : INT32_MAX;
+  };
+  advance(t0);
+
+#pragma unroll 1
+  for (int32_t t = t0; t < t1; t += kAhead) {
+    if ((t - t0) % kScanKeep == 0 && t > t0) {
+      const uint32_t col = here(l.col);
+      const int32_t N = here_uniform(a.N);
+      float* r = a.keep + (int64_t)(t / kScanKeep) * (N + 1) * a.cols;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const float e = __builtin_amdgcn_exp2f(d * A2[n]);
-      h[n] = __builtin_fmaf(e, h[n], dx * (n < a.N ? bf16_f32(B[n]) : 0.0f));
-      if (first) {
-        p[n] *= e;
-        mu[n] = __builtin_fmaf(p[n], g * (n < a.N ? bf16_f32(Cm[n]) : 0.0f), mu[n]);
+      for (int n = 0; n < NT; ++n)
+        if (n < N) (r + (int64_t)n * a.cols)[col] = h[n];
+      (r + (int64_t)N * a.cols)[col] = sum;
+    }
+    pB = uniform(pB);
+    pC = uniform(pC);
+    bc[0].B.pin();
+    bc[0].C.pin();
+    const bool whole = t + kAhead <= t1 && next >= t + kAhead;  // no start among the tokens
+    if (whole && in_first) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const Raw r = q[i];
+        q[i] = request();
+        token(std::true_type(), r, bc[i % 2], bc[1 - i % 2]);
+      }
+    } else if (whole) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const Raw r = q[i];
+        q[i] = request();
+        token(std::false_type(), r, bc[i % 2], bc[1 - i % 2]);
+      }
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < kAhead && t + i < t1; ++i) {
+        if (t + i == next) {
+          flags |= 2;
+          in_first = false;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) h[n] = 0.0f;
+          advance(t + i);
+        }
+        const Raw r = q[0];
+#pragma unroll
+        for (int j = 0; j + 1 < kAhead; ++j) q[j] = q[j + 1];
+        q[kAhead - 1] = request();
+        if (in_first) token(std::true_type(), r, bc[0], bc[1]);
+        else token(std::false_type(), r, bc[0], bc[1]);
+        bc[0] = bc[1];
       }
     }
   }
-  const int64_t ws = ((int64_t)k * a.N) * a.cols + l.col;
+  const uint32_t col = here(l.col);
+  const int32_t N = here_uniform(a.N);
 #pragma unroll
   for (int n = 0; n < NT; ++n)
-    if (n < a.N) {
-      a.hend[ws + (int64_t)n * a.cols] = h[n];
-      a.mu[ws + (int64_t)n * a.cols] = mu[n];
+    if (n < N) {
+      const int64_t r = ((int64_t)k * N + n) * a.cols;
+      (a.hend + r)[col] = h[n];
+      (a.mu + r)[col] = mu[n];
     }
-  a.sum[(int64_t)k * a.cols + l.col] = sum;
-  if (w == 0 && threadIdx.x == 0) a.flags[k] = flags;
+  (a.sum + (int64_t)k * a.cols)[col] = sum;
+  if (w == 0 && (threadIdx.x & 63) == 0) a.flags[k] = flags;
 }
 
-// The main pass runs a chunk backwards in blocks of kScanKeep tokens.  A lane
-// holds RC channels x RN states: lane = 4 * quad + part, channels
-// RC * quad .., states RN * part .. , so that the sums over states take two
-// exchanges within a quad, those over channels RC terms in registers first,
-// and neither direction dominates.  A block's states are computed forward
-// from its kept start twice: once for the starts of its sub-blocks, then for
-// each sub-block, whose decays and decayed states stay in registers for the
-// way back.
+// ---- the main pass
+//
+// Document starts of a chunk are a bitmask in LDS, one for each wave: bit i
+// for token t0 + i, the token after the chunk's last included.
+struct Starts {
+  uint32_t bits[kScanMaxChunk / 32 + 2];
+};
+
+// Orders a wave's own LDS writes before its lanes' reads.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Returns the first start at or behind t0 as an offset from it.
+__device__ __forceinline__ int32_t find_starts(const ScanArgs& a, Starts& m, int32_t t0, int32_t t1) {
+  const int32_t lane = threadIdx.x & 63;
+  const int32_t words = (t1 - t0) / 32 + 2;
+  for (int32_t i = lane; i < words; i += 64) m.bits[i] = 0u;
+  wave_sync();
+  const int32_t at = first_at_least(a.cu, a.num_docs + 1, t0);
+  for (int64_t i = (int64_t)at + lane; i <= a.num_docs; i += 64) {
+    const int32_t v = a.cu[i];
+    if (v > t1) break;
+    if (v >= t0) atomicOr(&m.bits[(v - t0) >> 5], 1u << ((v - t0) & 31));
+  }
+  wave_sync();
+  return at <= a.num_docs ? uniform_at(a.cu, at) - t0 : INT32_MAX;
+}
+
+// Bits i .. i + 31 of the mask, in a scalar register.
+__device__ __forceinline__ uint32_t starts_from(const Starts& m, int32_t i) {
+  return uniform(__builtin_amdgcn_alignbit(m.bits[(i >> 5) + 1], m.bits[i >> 5], (uint32_t)i & 31u));
+}
+
+template <int kCtrl>
+__device__ __forceinline__ float dpp(float v) {
+  return __uint_as_float(
+      (uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), kCtrl, 0xf, 0xf, true));
+}
+constexpr int kXor1 = 0xb1, kXor2 = 0x4e, kRor4 = 0x124, kRor8 = 0x128;  // quad_perm, row_ror
+
+// A lane's tile: RC channels x RN states.  P lanes share a channel set:
+// lane = P * set + part, states RN * part .. of channels RC * set .. .  More
+// states a lane make the sums over states cheap, more channels those over
+// channels; two lanes a channel cost the fewest instructions of both (for 16
+// states: 9 + 6 + 34 a token for the sums over states, the broadcasts within
+// a set and the sums over channels; four lanes 27 + 12 + 16, one lane 70).
+template <int NT>
+struct Tile {
+  static constexpr int P = NT <= 32 ? 2 : 4;
+  static constexpr int RN = NT / P;
+  static constexpr int RC = NT <= 16 ? 2 : 1;
+  static constexpr int CB = 64 / P * RC;  // channels of a wave
+};
+
+// The value of a set's lane r.
+template <int P, int R>
+__device__ __forceinline__ float set_from(float v) {
+  return dpp<(P == 2 ? 0xa0 : 0) + R * 0x55>(v);
+}
+template <int P, int RC>
+__device__ __forceinline__ void set_spread(float v, float (&o)[RC]) {
+  o[0] = set_from<P, 0>(v);
+  if constexpr (RC > 1) o[1] = set_from<P, 1>(v);
+}
+
+// Sum over a set's lanes of the lane's own channel's value.
+template <int P, int RC>
+__device__ __forceinline__ float set_sum(const float (&v)[RC], bool odd) {
+  if constexpr (RC == 2) {
+    const float keep = odd ? v[1] : v[0], send = odd ? v[0] : v[1];
+    return keep + dpp<kXor1>(send);
+  } else {
+    float s = v[0] + dpp<kXor1>(v[0]);
+    if constexpr (P == 4) s += dpp<kXor2>(s);
+    return s;
+  }
+}
+
+// Sums RN values over the sets of a wave.  The upper half of the wave takes
+// over half of the values from the lower and gives up the other half, the odd
+// rows of 16 lanes likewise (each value then costs half an exchange and half
+// an addition), and the rest is added within rows.  Value
+// (lane / 32) * RN / 2 + (lane / 16 % 2) * RN / 4 + i is left in v[i], i < RN / 4.
+template <int P, int RN>
+__device__ __forceinline__ void sets_sum(float (&v)[RN]) {
+#pragma unroll
+  for (int i = 0; i < RN / 2; ++i) {
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[i]), __float_as_uint(v[i + RN / 2]),
+                                                    false, false);
+    v[i] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  }
+#pragma unroll
+  for (int i = 0; i < RN / 4; ++i) {
+    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[i]), __float_as_uint(v[i + RN / 4]),
+                                                    false, false);
+    float x = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+    x += dpp<kRor8>(x);
+    x += dpp<kRor4>(x);
+    if constexpr (P == 2) x += dpp<kXor2>(x);
+    v[i] = x;
+  }
+}
+
+// Sum over all lanes.
+__device__ __forceinline__ float wave_sum(float v) {
+  v += dpp<kXor1>(v);
+  v += dpp<kXor2>(v);
+  v += dpp<kRor4>(v);
+  v += dpp<kRor8>(v);
+  auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+}
+
+// Runs a chunk backwards in blocks of kScanKeep tokens.  A block's states are
+// computed forward from its kept start twice: once for the starts of its
+// sub-blocks of kSub tokens (to LDS, each lane its own), then for each
+// sub-block, whose decays a and decayed states ah = a h[t-1] stay in registers
+// for the way back.  h itself is ah + d x B: its part in y and in dC needs only
+// sum_n C B and sum_c g d x, one number a token each.
 constexpr int kSub = 4;
 
-template <int R>
-__device__ __forceinline__ float quad_from(float v) {
-  return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), R * 0x55, 0xf, 0xf, true));
-}
-template <int RC>
-__device__ __forceinline__ void quad_spread(float v, float (&o)[RC]) {
-  o[0] = quad_from<0>(v);
-  if constexpr (RC > 1) o[1] = quad_from<1>(v);
-  if constexpr (RC > 2) o[2] = quad_from<2>(v), o[3] = quad_from<3>(v);
-}
-__device__ __forceinline__ float quad_sum(float v) {
-  v += __shfl_xor(v, 1);
-  return v + __shfl_xor(v, 2);
-}
-
-template <int NT>
-__global__ __launch_bounds__(64) void scan_bwd_main_kernel(ScanArgs a) {
-  constexpr int RN = NT / 4, RC = NT <= 16 ? 4 : NT == 32 ? 2 : 1, CB = 16 * RC;
-  __shared__ Starts m;
-  __shared__ float sub_h[kScanKeep / kSub][RC * RN][64];
-  const int32_t lane = threadIdx.x, part = lane & 3, quad = lane >> 2;
+template <int NT, bool kGate>
+__global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(NT <= 32 ? 2 : 1)))
+void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
+  typedef Tile<NT> T;
+  constexpr int P = T::P, RN = T::RN, RC = T::RC, CB = T::CB, kSubs = kScanKeep / kSub;
+  struct Lds {
+    Starts starts;
+    float h[kSubs - 1][RC * RN][64];  // states before the sub-blocks but the last
+    float bc[kScanKeep][2][NT];       // B and C of the block's tokens
+    float cb[kScanKeep];              // sum_n C B
+  };
+  __shared__ __align__(16) Lds lds[kWaves];
+  const int32_t place = place_of(work);
+  if (place < 0) return;
+  Lds& m = lds[threadIdx.x / 64u];
+  const int32_t lane = threadIdx.x & 63, part = lane % P, set = lane / P;
   const int32_t bpg = (a.per + CB - 1) / CB, blocks = a.G * bpg;
-  const int32_t k = blockIdx.x / blocks, wb = blockIdx.x - k * blocks;
+  const int32_t k = place / blocks, wb = place - k * blocks;
   const int32_t g = wb / bpg, i0 = (wb - g * bpg) * CB;
   const int32_t t0 = k * a.chunk;
   const int32_t t1 = (int32_t)min((int64_t)a.S, (int64_t)t0 + a.chunk);
-  find_starts(a, m, t0, t1);
-  // The channel whose loads and per-channel terms are this lane's.
+  const int32_t first_start = find_starts(a, m.starts, t0, t1);
+  // The channel whose loads and per-channel terms are this lane's.  A channel
+  // past the group reads zeros (out of the buffers' range): its x, g, h and
+  // lambda stay zero and add nothing.
   const int32_t mine = part % RC;
-  const bool active = i0 + RC * quad + mine < a.per, owner = active && part < RC;
-  const int64_t c = (int64_t)g * a.per + (active ? i0 + RC * quad + mine : 0);
-  const float Dc = a.D ? param_at(a.D, a.D_bf16, c) : 0.0f;
-  const StepBias bias = step_bias(a, c);
-  const int64_t col = (int64_t)g * a.wpg * 64 + i0 + RC * quad;
+  const bool odd = part & 1;
+  const bool active = i0 + RC * set + mine < a.per;
+  const uint32_t c = (uint32_t)(g * a.per + (active ? i0 + RC * set + mine : 0));
+  const float Dc = active && a.D ? param_at(a.D, a.D_bf16, c) : 0.0f;
+  StepBias bias = step_bias(a, c);
+  if (!active) bias = StepBias{0.0f, 0.0f};
+  const uint32_t col = (uint32_t)(g * a.wpg * 64 + i0 + RC * set);
   const int32_t n0 = RN * part;
 
-  float A[RC][RN], mu[RC][RN], dA[RC][RN];
+  // A times log2(e); the sums with A are taken with it and scaled at their end.
+  float A2[RC][RN], mu[RC][RN], dA[RC][RN];
 #pragma unroll
   for (int r = 0; r < RC; ++r) {
-    const int32_t i = i0 + RC * quad + r;
+    const int32_t i = i0 + RC * set + r;
 #pragma unroll
     for (int j = 0; j < RN; ++j) {
       const bool there = i < a.per && n0 + j < a.N;
-      A[r][j] = there ? param_at(a.A, a.A_bf16, ((int64_t)g * a.per + i) * a.N + n0 + j) : 0.0f;
+      A2[r][j] = there ? param_at(a.A, a.A_bf16, ((int64_t)g * a.per + i) * a.N + n0 + j) * kLog2E : 0.0f;
       dA[r][j] = 0.0f;
       // What the chunk to the right sends.
       mu[r][j] = there && k + 1 < a.chunks
-                     ? a.mu[((int64_t)(k + 1) * a.N + n0 + j) * a.cols + col + r] : 0.0f;
+                     ? (a.mu + ((int64_t)(k + 1) * a.N + n0 + j) * a.cols)[col + r] : 0.0f;
     }
   }
-  if (starts_at(m, t1 - t0)) {
+  float dD = 0.0f, dbias = 0.0f;
+  constexpr float kLn2 = 0.6931471805599453f;
+
+  RowBuffer bx, bd, bg, bz, ox, od, oz;
+  bx.open(a.x, t0, a.xs);
+  bd.open(a.dt, t0, a.dts);
+  bg.open(a.dy, t0, a.dys);
+  bz.open(kGate ? a.z : a.x, t0, kGate ? a.zs : a.xs);
+  ox.open(a.dx, t0, a.C);
+  od.open(a.ddt, t0, a.C);
+  oz.open(kGate ? a.dz : a.dx, t0, a.C);
+  const uint32_t get2 = active ? c * 2u : 0x80000000u, put2 = part < RC ? get2 : 0x80000000u;
+  const int32_t last = t1 - t0 - 1;  // tokens are counted from t0 from here on
+  auto get = [&](const RowBuffer& b, int32_t i) {
+    return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(b.r, (int)get2, (int)((uint32_t)min(i, last) * b.stride), 0);
+  };
+  auto put = [&](const RowBuffer& b, int32_t i, float v) {
+    __builtin_amdgcn_raw_buffer_store_b16(bf16_of(v), b.r, (int)put2, (int)((uint32_t)i * b.stride), 0);
+  };
+  // The activations of a sub-block's tokens, requested one sub-block ahead.
+  struct Raw {
+    uint16_t x, dt, dy, z;
+  };
+  Raw q[kSub];
+  auto request = [&](int32_t i, bool back) {
+#pragma unroll
+    for (int j = 0; j < kSub; ++j) {
+      q[j].x = get(bx, i + j);
+      q[j].dt = get(bd, i + j);
+    }
+    if (back) {
+#pragma unroll
+      for (int j = 0; j < kSub; ++j) {
+        q[j].dy = get(bg, i + j);
+        if (kGate) q[j].z = get(bz, i + j);
+      }
+    }
+  };
+  float h[RC][RN];
+  auto reset = [&](float (&v)[RC][RN]) {
 #pragma unroll
     for (int r = 0; r < RC; ++r)
 #pragma unroll
-      for (int j = 0; j < RN; ++j) mu[r][j] = 0.0f;
-  }
-  float dD = 0.0f, dbias = 0.0f;
-
-  struct Token {
-    float x, raw, d, dx;
+      for (int j = 0; j < RN; ++j) v[r][j] = 0.0f;
   };
-  auto token = [&](int32_t t) {
-    Token o;
-    const bool in = active && t < t1;
-    const int64_t tt = min(t, t1 - 1);
-    o.x = in ? bf16_f32(a.x[tt * a.xs + c]) : 0.0f;
-    const float dt = bf16_f32(a.dt[tt * a.dts + c]);
-    o.raw = dt + bias.b;
-    o.d = in ? step_size(a, dt, bias) : 0.0f;
-    o.dx = o.d * o.x;
-    return o;
-  };
-  auto states = [&](const uint16_t* p, int64_t stride, int32_t t, float (&o)[RN]) {
-    const uint16_t* q = p + (int64_t)min(t, t1 - 1) * stride + g * a.N + n0;
+  auto states = [&](const float* row, float (&o)[RN]) {
 #pragma unroll
-    for (int j = 0; j < RN; ++j) o[j] = n0 + j < a.N ? bf16_f32(q[j]) : 0.0f;
+    for (int j = 0; j < RN; j += 4) {
+      const f32x4_t v = *reinterpret_cast<const f32x4_t*>(row + n0 + j);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (j + e < RN) o[j + e] = v[e];
+    }
   };
 
-  for (int32_t ib = (t1 - t0 - 1) / kScanKeep; ib >= 0; --ib) {
-    const int32_t tb = t0 + ib * kScanKeep;
-    // The state before token tb: kept from zero history, plus what came into
+  request(last / kScanKeep * kScanKeep, false);
+#pragma unroll 1
+  for (int32_t ib = last / kScanKeep; ib >= 0; --ib) {
+    const int32_t i_first = ib * kScanKeep;
+    // Bit i: a document starts at the block's token i.
+    const uint32_t starts = starts_from(m.starts, i_first);
+    wave_sync();
+    for (int32_t e = lane; e < kScanKeep * 2 * NT; e += 64) {
+      const int32_t n = e % NT, half = e / NT % 2, i = min(i_first + e / (2 * NT), last);
+      const uint16_t* p = half ? a.Cm + (int64_t)(t0 + i) * a.Cs : a.B + (int64_t)(t0 + i) * a.Bs;
+      (&m.bc[0][0][0])[e] = n < a.N ? bf16_f32(p[g * a.N + n]) : 0.0f;
+    }
+    wave_sync();
+    {
+      static_assert(kScanKeep == 16, "four lanes a token");
+      float s = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NT / 4; ++j)
+        s = __builtin_fmaf(m.bc[lane / 4][0][lane % 4 + 4 * j], m.bc[lane / 4][1][lane % 4 + 4 * j], s);
+      s += dpp<kXor1>(s);
+      s += dpp<kXor2>(s);
+      if (lane % 4 == 0) m.cb[lane / 4] = s;
+    }
+    wave_sync();
+    // The state before the block: kept from zero history, plus what came into
     // the chunk, decayed, if no document has started since.
-    bool carried = k > 0;
-    for (int32_t i = 0; carried && i < ib * kScanKeep; ++i) carried = !starts_at(m, i);
-    float h[RC][RN];
-    float csum[RC];
-    const float* kept = a.keep + (int64_t)(tb / kScanKeep) * (a.N + 1) * a.cols + col;
+    {
+      const bool carried = k > 0 && first_start >= i_first;
+      const uint32_t at = here(col);
+      const int32_t N = here_uniform(a.N), per = here_uniform(a.per);
+      const float* kept = a.keep + (int64_t)((t0 + i_first) / kScanKeep) * (N + 1) * a.cols;
+      const float* in = a.hend + ((int64_t)(k - 1) * N + n0) * a.cols;
 #pragma unroll
-    for (int r = 0; r < RC; ++r) {
-      csum[r] = ib > 0 ? kept[(int64_t)a.N * a.cols + r] : 0.0f;
+      for (int r = 0; r < RC; ++r) {
+        const float sum = ib > 0 ? (kept + (int64_t)N * a.cols)[at + r] : 0.0f;
+        const bool there = i0 + RC * set + r < per;
 #pragma unroll
-      for (int j = 0; j < RN; ++j) {
-        float v = 0.0f;
-        if (i0 + RC * quad + r < a.per && n0 + j < a.N) {
-          if (ib > 0) v = kept[(int64_t)(n0 + j) * a.cols + r];
-          if (carried) {
-            const float in = a.hend[((int64_t)(k - 1) * a.N + n0 + j) * a.cols + col + r];
-            if (in != 0.0f)
-              v = __builtin_fmaf(__builtin_amdgcn_exp2f(A[r][j] * kLog2E * csum[r]), in, v);
+        for (int j = 0; j < RN; ++j) {
+          float v = 0.0f;
+          if (there && n0 + j < N) {
+            if (ib > 0) v = (kept + (int64_t)(n0 + j) * a.cols)[at + r];
+            if (carried) {
+              const float w = (in + (int64_t)j * a.cols)[at + r];
+              if (w != 0.0f) v = __builtin_fmaf(__builtin_amdgcn_exp2f(A2[r][j] * sum), w, v);
+            }
           }
-        }
-        h[r][j] = v;
-      }
-    }
-    for (int32_t s = 0; s < kScanKeep / kSub; ++s) {
-#pragma unroll
-      for (int e = 0; e < RC * RN; ++e) sub_h[s][e][lane] = h[e / RN][e % RN];
-      if (s + 1 < kScanKeep / kSub) {
-        for (int i = 0; i < kSub; ++i) {
-          const int32_t t = tb + s * kSub + i;
-          if (t < t1 && starts_at(m, t - t0)) {
-#pragma unroll
-            for (int r = 0; r < RC; ++r)
-#pragma unroll
-              for (int j = 0; j < RN; ++j) h[r][j] = 0.0f;
-          }
-          const Token o = token(t);
-          float B[RN], d[RC], dx[RC];
-          states(a.B, a.Bs, t, B);
-          quad_spread<RC>(o.d, d);
-          quad_spread<RC>(o.dx, dx);
-#pragma unroll
-          for (int r = 0; r < RC; ++r)
-#pragma unroll
-            for (int j = 0; j < RN; ++j)
-              h[r][j] = __builtin_fmaf(__builtin_amdgcn_exp2f(d[r] * (A[r][j] * kLog2E)), h[r][j],
-                                       dx[r] * B[j]);
+          h[r][j] = v;
         }
       }
     }
-    for (int32_t s = kScanKeep / kSub - 1; s >= 0; --s) {
-      const int32_t ts = tb + s * kSub;
-      if (ts >= t1) continue;
-      float aw[kSub][RC][RN], hw[kSub][RC][RN];
-      Token tok[kSub];
+    // Forward over sub-block s, for the state behind it.
+    auto forward = [&](auto plain, int32_t s) {
+      Raw v[kSub];
 #pragma unroll
-      for (int e = 0; e < RC * RN; ++e) h[e / RN][e % RN] = sub_h[s][e][lane];
+      for (int i = 0; i < kSub; ++i) v[i] = q[i];
+      request(i_first + (s + 1) * kSub, s + 2 == kSubs);
+#pragma unroll
+      for (int e = 0; e < RC * RN; ++e) m.h[s][e][lane] = h[e / RN][e % RN];
 #pragma unroll
       for (int i = 0; i < kSub; ++i) {
-        const int32_t t = ts + i;
-        if (t < t1 && starts_at(m, t - t0)) {
-#pragma unroll
-          for (int r = 0; r < RC; ++r)
-#pragma unroll
-            for (int j = 0; j < RN; ++j) h[r][j] = 0.0f;
-        }
-        tok[i] = token(t);
+        const int32_t at = s * kSub + i;
+        if (!plain.value && ((starts >> at) & 1u)) reset(h);
+        const float own = step_size(a, bf16_f32(v[i].dt), bias);
         float B[RN], d[RC], dx[RC];
-        states(a.B, a.Bs, t, B);
-        quad_spread<RC>(tok[i].d, d);
-        quad_spread<RC>(tok[i].dx, dx);
+        states(m.bc[at][0], B);
+        set_spread<P, RC>(own, d);
+        set_spread<P, RC>(own * bf16_f32(v[i].x), dx);
+#pragma unroll
+        for (int r = 0; r < RC; ++r)
+#pragma unroll
+          for (int j = 0; j < RN; ++j)
+            h[r][j] = __builtin_fmaf(__builtin_amdgcn_exp2f(d[r] * A2[r][j]), h[r][j], dx[r] * B[j]);
+      }
+    };
+    // Sub-block s forward once more from the state before it, then backward.
+    auto backward = [&](auto plain, int32_t s) {
+      const int32_t at0 = s * kSub;
+      Raw v[kSub];
+#pragma unroll
+      for (int i = 0; i < kSub; ++i) v[i] = q[i];
+      request(s > 0 ? i_first + (s - 1) * kSub : max(i_first - kScanKeep, 0), s > 0);
+      float aw[kSub][RC][RN], hw[kSub][RC][RN];
+      float own[kSub];
+#pragma unroll
+      for (int i = 0; i < kSub; ++i) {
+        if (!plain.value && ((starts >> (at0 + i)) & 1u)) reset(h);
+        own[i] = step_size(a, bf16_f32(v[i].dt), bias);
+        float B[RN], d[RC], dx[RC];
+        states(m.bc[at0 + i][0], B);
+        set_spread<P, RC>(own[i], d);
+        set_spread<P, RC>(own[i] * bf16_f32(v[i].x), dx);
 #pragma unroll
         for (int r = 0; r < RC; ++r)
 #pragma unroll
           for (int j = 0; j < RN; ++j) {
-            const float e = __builtin_amdgcn_exp2f(d[r] * (A[r][j] * kLog2E));
-            aw[i][r][j] = e;
-            hw[i][r][j] = e * h[r][j];  // the state of the token before, decayed
+            aw[i][r][j] = __builtin_amdgcn_exp2f(d[r] * A2[r][j]);
+            hw[i][r][j] = aw[i][r][j] * h[r][j];
             h[r][j] = __builtin_fmaf(dx[r], B[j], hw[i][r][j]);
           }
       }
 #pragma unroll
       for (int i = kSub - 1; i >= 0; --i) {
-        const int32_t t = ts + i;
-        if (t < t1) {
-          const Token& o = tok[i];
-          const float dy = active ? bf16_f32(a.dy[t * a.dys + c]) : 0.0f;
-          float z = 0.0f, sz = 0.0f, gate = 1.0f;
-          if (a.z && active) {
-            z = bf16_f32(a.z[t * a.zs + c]);
-            sz = sigmoid_f32(z);
-            gate = z * sz;
-          }
-          const float gy = dy * gate;
-          float B[RN], Cm[RN], d[RC], dx[RC], gr[RC];
-          states(a.B, a.Bs, t, B);
-          states(a.Cm, a.Cs, t, Cm);
-          quad_spread<RC>(o.d, d);
-          quad_spread<RC>(o.dx, dx);
-          quad_spread<RC>(gy, gr);
-          float dB[RN], dC[RN], lb[RC], va[RC], y0[RC];
+        const int32_t at = at0 + i, tok = i_first + at;
+        if (!plain.value && tok > last) continue;
+        const float x = bf16_f32(v[i].x), dy = bf16_f32(v[i].dy);
+        float gy = dy, z = 0.0f, sz = 0.0f;
+        if (kGate) {
+          z = bf16_f32(v[i].z);
+          sz = sigmoid_f32(z);
+          gy *= z * sz;
+        }
+        const float own_dx = own[i] * x;
+        float B[RN], Cm[RN], d[RC], dx[RC], gr[RC];
+        states(m.bc[at][0], B);
+        states(m.bc[at][1], Cm);
+        set_spread<P, RC>(own[i], d);
+        set_spread<P, RC>(own_dx, dx);
+        set_spread<P, RC>(gy, gr);
+        float dB[RN], dC[RN], lb[RC], va[RC], y0[RC];
 #pragma unroll
-          for (int j = 0; j < RN; ++j) dB[j] = 0.0f, dC[j] = 0.0f;
+        for (int j = 0; j < RN; ++j) dB[j] = 0.0f, dC[j] = 0.0f;
 #pragma unroll
-          for (int r = 0; r < RC; ++r) {
-            lb[r] = va[r] = y0[r] = 0.0f;
-#pragma unroll
-            for (int j = 0; j < RN; ++j) {
-              const float lam = __builtin_fmaf(gr[r], Cm[j], mu[r][j]);
-              const float ht = __builtin_fmaf(dx[r], B[j], hw[i][r][j]);
-              const float v = lam * hw[i][r][j];
-              y0[r] = __builtin_fmaf(Cm[j], ht, y0[r]);
-              lb[r] = __builtin_fmaf(lam, B[j], lb[r]);
-              va[r] = __builtin_fmaf(v, A[r][j], va[r]);
-              dA[r][j] = __builtin_fmaf(v, d[r], dA[r][j]);
-              dB[j] = __builtin_fmaf(lam, dx[r], dB[j]);
-              dC[j] = __builtin_fmaf(gr[r], ht, dC[j]);
-              mu[r][j] = aw[i][r][j] * lam;
-            }
-          }
-          if (starts_at(m, t - t0)) {
-#pragma unroll
-            for (int r = 0; r < RC; ++r)
-#pragma unroll
-              for (int j = 0; j < RN; ++j) mu[r][j] = 0.0f;
-          }
-          // Sums over the states, each lane keeping its own channel's.
-          float slb = 0.0f, sva = 0.0f, sy = 0.0f;
-#pragma unroll
-          for (int r = 0; r < RC; ++r) {
-            const float u = quad_sum(lb[r]), v = quad_sum(va[r]), y = quad_sum(y0[r]);
-            if (mine == r) slb = u, sva = v, sy = y;
-          }
-          const float ddt = __builtin_fmaf(o.x, slb, sva) * (a.softplus ? sigmoid_f32(o.raw) : 1.0f);
-          dD = __builtin_fmaf(gy, o.x, dD);
-          dbias += ddt;
-          if (owner) {
-            const int64_t at = (int64_t)t * a.C + c;
-            a.dx[at] = bf16_of(__builtin_fmaf(Dc, gy, o.d * slb));
-            a.ddt[at] = bf16_of(ddt);
-            if (a.z) a.dz[at] = bf16_of(dy * __builtin_fmaf(Dc, o.x, sy) * dsilu_f32(z, sz));
-          }
-          // Sums over the wave's channels.
+        for (int r = 0; r < RC; ++r) {
+          lb[r] = va[r] = y0[r] = 0.0f;
 #pragma unroll
           for (int j = 0; j < RN; ++j) {
-#pragma unroll
-            for (int x = 4; x < 64; x *= 2) dB[j] += __shfl_xor(dB[j], x), dC[j] += __shfl_xor(dC[j], x);
+            const float lam = __builtin_fmaf(gr[r], Cm[j], mu[r][j]);
+            const float w = lam * hw[i][r][j];
+            if (kGate) y0[r] = __builtin_fmaf(Cm[j], hw[i][r][j], y0[r]);
+            lb[r] = __builtin_fmaf(lam, B[j], lb[r]);
+            va[r] = __builtin_fmaf(w, A2[r][j], va[r]);
+            dA[r][j] = __builtin_fmaf(w, d[r], dA[r][j]);
+            dB[j] = __builtin_fmaf(lam, dx[r], dB[j]);
+            dC[j] = __builtin_fmaf(gr[r], hw[i][r][j], dC[j]);
+            mu[r][j] = aw[i][r][j] * lam;
           }
-          if (quad == 0) {
-            float* o2 = a.pbc + ((int64_t)wb * a.S + t) * (2 * NT) + n0;
+        }
+        if (!plain.value && ((starts >> at) & 1u)) reset(mu);
+        const float slb = set_sum<P, RC>(lb, odd), sva = set_sum<P, RC>(va, odd) * kLn2;
+        float ddt = __builtin_fmaf(x, slb, sva);
+        if (a.softplus) ddt *= sigmoid_f32(bf16_f32(v[i].dt) + bias.b);
+        dD = __builtin_fmaf(gy, x, dD);
+        dbias += ddt;
+        put(ox, tok, __builtin_fmaf(Dc, gy, own[i] * slb));
+        put(od, tok, ddt);
+        if (kGate) {
+          const float y = __builtin_fmaf(own_dx, m.cb[at], set_sum<P, RC>(y0, odd));
+          put(oz, tok, dy * __builtin_fmaf(Dc, x, y) * dsilu_f32(z, sz));
+        }
+        const float gdx = wave_sum(part < RC ? gy * own_dx : 0.0f);
+        sets_sum<P, RN>(dB);
+        sets_sum<P, RN>(dC);
+        if ((lane & 15) < P) {
+          const int32_t n = n0 + (lane >> 5) * (RN / 2) + ((lane >> 4) & 1) * (RN / 4);
+          float* out = a.pbc + ((int64_t)wb * a.S + t0 + tok) * (2 * NT);
 #pragma unroll
-            for (int j = 0; j < RN; ++j) o2[j] = dB[j], o2[NT + j] = dC[j];
+          for (int e = 0; e < RN / 4; ++e) {
+            out[n + e] = dB[e];
+            out[NT + n + e] = __builtin_fmaf(gdx, m.bc[at][0][n + e], dC[e]);
           }
         }
       }
+    };
+    constexpr uint32_t kSubMask = (1u << kSub) - 1u;
+#pragma unroll 1
+    for (int32_t s = 0; s + 1 < kSubs; ++s) {
+      if ((starts >> (s * kSub)) & kSubMask) forward(std::false_type(), s);
+      else forward(std::true_type(), s);
+    }
+#pragma unroll 1
+    for (int32_t s = kSubs - 1; s >= 0; --s) {
+      if (s + 1 < kSubs) {
+#pragma unroll
+        for (int e = 0; e < RC * RN; ++e) h[e / RN][e % RN] = m.h[s][e][lane];
+      }
+      if (((starts >> (s * kSub)) & kSubMask) || i_first + s * kSub + kSub - 1 > last)
+        backward(std::false_type(), s);
+      else
+        backward(std::true_type(), s);
     }
   }
   float* pp = a.pparam + (int64_t)k * (a.N + 2) * a.cols;
@@ -819,10 +1072,10 @@ __global__ __launch_bounds__(64) void scan_bwd_main_kernel(ScanArgs a) {
   for (int r = 0; r < RC; ++r)
 #pragma unroll
     for (int j = 0; j < RN; ++j)
-      if (n0 + j < a.N) pp[(int64_t)(n0 + j) * a.cols + col + r] = dA[r][j];
+      if (n0 + j < a.N) (pp + (int64_t)(n0 + j) * a.cols)[here(col) + r] = dA[r][j];
   if (part < RC) {
-    pp[(int64_t)a.N * a.cols + col + mine] = dD;
-    pp[(int64_t)(a.N + 1) * a.cols + col + mine] = dbias;
+    (pp + (int64_t)a.N * a.cols)[col + mine] = dD;
+    (pp + (int64_t)(a.N + 1) * a.cols)[col + mine] = dbias;
   }
 }
 
@@ -924,6 +1177,23 @@ hipError_t fwd(const ScanArgs& a, int32_t chunks, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <int NT>
+void bwd_main_nt(const ScanArgs& a, hipStream_t s) {
+  const int32_t cb = scan_bwd_channels(a.N), work = a.G * ((a.per + cb - 1) / cb) * a.chunks;
+  const dim3 grid(place_grid(work)), block(64 * kWaves);
+  if (a.z) hipLaunchKernelGGL((scan_bwd_main_kernel<NT, true>), grid, block, 0, s, a, work);
+  else hipLaunchKernelGGL((scan_bwd_main_kernel<NT, false>), grid, block, 0, s, a, work);
+}
+
+template <int NT>
+void bwd_local_nt(const ScanArgs& a, hipStream_t s) {
+  static_assert(Tile<NT>::CB == (NT <= 16 ? 64 : NT == 32 ? 32 : 16), "scan_bwd_channels");
+  const int32_t work = a.G * a.wpg * a.chunks;
+  const dim3 grid(place_grid(work)), block(64 * kWaves);
+  if (wide_rows(a)) hipLaunchKernelGGL((scan_bwd_local_kernel<NT, true>), grid, block, 0, s, a, work);
+  else hipLaunchKernelGGL((scan_bwd_local_kernel<NT, false>), grid, block, 0, s, a, work);
+}
+
 }  // namespace
 
 hipError_t launch_scan_local(const ScanArgs& a, hipStream_t s) { return fwd<false>(a, a.chunks - 1, s); }
@@ -935,24 +1205,21 @@ hipError_t launch_scan_join(const ScanArgs& a, bool backward, hipStream_t s) {
 }
 
 hipError_t launch_scan_bwd_local(const ScanArgs& a, hipStream_t s) {
-  const dim3 grid((uint32_t)((int64_t)a.G * a.wpg * a.chunks)), block(64);
   switch (scan_states(a.N)) {
-    case 8: hipLaunchKernelGGL(scan_bwd_local_kernel<8>, grid, block, 0, s, a); break;
-    case 16: hipLaunchKernelGGL(scan_bwd_local_kernel<16>, grid, block, 0, s, a); break;
-    case 32: hipLaunchKernelGGL(scan_bwd_local_kernel<32>, grid, block, 0, s, a); break;
-    default: hipLaunchKernelGGL(scan_bwd_local_kernel<64>, grid, block, 0, s, a); break;
+    case 8: bwd_local_nt<8>(a, s); break;
+    case 16: bwd_local_nt<16>(a, s); break;
+    case 32: bwd_local_nt<32>(a, s); break;
+    default: bwd_local_nt<64>(a, s); break;
   }
   return hipGetLastError();
 }
 
 hipError_t launch_scan_bwd_main(const ScanArgs& a, hipStream_t s) {
-  const int32_t cb = scan_bwd_channels(a.N), bpg = (a.per + cb - 1) / cb;
-  const dim3 grid((uint32_t)((int64_t)a.G * bpg * a.chunks)), block(64);
   switch (scan_states(a.N)) {
-    case 8: hipLaunchKernelGGL(scan_bwd_main_kernel<8>, grid, block, 0, s, a); break;
-    case 16: hipLaunchKernelGGL(scan_bwd_main_kernel<16>, grid, block, 0, s, a); break;
-    case 32: hipLaunchKernelGGL(scan_bwd_main_kernel<32>, grid, block, 0, s, a); break;
-    default: hipLaunchKernelGGL(scan_bwd_main_kernel<64>, grid, block, 0, s, a); break;
+    case 8: bwd_main_nt<8>(a, s); break;
+    case 16: bwd_main_nt<16>(a, s); break;
+    case 32: bwd_main_nt<32>(a, s); break;
+    default: bwd_main_nt<64>(a, s); break;
   }
   return hipGetLastError();
 }
