@@ -89,8 +89,8 @@ struct RowBuffer {
     row = 0;
     stride = (uint32_t)stride_ * 2u;
   }
-  __device__ __forceinline__ uint16_t get(uint32_t lane2) const {
-    return __builtin_amdgcn_raw_buffer_load_b16(r, (int)lane2, (int)row, 0);
+  __device__ __forceinline__ uint32_t get(uint32_t lane2) const {
+    return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)lane2, (int)row, 0);
   }
   __device__ __forceinline__ void put(uint32_t lane2, uint16_t v) const {
     __builtin_amdgcn_raw_buffer_store_b16(v, r, (int)lane2, (int)row, 0);
@@ -200,6 +200,12 @@ __device__ __forceinline__ uint32_t here(uint32_t v) {
   asm volatile("" : "+v"(v));
   return v;
 }
+// Values that are complete at this point of the program: without it the
+// compiler runs the tokens of an unrolled loop side by side, which takes more
+// registers than there are.
+__device__ __forceinline__ void settled(float& a, float& b, float& c) {
+  asm volatile("" : "+v"(a), "+v"(b), "+v"(c));
+}
 __device__ __forceinline__ int32_t here_uniform(int32_t v) {
   asm volatile("" : "+s"(v));
   return v;
@@ -299,7 +305,7 @@ void scan_fwd_kernel(ScanArgs a, int32_t work) {
   // below is unrolled by), B and C one token ahead;
   // past the chunk the last token's are requested again.
   struct Raw {
-    uint16_t x, dt, z;
+    uint32_t x, dt, z;
   };
   RowBuffer bx, bd, bz, by;
   bx.open(a.x, t0, a.xs);
@@ -348,8 +354,8 @@ void scan_fwd_kernel(ScanArgs a, int32_t work) {
     } else {
       then = request_bc();
     }
-    const float x = bf16_f32(r.x);
-    const float d = step_size(a, bf16_f32(r.dt), bias);
+    const float x = bf16_lo(r.x);
+    const float d = step_size(a, bf16_lo(r.dt), bias);
     const float dx = d * x;
     float y = Dc * x;
 #pragma unroll
@@ -359,7 +365,7 @@ void scan_fwd_kernel(ScanArgs a, int32_t work) {
     }
     if (kOut) {
       if (gated) {
-        const float z = bf16_f32(r.z);
+        const float z = bf16_lo(r.z);
         y *= z * sigmoid_f32(z);
       }
       by.put(put2, bf16_of(y));
@@ -490,8 +496,8 @@ template <int NT, bool kWide>
 __global__ __launch_bounds__(64 * kWaves)
 __attribute__((amdgpu_waves_per_eu(NT <= 16 ? 4 : NT == 32 ? 2 : 1)))
 void scan_bwd_local_kernel(ScanArgs a, int32_t work) {
-  constexpr int kAhead = 4;
-  static_assert(kScanKeep % kAhead == 0, "states are kept between groups of tokens");
+  constexpr int kAhead = 2;
+  static_assert(kAhead % 2 == 0, "two rows of B and C in turn");
   const int32_t place = place_of(work);
   if (place < 0) return;
   const int32_t waves = a.G * a.wpg;
@@ -508,7 +514,7 @@ void scan_bwd_local_kernel(ScanArgs a, int32_t work) {
   float sum = 0.0f;
 
   struct Raw {
-    uint16_t x, dt, dy, z;
+    uint32_t x, dt, dy, z;
   };
   RowBuffer bx, bd, bg, bz;
   bx.open(a.x, t0, a.xs);
@@ -544,8 +550,7 @@ void scan_bwd_local_kernel(ScanArgs a, int32_t work) {
     pC += left_bc > 0 ? a.Cs : 0;
     return r;
   };
-  bool in_first = true;  // still in the chunk's first document
-  auto token = [&](auto first, const Raw& r, const Rows& now, Rows& then) {
+  auto token = [&](const Raw& r, const Rows& now, Rows& then) {
     if (kWide) {
       __builtin_amdgcn_sched_barrier(0);
       __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0), as in the forward
@@ -554,27 +559,32 @@ void scan_bwd_local_kernel(ScanArgs a, int32_t work) {
     } else {
       then = request_bc();
     }
-    const float d = step_size(a, bf16_f32(r.dt), bias);
-    const float dx = d * bf16_f32(r.x);
+    const float d = step_size(a, bf16_lo(r.dt), bias);
+    const float dx = d * bf16_lo(r.x);
     sum += d;
-    if (first.value) {
-      float g = bf16_f32(r.dy);
-      if (gated) {
-        const float z = bf16_f32(r.z);
-        g *= z * sigmoid_f32(z);
-      }
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float e = __builtin_amdgcn_exp2f(d * A2[n]);
-        h[n] = __builtin_fmaf(e, h[n], dx * now.B.get(n));
-        p[n] *= e;
-        mu[n] = __builtin_fmaf(p[n], g * now.C.get(n), mu[n]);
-      }
-    } else {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        h[n] = __builtin_fmaf(__builtin_amdgcn_exp2f(d * A2[n]), h[n], dx * now.B.get(n));
+    float g = bf16_lo(r.dy);
+    if (gated) {
+      const float z = bf16_lo(r.z);
+      g *= z * sigmoid_f32(z);
     }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float e = __builtin_amdgcn_exp2f(d * A2[n]);
+      h[n] = __builtin_fmaf(e, h[n], dx * now.B.get(n));
+      p[n] *= e;
+      mu[n] = __builtin_fmaf(p[n], g * now.C.get(n), mu[n]);
+      settled(h[n], p[n], mu[n]);
+    }
+  };
+  // Past the first document mu is written and what it goes on to gather is
+  // never used.
+  bool in_first = true;
+  auto write_mu = [&]() {
+    const uint32_t col = here(l.col);
+    const int32_t kk = here_uniform(k), N = here_uniform(a.N);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      if (n < N) (a.mu + ((int64_t)kk * N + n) * a.cols)[col] = mu[n];
   };
 
   Raw q[kAhead];
@@ -592,65 +602,61 @@ void scan_bwd_local_kernel(ScanArgs a, int32_t work) {
   };
   advance(t0);
 
-#pragma unroll 1
-  for (int32_t t = t0; t < t1; t += kAhead) {
-    if ((t - t0) % kScanKeep == 0 && t > t0) {
-      const uint32_t col = here(l.col);
-      const int32_t N = here_uniform(a.N);
-      float* r = a.keep + (int64_t)(t / kScanKeep) * (N + 1) * a.cols;
+  // The state before token t, every kScanKeep tokens.
+  auto keep = [&](int32_t t) {
+    if ((t - t0) % kScanKeep != 0 || t == t0) return;
+    const uint32_t col = here(l.col);
+    const int32_t N = here_uniform(a.N);
+    float* r = a.keep + (int64_t)(t / kScanKeep) * (N + 1) * a.cols;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-        if (n < N) (r + (int64_t)n * a.cols)[col] = h[n];
-      (r + (int64_t)N * a.cols)[col] = sum;
+    for (int n = 0; n < NT; ++n)
+      if (n < N) (r + (int64_t)n * a.cols)[col] = h[n];
+    (r + (int64_t)N * a.cols)[col] = sum;
+  };
+
+  int32_t t = t0;
+#pragma unroll 1
+  while (t < t1) {
+    const int32_t end = min(next, t1);
+#pragma unroll 1
+    for (; t + kAhead <= end; t += kAhead) {
+      pB = uniform(pB);
+      pC = uniform(pC);
+      bc[0].B.pin();
+      bc[0].C.pin();
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        keep(t + i);
+        const Raw r = q[i];
+        q[i] = request();
+        token(r, bc[i % 2], bc[1 - i % 2]);
+      }
     }
-    pB = uniform(pB);
-    pC = uniform(pC);
-    bc[0].B.pin();
-    bc[0].C.pin();
-    const bool whole = t + kAhead <= t1 && next >= t + kAhead;  // no start among the tokens
-    if (whole && in_first) {
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const Raw r = q[i];
-        q[i] = request();
-        token(std::true_type(), r, bc[i % 2], bc[1 - i % 2]);
-      }
-    } else if (whole) {
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const Raw r = q[i];
-        q[i] = request();
-        token(std::false_type(), r, bc[i % 2], bc[1 - i % 2]);
-      }
-    } else {
 #pragma unroll 1
-      for (int i = 0; i < kAhead && t + i < t1; ++i) {
-        if (t + i == next) {
-          flags |= 2;
-          in_first = false;
+    for (; t < end; ++t) {
+      keep(t);
+      const Raw r = q[0];
 #pragma unroll
-          for (int n = 0; n < NT; ++n) h[n] = 0.0f;
-          advance(t + i);
-        }
-        const Raw r = q[0];
+      for (int j = 0; j + 1 < kAhead; ++j) q[j] = q[j + 1];
+      q[kAhead - 1] = request();
+      token(r, bc[0], bc[1]);
+      bc[0] = bc[1];
+    }
+    if (t < t1) {  // a document starts
+      flags |= 2;
+      if (in_first) write_mu();
+      in_first = false;
 #pragma unroll
-        for (int j = 0; j + 1 < kAhead; ++j) q[j] = q[j + 1];
-        q[kAhead - 1] = request();
-        if (in_first) token(std::true_type(), r, bc[0], bc[1]);
-        else token(std::false_type(), r, bc[0], bc[1]);
-        bc[0] = bc[1];
-      }
+      for (int n = 0; n < NT; ++n) h[n] = 0.0f;
+      advance(t);
     }
   }
   const uint32_t col = here(l.col);
   const int32_t N = here_uniform(a.N);
 #pragma unroll
   for (int n = 0; n < NT; ++n)
-    if (n < N) {
-      const int64_t r = ((int64_t)k * N + n) * a.cols;
-      (a.hend + r)[col] = h[n];
-      (a.mu + r)[col] = mu[n];
-    }
+    if (n < N) (a.hend + ((int64_t)k * N + n) * a.cols)[col] = h[n];
+  if (in_first) write_mu();
   (a.sum + (int64_t)k * a.cols)[col] = sum;
   if (w == 0 && (threadIdx.x & 63) == 0) a.flags[k] = flags;
 }
@@ -696,7 +702,8 @@ __device__ __forceinline__ float dpp(float v) {
   return __uint_as_float(
       (uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), kCtrl, 0xf, 0xf, true));
 }
-constexpr int kXor1 = 0xb1, kXor2 = 0x4e, kRor4 = 0x124, kRor8 = 0x128;  // quad_perm, row_ror
+constexpr int kXor1 = 0xb1, kXor2 = 0x4e, kRor4 = 0x124, kRor8 = 0x128,  // quad_perm, row_ror
+              kHalfMirror = 0x141;
 
 // A lane's tile: RC channels x RN states.  P lanes share a channel set:
 // lane = P * set + part, states RN * part .. of channels RC * set .. .  More
@@ -761,6 +768,15 @@ __device__ __forceinline__ void sets_sum(float (&v)[RN]) {
   }
 }
 
+// a b + c where c is needed afterwards: written out, as the compiler copies c
+// and adds to the copy.  No operand may come straight from an exponential, a
+// reciprocal or a root, whose results take a cycle more.
+__device__ __forceinline__ float fma_apart(float a, float b, float c) {
+  float r;
+  asm("v_fma_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+
 // Sum over all lanes.
 __device__ __forceinline__ float wave_sum(float v) {
   v += dpp<kXor1>(v);
@@ -779,7 +795,7 @@ __device__ __forceinline__ float wave_sum(float v) {
 // sub-block, whose decays a and decayed states ah = a h[t-1] stay in registers
 // for the way back.  h itself is ah + d x B: its part in y and in dC needs only
 // sum_n C B and sum_c g d x, one number a token each.
-constexpr int kSub = 4;
+constexpr int kSub = 2;
 
 template <int NT, bool kGate>
 __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(NT <= 32 ? 2 : 1)))
@@ -788,7 +804,7 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
   constexpr int P = T::P, RN = T::RN, RC = T::RC, CB = T::CB, kSubs = kScanKeep / kSub;
   struct Lds {
     Starts starts;
-    float h[kSubs - 1][RC * RN][64];  // states before the sub-blocks but the last
+    f32x4_t h[kSubs - 1][RC * RN / 4][64];  // states before the sub-blocks but the last
     float bc[kScanKeep][2][NT];       // B and C of the block's tokens
     float cb[kScanKeep];              // sum_n C B
   };
@@ -845,14 +861,15 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
   const uint32_t get2 = active ? c * 2u : 0x80000000u, put2 = part < RC ? get2 : 0x80000000u;
   const int32_t last = t1 - t0 - 1;  // tokens are counted from t0 from here on
   auto get = [&](const RowBuffer& b, int32_t i) {
-    return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(b.r, (int)get2, (int)((uint32_t)min(i, last) * b.stride), 0);
+    return (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(b.r, (int)get2, (int)((uint32_t)min(i, last) * b.stride), 0);
   };
-  auto put = [&](const RowBuffer& b, int32_t i, float v) {
-    __builtin_amdgcn_raw_buffer_store_b16(bf16_of(v), b.r, (int)put2, (int)((uint32_t)i * b.stride), 0);
+  auto put = [&](const RowBuffer& b, int32_t i, float v) {  // past the end: out of range, dropped
+    const uint32_t row = i <= last ? (uint32_t)i * b.stride : 0x7fffffffu;
+    __builtin_amdgcn_raw_buffer_store_b16(bf16_of(v), b.r, (int)put2, (int)row, 0);
   };
   // The activations of a sub-block's tokens, requested one sub-block ahead.
   struct Raw {
-    uint16_t x, dt, dy, z;
+    uint32_t x, dt, dy, z;
   };
   Raw q[kSub];
   auto request = [&](int32_t i, bool back) {
@@ -900,14 +917,15 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
     }
     wave_sync();
     {
-      static_assert(kScanKeep == 16, "four lanes a token");
+      static_assert(kScanKeep == 8, "eight lanes a token");
       float s = 0.0f;
 #pragma unroll
-      for (int j = 0; j < NT / 4; ++j)
-        s = __builtin_fmaf(m.bc[lane / 4][0][lane % 4 + 4 * j], m.bc[lane / 4][1][lane % 4 + 4 * j], s);
+      for (int j = 0; j < NT / 8; ++j)
+        s = __builtin_fmaf(m.bc[lane / 8][0][lane % 8 + 8 * j], m.bc[lane / 8][1][lane % 8 + 8 * j], s);
       s += dpp<kXor1>(s);
       s += dpp<kXor2>(s);
-      if (lane % 4 == 0) m.cb[lane / 4] = s;
+      s += dpp<kHalfMirror>(s);
+      if (lane % 8 == 0) m.cb[lane / 8] = s;
     }
     wave_sync();
     // The state before the block: kept from zero history, plus what came into
@@ -937,22 +955,24 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
       }
     }
     // Forward over sub-block s, for the state behind it.
-    auto forward = [&](auto plain, int32_t s) {
+    auto forward = [&](int32_t s) {
       Raw v[kSub];
 #pragma unroll
       for (int i = 0; i < kSub; ++i) v[i] = q[i];
       request(i_first + (s + 1) * kSub, s + 2 == kSubs);
 #pragma unroll
-      for (int e = 0; e < RC * RN; ++e) m.h[s][e][lane] = h[e / RN][e % RN];
+      for (int e = 0; e < RC * RN; e += 4)
+        m.h[s][e / 4][lane] = (f32x4_t){h[e / RN][e % RN], h[e / RN][e % RN + 1], h[e / RN][e % RN + 2],
+                                        h[e / RN][e % RN + 3]};
 #pragma unroll
       for (int i = 0; i < kSub; ++i) {
         const int32_t at = s * kSub + i;
-        if (!plain.value && ((starts >> at) & 1u)) reset(h);
-        const float own = step_size(a, bf16_f32(v[i].dt), bias);
+        if ((starts >> at) & 1u) reset(h);
+        const float own = step_size(a, bf16_lo(v[i].dt), bias);
         float B[RN], d[RC], dx[RC];
         states(m.bc[at][0], B);
         set_spread<P, RC>(own, d);
-        set_spread<P, RC>(own * bf16_f32(v[i].x), dx);
+        set_spread<P, RC>(own * bf16_lo(v[i].x), dx);
 #pragma unroll
         for (int r = 0; r < RC; ++r)
 #pragma unroll
@@ -961,7 +981,7 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
       }
     };
     // Sub-block s forward once more from the state before it, then backward.
-    auto backward = [&](auto plain, int32_t s) {
+    auto backward = [&](int32_t s) {
       const int32_t at0 = s * kSub;
       Raw v[kSub];
 #pragma unroll
@@ -971,29 +991,30 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
       float own[kSub];
 #pragma unroll
       for (int i = 0; i < kSub; ++i) {
-        if (!plain.value && ((starts >> (at0 + i)) & 1u)) reset(h);
-        own[i] = step_size(a, bf16_f32(v[i].dt), bias);
+        if ((starts >> (at0 + i)) & 1u) reset(h);
+        // A token past the end does nothing: no step, and no gradient below.
+        own[i] = i_first + at0 + i <= last ? step_size(a, bf16_lo(v[i].dt), bias) : 0.0f;
         float B[RN], d[RC], dx[RC];
         states(m.bc[at0 + i][0], B);
         set_spread<P, RC>(own[i], d);
-        set_spread<P, RC>(own[i] * bf16_f32(v[i].x), dx);
+        set_spread<P, RC>(own[i] * bf16_lo(v[i].x), dx);
 #pragma unroll
         for (int r = 0; r < RC; ++r)
 #pragma unroll
           for (int j = 0; j < RN; ++j) {
             aw[i][r][j] = __builtin_amdgcn_exp2f(d[r] * A2[r][j]);
             hw[i][r][j] = aw[i][r][j] * h[r][j];
-            h[r][j] = __builtin_fmaf(dx[r], B[j], hw[i][r][j]);
+            h[r][j] = fma_apart(dx[r], B[j], hw[i][r][j]);
           }
       }
 #pragma unroll
       for (int i = kSub - 1; i >= 0; --i) {
         const int32_t at = at0 + i, tok = i_first + at;
-        if (!plain.value && tok > last) continue;
-        const float x = bf16_f32(v[i].x), dy = bf16_f32(v[i].dy);
+        const bool real = tok <= last;
+        const float x = bf16_lo(v[i].x), dy = real ? bf16_lo(v[i].dy) : 0.0f;
         float gy = dy, z = 0.0f, sz = 0.0f;
         if (kGate) {
-          z = bf16_f32(v[i].z);
+          z = bf16_lo(v[i].z);
           sz = sigmoid_f32(z);
           gy *= z * sz;
         }
@@ -1023,12 +1044,12 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
             mu[r][j] = aw[i][r][j] * lam;
           }
         }
-        if (!plain.value && ((starts >> at) & 1u)) reset(mu);
+        if ((starts >> at) & 1u) reset(mu);
         const float slb = set_sum<P, RC>(lb, odd), sva = set_sum<P, RC>(va, odd) * kLn2;
         float ddt = __builtin_fmaf(x, slb, sva);
-        if (a.softplus) ddt *= sigmoid_f32(bf16_f32(v[i].dt) + bias.b);
+        if (a.softplus) ddt *= sigmoid_f32(bf16_lo(v[i].dt) + bias.b);
         dD = __builtin_fmaf(gy, x, dD);
-        dbias += ddt;
+        dbias += real ? ddt : 0.0f;
         put(ox, tok, __builtin_fmaf(Dc, gy, own[i] * slb));
         put(od, tok, ddt);
         if (kGate) {
@@ -1038,7 +1059,7 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
         const float gdx = wave_sum(part < RC ? gy * own_dx : 0.0f);
         sets_sum<P, RN>(dB);
         sets_sum<P, RN>(dC);
-        if ((lane & 15) < P) {
+        if ((lane & 15) < P && real) {
           const int32_t n = n0 + (lane >> 5) * (RN / 2) + ((lane >> 4) & 1) * (RN / 4);
           float* out = a.pbc + ((int64_t)wb * a.S + t0 + tok) * (2 * NT);
 #pragma unroll
@@ -1049,22 +1070,19 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
         }
       }
     };
-    constexpr uint32_t kSubMask = (1u << kSub) - 1u;
 #pragma unroll 1
-    for (int32_t s = 0; s + 1 < kSubs; ++s) {
-      if ((starts >> (s * kSub)) & kSubMask) forward(std::false_type(), s);
-      else forward(std::true_type(), s);
-    }
+    for (int32_t s = 0; s + 1 < kSubs; ++s) forward(s);
 #pragma unroll 1
     for (int32_t s = kSubs - 1; s >= 0; --s) {
       if (s + 1 < kSubs) {
 #pragma unroll
-        for (int e = 0; e < RC * RN; ++e) h[e / RN][e % RN] = m.h[s][e][lane];
+        for (int e = 0; e < RC * RN; e += 4) {
+          const f32x4_t v = m.h[s][e / 4][lane];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) h[e / RN][e % RN + i] = v[i];
+        }
       }
-      if (((starts >> (s * kSub)) & kSubMask) || i_first + s * kSub + kSub - 1 > last)
-        backward(std::false_type(), s);
-      else
-        backward(std::true_type(), s);
+      backward(s);
     }
   }
   float* pp = a.pparam + (int64_t)k * (a.N + 2) * a.cols;

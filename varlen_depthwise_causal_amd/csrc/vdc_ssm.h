@@ -38,7 +38,7 @@ hipError_t launch_conv_edges(const ConvStateArgs& a, int64_t docs, hipStream_t s
 constexpr int kMaxStates = 64;
 // Backward: tokens between two kept states, and the longest chunk (its
 // document starts are a bitmask in LDS).
-constexpr int kScanKeep = 16;
+constexpr int kScanKeep = 8;
 constexpr int kScanMaxChunk = 2048;
 
 struct ScanArgs {

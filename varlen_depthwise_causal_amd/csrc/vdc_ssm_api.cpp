@@ -178,7 +178,7 @@ bool scan_plan(int dir, int64_t S, int64_t C, int64_t N, int64_t G, ScanPlan* ou
   const int64_t blocks = dir == VDC_BWD ? G * ceil_div(per, scan_bwd_channels(N)) : waves;
   const int64_t want = std::max<int64_t>(1, kScanWaves / blocks);
   int64_t chunk = ceil_div(std::max<int64_t>(S, 1), want);
-  chunk = std::max(kScanMinChunk, ceil_div(chunk, kScanKeep) * kScanKeep);
+  chunk = std::max(kScanMinChunk, ceil_div(chunk, 16) * 16);
   // A chunk's rows are addressed by 32-bit offsets from its first: with at
   // most 2^28 / C tokens, row strides up to scan_stride_limit fit.
   chunk = std::min<int64_t>(chunk, std::min<int64_t>(kScanMaxChunk, (int64_t(1) << 28) / C / 32 * 32));
