@@ -805,6 +805,7 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
   struct Lds {
     Starts starts;
     f32x4_t h[kSubs - 1][RC * RN / 4][64];  // states before the sub-blocks but the last
+    f32x4_t in[RC * RN / 4][64];            // what came into the chunk
     float bc[kScanKeep][2][NT];       // B and C of the block's tokens
     float cb[kScanKeep];              // sum_n C B
   };
@@ -846,6 +847,17 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
       mu[r][j] = there && k + 1 < a.chunks
                      ? (a.mu + ((int64_t)(k + 1) * a.N + n0 + j) * a.cols)[col + r] : 0.0f;
     }
+  }
+#pragma unroll
+  for (int e = 0; e < RC * RN; e += 4) {
+    f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int r = (e + q) / RN, j = (e + q) % RN;
+      if (k > 0 && i0 + RC * set + r < a.per && n0 + j < a.N)
+        v[q] = (a.hend + ((int64_t)(k - 1) * a.N + n0 + j) * a.cols)[col + r];
+    }
+    m.in[e / 4][lane] = v;
   }
   float dD = 0.0f, dbias = 0.0f;
   constexpr float kLn2 = 0.6931471805599453f;
@@ -903,17 +915,45 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
     }
   };
 
+  // What a block starts from, requested while the block behind it is at work:
+  // its B and C, its kept state (to h, which is free then) and the sum of the
+  // step sizes before it.
+  constexpr int kRaw = kScanKeep * 2 * NT / 64;
+  uint32_t raw_bc[kRaw];
+  float sum[RC];
+  auto request_block = [&](int32_t ib) {
+    const int32_t i_first = ib * kScanKeep;
+    const uint32_t at = here(col);
+    const int32_t N = here_uniform(a.N);
+#pragma unroll
+    for (int u = 0; u < kRaw; ++u) {
+      const int32_t e = lane + 64 * u, n = min(e % NT, N - 1), i = min(i_first + e / (2 * NT), last);
+      const uint16_t* p = e / NT % 2 ? a.Cm + (int64_t)(t0 + i) * a.Cs : a.B + (int64_t)(t0 + i) * a.Bs;
+      raw_bc[u] = p[g * N + n];
+    }
+    if (ib > 0) {
+      const float* kept = a.keep + (int64_t)((t0 + i_first) / kScanKeep) * (N + 1) * a.cols;
+#pragma unroll
+      for (int r = 0; r < RC; ++r) {
+        sum[r] = (kept + (int64_t)N * a.cols)[at + r];
+#pragma unroll
+        for (int j = 0; j < RN; ++j) h[r][j] = (kept + (int64_t)min(n0 + j, N - 1) * a.cols)[at + r];
+      }
+    }
+  };
+
   request(last / kScanKeep * kScanKeep, false);
+  request_block(last / kScanKeep);
 #pragma unroll 1
   for (int32_t ib = last / kScanKeep; ib >= 0; --ib) {
     const int32_t i_first = ib * kScanKeep;
     // Bit i: a document starts at the block's token i.
     const uint32_t starts = starts_from(m.starts, i_first);
     wave_sync();
-    for (int32_t e = lane; e < kScanKeep * 2 * NT; e += 64) {
-      const int32_t n = e % NT, half = e / NT % 2, i = min(i_first + e / (2 * NT), last);
-      const uint16_t* p = half ? a.Cm + (int64_t)(t0 + i) * a.Cs : a.B + (int64_t)(t0 + i) * a.Bs;
-      (&m.bc[0][0][0])[e] = n < a.N ? bf16_f32(p[g * a.N + n]) : 0.0f;
+#pragma unroll
+    for (int u = 0; u < kRaw; ++u) {
+      const int32_t e = lane + 64 * u;
+      (&m.bc[0][0][0])[e] = e % NT < a.N ? bf16_lo(raw_bc[u]) : 0.0f;
     }
     wave_sync();
     {
@@ -932,24 +972,16 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
     // the chunk, decayed, if no document has started since.
     {
       const bool carried = k > 0 && first_start >= i_first;
-      const uint32_t at = here(col);
-      const int32_t N = here_uniform(a.N), per = here_uniform(a.per);
-      const float* kept = a.keep + (int64_t)((t0 + i_first) / kScanKeep) * (N + 1) * a.cols;
-      const float* in = a.hend + ((int64_t)(k - 1) * N + n0) * a.cols;
 #pragma unroll
-      for (int r = 0; r < RC; ++r) {
-        const float sum = ib > 0 ? (kept + (int64_t)N * a.cols)[at + r] : 0.0f;
-        const bool there = i0 + RC * set + r < per;
+      for (int e = 0; e < RC * RN; e += 4) {
+        const f32x4_t in = m.in[e / 4][lane];
 #pragma unroll
-        for (int j = 0; j < RN; ++j) {
-          float v = 0.0f;
-          if (there && n0 + j < N) {
-            if (ib > 0) v = (kept + (int64_t)(n0 + j) * a.cols)[at + r];
-            if (carried) {
-              const float w = (in + (int64_t)j * a.cols)[at + r];
-              if (w != 0.0f) v = __builtin_fmaf(__builtin_amdgcn_exp2f(A2[r][j] * sum), w, v);
-            }
-          }
+        for (int q = 0; q < 4; ++q) {
+          const int r = (e + q) / RN, j = (e + q) % RN;
+          const bool there = i0 + RC * set + r < a.per && n0 + j < a.N;
+          float v = there && ib > 0 ? h[r][j] : 0.0f;
+          const float decay = ib > 0 ? __builtin_amdgcn_exp2f(A2[r][j] * sum[r]) : 1.0f;
+          if (carried && in[q] != 0.0f) v = __builtin_fmaf(decay, in[q], v);
           h[r][j] = v;
         }
       }
@@ -1007,6 +1039,7 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
             h[r][j] = fma_apart(dx[r], B[j], hw[i][r][j]);
           }
       }
+      if (s == 0 && ib > 0) request_block(ib - 1);
 #pragma unroll
       for (int i = kSub - 1; i >= 0; --i) {
         const int32_t at = at0 + i, tok = i_first + at;
@@ -1026,21 +1059,21 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
         set_spread<P, RC>(own_dx, dx);
         set_spread<P, RC>(gy, gr);
         float dB[RN], dC[RN], lb[RC], va[RC], y0[RC];
-#pragma unroll
-        for (int j = 0; j < RN; ++j) dB[j] = 0.0f, dC[j] = 0.0f;
+        auto add = [](bool first, float a, float b, float& sum) {
+          sum = first ? a * b : __builtin_fmaf(a, b, sum);
+        };
 #pragma unroll
         for (int r = 0; r < RC; ++r) {
-          lb[r] = va[r] = y0[r] = 0.0f;
 #pragma unroll
           for (int j = 0; j < RN; ++j) {
             const float lam = __builtin_fmaf(gr[r], Cm[j], mu[r][j]);
             const float w = lam * hw[i][r][j];
-            if (kGate) y0[r] = __builtin_fmaf(Cm[j], hw[i][r][j], y0[r]);
-            lb[r] = __builtin_fmaf(lam, B[j], lb[r]);
-            va[r] = __builtin_fmaf(w, A2[r][j], va[r]);
+            if (kGate) add(j == 0, Cm[j], hw[i][r][j], y0[r]);
+            add(j == 0, lam, B[j], lb[r]);
+            add(j == 0, w, A2[r][j], va[r]);
             dA[r][j] = __builtin_fmaf(w, d[r], dA[r][j]);
-            dB[j] = __builtin_fmaf(lam, dx[r], dB[j]);
-            dC[j] = __builtin_fmaf(gr[r], hw[i][r][j], dC[j]);
+            add(r == 0, lam, dx[r], dB[j]);
+            add(r == 0, gr[r], hw[i][r][j], dC[j]);
             mu[r][j] = aw[i][r][j] * lam;
           }
         }
