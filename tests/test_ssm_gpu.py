@@ -211,7 +211,8 @@ def test_selective_scan_keeps_documents_apart(vdc):
 
 NORM = [(1, 8, 1, F32, True), (33, 520, 8, F32, False), (5, 6, 2, BF, True), (64, 4096, 32, F32, True),
         (3, 16384, 1, BF, False), (9, 1000, 1, F32, True), (200, 65, 65, F32, True), (0, 64, 4, F32, True),
-        (17, 2048, 1, BF, True), (2, 5000, 1, F32, False), (40, 264, 3, F32, True)]
+        (17, 2048, 1, BF, True), (2, 5000, 1, F32, False), (40, 264, 3, F32, True), (70, 512, 2, F32, False),
+        (70, 1024, 2, BF, True), (13, 8192, 2, F32, True), (1100, 64, 1, F32, True)]
 
 
 @pytest.mark.parametrize("S,C,G,dtype,gate", NORM)

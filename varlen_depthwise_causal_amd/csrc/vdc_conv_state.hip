@@ -39,13 +39,37 @@ struct Taps8 {
   float b[8];
 };
 
+// Weight and bias of eight channels: 16-byte loads for either dtype.
 __device__ __forceinline__ Taps8 load_taps(const ConvStateArgs& a, int64_t c) {
   Taps8 t;
+  if (a.w_bf16) {
+    const u32x4_t* p = reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(a.w) + c * 4);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+    for (int q = 0; q < 4; ++q) {
+      const Row8 r = unpack8(p[q]);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) t.w[i][k] = param_at(a.w, a.w_bf16, (c + i) * 4 + k);
-    t.b[i] = a.b ? param_at(a.b, a.b_bf16, c + i) : 0.0f;
+      for (int k = 0; k < 8; ++k) t.w[2 * q + k / 4][k % 4] = r.v[k];
+    }
+  } else {
+    const f32x4_t* p = reinterpret_cast<const f32x4_t*>(static_cast<const float*>(a.w) + c * 4);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const f32x4_t v = p[i];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) t.w[i][k] = v[k];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t.b[i] = 0.0f;
+  if (a.b && a.b_bf16) {
+    const Row8 r = unpack8(load8(static_cast<const uint16_t*>(a.b) + c));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t.b[i] = r.v[i];
+  } else if (a.b) {
+    const f32x4_t* p = reinterpret_cast<const f32x4_t*>(static_cast<const float*>(a.b) + c);
+    const f32x4_t lo = p[0], hi = p[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t.b[i] = lo[i], t.b[4 + i] = hi[i];
   }
   return t;
 }
@@ -95,26 +119,52 @@ __device__ __forceinline__ u32x4_t conv_row(const Taps8& t, bool bias, const Row
 }
 
 // One token of each row: reads the row's three last inputs, writes the
-// output and the inputs moved up by one.
-__global__ __launch_bounds__(256) void conv_step_kernel(ConvStateArgs a) {
-  const int64_t nvec = a.C / 8;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= a.rows * nvec) return;
-  const int64_t row = i / nvec, c = (i - row * nvec) * 8;
-  uint16_t* y = a.y + row * a.C + c;
-  const int64_t slot = slot_of(a.index, row, a.slots);
-  if (slot < 0) {
-    store8(y, (u32x4_t){0u, 0u, 0u, 0u});
-    return;
-  }
-  uint16_t* st = a.state + slot * 3 * a.C + c;
+// output and the inputs moved up by one.  A wave has 64 vectors of eight
+// channels, keeps their weights and takes `rows` rows one after another, the
+// next row's loads requested before the current is computed.
+__global__ __launch_bounds__(256) void conv_step_kernel(ConvStateArgs a, int32_t rows) {
+  const int64_t nvec = a.C / 8, vblocks = (nvec + 63) / 64;
+  const int64_t wave = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64u);
+  const int64_t rb = wave / vblocks;
+  const int64_t v = (wave - rb * vblocks) * 64 + (threadIdx.x & 63);
+  if (v >= nvec) return;
+  const uint32_t c = (uint32_t)v * 8;
+  const int64_t row1 = min((rb + 1) * rows, a.rows);
+  struct Row {
+    int64_t slot;
+    u32x4_t h3, h2, h1, x;
+  };
+  auto load = [&](int64_t row) {
+    Row r;
+    r.slot = slot_of(a.index, row, a.slots);
+    r.x = load8(a.x + row * a.x_stride + c);
+    if (r.slot >= 0) {
+      const uint16_t* st = a.state + r.slot * 3 * a.C + c;
+      r.h3 = load8(st);
+      r.h2 = load8(st + a.C);
+      r.h1 = load8(st + 2 * a.C);
+    }
+    return r;
+  };
+  int64_t row = rb * rows;
+  if (row >= row1) return;
+  Row next = load(row);
   const Taps8 t = load_taps(a, c);
-  const u32x4_t h3 = load8(st), h2 = load8(st + a.C), h1 = load8(st + 2 * a.C);
-  const u32x4_t x = load8(a.x + row * a.x_stride + c);
-  store8(y, conv_row(t, a.b != nullptr, unpack8(h3), unpack8(h2), unpack8(h1), unpack8(x)));
-  store8(st, h2);
-  store8(st + a.C, h1);
-  store8(st + 2 * a.C, x);
+#pragma unroll 1
+  for (; row < row1; ++row) {
+    const Row r = next;
+    if (row + 1 < row1) next = load(row + 1);
+    uint16_t* y = a.y + row * a.C + c;
+    if (r.slot < 0) {
+      store8(y, (u32x4_t){0u, 0u, 0u, 0u});
+      continue;
+    }
+    uint16_t* st = a.state + r.slot * 3 * a.C + c;
+    store8(y, conv_row(t, a.b != nullptr, unpack8(r.h3), unpack8(r.h2), unpack8(r.h1), unpack8(r.x)));
+    store8(st, r.h2);
+    store8(st + a.C, r.h1);
+    store8(st + 2 * a.C, r.x);
+  }
 }
 
 // What a prompt's carried state changes after the packed forward has run
@@ -161,8 +211,12 @@ __global__ __launch_bounds__(64) void conv_edges_kernel(ConvStateArgs a) {
 }  // namespace
 
 hipError_t launch_conv_step(const ConvStateArgs& a, hipStream_t s) {
-  const int64_t n = a.rows * (a.C / 8);
-  hipLaunchKernelGGL(conv_step_kernel, dim3((uint32_t)((n + 255) / 256)), dim3(256), 0, s, a);
+  const int64_t vblocks = (a.C / 8 + 63) / 64;
+  // Rows a wave takes: as many as leave four waves a SIMD, at most 8.
+  int64_t rows = vblocks * a.rows / 4096;
+  rows = rows < 1 ? 1 : rows > 8 ? 8 : rows;
+  const int64_t waves = vblocks * ((a.rows + rows - 1) / rows);
+  hipLaunchKernelGGL(conv_step_kernel, dim3((uint32_t)((waves + 3) / 4)), dim3(256), 0, s, a, (int32_t)rows);
   return hipGetLastError();
 }
 

@@ -26,12 +26,6 @@
 namespace vdc {
 namespace {
 
-typedef const __attribute__((address_space(4))) uint32_t* scalar_ptr;
-
-// Entry i of an int32 array the whole wave asks for, in a scalar register.
-__device__ __forceinline__ int32_t uniform_at(const int32_t* p, int32_t i) {
-  return (int32_t)((scalar_ptr)(uintptr_t)p)[i];
-}
 // A value that is the same in all lanes, back in scalar registers: where
 // control flow joins the compiler may have moved it to vector registers.
 __device__ __forceinline__ const uint16_t* uniform(const uint16_t* p) {
@@ -42,13 +36,12 @@ __device__ __forceinline__ const uint16_t* uniform(const uint16_t* p) {
 }
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// Whether document d resumes, and its slot (-1: none).
+// Whether document d resumes, and its slot.
 __device__ __forceinline__ bool resumes(const ScanArgs& a, int32_t d) {
   return a.resume && __builtin_amdgcn_readfirstlane((int32_t)a.resume[d]) != 0;
 }
 __device__ __forceinline__ int64_t doc_slot(const ScanArgs& a, int32_t d) {
-  const int64_t s = a.index ? (int64_t)uniform_at(a.index, d) : (int64_t)d;
-  return s >= 0 && s < a.slots ? s : -1;
+  return slot_of(a.index, d, a.slots);
 }
 
 // First index i in [0, n) with cu[i] >= v (n if none), by a whole wave.
@@ -697,14 +690,6 @@ __device__ __forceinline__ uint32_t starts_from(const Starts& m, int32_t i) {
   return uniform(__builtin_amdgcn_alignbit(m.bits[(i >> 5) + 1], m.bits[i >> 5], (uint32_t)i & 31u));
 }
 
-template <int kCtrl>
-__device__ __forceinline__ float dpp(float v) {
-  return __uint_as_float(
-      (uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), kCtrl, 0xf, 0xf, true));
-}
-constexpr int kXor1 = 0xb1, kXor2 = 0x4e, kRor4 = 0x124, kRor8 = 0x128,  // quad_perm, row_ror
-              kHalfMirror = 0x141;
-
 // A lane's tile: RC channels x RN states.  P lanes share a channel set:
 // lane = P * set + part, states RN * part .. of channels RC * set .. .  More
 // states a lane make the sums over states cheap, more channels those over
@@ -775,18 +760,6 @@ __device__ __forceinline__ float fma_apart(float a, float b, float c) {
   float r;
   asm("v_fma_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
   return r;
-}
-
-// Sum over all lanes.
-__device__ __forceinline__ float wave_sum(float v) {
-  v += dpp<kXor1>(v);
-  v += dpp<kXor2>(v);
-  v += dpp<kRor4>(v);
-  v += dpp<kRor8>(v);
-  auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
-  s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return __uint_as_float(s[0]) + __uint_as_float(s[1]);
 }
 
 // Runs a chunk backwards in blocks of kScanKeep tokens.  A block's states are
@@ -1089,7 +1062,7 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
           const float y = __builtin_fmaf(own_dx, m.cb[at], set_sum<P, RC>(y0, odd));
           put(oz, tok, dy * __builtin_fmaf(Dc, x, y) * dsilu_f32(z, sz));
         }
-        const float gdx = wave_sum(part < RC ? gy * own_dx : 0.0f);
+        const float gdx = lanes_sum<64>(part < RC ? gy * own_dx : 0.0f);
         sets_sum<P, RN>(dB);
         sets_sum<P, RN>(dC);
         if ((lane & 15) < P && real) {
@@ -1136,8 +1109,17 @@ __global__ __launch_bounds__(256) void scan_param_sum_kernel(ScanArgs a) {
   const int32_t g = col / (a.wpg * 64), i = col - g * a.wpg * 64;
   if (col >= a.cols || i >= a.per) return;
   const float* p = a.pparam + (int64_t)n * a.cols + col;
+  const int64_t row = (int64_t)(a.N + 2) * a.cols;
   double sum = 0.0;
-  for (int32_t k = 0; k < a.chunks; ++k) sum += p[(int64_t)k * (a.N + 2) * a.cols];
+  int32_t k = 0;
+  for (; k + 16 <= a.chunks; k += 16) {  // 16 loads at once
+    float v[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = p[(k + j) * row];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) sum += v[j];
+  }
+  for (; k < a.chunks; ++k) sum += p[k * row];
   const int64_t c = (int64_t)g * a.per + i;
   if (n < a.N) param_put(a.dA, a.A_bf16, c * a.N + n, (float)sum);
   else if (n == a.N) {
@@ -1162,42 +1144,122 @@ __global__ __launch_bounds__(256) void scan_bc_sum_kernel(ScanArgs a, int32_t bp
 
 // --------------------------------------------------------- single tokens --
 
-// One token a row: NL lanes hold a channel's states, four each.
-template <int NL>
-__global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs a) {
-  const int64_t e = (int64_t)blockIdx.x * (256 / NL) + threadIdx.x / NL;
-  const int32_t part = threadIdx.x % NL;
-  const bool there = e < (int64_t)a.S * a.C;
-  const int64_t row = there ? e / a.C : 0, c = there ? e - row * a.C : 0;
-  const int64_t slot = slot_of(a.index, row, a.slots);
-  float y = 0.0f, x = 0.0f;
-  if (there && slot >= 0) {
-    x = bf16_f32(a.x[row * a.xs + c]);
-    const float d = step_size(a, bf16_f32(a.dt[row * a.dts + c]), step_bias(a, c));
-    const int64_t g = c / a.per;
-    float* h = a.state + (slot * a.C + c) * a.N;
+// One token a row.  NL lanes hold a channel's states, four each, so that a
+// wave reads and writes 1 KiB of states in a row; it keeps its channels' A, D
+// and bias and takes `rows` rows one after another, the next row's loads
+// requested before the current is computed.  kVec: N is a multiple of 4 and
+// the states are 16-byte aligned.
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+
+template <int NL, bool kVec, bool kGate>
+__global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs a, int32_t rows) {
+  constexpr int kChannels = 64 / NL;
+  const int32_t cblocks = (a.C + kChannels - 1) / kChannels;
+  const int64_t wave = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64u);
+  const int64_t rb = wave / cblocks;
+  const int32_t lane = threadIdx.x & 63, part = lane % NL;
+  const int32_t c0 = (int32_t)(wave - rb * cblocks) * kChannels + lane / NL;
+  const bool there = c0 < a.C;
+  const uint32_t c = there ? c0 : 0;
+  const int32_t row0 = (int32_t)min(rb * rows, (int64_t)a.S), row1 = (int32_t)min((rb + 1) * rows, (int64_t)a.S);
+  const int32_t n0 = 4 * part;
+  float A2[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int32_t n = 4 * part + j;
-      if (n < a.N) {
-        const float e2 = __builtin_amdgcn_exp2f(d * (param_at(a.A, a.A_bf16, c * a.N + n) * kLog2E));
-        const float v = __builtin_fmaf(e2, h[n], d * x * bf16_f32(a.B[row * a.Bs + g * a.N + n]));
-        h[n] = v;
-        y = __builtin_fmaf(bf16_f32(a.Cm[row * a.Cs + g * a.N + n]), v, y);
+  for (int j = 0; j < 4; ++j)
+    A2[j] = n0 + j < a.N ? param_at(a.A, a.A_bf16, (int64_t)c * a.N + n0 + j) * kLog2E : 0.0f;
+  const StepBias bias = step_bias(a, c);
+  const float Dc = a.D ? param_at(a.D, a.D_bf16, c) : 0.0f;
+  const uint32_t bc0 = c / (uint32_t)a.per * (uint32_t)a.N + n0;
+  const uint32_t h0 = c * (uint32_t)a.N + n0;
+
+  struct Row {
+    int64_t slot;
+    float h[4], b[4], c[4];
+    uint16_t x, dt, z;
+  };
+  auto states = [&](const uint16_t* p, float (&o)[4]) {
+    if (kVec) {
+      const u32x2_any v = *reinterpret_cast<const u32x2_any*>(p);
+      o[0] = bf16_lo(v.x), o[1] = bf16_hi(v.x), o[2] = bf16_lo(v.y), o[3] = bf16_hi(v.y);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = n0 + j < a.N ? bf16_f32(p[j]) : 0.0f;
+    }
+  };
+  const bool some = kVec ? n0 < a.N : true;  // NL lanes may hold more than N states
+  auto load = [&](int32_t row) {
+    Row r;
+    r.slot = slot_of(a.index, row, a.slots);
+    r.x = (a.x + row * a.xs)[c];
+    r.dt = (a.dt + row * a.dts)[c];
+    r.z = kGate ? (a.z + row * a.zs)[c] : (uint16_t)0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.h[j] = r.b[j] = r.c[j] = 0.0f;
+    if (r.slot >= 0 && some) {
+      states(a.B + row * a.Bs + bc0, r.b);
+      states(a.Cm + row * a.Cs + bc0, r.c);
+      const float* h = a.state + r.slot * a.C * a.N + h0;
+      if (kVec) {
+        const f32x4_t v = *reinterpret_cast<const f32x4_t*>(h);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r.h[j] = v[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r.h[j] = n0 + j < a.N ? h[j] : 0.0f;
       }
     }
-  }
+    return r;
+  };
+  if (row0 >= row1) return;
+  Row next = load(row0);
+#pragma unroll 1
+  for (int32_t row = row0; row < row1; ++row) {
+    Row r = next;
+    if (row + 1 < row1) next = load(row + 1);
+    float y = 0.0f;
+    if (r.slot >= 0) {
+      const float x = bf16_f32(r.x), d = step_size(a, bf16_f32(r.dt), bias), dx = d * x;
 #pragma unroll
-  for (int o = 1; o < NL; o *= 2) y += __shfl_xor(y, o);
-  if (there && part == 0) {
-    if (slot >= 0) {
-      if (a.D) y = __builtin_fmaf(param_at(a.D, a.D_bf16, c), x, y);
-      if (a.z) {
-        const float z = bf16_f32(a.z[row * a.zs + c]);
+      for (int j = 0; j < 4; ++j) {
+        r.h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(d * A2[j]), r.h[j], dx * r.b[j]);
+        y = __builtin_fmaf(r.c[j], r.h[j], y);
+      }
+      y = __builtin_fmaf(Dc, x, lanes_sum<NL>(y));
+      if (kGate) {
+        const float z = bf16_f32(r.z);
         y *= z * sigmoid_f32(z);
       }
+      if (there && some) {
+        float* h = a.state + r.slot * a.C * a.N + h0;
+        if (kVec) {
+          *reinterpret_cast<f32x4_t*>(h) = (f32x4_t){r.h[0], r.h[1], r.h[2], r.h[3]};
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (n0 + j < a.N) h[j] = r.h[j];
+        }
+      }
     }
-    a.y[row * a.C + c] = slot >= 0 ? bf16_of(y) : (uint16_t)0;
+    if (there && part == 0) (a.y + (int64_t)row * a.C)[c] = bf16_of(y);
+  }
+}
+
+template <int NL>
+void step_nl(const ScanArgs& a, hipStream_t s) {
+  constexpr int kChannels = 64 / NL;
+  const int64_t cblocks = (a.C + kChannels - 1) / kChannels;
+  // Rows a wave takes: as many as leave four waves a SIMD, at most 8.
+  int64_t rows = cblocks * a.S / 4096;
+  rows = rows < 1 ? 1 : rows > 8 ? 8 : rows;
+  const int64_t waves = cblocks * ((a.S + rows - 1) / rows);
+  const dim3 grid((uint32_t)((waves + 3) / 4)), block(256);
+  const bool vec = a.N % 4 == 0 && reinterpret_cast<uintptr_t>(a.state) % 16 == 0;
+  if (a.z) {
+    if (vec) hipLaunchKernelGGL((scan_step_kernel<NL, true, true>), grid, block, 0, s, a, (int32_t)rows);
+    else hipLaunchKernelGGL((scan_step_kernel<NL, false, true>), grid, block, 0, s, a, (int32_t)rows);
+  } else {
+    if (vec) hipLaunchKernelGGL((scan_step_kernel<NL, true, false>), grid, block, 0, s, a, (int32_t)rows);
+    else hipLaunchKernelGGL((scan_step_kernel<NL, false, false>), grid, block, 0, s, a, (int32_t)rows);
   }
 }
 
@@ -1288,16 +1350,11 @@ hipError_t launch_scan_bwd_sum(const ScanArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_scan_step(const ScanArgs& a, hipStream_t s) {
-  const int64_t n = (int64_t)a.S * a.C;
-  const int nl = a.N <= 4 ? 1 : a.N <= 8 ? 2 : a.N <= 16 ? 4 : a.N <= 32 ? 8 : 16;
-  const dim3 grid((uint32_t)((n + 256 / nl - 1) / (256 / nl))), block(256);
-  switch (nl) {
-    case 1: hipLaunchKernelGGL(scan_step_kernel<1>, grid, block, 0, s, a); break;
-    case 2: hipLaunchKernelGGL(scan_step_kernel<2>, grid, block, 0, s, a); break;
-    case 4: hipLaunchKernelGGL(scan_step_kernel<4>, grid, block, 0, s, a); break;
-    case 8: hipLaunchKernelGGL(scan_step_kernel<8>, grid, block, 0, s, a); break;
-    default: hipLaunchKernelGGL(scan_step_kernel<16>, grid, block, 0, s, a); break;
-  }
+  if (a.N <= 4) step_nl<1>(a, s);
+  else if (a.N <= 8) step_nl<2>(a, s);
+  else if (a.N <= 16) step_nl<4>(a, s);
+  else if (a.N <= 32) step_nl<8>(a, s);
+  else step_nl<16>(a, s);
   return hipGetLastError();
 }
 

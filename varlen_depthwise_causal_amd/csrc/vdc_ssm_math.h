@@ -69,10 +69,46 @@ __device__ __forceinline__ float softplus_f32(float p, float q, float q2) {
   return __builtin_fmaf(0.5f, v + __builtin_fabsf(v), s * r);
 }
 
-// The slot of sequence `i` in a cache of `slots` sequences, or -1 where it
-// has none (an index outside the cache marks a row of padding).
+// The value of the lane that the DPP control kCtrl names.
+template <int kCtrl>
+__device__ __forceinline__ float dpp(float v) {
+  return __uint_as_float(
+      (uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), kCtrl, 0xf, 0xf, true));
+}
+constexpr int kXor1 = 0xb1, kXor2 = 0x4e, kRor4 = 0x124, kRor8 = 0x128,  // quad_perm, row_ror
+              kMirror = 0x140, kHalfMirror = 0x141;
+
+// Sum over the aligned group of L lanes that a lane is in, left in all of
+// them, in one fixed order.
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+  if constexpr (L >= 2) v += dpp<kXor1>(v);
+  if constexpr (L >= 4) v += dpp<kXor2>(v);
+  if constexpr (L >= 8) v += dpp<kHalfMirror>(v);
+  if constexpr (L >= 16) v += dpp<kMirror>(v);
+  if constexpr (L >= 32) {
+    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  }
+  if constexpr (L >= 64) {
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  }
+  return v;
+}
+
+typedef const __attribute__((address_space(4))) uint32_t* scalar_ptr;
+
+// Entry i of an int32 array the whole wave asks for, in a scalar register.
+__device__ __forceinline__ int32_t uniform_at(const int32_t* p, int64_t i) {
+  return (int32_t)((scalar_ptr)(uintptr_t)p)[i];
+}
+
+// The slot of sequence `i`, the same for a whole wave, in a cache of `slots`
+// sequences, or -1 where it has none (an index outside the cache marks a row
+// of padding).
 __device__ __forceinline__ int64_t slot_of(const int32_t* index, int64_t i, int64_t slots) {
-  const int64_t s = index ? (int64_t)index[i] : i;
+  const int64_t s = index ? (int64_t)uniform_at(index, i) : i;
   return s >= 0 && s < slots ? s : -1;
 }
 
