@@ -1263,6 +1263,189 @@ void step_nl(const ScanArgs& a, hipStream_t s) {
   }
 }
 
+// ----------------------------------------------------------- short prompts --
+//
+// The forward of a row of tokens too short to be worth cutting: the lanes of
+// the single-token form, walking the row.  A token then takes a wave a third
+// of the instructions that it takes with all states in a lane, and the row
+// one launch instead of three.  kVec: N a multiple of 4.
+
+template <int NL, bool kVec, bool kGate>
+__global__ __launch_bounds__(64) void scan_short_kernel(ScanArgs a) {
+  constexpr int kChannels = 64 / NL, kAhead = 8;
+  // The outputs wait here for the end: loads and stores share one counter of
+  // outstanding accesses, and a store among the loads would be waited for with
+  // every group of them.
+  __shared__ uint16_t out[kScanShort][kChannels];
+  const int32_t lane = threadIdx.x & 63, part = lane % NL, n0 = 4 * part;
+  const int32_t c0 = (int32_t)blockIdx.x * kChannels + lane / NL;
+  const bool there = c0 < a.C, some = n0 < a.N;
+  const uint32_t c = there ? c0 : 0;
+  const int32_t S = a.S;
+  float A2[4], h[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    A2[j] = n0 + j < a.N ? param_at(a.A, a.A_bf16, (int64_t)c * a.N + n0 + j) * kLog2E : 0.0f;
+    h[j] = 0.0f;
+  }
+  const StepBias bias = step_bias(a, c);
+  const float Dc = a.D ? param_at(a.D, a.D_bf16, c) : 0.0f;
+  const uint32_t bc0 = c / (uint32_t)a.per * (uint32_t)a.N + (some ? n0 : 0);
+  const uint32_t h0 = c * (uint32_t)a.N + n0;
+
+  struct Raw {
+    uint32_t x, dt, z;
+    u32x2_any B, C;  // four states
+  };
+  auto four = [&](const uint16_t* p) {
+    if (kVec) return *reinterpret_cast<const u32x2_any*>(p);
+    uint32_t v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = n0 + j < a.N ? (uint32_t)p[j] : 0u;
+    return (u32x2_any){v[0] | v[1] << 16, v[2] | v[3] << 16};
+  };
+  // The next token's; past the end the last token's again.  A wave here has
+  // its SIMD to itself and is bound by the instructions it issues, addresses
+  // among them.
+  RowBuffer bx, bd, bz;
+  bx.open(a.x, 0, a.xs);
+  bd.open(a.dt, 0, a.dts);
+  bz.open(kGate ? a.z : a.x, 0, kGate ? a.zs : a.xs);
+  const uint16_t *pB = a.B, *pC = a.Cm;
+  const uint32_t lane2 = c * 2u;
+  int32_t left = S;
+  auto request = [&]() {
+    Raw r;
+    r.x = bx.get(lane2);
+    r.dt = bd.get(lane2);
+    r.z = kGate ? bz.get(lane2) : 0u;
+    r.B = four(pB + bc0);
+    r.C = four(pC + bc0);
+    --left;
+    const bool more = left > 0;
+    bx.row += more ? bx.stride : 0u;
+    bd.row += more ? bd.stride : 0u;
+    if (kGate) bz.row += more ? bz.stride : 0u;
+    pB += more ? a.Bs : 0;
+    pC += more ? a.Cs : 0;
+    return r;
+  };
+  int32_t doc = -1, next = 0;
+  auto write = [&](int32_t d) {
+    const int64_t slot = a.state ? slot_of(a.index, d, a.slots) : -1;
+    if (slot < 0 || !there) return;
+    float* s = a.state + slot * a.C * a.N + h0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (n0 + j < a.N) s[j] = h[j];
+  };
+  // The document that starts at t, past the empty ones before it.
+  auto open = [&](int32_t d, int32_t t) {
+    while (true) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[j] = 0.0f;
+      if (d >= a.num_docs || uniform_at(a.cu, d + 1) > t) break;
+      if (!resumes(a, d)) write(d);
+      ++d;
+    }
+    doc = d;
+    next = d < a.num_docs ? uniform_at(a.cu, d + 1) : INT32_MAX;
+    if (a.state && d < a.num_docs && resumes(a, d)) {
+      const int64_t slot = slot_of(a.index, d, a.slots);
+      if (slot >= 0) {
+        const float* s = a.state + slot * a.C * a.N + h0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (n0 + j < a.N) h[j] = s[j];
+      }
+    }
+  };
+  // kTokens tokens from t on.  What does not wait for the states, and the sums
+  // over the lanes, stand side by side for all of them: a wave alone on its
+  // SIMD would otherwise wait for most of its own results.
+  auto tokens = [&](auto count, const Raw* r, int32_t t) {
+    constexpr int kTokens = decltype(count)::value;
+    float x[kTokens], d[kTokens], y[kTokens];
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+      x[i] = bf16_lo(r[i].x);
+      d[i] = step_size(a, bf16_lo(r[i].dt), bias);
+    }
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+      const float dx = d[i] * x[i];
+      const float b[4] = {bf16_lo(r[i].B.x), bf16_hi(r[i].B.x), bf16_lo(r[i].B.y), bf16_hi(r[i].B.y)};
+      const float cm[4] = {bf16_lo(r[i].C.x), bf16_hi(r[i].C.x), bf16_lo(r[i].C.y), bf16_hi(r[i].C.y)};
+      y[i] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(d[i] * A2[j]), h[j], dx * b[j]);
+        y[i] = __builtin_fmaf(cm[j], h[j], y[i]);
+      }
+      if (!some) y[i] = 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+      float v = __builtin_fmaf(Dc, x[i], lanes_sum<NL>(y[i]));
+      if (kGate) {
+        const float z = bf16_lo(r[i].z);
+        v *= z * sigmoid_f32(z);
+      }
+      if (part == 0) out[t + i][lane / NL] = bf16_of(v);
+    }
+  };
+
+  Raw q[kAhead];
+  if (S > 0) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) q[i] = request();
+  }
+  open(0, 0);
+  int32_t t = 0;
+#pragma unroll 1
+  while (t < S) {
+    const int32_t end = next > t && next < S ? next : S;
+#pragma unroll 1
+    for (; t + kAhead <= end; t += kAhead) {
+      Raw r[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        r[i] = q[i];
+        q[i] = request();
+      }
+      tokens(std::integral_constant<int, kAhead>(), r, t);
+    }
+#pragma unroll 1
+    for (; t < end; ++t) {
+      const Raw r = q[0];
+#pragma unroll
+      for (int i = 0; i + 1 < kAhead; ++i) q[i] = q[i + 1];
+      q[kAhead - 1] = request();
+      tokens(std::integral_constant<int, 1>(), &r, t);
+    }
+    if (t == next && doc < a.num_docs) {
+      write(doc);
+      open(doc + 1, t);
+    }
+  }
+  for (int32_t i = lane / kChannels; i < S; i += NL) {
+    const int32_t k = (int32_t)blockIdx.x * kChannels + lane % kChannels;
+    if (k < a.C) a.y[(int64_t)i * a.C + k] = out[i][lane % kChannels];
+  }
+}
+
+template <int NL>
+void short_nl(const ScanArgs& a, hipStream_t s) {
+  const dim3 grid((uint32_t)((a.C + 64 / NL - 1) / (64 / NL))), block(64);
+  if (a.z) {
+    if (a.N % 4 == 0) hipLaunchKernelGGL((scan_short_kernel<NL, true, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((scan_short_kernel<NL, false, true>), grid, block, 0, s, a);
+  } else {
+    if (a.N % 4 == 0) hipLaunchKernelGGL((scan_short_kernel<NL, true, false>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((scan_short_kernel<NL, false, false>), grid, block, 0, s, a);
+  }
+}
+
 // Whether B's and C's rows can be read by whole dwords (see Uniform).
 bool wide_rows(const ScanArgs& a) {
   const auto even = [](const uint16_t* p, int64_t stride) {
@@ -1346,6 +1529,15 @@ hipError_t launch_scan_bwd_sum(const ScanArgs& a, hipStream_t s) {
   if (n == 0) return hipSuccess;
   hipLaunchKernelGGL(scan_bc_sum_kernel, dim3((uint32_t)((n + 255) / 256)), dim3(256), 0, s, a, bpg,
                      scan_states(a.N));
+  return hipGetLastError();
+}
+
+hipError_t launch_scan_short(const ScanArgs& a, hipStream_t s) {
+  if (a.N <= 4) short_nl<1>(a, s);
+  else if (a.N <= 8) short_nl<2>(a, s);
+  else if (a.N <= 16) short_nl<4>(a, s);
+  else if (a.N <= 32) short_nl<8>(a, s);
+  else short_nl<16>(a, s);
   return hipGetLastError();
 }
 

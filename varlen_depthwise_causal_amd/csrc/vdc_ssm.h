@@ -40,6 +40,9 @@ constexpr int kMaxStates = 64;
 // document starts are a bitmask in LDS).
 constexpr int kScanKeep = 8;
 constexpr int kScanMaxChunk = 2048;
+// Forward rows of at most this many tokens are not cut: one launch, against
+// three.
+constexpr int kScanShort = 80;
 
 struct ScanArgs {
   const uint16_t *x, *dt, *z, *B, *Cm, *dy;
@@ -89,6 +92,7 @@ hipError_t launch_scan_bwd_local(const ScanArgs& a, hipStream_t s);
 hipError_t launch_scan_bwd_main(const ScanArgs& a, hipStream_t s);
 hipError_t launch_scan_bwd_sum(const ScanArgs& a, hipStream_t s);
 hipError_t launch_scan_step(const ScanArgs& a, hipStream_t s);
+hipError_t launch_scan_short(const ScanArgs& a, hipStream_t s);
 
 // ------------------------------------------------------------ group norm --
 
