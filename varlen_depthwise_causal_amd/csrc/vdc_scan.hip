@@ -430,9 +430,9 @@ void scan_fwd_kernel(ScanArgs a, int32_t work) {
 // Joins the chunks: forward in time the states after each chunk, and for the
 // backward (blockIdx.z = 1) against it the gradients that leave each chunk.
 // A lane has one column and state; the chain is short, the loads are what
-// takes time, so those of kJoin chunks are requested at once.
+// takes time, so those of kJoin chunks are requested at once, a batch ahead.
 __global__ __launch_bounds__(64) void scan_join_kernel(ScanArgs a) {
-  constexpr int kJoin = 16;
+  constexpr int kJoin = 8;
   const int32_t col = blockIdx.x * 64 + threadIdx.x, n = blockIdx.y;
   const int32_t g = col / (a.wpg * 64), i = col - g * a.wpg * 64;
   if (i >= a.per) return;
@@ -441,28 +441,38 @@ __global__ __launch_bounds__(64) void scan_join_kernel(ScanArgs a) {
   float* v = (back ? a.mu : a.hend) + (int64_t)n * a.cols + col;
   const int64_t row = (int64_t)a.N * a.cols;
   const int32_t steps = a.chunks - 1;
-  float carry = 0.0f;
-  for (int32_t s0 = 0; s0 < steps; s0 += kJoin) {
-    float own[kJoin], decay[kJoin];
+  struct Batch {
+    float own[kJoin], sum[kJoin];
+    int32_t flags[kJoin];
+  };
+  auto chunk_at = [&](int32_t s) { return back ? a.chunks - 1 - s : s; };
+  auto load = [&](int32_t s0) {
+    Batch r;
 #pragma unroll
     for (int j = 0; j < kJoin; ++j) {
-      const int32_t s = min(s0 + j, steps - 1), k = back ? a.chunks - 1 - s : s;
-      own[j] = v[k * row];
-      decay[j] = a.sum[(int64_t)k * a.cols + col];
+      const int32_t k = chunk_at(min(s0 + j, steps - 1));
+      r.own[j] = v[k * row];
+      r.sum[j] = a.sum[(int64_t)k * a.cols + col];
+      r.flags[j] = uniform_at(a.flags, k);
     }
+    return r;
+  };
+  float carry = 0.0f;
+  Batch next = load(0);
+#pragma unroll 1
+  for (int32_t s0 = 0; s0 < steps; s0 += kJoin) {
+    const Batch now = next;
+    if (s0 + kJoin < steps) next = load(s0 + kJoin);
+    float decay[kJoin];
+#pragma unroll
+    for (int j = 0; j < kJoin; ++j) decay[j] = __builtin_amdgcn_exp2f(A2 * now.sum[j]);
 #pragma unroll
     for (int j = 0; j < kJoin; ++j) {
-      if (s0 + j >= steps) break;
-      const int32_t k = back ? a.chunks - 1 - (s0 + j) : s0 + j;
-      const int32_t f = uniform_at(a.flags, k);
-      if (back && (f & 1)) {
-        carry = 0.0f;  // a document starts with the chunk: nothing leaves it
-      } else if (f == 0 && carry != 0.0f) {
-        carry = __builtin_fmaf(__builtin_amdgcn_exp2f(A2 * decay[j]), carry, own[j]);
-      } else {
-        carry = own[j];
-      }
-      v[k * row] = carry;
+      const int32_t f = now.flags[j];
+      // Nothing goes past a document's start; 0 times an infinite decay is 0.
+      carry = f == 0 && carry != 0.0f ? __builtin_fmaf(decay[j], carry, now.own[j]) : now.own[j];
+      if (back && (f & 1)) carry = 0.0f;  // nothing leaves a chunk that a document starts with
+      if (s0 + j < steps) v[chunk_at(s0 + j) * row] = carry;
     }
   }
 }

@@ -163,11 +163,16 @@ int scan_sizes(int64_t S, int64_t C, int64_t N, int64_t G) {
 // SIMDs only at C = 65536 and more, so a row of tokens is cut until about
 // kScanWaves waves run.  A function of the sizes only.
 constexpr int64_t kScanWaves = 4096;
-// Rows that do not fill the machine are cut further than that would ask, as
-// long as the chunks save more than joining them costs: forward into about
-// 24, of 8 to 32 tokens (C = 2048: 22 us for 128 tokens in chunks of 8 and 37
-// in chunks of 32; 1024 tokens 64 and 43).
-constexpr int64_t kScanCut = 24, kScanMinChunk = 8, kScanCutChunk = 32;
+// Rows that do not fill the machine are cut as far as the chunks save more
+// than joining them costs: to about a wave for each SIMD, into 24 (backward
+// 64, a token takes five times as long) to 96 chunks, but not below 8
+// (backward 16) tokens, and no further than to 32.  Forward, C = 512 and 512
+// tokens: 64 chunks 30 us, 22 chunks 35; C = 4096: 55 and 47.  Backward,
+// C = 4096: 64 chunks 98 us, 22 chunks 116.
+constexpr int64_t kScanSimds = 1024, kScanMinCut[2] = {24, 64}, kScanMaxCut = 96;
+constexpr int64_t kScanMinChunk[2] = {8, 16}, kScanCutChunk = 32;
+static_assert(VDC_FWD == 0 && VDC_BWD == 1, "both are indexed by the direction");
+
 // Largest row stride of x, dt, z and dy: a chunk of it stays below 2^31 bytes.
 int64_t scan_stride_limit(int64_t C) { return std::max<int64_t>(int64_t(1) << 19, 4 * C) - 1; }
 
@@ -182,8 +187,8 @@ bool scan_plan(int dir, int64_t S, int64_t C, int64_t N, int64_t G, ScanPlan* ou
   const int64_t blocks = dir == VDC_BWD ? G * ceil_div(per, scan_bwd_channels(N)) : waves;
   const int64_t want = std::max<int64_t>(1, kScanWaves / blocks);
   int64_t chunk = ceil_div(std::max<int64_t>(S, 1), want);
-  const int64_t cut = ceil_div(std::max<int64_t>(S, 1), kScanCut);
-  const int64_t least = dir == VDC_BWD ? kScanCutChunk : std::min(std::max(cut, kScanMinChunk), kScanCutChunk);
+  const int64_t cuts = std::min(std::max(kScanSimds / blocks, kScanMinCut[dir]), kScanMaxCut);
+  const int64_t least = std::min(std::max(ceil_div(S, cuts), kScanMinChunk[dir]), kScanCutChunk);
   chunk = ceil_div(std::max(chunk, least), 8) * 8;
   // A chunk's rows are addressed by 32-bit offsets from its first: with at
   // most 2^28 / C tokens, row strides up to scan_stride_limit fit.
