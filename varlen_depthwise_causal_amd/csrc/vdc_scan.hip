@@ -17,6 +17,7 @@
 // Everything between documents is assigned, never multiplied by zero, so
 // that an infinity or a NaN stays in its document.
 
+#include <cfloat>
 #include <type_traits>
 
 #include "vdc_search.h"
@@ -526,7 +527,9 @@ void scan_bwd_local_kernel(ScanArgs a, int32_t work) {
   bz.open(gated ? a.z : a.x, t0, gated ? a.zs : a.xs);  // without a gate nothing uses it
   const uint16_t* pB = a.B + t0 * a.Bs + l.group * a.N;
   const uint16_t* pC = a.Cm + t0 * a.Cs + l.group * a.N;
-  const uint32_t lane2 = l.c * 2u;
+  // Past a group's channels a lane reads zeros (out of the buffers' range), and
+  // its state and gradient, which the main pass reads, stay zero.
+  const uint32_t lane2 = l.active ? l.c * 2u : 0x80000000u;
   int32_t left = t1 - t0, left_bc = left;
   auto request = [&]() {
     Raw r;
@@ -772,6 +775,22 @@ __device__ __forceinline__ float fma_apart(float a, float b, float c) {
   return r;
 }
 
+// Sets eight values to zero where the uniform `bit` is set, which it hardly
+// ever is.  As control flow of the compiler's own this would cost a copy of
+// the values on the usual path, to bring both into the same registers.
+__device__ __forceinline__ void zero_if(uint32_t bit, float& a, float& b, float& c, float& d, float& e,
+                                        float& f, float& g, float& h) {
+  asm volatile(
+      "s_cmp_eq_u32 %8, 0\n\t"
+      "s_cbranch_scc1 .Lkeep%=\n\t"
+      "v_mov_b32 %0, 0\n\tv_mov_b32 %1, 0\n\tv_mov_b32 %2, 0\n\tv_mov_b32 %3, 0\n\t"
+      "v_mov_b32 %4, 0\n\tv_mov_b32 %5, 0\n\tv_mov_b32 %6, 0\n\tv_mov_b32 %7, 0\n"
+      ".Lkeep%=:"
+      : "+v"(a), "+v"(b), "+v"(c), "+v"(d), "+v"(e), "+v"(f), "+v"(g), "+v"(h)
+      : "s"(bit)
+      : "scc");
+}
+
 // Runs a chunk backwards in blocks of kScanKeep tokens.  A block's states are
 // computed forward from its kept start twice: once for the starts of its
 // sub-blocks of kSub tokens (to LDS, each lane its own), then for each
@@ -789,6 +808,7 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
     Starts starts;
     f32x4_t h[kSubs - 1][RC * RN / 4][64];  // states before the sub-blocks but the last
     f32x4_t in[RC * RN / 4][64];            // what came into the chunk
+    float step[kScanKeep - kSub][64];       // step sizes of the tokens but the last sub-block's
     float bc[kScanKeep][2][NT];       // B and C of the block's tokens
     float cb[kScanKeep];              // sum_n C B
   };
@@ -882,11 +902,12 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
     }
   };
   float h[RC][RN];
-  auto reset = [&](float (&v)[RC][RN]) {
+  auto reset_if = [&](uint32_t bit, float (&v)[RC][RN]) {
 #pragma unroll
-    for (int r = 0; r < RC; ++r)
-#pragma unroll
-      for (int j = 0; j < RN; ++j) v[r][j] = 0.0f;
+    for (int e = 0; e < RC * RN; e += 8)
+      zero_if(bit, v[e / RN][e % RN], v[(e + 1) / RN][(e + 1) % RN], v[(e + 2) / RN][(e + 2) % RN],
+              v[(e + 3) / RN][(e + 3) % RN], v[(e + 4) / RN][(e + 4) % RN], v[(e + 5) / RN][(e + 5) % RN],
+              v[(e + 6) / RN][(e + 6) % RN], v[(e + 7) / RN][(e + 7) % RN]);
   };
   auto states = [&](const float* row, float (&o)[RN]) {
 #pragma unroll
@@ -954,18 +975,25 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
     // The state before the block: kept from zero history, plus what came into
     // the chunk, decayed, if no document has started since.
     {
-      const bool carried = k > 0 && first_start >= i_first;
+      if (ib == 0) {
 #pragma unroll
-      for (int e = 0; e < RC * RN; e += 4) {
-        const f32x4_t in = m.in[e / 4][lane];
+        for (int r = 0; r < RC; ++r) {
+          sum[r] = 0.0f;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int r = (e + q) / RN, j = (e + q) % RN;
-          const bool there = i0 + RC * set + r < a.per && n0 + j < a.N;
-          float v = there && ib > 0 ? h[r][j] : 0.0f;
-          const float decay = ib > 0 ? __builtin_amdgcn_exp2f(A2[r][j] * sum[r]) : 1.0f;
-          if (carried && in[q] != 0.0f) v = __builtin_fmaf(decay, in[q], v);
-          h[r][j] = v;
+          for (int j = 0; j < RN; ++j) h[r][j] = 0.0f;
+        }
+      }
+      if (k > 0 && first_start >= i_first) {
+#pragma unroll
+        for (int e = 0; e < RC * RN; e += 4) {
+          const f32x4_t in = m.in[e / 4][lane];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int r = (e + q) / RN, j = (e + q) % RN;
+            // Finite, so that nothing that came in stays nothing.
+            const float decay = __builtin_fminf(__builtin_amdgcn_exp2f(A2[r][j] * sum[r]), FLT_MAX);
+            h[r][j] = __builtin_fmaf(decay, in[q], h[r][j]);
+          }
         }
       }
     }
@@ -982,8 +1010,9 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
 #pragma unroll
       for (int i = 0; i < kSub; ++i) {
         const int32_t at = s * kSub + i;
-        if ((starts >> at) & 1u) reset(h);
+        reset_if((starts >> at) & 1u, h);
         const float own = step_size(a, bf16_lo(v[i].dt), bias);
+        m.step[at][lane] = own;
         float B[RN], d[RC], dx[RC];
         states(m.bc[at][0], B);
         set_spread<P, RC>(own, d);
@@ -1003,12 +1032,19 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
       for (int i = 0; i < kSub; ++i) v[i] = q[i];
       request(s > 0 ? i_first + (s - 1) * kSub : max(i_first - kScanKeep, 0), s > 0);
       float aw[kSub][RC][RN], hw[kSub][RC][RN];
-      float own[kSub];
+      float own[kSub];  // step sizes, of all but the last sub-block as the way forward left them
+      if (s + 1 < kSubs) {
+#pragma unroll
+        for (int i = 0; i < kSub; ++i) own[i] = m.step[at0 + i][lane];
+      } else {
+#pragma unroll
+        for (int i = 0; i < kSub; ++i) own[i] = step_size(a, bf16_lo(v[i].dt), bias);
+      }
 #pragma unroll
       for (int i = 0; i < kSub; ++i) {
-        if ((starts >> (at0 + i)) & 1u) reset(h);
+        reset_if((starts >> (at0 + i)) & 1u, h);
         // A token past the end does nothing: no step, and no gradient below.
-        own[i] = i_first + at0 + i <= last ? step_size(a, bf16_lo(v[i].dt), bias) : 0.0f;
+        own[i] = i_first + at0 + i <= last ? own[i] : 0.0f;
         float B[RN], d[RC], dx[RC];
         states(m.bc[at0 + i][0], B);
         set_spread<P, RC>(own[i], d);
@@ -1060,7 +1096,7 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
             mu[r][j] = aw[i][r][j] * lam;
           }
         }
-        if ((starts >> at) & 1u) reset(mu);
+        reset_if((starts >> at) & 1u, mu);
         const float slb = set_sum<P, RC>(lb, odd), sva = set_sum<P, RC>(va, odd) * kLn2;
         float ddt = __builtin_fmaf(x, slb, sva);
         if (a.softplus) ddt *= sigmoid_f32(bf16_lo(v[i].dt) + bias.b);
