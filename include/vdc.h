@@ -306,7 +306,8 @@ int conv1d_update(const void *x, int64_t x_stride, const void *weight, int w_dty
  * zero, or its slot's state where the document resumes.
  */
 typedef struct vdc_scan {
-    int64_t S;        /* tokens; for selective_update rows, one token each   */
+    int64_t S;        /* tokens, at most 2^31 - 4096; for selective_update
+                         rows, one token each                                */
     int64_t C;        /* channels, 1 .. 2^20                                 */
     int64_t N;        /* states of a channel, 1 .. 64                        */
     int64_t groups;   /* groups of B and Cm; divides C                       */

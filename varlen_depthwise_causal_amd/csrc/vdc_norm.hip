@@ -290,18 +290,19 @@ __device__ __forceinline__ Stats stats_of(const NormArgs& a, const uint16_t* x) 
 }
 
 __global__ __launch_bounds__(256) void norm_fwd_any_kernel(NormArgs a) {
-  const int64_t e = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
   const int lane = threadIdx.x & 63;
-  if (e >= a.S * a.G) return;
-  const int64_t t = e / a.G, c0 = (e - t * a.G) * a.per;
-  const uint16_t* x = a.x + t * a.xs + c0;
-  const Stats st = stats_of(a, x);
-  for (int i = lane; i < a.per; i += 64) {
-    const float xh = (bf16_f32(x[i]) - st.mean) * st.rstd;
-    const float v = __builtin_fmaf(xh, param_at(a.w, a.w_bf16, c0 + i),
-                                   a.b ? param_at(a.b, a.b_bf16, c0 + i) : 0.0f);
-    const float u = a.z ? bf16_f32(a.z[t * a.zs + c0 + i]) : v;
-    a.y[t * a.C + c0 + i] = bf16_of(v * (a.z ? u * sigmoid_f32(u) : sigmoid_f32(v)));
+  const int64_t step = (int64_t)gridDim.x * 4;
+  for (int64_t e = (int64_t)blockIdx.x * 4 + threadIdx.x / 64; e < a.S * a.G; e += step) {
+    const int64_t t = e / a.G, c0 = (e - t * a.G) * a.per;
+    const uint16_t* x = a.x + t * a.xs + c0;
+    const Stats st = stats_of(a, x);
+    for (int i = lane; i < a.per; i += 64) {
+      const float xh = (bf16_f32(x[i]) - st.mean) * st.rstd;
+      const float v = __builtin_fmaf(xh, param_at(a.w, a.w_bf16, c0 + i),
+                                     a.b ? param_at(a.b, a.b_bf16, c0 + i) : 0.0f);
+      const float u = a.z ? bf16_f32(a.z[t * a.zs + c0 + i]) : v;
+      a.y[t * a.C + c0 + i] = bf16_of(v * (a.z ? u * sigmoid_f32(u) : sigmoid_f32(v)));
+    }
   }
 }
 
@@ -434,7 +435,11 @@ int norm_bwd_rows(int64_t S, int64_t C, int64_t G) {
 
 hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t s) {
   if (in_registers(a)) launch_shape(a, false, s);
-  else hipLaunchKernelGGL(norm_fwd_any_kernel, dim3((uint32_t)((a.S * a.G + 3) / 4)), dim3(256), 0, s, a);
+  else {
+    const int64_t blocks = (a.S * a.G + 3) / 4;
+    hipLaunchKernelGGL(norm_fwd_any_kernel, dim3((uint32_t)(blocks < 65536 ? blocks : 65536)), dim3(256), 0,
+                       s, a);
+  }
   return hipGetLastError();
 }
 

@@ -797,6 +797,12 @@ __device__ __forceinline__ void zero_if(uint32_t bit, float& a, float& b, float&
 // sub-block, whose decays a and decayed states ah = a h[t-1] stay in registers
 // for the way back.  h itself is ah + d x B: its part in y and in dC needs only
 // sum_n C B and sum_c g d x, one number a token each.
+//
+// Two waves a SIMD up to 32 states.  With 32 the registers then fall a few
+// short and 5 to 19 of them go to scratch memory, outside the loop over a
+// token's states; that is still faster than one wave a SIMD with none in
+// scratch: 453 against 554 us at C 1024, 8192 tokens, 826 against 1014 us at
+// C 2048, the whole backward pass.  64 states need one wave's registers.
 constexpr int kSub = 2;
 
 template <int NT, bool kGate>
@@ -1175,17 +1181,37 @@ __global__ __launch_bounds__(256) void scan_param_sum_kernel(ScanArgs a) {
   }
 }
 
-// dB and dC: the partial rows of a group's channel blocks, in order.
+// dB and dC: the partial rows of a group's channel blocks, in order.  A lane
+// has four values of a token's row, so that a wave reads 1 KiB of each block.
 __global__ __launch_bounds__(256) void scan_bc_sum_kernel(ScanArgs a, int32_t bpg, int32_t NT) {
-  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t row = (int64_t)a.G * a.N;
-  if (e >= 2 * (int64_t)a.S * row) return;
-  const int64_t half = e / ((int64_t)a.S * row), q = e - half * a.S * row;
-  const int64_t t = q / row, gn = q - t * row, g = gn / a.N, n = gn - g * a.N;
-  const float* p = a.pbc + (g * bpg * a.S + t) * (2 * NT) + half * NT + n;
-  float sum = 0.0f;
-  for (int32_t b = 0; b < bpg; ++b) sum += p[(int64_t)b * a.S * 2 * NT];
-  (half ? a.dC : a.dB)[q] = bf16_of(sum);
+  const int64_t rows = (int64_t)a.S * 2 * NT;  // of one block
+  const int64_t per = (rows / 4 + 255) / 256;   // workgroups of one group
+  const int64_t g = blockIdx.x / per;
+  const int64_t e = ((blockIdx.x - g * per) * 256 + threadIdx.x) * 4;
+  if (e >= rows) return;
+  const float* p = a.pbc + g * bpg * rows + e;
+  f32x4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
+  int32_t b = 0;
+  for (; b + 8 <= bpg; b += 8) {  // 8 loads at once
+    f32x4_t v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = *reinterpret_cast<const f32x4_t*>(p + (b + j) * rows);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) sum[q] += v[j][q];
+  }
+  for (; b < bpg; ++b) {
+    const f32x4_t v = *reinterpret_cast<const f32x4_t*>(p + b * rows);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) sum[q] += v[q];
+  }
+  const int64_t t = e / (2 * NT);
+  const int32_t i = (int32_t)(e - t * 2 * NT), half = i / NT, n = i - half * NT;
+  uint16_t* o = (half ? a.dC : a.dB) + (t * a.G + g) * a.N + n;
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    if (n + q < a.N) o[q] = bf16_of(sum[q]);
 }
 
 // --------------------------------------------------------- single tokens --
@@ -1571,10 +1597,11 @@ hipError_t launch_scan_bwd_sum(const ScanArgs& a, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int32_t cb = scan_bwd_channels(a.N), bpg = (a.per + cb - 1) / cb;
-  const int64_t n = 2 * (int64_t)a.S * a.G * a.N;
-  if (n == 0) return hipSuccess;
-  hipLaunchKernelGGL(scan_bc_sum_kernel, dim3((uint32_t)((n + 255) / 256)), dim3(256), 0, s, a, bpg,
-                     scan_states(a.N));
+  const int32_t NT = scan_states(a.N);
+  const int64_t quads = (int64_t)a.S * NT / 2;
+  if (quads == 0) return hipSuccess;
+  hipLaunchKernelGGL(scan_bc_sum_kernel, dim3((uint32_t)((quads + 255) / 256 * a.G)), dim3(256), 0, s,
+                     a, bpg, NT);
   return hipGetLastError();
 }
 

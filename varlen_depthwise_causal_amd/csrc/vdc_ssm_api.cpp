@@ -17,7 +17,8 @@ namespace {
 
 constexpr int64_t kMaxC = int64_t(1) << 20;
 constexpr int64_t kMaxS = (int64_t(1) << 31) - 1;
-constexpr int64_t kMaxGrid = (int64_t(1) << 31) - 1;
+// Threads of a launch, all dimensions together.
+constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1;
 constexpr int64_t kMaxStride = int64_t(1) << 31;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -89,7 +90,7 @@ extern "C" int conv1d_prefill(const void* x, const void* weight, int w_dtype, co
   if (rc || num_docs == 0) return rc;
   if (!cu_seqlens) return VDC_EINVAL;
   const int64_t per = ceil_div(C / 8, 64);
-  if (num_docs * per > kMaxGrid) return VDC_EINVAL;
+  if (num_docs * per * 64 > kMaxThreads) return VDC_EINVAL;
   const size_t act = (size_t)S * C * 2;
   if (clash({{state, (size_t)slots * 3 * C * 2}, {y, act}},
             {{x, act}, {weight, (size_t)C * 4 * dtype_bytes(w_dtype)},
@@ -127,7 +128,7 @@ extern "C" int conv1d_update(const void* x, int64_t x_stride, const void* weight
   if (rows == 0) return VDC_OK;
   if (!x || !y) return VDC_EINVAL;
   if (!aligned(x, 16) || !aligned(y, 16)) return VDC_EALIGN;
-  if (ceil_div(rows * (C / 8), 256) > kMaxGrid) return VDC_EINVAL;
+  if (rows * ceil_div(C / 8, 64) * 64 > kMaxThreads) return VDC_EINVAL;
   if (clash({{y, (size_t)rows * C * 2}, {state, (size_t)slots * 3 * C * 2}},
             {{x, rows_bytes(rows, C, x_stride)}, {weight, (size_t)C * 4 * dtype_bytes(w_dtype)},
              {bias, bias ? (size_t)C * dtype_bytes(b_dtype) : 0}, {state_index, (size_t)rows * 4}}))
@@ -153,8 +154,11 @@ extern "C" int conv1d_update(const void* x, int64_t x_stride, const void* weight
 namespace vdc {
 namespace {
 
+// The kernels count tokens, and a few past the last, in 32 bits.
+constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 4096;
+
 int scan_sizes(int64_t S, int64_t C, int64_t N, int64_t G) {
-  if (S < 0 || S > kMaxS || C < 1 || C > kMaxC || N < 1 || N > kMaxStates) return VDC_EINVAL;
+  if (S < 0 || S > kMaxTokens || C < 1 || C > kMaxC || N < 1 || N > kMaxStates) return VDC_EINVAL;
   if (G < 1 || C % G != 0) return VDC_EINVAL;
   return VDC_OK;
 }
@@ -196,7 +200,8 @@ bool scan_plan(int dir, int64_t S, int64_t C, int64_t N, int64_t G, ScanPlan* ou
   out->brief = dir == VDC_FWD && S <= kScanShort;
   if (out->brief) chunk = kScanShort;
   const int64_t chunks = std::max<int64_t>(1, ceil_div(S, chunk));
-  if (chunk > INT32_MAX || chunks * std::max(blocks, waves) > kMaxGrid - 64) return false;
+  if (chunk > INT32_MAX || (chunks * std::max(blocks, waves) + 64) * 64 > kMaxThreads) return false;
+  if (dir == VDC_BWD && G * (ceil_div(S * scan_states(N) / 2, 256) * 256) > kMaxThreads) return false;
   out->wpg = (int32_t)wpg;
   out->cols = (int32_t)(waves * 64);
   out->chunk = (int32_t)chunk;
@@ -428,7 +433,7 @@ extern "C" int selective_update(const vdc_scan* v, void* y, hipStream_t stream) 
   if (!y || (!v->state && v->slots > 0)) return VDC_EINVAL;
   if (!v->state_index && v->S > v->slots) return VDC_EINVAL;
   if (!aligned(y, 2)) return VDC_EALIGN;
-  if (ceil_div(v->S * v->C, 16) > kMaxGrid) return VDC_EINVAL;
+  if (v->S * ceil_div(v->C * scan_states(v->N) / 4, 64) * 64 > kMaxThreads) return VDC_EINVAL;
   const Span out{y, (size_t)v->S * v->C * 2}, st = state_span(v);
   if (hits_input(v, out, false) || hits_input(v, st, false) || overlaps(out, st)) return VDC_EINVAL;
   a.y = static_cast<uint16_t*>(y);
@@ -451,7 +456,6 @@ int norm_common(const void* x, int64_t xs, const void* w, int w_dtype, const voi
   if (!aligned(x, 2) || !aligned(z, 2) || !aligned(w, dtype_bytes(w_dtype)) ||
       (b && !aligned(b, dtype_bytes(b_dtype))))
     return VDC_EALIGN;
-  if (ceil_div(S * G, 4) > kMaxGrid) return VDC_EINVAL;
   a->x = static_cast<const uint16_t*>(x);
   a->z = static_cast<const uint16_t*>(z);
   a->xs = xs;
