@@ -952,11 +952,12 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
     }
   };
 
-  request(last / kScanKeep * kScanKeep, false);
+  request(last / kScanKeep * kScanKeep, last % kScanKeep < kSub);
   request_block(last / kScanKeep);
 #pragma unroll 1
   for (int32_t ib = last / kScanKeep; ib >= 0; --ib) {
     const int32_t i_first = ib * kScanKeep;
+    const int32_t subs = min(kSubs, (last - i_first) / kSub + 1);  // sub-blocks that have tokens
     // Bit i: a document starts at the block's token i.
     const uint32_t starts = starts_from(m.starts, i_first);
     wave_sync();
@@ -1008,7 +1009,7 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
       Raw v[kSub];
 #pragma unroll
       for (int i = 0; i < kSub; ++i) v[i] = q[i];
-      request(i_first + (s + 1) * kSub, s + 2 == kSubs);
+      request(i_first + (s + 1) * kSub, s + 2 == subs);
 #pragma unroll
       for (int e = 0; e < RC * RN; e += 4)
         m.h[s][e / 4][lane] = (f32x4_t){h[e / RN][e % RN], h[e / RN][e % RN + 1], h[e / RN][e % RN + 2],
@@ -1039,7 +1040,7 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
       request(s > 0 ? i_first + (s - 1) * kSub : max(i_first - kScanKeep, 0), s > 0);
       float aw[kSub][RC][RN], hw[kSub][RC][RN];
       float own[kSub];  // step sizes, of all but the last sub-block as the way forward left them
-      if (s + 1 < kSubs) {
+      if (s + 1 < subs) {
 #pragma unroll
         for (int i = 0; i < kSub; ++i) own[i] = m.step[at0 + i][lane];
       } else {
@@ -1129,10 +1130,10 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
       }
     };
 #pragma unroll 1
-    for (int32_t s = 0; s + 1 < kSubs; ++s) forward(s);
+    for (int32_t s = 0; s + 1 < subs; ++s) forward(s);
 #pragma unroll 1
-    for (int32_t s = kSubs - 1; s >= 0; --s) {
-      if (s + 1 < kSubs) {
+    for (int32_t s = subs - 1; s >= 0; --s) {
+      if (s + 1 < subs) {
 #pragma unroll
         for (int e = 0; e < RC * RN; e += 4) {
           const f32x4_t v = m.h[s][e / 4][lane];
