@@ -430,14 +430,23 @@ void scan_fwd_kernel(ScanArgs a, int32_t work) {
 
 // Joins the chunks: forward in time the states after each chunk, and for the
 // backward (blockIdx.z = 1) against it the gradients that leave each chunk.
-// A lane has one column and state; the chain is short, the loads are what
-// takes time, so those of kJoin chunks are requested at once, a batch ahead.
-__global__ __launch_bounds__(64) void scan_join_kernel(ScanArgs a) {
-  constexpr int kJoin = 8;
-  const int32_t col = blockIdx.x * 64 + threadIdx.x, n = blockIdx.y;
+// A lane has one column and state.  The chain is short, the loads are what
+// takes time: the waves of a workgroup have kJoin chunks each, all requested
+// at once and the next ones ahead, and tell each other through LDS what their
+// chunks do to what comes in.
+constexpr int kJoin = 8, kJoinWaves = 8;
+
+__global__ __launch_bounds__(64 * kJoinWaves) void scan_join_kernel(ScanArgs a) {
+  struct Piece {
+    float decay[64], own[64];
+    int32_t apart;  // a document starts in it: what comes in does not pass
+  };
+  __shared__ Piece pieces[2][kJoinWaves];
+  const int32_t lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64u);
+  const int32_t col = blockIdx.x * 64 + lane, n = blockIdx.y;
   const int32_t g = col / (a.wpg * 64), i = col - g * a.wpg * 64;
-  if (i >= a.per) return;
-  const float A2 = param_at(a.A, a.A_bf16, ((int64_t)g * a.per + i) * a.N + n) * kLog2E;
+  const bool active = i < a.per;  // columns without a channel are read and not written
+  const float A2 = active ? param_at(a.A, a.A_bf16, ((int64_t)g * a.per + i) * a.N + n) * kLog2E : 0.0f;
   const bool back = blockIdx.z == 1;
   float* v = (back ? a.mu : a.hend) + (int64_t)n * a.cols + col;
   const int64_t row = (int64_t)a.N * a.cols;
@@ -458,22 +467,46 @@ __global__ __launch_bounds__(64) void scan_join_kernel(ScanArgs a) {
     }
     return r;
   };
+  // What passes a chunk or several; 0 times an infinite decay is 0.
+  auto pass = [](bool apart, float decay, float in, float own) {
+    return !apart && in != 0.0f ? __builtin_fmaf(decay, in, own) : own;
+  };
   float carry = 0.0f;
-  Batch next = load(0);
+  Batch next = load(w * kJoin);
 #pragma unroll 1
-  for (int32_t s0 = 0; s0 < steps; s0 += kJoin) {
+  for (int32_t s0 = 0, turn = 0; s0 < steps; s0 += kJoin * kJoinWaves, turn ^= 1) {
+    const int32_t s = s0 + w * kJoin;
     const Batch now = next;
-    if (s0 + kJoin < steps) next = load(s0 + kJoin);
-    float decay[kJoin];
-#pragma unroll
-    for (int j = 0; j < kJoin; ++j) decay[j] = __builtin_amdgcn_exp2f(A2 * now.sum[j]);
+    if (s0 + kJoin * kJoinWaves < steps) next = load(s + kJoin * kJoinWaves);
+    float decay[kJoin], all = 1.0f, own = 0.0f;
+    int32_t apart = 0;
+    auto step = [&](int j, float in) {
+      const int32_t f = now.flags[j];
+      const float out = pass(f != 0, decay[j], in, now.own[j]);
+      return back && (f & 1) ? 0.0f : out;  // nothing leaves a chunk that a document starts with
+    };
 #pragma unroll
     for (int j = 0; j < kJoin; ++j) {
-      const int32_t f = now.flags[j];
-      // Nothing goes past a document's start; 0 times an infinite decay is 0.
-      carry = f == 0 && carry != 0.0f ? __builtin_fmaf(decay[j], carry, now.own[j]) : now.own[j];
-      if (back && (f & 1)) carry = 0.0f;  // nothing leaves a chunk that a document starts with
-      if (s0 + j < steps) v[chunk_at(s0 + j) * row] = carry;
+      decay[j] = __builtin_amdgcn_exp2f(A2 * now.sum[j]);
+      own = step(j, own);
+      all *= decay[j];
+      apart |= now.flags[j];
+    }
+    Piece* const p = pieces[turn];
+    p[w].decay[lane] = all;
+    p[w].own[lane] = own;
+    if (lane == 0) p[w].apart = apart;
+    __syncthreads();
+    float in = carry;
+#pragma unroll
+    for (int u = 0; u < kJoinWaves; ++u) {
+      if (u == w) in = carry;
+      carry = pass(p[u].apart != 0, p[u].decay[lane], carry, p[u].own[lane]);
+    }
+#pragma unroll
+    for (int j = 0; j < kJoin; ++j) {
+      in = step(j, in);
+      if (active && s + j < steps) v[chunk_at(s + j) * row] = in;
     }
   }
 }
@@ -1157,8 +1190,7 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
 }
 
 // dA, dD and ddt_bias: the chunks' partial rows in order, summed in FP64.
-__global__ __launch_bounds__(256) void scan_param_sum_kernel(ScanArgs a) {
-  const int32_t col = blockIdx.x * 256 + threadIdx.x, n = blockIdx.y;
+__device__ __forceinline__ void param_sum(const ScanArgs& a, int32_t col, int32_t n) {
   const int32_t g = col / (a.wpg * 64), i = col - g * a.wpg * 64;
   if (col >= a.cols || i >= a.per) return;
   const float* p = a.pparam + (int64_t)n * a.cols + col;
@@ -1184,11 +1216,11 @@ __global__ __launch_bounds__(256) void scan_param_sum_kernel(ScanArgs a) {
 
 // dB and dC: the partial rows of a group's channel blocks, in order.  A lane
 // has four values of a token's row, so that a wave reads 1 KiB of each block.
-__global__ __launch_bounds__(256) void scan_bc_sum_kernel(ScanArgs a, int32_t bpg, int32_t NT) {
+__device__ __forceinline__ void bc_sum(const ScanArgs& a, int64_t block, int32_t bpg, int32_t NT) {
   const int64_t rows = (int64_t)a.S * 2 * NT;  // of one block
-  const int64_t per = (rows / 4 + 255) / 256;   // workgroups of one group
-  const int64_t g = blockIdx.x / per;
-  const int64_t e = ((blockIdx.x - g * per) * 256 + threadIdx.x) * 4;
+  const int64_t per = (rows / 4 + 255) / 256;  // workgroups of one group
+  const int64_t g = block / per;
+  const int64_t e = ((block - g * per) * 256 + threadIdx.x) * 4;
   if (e >= rows) return;
   const float* p = a.pbc + g * bpg * rows + e;
   f32x4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -1213,6 +1245,15 @@ __global__ __launch_bounds__(256) void scan_bc_sum_kernel(ScanArgs a, int32_t bp
 #pragma unroll
   for (int q = 0; q < 4; ++q)
     if (n + q < a.N) o[q] = bf16_of(sum[q]);
+}
+
+// Both in one launch, the parameters' workgroups first.
+__global__ __launch_bounds__(256) void scan_sum_kernel(ScanArgs a, int32_t bpg, int32_t NT) {
+  const uint32_t cb = (uint32_t)(a.cols + 255) / 256, params = cb * (a.N + 2);
+  if (blockIdx.x < params)
+    param_sum(a, (int32_t)(blockIdx.x % cb * 256 + threadIdx.x), (int32_t)(blockIdx.x / cb));
+  else
+    bc_sum(a, blockIdx.x - params, bpg, NT);
 }
 
 // --------------------------------------------------------- single tokens --
@@ -1569,7 +1610,8 @@ hipError_t launch_scan_local(const ScanArgs& a, hipStream_t s) { return fwd<fals
 hipError_t launch_scan_out(const ScanArgs& a, hipStream_t s) { return fwd<true>(a, a.chunks, s); }
 
 hipError_t launch_scan_join(const ScanArgs& a, bool backward, hipStream_t s) {
-  hipLaunchKernelGGL(scan_join_kernel, dim3(a.cols / 64, a.N, backward ? 2 : 1), dim3(64), 0, s, a);
+  hipLaunchKernelGGL(scan_join_kernel, dim3(a.cols / 64, a.N, backward ? 2 : 1),
+                     dim3(64 * kJoinWaves), 0, s, a);
   return hipGetLastError();
 }
 
@@ -1594,15 +1636,12 @@ hipError_t launch_scan_bwd_main(const ScanArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_scan_bwd_sum(const ScanArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL(scan_param_sum_kernel, dim3((a.cols + 255) / 256, a.N + 2), dim3(256), 0, s, a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
   const int32_t cb = scan_bwd_channels(a.N), bpg = (a.per + cb - 1) / cb;
   const int32_t NT = scan_states(a.N);
+  const int64_t params = (int64_t)((a.cols + 255) / 256) * (a.N + 2);
   const int64_t quads = (int64_t)a.S * NT / 2;
-  if (quads == 0) return hipSuccess;
-  hipLaunchKernelGGL(scan_bc_sum_kernel, dim3((uint32_t)((quads + 255) / 256 * a.G)), dim3(256), 0, s,
-                     a, bpg, NT);
+  hipLaunchKernelGGL(scan_sum_kernel, dim3((uint32_t)(params + (quads + 255) / 256 * a.G)), dim3(256), 0, s, a,
+                     bpg, NT);
   return hipGetLastError();
 }
 

@@ -201,7 +201,8 @@ bool scan_plan(int dir, int64_t S, int64_t C, int64_t N, int64_t G, ScanPlan* ou
   if (out->brief) chunk = kScanShort;
   const int64_t chunks = std::max<int64_t>(1, ceil_div(S, chunk));
   if (chunk > INT32_MAX || (chunks * std::max(blocks, waves) + 64) * 64 > kMaxThreads) return false;
-  if (dir == VDC_BWD && G * (ceil_div(S * scan_states(N) / 2, 256) * 256) > kMaxThreads) return false;
+  const int64_t params = ceil_div(waves * 64, 256) * (N + 2);
+  if (dir == VDC_BWD && (G * ceil_div(S * scan_states(N) / 2, 256) + params) * 256 > kMaxThreads) return false;
   out->wpg = (int32_t)wpg;
   out->cols = (int32_t)(waves * 64);
   out->chunk = (int32_t)chunk;
@@ -420,7 +421,6 @@ extern "C" int selective_scan_bwd(const vdc_scan* v, const void* dy, int64_t dy_
     if ((rc = done(launch_scan_bwd_local(a, stream)))) return rc;
     if (p.chunks > 1 && (rc = done(launch_scan_join(a, true, stream)))) return rc;
     if ((rc = done(launch_scan_bwd_main(a, stream)))) return rc;
-    count_launch();  // the sums are two launches
   }
   return done(launch_scan_bwd_sum(a, stream));
 }
