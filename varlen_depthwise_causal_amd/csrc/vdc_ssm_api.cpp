@@ -164,17 +164,18 @@ int scan_sizes(int64_t S, int64_t C, int64_t N, int64_t G) {
 }
 
 // Chunks of time: the waves of 64 channels alone fill the machine's 1024
-// SIMDs only at C = 65536 and more, so a row of tokens is cut until about
-// kScanWaves waves run.  A function of the sizes only.
-constexpr int64_t kScanWaves = 4096;
+// SIMDs only at C = 65536 and more, so a row of tokens is cut, into at most as
+// many chunks as make kScanWaves waves.  A function of the sizes only.
+constexpr int64_t kScanWaves = 4096, kScanSimds = 1024;
 // Rows that do not fill the machine are cut as far as the chunks save more
 // than joining them costs: to about a wave for each SIMD, into 24 (backward
-// 64, a token takes five times as long) to 96 chunks, but not below 8
-// (backward 16) tokens, and no further than to 32.  Forward, C = 512 and 512
-// tokens: 64 chunks 30 us, 22 chunks 35; C = 4096: 55 and 47.  Backward,
-// C = 4096: 64 chunks 98 us, 22 chunks 116.
-constexpr int64_t kScanSimds = 1024, kScanMinCut[2] = {24, 64}, kScanMaxCut = 96;
-constexpr int64_t kScanMinChunk[2] = {8, 16}, kScanCutChunk = 32;
+// 64, a token takes five times as long) to 192 chunks, but not below 8 tokens,
+// and no further than to 32.  Forward, C = 4096 and 300 tokens: 19 chunks 41
+// us, 38 chunks 44.  Backward, C = 512: 300 tokens in 38 chunks 42 us, in 19
+// 54; 2048 tokens in 128 chunks 65 us, in 86 77; 4096 tokens in chunks of 32
+// 93 us and of 16 87, but at C = 1024 122 and 137.
+constexpr int64_t kScanMinCut[2] = {24, 64}, kScanMaxCut = 192;
+constexpr int64_t kScanMinChunk = 8, kScanCutChunk = 32;
 static_assert(VDC_FWD == 0 && VDC_BWD == 1, "both are indexed by the direction");
 
 // Largest row stride of x, dt, z and dy: a chunk of it stays below 2^31 bytes.
@@ -190,10 +191,19 @@ bool scan_plan(int dir, int64_t S, int64_t C, int64_t N, int64_t G, ScanPlan* ou
   if (waves * 64 > INT32_MAX / 4) return false;
   const int64_t blocks = dir == VDC_BWD ? G * ceil_div(per, scan_bwd_channels(N)) : waves;
   const int64_t want = std::max<int64_t>(1, kScanWaves / blocks);
-  int64_t chunk = ceil_div(std::max<int64_t>(S, 1), want);
+  int64_t low = ceil_div(std::max<int64_t>(S, 1), want);
   const int64_t cuts = std::min(std::max(kScanSimds / blocks, kScanMinCut[dir]), kScanMaxCut);
-  const int64_t least = std::min(std::max(ceil_div(S, cuts), kScanMinChunk[dir]), kScanCutChunk);
-  chunk = ceil_div(std::max(chunk, least), 8) * 8;
+  const int64_t least = std::min(std::max(ceil_div(S, cuts), kScanMinChunk), kScanCutChunk);
+  low = ceil_div(std::max(low, least), 8) * 8;
+  // The kernels end with the fullest SIMD: of the chunks up to twice that long,
+  // the one that gives it the fewest tokens.  C = 1500, 7000 tokens, forward
+  // and backward: 125 chunks of 56 (2.9 waves a SIMD) 100 and 266 us, 146 of
+  // 48 (3.4) 111 and 286.  Fewer than two waves save nothing, they wait.
+  int64_t chunk = low, least_load = INT64_MAX;
+  for (int64_t c = low; c <= 2 * low && c <= kScanMaxChunk; c += 8) {
+    const int64_t load = std::max<int64_t>(ceil_div(ceil_div(S, c) * blocks, kScanSimds), 2) * c;
+    if (load < least_load) least_load = load, chunk = c;
+  }
   // A chunk's rows are addressed by 32-bit offsets from its first: with at
   // most 2^28 / C tokens, row strides up to scan_stride_limit fit.
   chunk = std::min<int64_t>(chunk, std::min<int64_t>(kScanMaxChunk, (int64_t(1) << 28) / C / 8 * 8));
