@@ -75,7 +75,8 @@ def load(path: str | None = None):
         lib.conv1d_status_string.restype = ctypes.c_char_p
         lib.conv1d_plan.argtypes = [i32, i64, i64, i32, ctypes.POINTER(i64)]
         lib.conv1d_plan.restype = i32
-        scan, size_t, f32 = ctypes.POINTER(VdcScan), ctypes.c_size_t, ctypes.c_float
+        # a VdcScan by reference, or its bytes
+        scan, size_t, f32 = vp, ctypes.c_size_t, ctypes.c_float
         for name, restype, argtypes in (
                 ("conv1d_prefill", i32, [vp, vp, i32, vp, i32, vp, i64, i64, i64, vp, i64, vp, vp, vp,
                                          vp]),

@@ -10,6 +10,7 @@ are BF16 with dense rows (a slice of wider rows is fine), outputs are dense.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -23,19 +24,27 @@ _CODES = {torch.float32: VDC_F32, torch.bfloat16: VDC_BF16}
 _BF16 = torch.bfloat16
 
 
-def _rows(t, what, shape, device):
-    """Row stride of a BF16 activation of this shape; a row itself is dense."""
+# The checks below are most of what a call costs the host, and for single tokens
+# most of what it costs at all, so each first asks, in one expression, whether a
+# tensor is the usual one, and looks for what is wrong with it only if not.  The
+# device is x's, which _x_rows has found to be a GPU.
+
+def _rows(t, what, shape, dense, device):
+    """Row stride of a BF16 activation of this shape, whose rows of `dense`
+    elements are dense themselves."""
+    if t.dtype is _BF16 and t.shape == shape and t.device == device and t.is_contiguous():
+        return dense
     if t.dtype != _BF16:
         raise TypeError("%s must be bfloat16" % what)
     if t.shape != shape:
         raise ValueError("%s must be %s, got %s" % (what, list(shape), list(t.shape)))
-    if t.device != device or not t.is_cuda:
+    if t.device != device:
         raise ValueError("%s must be a device tensor on %s" % (what, device))
-    strides, dense = t.stride(), 1
+    strides, inner = t.stride(), 1
     for n, s in zip(reversed(shape[1:]), reversed(strides[1:])):
-        if n != 1 and s != dense:
+        if n != 1 and s != inner:
             raise ValueError("%s must have dense rows, got strides %s" % (what, strides))
-        dense *= n
+        inner *= n
     # One row has no stride of its own, and neither has a row of a tensor
     # without elements.
     if shape[0] <= 1 or dense == 0:
@@ -45,41 +54,55 @@ def _rows(t, what, shape, device):
     return strides[0]
 
 
+def _x_rows(x, C, device):
+    stride = _rows(x, "x", x.shape, C, device)
+    if not x.is_cuda:
+        raise ValueError("x must be a device tensor")
+    return stride
+
+
 def _param(t, what, shape, device):
     """dtype code of an FP32 or BF16 parameter of this shape."""
     code = _CODES.get(t.dtype)
     if code is None:
         raise TypeError("%s must be float32 or bfloat16, got %s" % (what, t.dtype))
-    _dense(t, what, t.dtype, shape, device)
+    if not (t.shape == shape and t.device == device and t.is_contiguous()):
+        _dense(t, what, t.dtype, shape, device)
     return code
 
 
 def _dense(t, what, dtype, shape, device):
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
     if t.shape != shape:
         raise ValueError("%s must be %s, got %s" % (what, list(shape), list(t.shape)))
-    if t.device != device or not t.is_cuda:
+    if t.device != device:
         raise ValueError("%s must be a device tensor on %s" % (what, device))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % what)
+    raise ValueError("%s must be contiguous" % what)
 
 
 def _activation(x):
     if x.dim() != 2:
         raise ValueError("x must be [rows, C], got %s" % (list(x.shape),))
-    return x.shape[0], x.shape[1], x.device
+    rows, C = x.shape
+    return rows, C, x.device
 
 
-def _out(out, shape, what, device, dtype=_BF16):
+def _out(out, like, stride, shape, what, device):
+    """The caller's output, or a new one, shaped like an input whose row stride
+    is known."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _dense(out, what, dtype, shape, device)
+        if stride == shape[-1] and like.is_contiguous():
+            return torch.empty_like(like)  # the quickest of torch's ways
+        return torch.empty(shape, dtype=_BF16, device=device)
+    _dense(out, what, _BF16, shape, device)
     return out
 
 
 def _cu(cu_seqlens, device):
-    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+    if cu_seqlens.dtype is not torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
         raise ValueError("cu_seqlens must be a non-empty 1-D int32 tensor")
     _dense(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape, device)
     return cu_seqlens.numel() - 1
@@ -142,13 +165,16 @@ def conv1d_prefill(x, weight, cu_seqlens, state, *, bias=None, state_index=None,
     else:
         shape = x.shape
     S, C, dev = _activation(x)
-    if _rows(x, "x", (S, C), dev) != C:
+    if _x_rows(x, C, dev) != C:
         raise ValueError("x must be contiguous")
     w_code = _param(weight, "weight", (C, 4), dev)
     b_code = 0 if bias is None else _param(bias, "bias", (C,), dev)
     docs = _cu(cu_seqlens, dev)
     slots = _cache(state, "state", (3, C), _BF16, state_index, resume, docs, dev)
-    out = _out(out, shape, "out", dev)
+    if out is None:
+        out = torch.empty_like(x) if len(shape) == 2 else torch.empty(shape, dtype=_BF16, device=dev)
+    else:
+        _dense(out, "out", _BF16, shape, dev)
     rc = load().conv1d_prefill(_ptr(x), _ptr(weight), w_code, _ptr(bias), b_code, _ptr(cu_seqlens),
                                docs, S, C, _ptr(state), slots, _ptr(state_index), _ptr(resume),
                                _ptr(out), _stream(dev))
@@ -162,11 +188,11 @@ def conv1d_update(x, state, weight, *, bias=None, state_index=None, out=None):
     state as in conv1d_prefill, read and moved up by the token.  A row without
     a slot is padding and gives zeros.  Returns y [rows, C]."""
     rows, C, dev = _activation(x)
-    stride = _rows(x, "x", (rows, C), dev)
+    stride = _x_rows(x, C, dev)
     w_code = _param(weight, "weight", (C, 4), dev)
     b_code = 0 if bias is None else _param(bias, "bias", (C,), dev)
     slots = _cache(state, "state", (3, C), _BF16, state_index, None, rows, dev)
-    out = _out(out, (rows, C), "out", dev)
+    out = _out(out, x, stride, x.shape, "out", dev)
     rc = load().conv1d_update(_ptr(x), stride, _ptr(weight), w_code, _ptr(bias), b_code, rows, C,
                               _ptr(state), slots, _ptr(state_index), _ptr(out), _stream(dev))
     if rc:
@@ -176,6 +202,16 @@ def conv1d_update(x, state, weight, *, bias=None, state_index=None, out=None):
 
 # -------------------------------------------------------- selective scan --
 
+# struct vdc_scan of include/vdc.h, field by field; bytes, made by one call,
+# where a ctypes structure takes one for each field.
+_SCAN = struct.Struct("@4q5P5q3P4iPqPqPP")
+assert _SCAN.size == ctypes.sizeof(VdcScan)
+
+
+def _at(t):
+    return 0 if t is None else t.data_ptr()
+
+
 def _scan_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, cu_seqlens, state, state_index, resume):
     S, width, dev = _activation(x)
     if A.dim() != 2 or B.dim() not in (2, 3):
@@ -184,31 +220,29 @@ def _scan_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, cu_seqlens, state, st
     if B.dim() == 2:
         B, C = B.unsqueeze(1), C.unsqueeze(1)
     groups = B.shape[1]
-    a = VdcScan()
-    a.S, a.C, a.N, a.groups = S, width, N, groups
-    a.x, a.x_stride = x.data_ptr(), _rows(x, "x", (S, width), dev)
-    a.dt, a.dt_stride = dt.data_ptr(), _rows(dt, "dt", (S, width), dev)
+    shape, bc_shape, per_row = x.shape, (S, groups, N), groups * N
+    zs, d_code, bias_code = width, 0, 0
+    xs, dts = _x_rows(x, width, dev), _rows(dt, "dt", shape, width, dev)
     if z is not None:
-        a.z, a.z_stride = z.data_ptr(), _rows(z, "z", (S, width), dev)
-    a.B, a.B_stride = B.data_ptr(), _rows(B, "B", (S, groups, N), dev)
-    a.Cm, a.C_stride = C.data_ptr(), _rows(C, "C", (S, groups, N), dev)
-    a.A, a.A_dtype = A.data_ptr(), _param(A, "A", (width, N), dev)
+        zs = _rows(z, "z", shape, width, dev)
+    Bs, Cs = _rows(B, "B", bc_shape, per_row, dev), _rows(C, "C", bc_shape, per_row, dev)
+    a_code = _param(A, "A", (width, N), dev)
     if D is not None:
-        a.D, a.D_dtype = D.data_ptr(), _param(D, "D", (width,), dev)
+        d_code = _param(D, "D", (width,), dev)
     if dt_bias is not None:
-        a.dt_bias, a.dt_bias_dtype = dt_bias.data_ptr(), _param(dt_bias, "dt_bias", (width,), dev)
-    a.dt_softplus = 1 if dt_softplus else 0
-    sequences = S
+        bias_code = _param(dt_bias, "dt_bias", (width,), dev)
+    sequences, docs, slots = S, 0, 0
     if cu_seqlens is not None:
-        sequences = a.num_docs = _cu(cu_seqlens, dev)
-        a.cu_seqlens = cu_seqlens.data_ptr()
+        sequences = docs = _cu(cu_seqlens, dev)
     if state is not None:
-        a.slots = _cache(state, "state", (width, N), torch.float32, state_index, resume, sequences, dev)
-        a.state = state.data_ptr()
-        a.state_index, a.resume = _ptr(state_index), _ptr(resume)
+        slots = _cache(state, "state", (width, N), torch.float32, state_index, resume, sequences, dev)
     elif state_index is not None or resume is not None:
         raise ValueError("state_index and resume need a state")
-    return a, S, width, N, groups, dev
+    a = _SCAN.pack(S, width, N, groups, x.data_ptr(), dt.data_ptr(), _at(z), B.data_ptr(), C.data_ptr(),
+                   xs, dts, zs, Bs, Cs, A.data_ptr(), _at(D), _at(dt_bias), a_code, d_code, bias_code,
+                   1 if dt_softplus else 0, _at(cu_seqlens), docs, _at(state), slots, _at(state_index),
+                   _at(resume))
+    return a, S, width, N, groups, dev, xs
 
 
 def selective_scan_workspace_bytes(direction: str, S: int, C: int, N: int, groups: int = 1) -> int:
@@ -226,16 +260,16 @@ def selective_scan_fwd(x, dt, A, B, C, cu_seqlens, *, D=None, z=None, dt_bias=No
     or their sum without dt_softplus; y is gated by silu(z) where z is given.
     state: FP32 [slots, C, N], where every document leaves its last state;
     state_index and resume as in conv1d_prefill."""
-    a, S, width, N, groups, dev = _scan_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, cu_seqlens,
-                                             state, state_index, resume)
-    out = _out(out, (S, width), "out", dev)
+    a, S, width, N, groups, dev, xs = _scan_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, cu_seqlens,
+                                                 state, state_index, resume)
+    out = _out(out, x, xs, x.shape, "out", dev)
     lib = load()
     need = lib.selective_scan_workspace_bytes(VDC_FWD, S, width, N, groups)
     ws, ws_n = None, 0
     if need or workspace is not None:
         workspace, ws_n = _workspace(need, workspace, dev)
         ws = workspace.data_ptr()
-    rc = lib.selective_scan_fwd(ctypes.byref(a), out.data_ptr(), ws, ws_n, _stream(dev))
+    rc = lib.selective_scan_fwd(a, out.data_ptr(), ws, ws_n, _stream(dev))
     if rc:
         raise VdcError(rc, "selective_scan_fwd")
     return out
@@ -246,10 +280,10 @@ def selective_scan_bwd(x, dt, A, B, C, cu_seqlens, dy, *, D=None, z=None, dt_bia
     """Gradients of selective_scan_fwd without a state, from its inputs alone:
     (dx, ddt, dA, dB, dC, dD, dz, ddt_bias), None for what was not given.
     dA, dD and ddt_bias have the parameters' dtypes, the others BF16."""
-    a, S, width, N, groups, dev = _scan_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, cu_seqlens,
-                                             None, None, None)
-    dy_stride = _rows(dy, "dy", (S, width), dev)
-    dx = torch.empty((S, width), dtype=_BF16, device=dev)
+    a, S, width, N, groups, dev, xs = _scan_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, cu_seqlens,
+                                                 None, None, None)
+    dy_stride = _rows(dy, "dy", x.shape, width, dev)
+    dx = _out(None, x, xs, x.shape, "dx", dev)
     ddt = torch.empty_like(dx)
     dz = None if z is None else torch.empty_like(dx)
     dB = torch.empty(B.shape, dtype=_BF16, device=dev)
@@ -260,7 +294,7 @@ def selective_scan_bwd(x, dt, A, B, C, cu_seqlens, dy, *, D=None, z=None, dt_bia
     lib = load()
     need = lib.selective_scan_workspace_bytes(VDC_BWD, S, width, N, groups)
     workspace, ws_n = _workspace(need, workspace, dev)
-    rc = lib.selective_scan_bwd(ctypes.byref(a), dy.data_ptr(), dy_stride, dx.data_ptr(), ddt.data_ptr(),
+    rc = lib.selective_scan_bwd(a, dy.data_ptr(), dy_stride, dx.data_ptr(), ddt.data_ptr(),
                                 _ptr(dz), dB.data_ptr(), dC.data_ptr(), dA.data_ptr(), _ptr(dD),
                                 _ptr(dbias), workspace.data_ptr(), ws_n, _stream(dev))
     if rc:
@@ -275,10 +309,10 @@ def selective_update(x, dt, A, B, C, state, *, D=None, z=None, dt_bias=None, dt_
     replaced.  A row without a slot is padding and gives zeros.  Returns y."""
     if state is None:
         raise ValueError("selective_update needs a state")
-    a, S, width, _, _, dev = _scan_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, None, state,
-                                        state_index, None)
-    out = _out(out, (S, width), "out", dev)
-    rc = load().selective_update(ctypes.byref(a), out.data_ptr(), _stream(dev))
+    a, _, _, _, _, dev, xs = _scan_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, None, state, state_index,
+                                        None)
+    out = _out(out, x, xs, x.shape, "out", dev)
+    rc = load().selective_update(a, out.data_ptr(), _stream(dev))
     if rc:
         raise VdcError(rc, "selective_update")
     return out
@@ -291,10 +325,10 @@ def _norm_args(x, weight, groups, bias, z):
     groups = int(groups)
     if groups < 1 or C % groups:
         raise ValueError("groups must divide C = %d, got %d" % (C, groups))
-    xs = _rows(x, "x", (S, C), dev)
+    xs = _x_rows(x, C, dev)
     w_code = _param(weight, "weight", (C,), dev)
     b_code = 0 if bias is None else _param(bias, "bias", (C,), dev)
-    zs = C if z is None else _rows(z, "z", (S, C), dev)
+    zs = C if z is None else _rows(z, "z", x.shape, C, dev)
     return S, C, dev, groups, xs, w_code, b_code, zs
 
 
@@ -303,7 +337,7 @@ def group_norm_silu_fwd(x, weight, groups, *, bias=None, z=None, eps=1e-5, out=N
     weight * xhat + bias, y = silu(v), or v * silu(z) where a gate z is given.
     x, z: BF16 [S, C]; weight, bias: FP32 or BF16 [C].  Returns y."""
     S, C, dev, groups, xs, w_code, b_code, zs = _norm_args(x, weight, groups, bias, z)
-    out = _out(out, (S, C), "out", dev)
+    out = _out(out, x, xs, x.shape, "out", dev)
     rc = load().group_norm_silu_fwd(x.data_ptr(), xs, weight.data_ptr(), w_code, _ptr(bias), b_code,
                                     _ptr(z), zs, S, C, groups, eps, out.data_ptr(), _stream(dev))
     if rc:
@@ -321,8 +355,8 @@ def group_norm_silu_bwd(x, weight, groups, dy, *, bias=None, z=None, eps=1e-5, w
     dz), None for what was not given, dweight and dbias of the parameters'
     dtypes."""
     S, C, dev, groups, xs, w_code, b_code, zs = _norm_args(x, weight, groups, bias, z)
-    dys = _rows(dy, "dy", (S, C), dev)
-    dx = torch.empty((S, C), dtype=_BF16, device=dev)
+    dys = _rows(dy, "dy", x.shape, C, dev)
+    dx = _out(None, x, xs, x.shape, "dx", dev)
     dz = None if z is None else torch.empty_like(dx)
     dw = torch.empty_like(weight)
     db = None if bias is None else torch.empty_like(bias)
