@@ -53,6 +53,24 @@ def test_scan_fwd_around_one_launch(vdc, lengths, N):
     R.close("state", state, ref.after, ref.eafter)
 
 
+@pytest.mark.parametrize("N,S", [(5, 160), (5, 161), (16, 224), (16, 225), (24, 320), (24, 321), (64, 512),
+                                 (64, 513)])
+def test_scan_fwd_around_longer_launches(vdc, N, S):
+    """Documents that end with the parts of a row, inside them, and run over
+    several; resumed ones among them."""
+    C, lengths = 40, [20, 0, S // 2 - 20, 3, 0, 1, S - S // 2 - 4, 0]
+    k, docs, cu = scan_inputs(305, lengths, C, N, 1, device=DEV, wide=True)
+    n = len(lengths)
+    for flip in (0, 1):
+        state = Maker(306, DEV).normal(n, C, N, dtype=F32)
+        resume = [i % 2 == flip for i in range(n)]
+        ref = _ref(k, docs, state=state, slots=list(range(n)), resume=resume)
+        y = vdc.selective_scan_fwd(*_head(k), cu, **_rest(k), state=state,
+                                   resume=torch.tensor(resume, device=DEV))
+        R.close("y", y, ref.y, ref.ey)
+        R.close("state", state, ref.after, ref.eafter)
+
+
 def test_scan_chunks_of_many_blocks(vdc):
     """32768 channels leave few chunks, each of many blocks; three of the 512
     groups are held to the definition."""

@@ -172,20 +172,44 @@ __device__ __forceinline__ Column column_of(const ScanArgs& a, int32_t wave) {
   return o;
 }
 
-// A's row of a channel times log2(e); 0 past the last state.
-template <int NT>
+// Vectors at any address that holds their elements.
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+
+// A's row of a channel times log2(e); 0 past the last state.  kAll: there are
+// exactly NT states, which are then loaded by vectors.
+template <int NT, bool kAll>
 __device__ __forceinline__ void load_decay(const ScanArgs& a, const Column& l, float (&A2)[NT]) {
   const int64_t at = (int64_t)l.c * a.N;
   if (a.A_bf16) {
+    const uint16_t* p = static_cast<const uint16_t*>(a.A) + at;
+    if constexpr (kAll) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-      A2[n] = bf16_f32(static_cast<const uint16_t*>(a.A)[at + min(n, a.N - 1)]);
+      for (int n = 0; n < NT; n += 8) {
+        const u32x4_any v = *reinterpret_cast<const u32x4_any*>(p + n);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) A2[n + 2 * j] = bf16_lo(v[j]), A2[n + 2 * j + 1] = bf16_hi(v[j]);
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) A2[n] = bf16_f32(p[min(n, a.N - 1)]);
+    }
   } else {
+    const float* p = static_cast<const float*>(a.A) + at;
+    if constexpr (kAll) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) A2[n] = static_cast<const float*>(a.A)[at + min(n, a.N - 1)];
+      for (int n = 0; n < NT; n += 4) {
+        const f32x4_any v = *reinterpret_cast<const f32x4_any*>(p + n);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) A2[n + j] = v[j];
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) A2[n] = p[min(n, a.N - 1)];
+    }
   }
 #pragma unroll
-  for (int n = 0; n < NT; ++n) A2[n] = n < a.N ? A2[n] * kLog2E : 0.0f;
+  for (int n = 0; n < NT; ++n) A2[n] = kAll || n < a.N ? A2[n] * kLog2E : 0.0f;
 }
 
 // A value the compiler must not compute addresses from ahead of its use: the
@@ -226,7 +250,7 @@ void scan_fwd_kernel(ScanArgs a, int32_t work) {
     return base + ((int64_t)chunk * a.N + n) * a.cols;
   };
   float A2[NT], h[NT];
-  load_decay<NT>(a, l, A2);
+  load_decay<NT, kWide>(a, l, A2);
   const float Dc = a.D ? param_at(a.D, a.D_bf16, l.c) : 0.0f;
   const StepBias bias = step_bias(a, l.c);
   const bool gated = kOut && a.z != nullptr;
@@ -543,7 +567,7 @@ void scan_bwd_local_kernel(ScanArgs a, int32_t work) {
   const int32_t t0 = k * a.chunk;
   const int32_t t1 = (int32_t)min((int64_t)a.S, (int64_t)t0 + a.chunk);
   float A2[NT], h[NT], mu[NT], p[NT];
-  load_decay<NT>(a, l, A2);
+  load_decay<NT, kWide>(a, l, A2);
 #pragma unroll
   for (int n = 0; n < NT; ++n) h[n] = 0.0f, mu[n] = 0.0f, p[n] = 1.0f;
   const StepBias bias = step_bias(a, l.c);
@@ -1379,23 +1403,33 @@ void step_nl(const ScanArgs& a, hipStream_t s) {
 
 // ----------------------------------------------------------- short prompts --
 //
-// The forward of a row of tokens too short to be worth cutting: the lanes of
-// the single-token form, walking the row.  A token then takes a wave a third
-// of the instructions that it takes with all states in a lane, and the row
-// one launch instead of three.  kVec: N a multiple of 4.
+// The forward of a row of tokens that is short: the lanes of the single-token
+// form, walking the row.  A token takes a wave a third of the instructions that
+// it takes with all states in a lane, and the row one launch instead of three.
+// The waves of a workgroup have the same channels and a part of the row each:
+// they find the state behind their part from zero history, join these through
+// LDS, and go over their part again for the outputs.  kVec: N a multiple of 4.
+
+constexpr int kShortWaves = 8, kShortAhead = 4;
 
 template <int NL, bool kVec, bool kGate>
-__global__ __launch_bounds__(64) void scan_short_kernel(ScanArgs a) {
-  constexpr int kChannels = 64 / NL, kAhead = 8;
+__global__ __launch_bounds__(64 * kShortWaves) void scan_short_kernel(ScanArgs a, int32_t each) {
+  constexpr int kChannels = 64 / NL;
+  struct Piece {
+    float h[4][64], sum[64];
+    int32_t apart;  // a document starts in the part
+  };
+  __shared__ Piece pieces[kShortWaves - 1];
   // The outputs wait here for the end: loads and stores share one counter of
   // outstanding accesses, and a store among the loads would be waited for with
   // every group of them.
-  __shared__ uint16_t out[kScanShort][kChannels];
+  __shared__ uint16_t out[scan_short(4 * NL)][kChannels];
+  const int32_t w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64u);
   const int32_t lane = threadIdx.x & 63, part = lane % NL, n0 = 4 * part;
   const int32_t c0 = (int32_t)blockIdx.x * kChannels + lane / NL;
   const bool there = c0 < a.C, some = n0 < a.N;
   const uint32_t c = there ? c0 : 0;
-  const int32_t S = a.S;
+  const int32_t t0 = w * each, t1 = min(a.S, t0 + each);
   float A2[4], h[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -1406,11 +1440,6 @@ __global__ __launch_bounds__(64) void scan_short_kernel(ScanArgs a) {
   const float Dc = a.D ? param_at(a.D, a.D_bf16, c) : 0.0f;
   const uint32_t bc0 = c / (uint32_t)a.per * (uint32_t)a.N + (some ? n0 : 0);
   const uint32_t h0 = c * (uint32_t)a.N + n0;
-
-  struct Raw {
-    uint32_t x, dt, z;
-    u32x2_any B, C;  // four states
-  };
   auto four = [&](const uint16_t* p) {
     if (kVec) return *reinterpret_cast<const u32x2_any*>(p);
     uint32_t v[4];
@@ -1418,145 +1447,195 @@ __global__ __launch_bounds__(64) void scan_short_kernel(ScanArgs a) {
     for (int j = 0; j < 4; ++j) v[j] = n0 + j < a.N ? (uint32_t)p[j] : 0u;
     return (u32x2_any){v[0] | v[1] << 16, v[2] | v[3] << 16};
   };
-  // The next token's; past the end the last token's again.  A wave here has
-  // its SIMD to itself and is bound by the instructions it issues, addresses
-  // among them.
-  RowBuffer bx, bd, bz;
-  bx.open(a.x, 0, a.xs);
-  bd.open(a.dt, 0, a.dts);
-  bz.open(kGate ? a.z : a.x, 0, kGate ? a.zs : a.xs);
-  const uint16_t *pB = a.B, *pC = a.Cm;
-  const uint32_t lane2 = c * 2u;
-  int32_t left = S;
-  auto request = [&]() {
-    Raw r;
-    r.x = bx.get(lane2);
-    r.dt = bd.get(lane2);
-    r.z = kGate ? bz.get(lane2) : 0u;
-    r.B = four(pB + bc0);
-    r.C = four(pC + bc0);
-    --left;
-    const bool more = left > 0;
-    bx.row += more ? bx.stride : 0u;
-    bd.row += more ? bd.stride : 0u;
-    if (kGate) bz.row += more ? bz.stride : 0u;
-    pB += more ? a.Bs : 0;
-    pC += more ? a.Cs : 0;
-    return r;
-  };
-  int32_t doc = -1, next = 0;
-  auto write = [&](int32_t d) {
-    const int64_t slot = a.state ? slot_of(a.index, d, a.slots) : -1;
-    if (slot < 0 || !there) return;
-    float* s = a.state + slot * a.C * a.N + h0;
+  // The document that starts at t0 or before it, and whether it starts there.
+  const int32_t at = first_at_least(a.cu, a.num_docs + 1, t0);
+  const bool starts = at <= a.num_docs && uniform_at(a.cu, at) == t0;
+  float first[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // what a document that runs past the part resumed with
+  float sum = 0.0f;
+  int32_t apart = 0;
+
+  // One pass over the part: from zero history for the state behind it and the
+  // sum of the step sizes, or from h for the outputs.
+  auto pass = [&](auto outputs) {
+    constexpr bool kOut = decltype(outputs)::value;
+    struct Raw {
+      uint32_t x, dt, z;
+      u32x2_any B, C;  // four states
+    };
+    // The next token's; past the end the last token's again.  A wave is bound by
+    // the instructions it issues, addresses among them.
+    RowBuffer bx, bd, bz;
+    bx.open(a.x, t0, a.xs);
+    bd.open(a.dt, t0, a.dts);
+    bz.open(kGate ? a.z : a.x, t0, kGate ? a.zs : a.xs);
+    const uint16_t *pB = a.B + t0 * a.Bs, *pC = a.Cm + t0 * a.Cs;
+    const uint32_t lane2 = c * 2u;
+    int32_t left = t1 - t0;
+    auto request = [&]() {
+      Raw r;
+      r.x = bx.get(lane2);
+      r.dt = bd.get(lane2);
+      r.z = kOut && kGate ? bz.get(lane2) : 0u;
+      r.B = four(pB + bc0);
+      if (kOut) r.C = four(pC + bc0);
+      --left;
+      const bool more = left > 0;
+      bx.row += more ? bx.stride : 0u;
+      bd.row += more ? bd.stride : 0u;
+      if (kOut && kGate) bz.row += more ? bz.stride : 0u;
+      pB += more ? a.Bs : 0;
+      if (kOut) pC += more ? a.Cs : 0;
+      return r;
+    };
+    int32_t doc = at - 1, t = t0;
+    int32_t next = doc >= 0 && doc < a.num_docs ? uniform_at(a.cu, doc + 1) : INT32_MAX;
+    auto write = [&](int32_t d) {
+      const int64_t slot = kOut && a.state ? slot_of(a.index, d, a.slots) : -1;
+      if (slot < 0 || !there) return;
+      float* s = a.state + slot * a.C * a.N + h0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (n0 + j < a.N) s[j] = h[j];
-  };
-  // The document that starts at t, past the empty ones before it.
-  auto open = [&](int32_t d, int32_t t) {
-    while (true) {
+      for (int j = 0; j < 4; ++j)
+        if (n0 + j < a.N) s[j] = h[j];
+    };
+    // The document that starts at t, past the empty ones before it.
+    auto open = [&](int32_t d) {
+      apart = 1;
+      while (true) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) h[j] = 0.0f;
-      if (d >= a.num_docs || uniform_at(a.cu, d + 1) > t) break;
-      if (!resumes(a, d)) write(d);
-      ++d;
-    }
-    doc = d;
-    next = d < a.num_docs ? uniform_at(a.cu, d + 1) : INT32_MAX;
-    if (a.state && d < a.num_docs && resumes(a, d)) {
-      const int64_t slot = slot_of(a.index, d, a.slots);
-      if (slot >= 0) {
-        const float* s = a.state + slot * a.C * a.N + h0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (n0 + j < a.N) h[j] = s[j];
+        for (int j = 0; j < 4; ++j) h[j] = 0.0f;
+        if (d >= a.num_docs || uniform_at(a.cu, d + 1) > t) break;
+        if (kOut && !resumes(a, d)) write(d);
+        ++d;
       }
-    }
-  };
-  // kTokens tokens from t on.  What does not wait for the states, and the sums
-  // over the lanes, stand side by side for all of them: a wave alone on its
-  // SIMD would otherwise wait for most of its own results.
-  auto tokens = [&](auto count, const Raw* r, int32_t t) {
-    constexpr int kTokens = decltype(count)::value;
-    float x[kTokens], d[kTokens], y[kTokens];
-#pragma unroll
-    for (int i = 0; i < kTokens; ++i) {
-      x[i] = bf16_lo(r[i].x);
-      d[i] = step_size(a, bf16_lo(r[i].dt), bias);
-    }
-#pragma unroll
-    for (int i = 0; i < kTokens; ++i) {
-      const float dx = d[i] * x[i];
-      const float b[4] = {bf16_lo(r[i].B.x), bf16_hi(r[i].B.x), bf16_lo(r[i].B.y), bf16_hi(r[i].B.y)};
-      const float cm[4] = {bf16_lo(r[i].C.x), bf16_hi(r[i].C.x), bf16_lo(r[i].C.y), bf16_hi(r[i].C.y)};
-      y[i] = 0.0f;
+      doc = d;
+      next = d < a.num_docs ? uniform_at(a.cu, d + 1) : INT32_MAX;
+      if (!a.state || d >= a.num_docs || !resumes(a, d)) return;
+      const int64_t slot = slot_of(a.index, d, a.slots);
+      if (slot < 0) return;
+      // The wave that ends the document writes its slot while this one is at
+      // its second pass: that pass has the state from the first.
+      const bool past = next > t1;
+      const float* s = a.state + slot * a.C * a.N + h0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(d[i] * A2[j]), h[j], dx * b[j]);
-        y[i] = __builtin_fmaf(cm[j], h[j], y[i]);
+        float v = 0.0f;
+        if (n0 + j < a.N && !(kOut && past)) v = s[j];
+        h[j] = kOut && past ? first[j] : v;
+        if (!kOut) first[j] = v;
       }
-      if (!some) y[i] = 0.0f;
-    }
+    };
+    // kTokens tokens from t on.  What does not wait for the states, and the sums
+    // over the lanes, stand side by side for all of them: a wave alone on its
+    // SIMD would otherwise wait for most of its own results.
+    auto tokens = [&](auto count, const Raw* r) {
+      constexpr int kTokens = decltype(count)::value;
+      float x[kTokens], d[kTokens], y[kTokens];
 #pragma unroll
-    for (int i = 0; i < kTokens; ++i) {
-      float v = __builtin_fmaf(Dc, x[i], lanes_sum<NL>(y[i]));
-      if (kGate) {
-        const float z = bf16_lo(r[i].z);
-        v *= z * sigmoid_f32(z);
+      for (int i = 0; i < kTokens; ++i) {
+        x[i] = bf16_lo(r[i].x);
+        d[i] = step_size(a, bf16_lo(r[i].dt), bias);
+        if (!kOut) sum += d[i];
       }
-      if (part == 0) out[t + i][lane / NL] = bf16_of(v);
+#pragma unroll
+      for (int i = 0; i < kTokens; ++i) {
+        const float dx = d[i] * x[i];
+        const float b[4] = {bf16_lo(r[i].B.x), bf16_hi(r[i].B.x), bf16_lo(r[i].B.y), bf16_hi(r[i].B.y)};
+        y[i] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(d[i] * A2[j]), h[j], dx * b[j]);
+        if (kOut) {
+          const float cm[4] = {bf16_lo(r[i].C.x), bf16_hi(r[i].C.x), bf16_lo(r[i].C.y), bf16_hi(r[i].C.y)};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) y[i] = __builtin_fmaf(cm[j], h[j], y[i]);
+          if (!some) y[i] = 0.0f;
+        }
+      }
+      if (!kOut) return;
+#pragma unroll
+      for (int i = 0; i < kTokens; ++i) {
+        float v = __builtin_fmaf(Dc, x[i], lanes_sum<NL>(y[i]));
+        if (kGate) {
+          const float z = bf16_lo(r[i].z);
+          v *= z * sigmoid_f32(z);
+        }
+        if (part == 0) out[t + i][lane / NL] = bf16_of(v);
+      }
+    };
+    Raw q[kShortAhead];
+    if (t0 < t1) {
+#pragma unroll
+      for (int i = 0; i < kShortAhead; ++i) q[i] = request();
+    }
+    if (starts) open(at);
+#pragma unroll 1
+    while (t < t1) {
+      const int32_t end = next > t && next < t1 ? next : t1;
+#pragma unroll 1
+      for (; t + kShortAhead <= end; t += kShortAhead) {
+        Raw r[kShortAhead];
+#pragma unroll
+        for (int i = 0; i < kShortAhead; ++i) {
+          r[i] = q[i];
+          q[i] = request();
+        }
+        tokens(std::integral_constant<int, kShortAhead>(), r);
+      }
+#pragma unroll 1
+      for (; t < end; ++t) {
+        const Raw r = q[0];
+#pragma unroll
+        for (int i = 0; i + 1 < kShortAhead; ++i) q[i] = q[i + 1];
+        q[kShortAhead - 1] = request();
+        tokens(std::integral_constant<int, 1>(), &r);
+      }
+      if (t == next && doc >= 0 && doc < a.num_docs) {
+        write(doc);
+        if (t < t1 || t == a.S) open(doc + 1);
+      }
     }
   };
 
-  Raw q[kAhead];
-  if (S > 0) {
+  if (t1 < a.S) {
+    pass(std::false_type());
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) q[i] = request();
+    for (int j = 0; j < 4; ++j) pieces[w].h[j][lane] = h[j];
+    pieces[w].sum[lane] = sum;
+    if (lane == 0) pieces[w].apart = apart;
   }
-  open(0, 0);
-  int32_t t = 0;
-#pragma unroll 1
-  while (t < S) {
-    const int32_t end = next > t && next < S ? next : S;
-#pragma unroll 1
-    for (; t + kAhead <= end; t += kAhead) {
-      Raw r[kAhead];
+  __syncthreads();
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        r[i] = q[i];
-        q[i] = request();
-      }
-      tokens(std::integral_constant<int, kAhead>(), r, t);
-    }
+  for (int j = 0; j < 4; ++j) h[j] = 0.0f;
 #pragma unroll 1
-    for (; t < end; ++t) {
-      const Raw r = q[0];
+  for (int32_t u = 0; u < w; ++u) {
+    const float s = pieces[u].sum[lane];
+    const bool cut = pieces[u].apart != 0;
 #pragma unroll
-      for (int i = 0; i + 1 < kAhead; ++i) q[i] = q[i + 1];
-      q[kAhead - 1] = request();
-      tokens(std::integral_constant<int, 1>(), &r, t);
-    }
-    if (t == next && doc < a.num_docs) {
-      write(doc);
-      open(doc + 1, t);
+    for (int j = 0; j < 4; ++j) {  // 0 times an infinite decay is 0
+      const float own = pieces[u].h[j][lane];
+      h[j] = !cut && h[j] != 0.0f ? __builtin_fmaf(__builtin_amdgcn_exp2f(A2[j] * s), h[j], own) : own;
     }
   }
-  for (int32_t i = lane / kChannels; i < S; i += NL) {
-    const int32_t k = (int32_t)blockIdx.x * kChannels + lane % kChannels;
-    if (k < a.C) a.y[(int64_t)i * a.C + k] = out[i][lane % kChannels];
-  }
+  pass(std::true_type());
+  __syncthreads();
+  const int32_t k = (int32_t)blockIdx.x * kChannels + threadIdx.x % kChannels;
+  for (int32_t i = threadIdx.x / kChannels; i < a.S; i += blockDim.x / kChannels)
+    if (k < a.C) a.y[(int64_t)i * a.C + k] = out[i][threadIdx.x % kChannels];
 }
 
 template <int NL>
 void short_nl(const ScanArgs& a, hipStream_t s) {
-  const dim3 grid((uint32_t)((a.C + 64 / NL - 1) / (64 / NL))), block(64);
+  // Parts of whole groups of tokens, as even as they get.
+  int32_t each = (a.S + kShortWaves - 1) / kShortWaves;
+  each = (each + kShortAhead - 1) / kShortAhead * kShortAhead;
+  const int32_t waves = a.S > 0 ? (a.S + each - 1) / each : 1;
+  const dim3 grid((uint32_t)((a.C + 64 / NL - 1) / (64 / NL))), block(64 * waves);
   if (a.z) {
-    if (a.N % 4 == 0) hipLaunchKernelGGL((scan_short_kernel<NL, true, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((scan_short_kernel<NL, false, true>), grid, block, 0, s, a);
+    if (a.N % 4 == 0) hipLaunchKernelGGL((scan_short_kernel<NL, true, true>), grid, block, 0, s, a, each);
+    else hipLaunchKernelGGL((scan_short_kernel<NL, false, true>), grid, block, 0, s, a, each);
   } else {
-    if (a.N % 4 == 0) hipLaunchKernelGGL((scan_short_kernel<NL, true, false>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((scan_short_kernel<NL, false, false>), grid, block, 0, s, a);
+    if (a.N % 4 == 0) hipLaunchKernelGGL((scan_short_kernel<NL, true, false>), grid, block, 0, s, a, each);
+    else hipLaunchKernelGGL((scan_short_kernel<NL, false, false>), grid, block, 0, s, a, each);
   }
 }
 

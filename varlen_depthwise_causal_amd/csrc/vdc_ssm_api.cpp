@@ -207,8 +207,8 @@ bool scan_plan(int dir, int64_t S, int64_t C, int64_t N, int64_t G, ScanPlan* ou
   // A chunk's rows are addressed by 32-bit offsets from its first: with at
   // most 2^28 / C tokens, row strides up to scan_stride_limit fit.
   chunk = std::min<int64_t>(chunk, std::min<int64_t>(kScanMaxChunk, (int64_t(1) << 28) / C / 8 * 8));
-  out->brief = dir == VDC_FWD && S <= kScanShort;
-  if (out->brief) chunk = kScanShort;
+  out->brief = dir == VDC_FWD && S <= scan_short(N);
+  if (out->brief) chunk = scan_short(N);
   const int64_t chunks = std::max<int64_t>(1, ceil_div(S, chunk));
   if (chunk > INT32_MAX || (chunks * std::max(blocks, waves) + 64) * 64 > kMaxThreads) return false;
   const int64_t params = ceil_div(waves * 64, 256) * (N + 2);
