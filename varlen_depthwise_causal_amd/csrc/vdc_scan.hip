@@ -900,20 +900,35 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
   const int32_t n0 = RN * part;
 
   // A times log2(e); the sums with A are taken with it and scaled at their end.
+  // Loads without a condition, all under way at once: what is past the group or
+  // the states is read at the last of them and set to zero.
   float A2[RC][RN], mu[RC][RN], dA[RC][RN];
+  auto state_at = [&](int j) { return min(n0 + j, a.N - 1); };
+  auto decays = [&](auto* A) {
 #pragma unroll
-  for (int r = 0; r < RC; ++r) {
-    const int32_t i = i0 + RC * set + r;
+    for (int r = 0; r < RC; ++r) {
+      const int32_t i = min(i0 + RC * set + r, a.per - 1);
+#pragma unroll
+      for (int j = 0; j < RN; ++j) {
+        const auto v = A[((int64_t)g * a.per + i) * a.N + state_at(j)];
+        if constexpr (sizeof(v) == 2) A2[r][j] = bf16_f32(v);
+        else A2[r][j] = v;
+      }
+    }
+  };
+  if (a.A_bf16) decays(static_cast<const uint16_t*>(a.A));
+  else decays(static_cast<const float*>(a.A));
+#pragma unroll
+  for (int r = 0; r < RC; ++r)
 #pragma unroll
     for (int j = 0; j < RN; ++j) {
-      const bool there = i < a.per && n0 + j < a.N;
-      A2[r][j] = there ? param_at(a.A, a.A_bf16, ((int64_t)g * a.per + i) * a.N + n0 + j) * kLog2E : 0.0f;
+      const bool there = i0 + RC * set + r < a.per && n0 + j < a.N;
+      A2[r][j] = there ? A2[r][j] * kLog2E : 0.0f;
       dA[r][j] = 0.0f;
       // What the chunk to the right sends.
       mu[r][j] = there && k + 1 < a.chunks
                      ? (a.mu + ((int64_t)(k + 1) * a.N + n0 + j) * a.cols)[col + r] : 0.0f;
     }
-  }
 #pragma unroll
   for (int e = 0; e < RC * RN; e += 4) {
     f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
