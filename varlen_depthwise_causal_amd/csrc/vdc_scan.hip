@@ -473,7 +473,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void scan_join_kernel(ScanArgs a) 
   const float A2 = active ? param_at(a.A, a.A_bf16, ((int64_t)g * a.per + i) * a.N + n) * kLog2E : 0.0f;
   const bool back = blockIdx.z == 1;
   float* v = (back ? a.mu : a.hend) + (int64_t)n * a.cols + col;
-  const int64_t row = (int64_t)a.N * a.cols;
+  const int64_t row = (int64_t)a.rows * a.cols;
   const int32_t steps = a.chunks - 1;
   struct Batch {
     float own[kJoin], sum[kJoin];
@@ -569,8 +569,11 @@ void scan_bwd_local_kernel(ScanArgs a, int32_t work) {
   float A2[NT], h[NT], mu[NT], p[NT];
   load_decay<NT, kWide>(a, l, A2);
 #pragma unroll
-  for (int n = 0; n < NT; ++n) h[n] = 0.0f, mu[n] = 0.0f, p[n] = 1.0f;
-  const StepBias bias = step_bias(a, l.c);
+  for (int n = 0; n < NT; ++n) {
+    h[n] = 0.0f, mu[n] = 0.0f, p[n] = 1.0f;
+    A2[n] = l.active ? A2[n] : 0.0f;
+  }
+  const StepBias bias = l.active ? step_bias(a, l.c) : StepBias{0.0f, 0.0f};
   const bool gated = a.z != nullptr;
   float sum = 0.0f;
 
@@ -585,7 +588,8 @@ void scan_bwd_local_kernel(ScanArgs a, int32_t work) {
   const uint16_t* pB = a.B + t0 * a.Bs + l.group * a.N;
   const uint16_t* pC = a.Cm + t0 * a.Cs + l.group * a.N;
   // Past a group's channels a lane reads zeros (out of the buffers' range), and
-  // its state and gradient, which the main pass reads, stay zero.
+  // its state and gradient, which the main pass reads, stay zero, as do those
+  // past the last state.
   const uint32_t lane2 = l.active ? l.c * 2u : 0x80000000u;
   int32_t left = t1 - t0, left_bc = left;
   auto request = [&]() {
@@ -644,10 +648,9 @@ void scan_bwd_local_kernel(ScanArgs a, int32_t work) {
   bool in_first = true;
   auto write_mu = [&]() {
     const uint32_t col = here(l.col);
-    const int32_t kk = here_uniform(k), N = here_uniform(a.N);
+    const int32_t kk = here_uniform(k);
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-      if (n < N) (a.mu + ((int64_t)kk * N + n) * a.cols)[col] = mu[n];
+    for (int n = 0; n < NT; ++n) (a.mu + ((int64_t)kk * NT + n) * a.cols)[col] = mu[n];
   };
 
   Raw q[kAhead];
@@ -669,12 +672,10 @@ void scan_bwd_local_kernel(ScanArgs a, int32_t work) {
   auto keep = [&](int32_t t) {
     if ((t - t0) % kScanKeep != 0 || t == t0) return;
     const uint32_t col = here(l.col);
-    const int32_t N = here_uniform(a.N);
-    float* r = a.keep + (int64_t)(t / kScanKeep) * (N + 1) * a.cols;
+    float* r = a.keep + (int64_t)(t / kScanKeep) * (NT + 1) * a.cols;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-      if (n < N) (r + (int64_t)n * a.cols)[col] = h[n];
-    (r + (int64_t)N * a.cols)[col] = sum;
+    for (int n = 0; n < NT; ++n) (r + (int64_t)n * a.cols)[col] = h[n];
+    (r + (int64_t)NT * a.cols)[col] = sum;
   };
 
   int32_t t = t0;
@@ -715,10 +716,8 @@ void scan_bwd_local_kernel(ScanArgs a, int32_t work) {
     }
   }
   const uint32_t col = here(l.col);
-  const int32_t N = here_uniform(a.N);
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
-    if (n < N) (a.hend + ((int64_t)k * N + n) * a.cols)[col] = h[n];
+  for (int n = 0; n < NT; ++n) (a.hend + ((int64_t)k * NT + n) * a.cols)[col] = h[n];
   if (in_first) write_mu();
   (a.sum + (int64_t)k * a.cols)[col] = sum;
   if (w == 0 && (threadIdx.x & 63) == 0) a.flags[k] = flags;
@@ -855,11 +854,7 @@ __device__ __forceinline__ void zero_if(uint32_t bit, float& a, float& b, float&
 // for the way back.  h itself is ah + d x B: its part in y and in dC needs only
 // sum_n C B and sum_c g d x, one number a token each.
 //
-// Two waves a SIMD up to 32 states.  With 32 the registers then fall a few
-// short and 5 to 19 of them go to scratch memory, outside the loop over a
-// token's states; that is still faster than one wave a SIMD with none in
-// scratch: 453 against 554 us at C 1024, 8192 tokens, 826 against 1014 us at
-// C 2048, the whole backward pass.  64 states need one wave's registers.
+// Two waves a SIMD up to 32 states; 64 states need one wave's registers.
 constexpr int kSub = 2;
 
 template <int NT, bool kGate>
@@ -903,14 +898,13 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
   // Loads without a condition, all under way at once: what is past the group or
   // the states is read at the last of them and set to zero.
   float A2[RC][RN], mu[RC][RN], dA[RC][RN];
-  auto state_at = [&](int j) { return min(n0 + j, a.N - 1); };
   auto decays = [&](auto* A) {
 #pragma unroll
     for (int r = 0; r < RC; ++r) {
-      const int32_t i = min(i0 + RC * set + r, a.per - 1);
+      const uint32_t row = (uint32_t)(g * a.per + min(i0 + RC * set + r, a.per - 1)) * (uint32_t)a.N;
 #pragma unroll
       for (int j = 0; j < RN; ++j) {
-        const auto v = A[((int64_t)g * a.per + i) * a.N + state_at(j)];
+        const auto v = A[row + (uint32_t)min(n0 + j, a.N - 1)];
         if constexpr (sizeof(v) == 2) A2[r][j] = bf16_f32(v);
         else A2[r][j] = v;
       }
@@ -922,23 +916,35 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
   for (int r = 0; r < RC; ++r)
 #pragma unroll
     for (int j = 0; j < RN; ++j) {
-      const bool there = i0 + RC * set + r < a.per && n0 + j < a.N;
-      A2[r][j] = there ? A2[r][j] * kLog2E : 0.0f;
-      dA[r][j] = 0.0f;
-      // What the chunk to the right sends.
-      mu[r][j] = there && k + 1 < a.chunks
-                     ? (a.mu + ((int64_t)(k + 1) * a.N + n0 + j) * a.cols)[col + r] : 0.0f;
+      A2[r][j] = i0 + RC * set + r < a.per && n0 + j < a.N ? A2[r][j] * kLog2E : 0.0f;
+      mu[r][j] = dA[r][j] = 0.0f;
     }
+  // The lane's tile of NT rows of the workspace, whose states past the last and
+  // columns past a group hold zeros; the host keeps the rows below 2^31 bytes.
+  const uint32_t stride4 = (uint32_t)a.cols * 4u;
+  auto tile = [&](const float* rows, uint32_t at4, float (&o)[RC][RN]) {
+    const auto b = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(rows), (short)0, 0x7fffffff, 0x00020000);
+    const uint32_t lane4 = (uint32_t)n0 * stride4 + at4;
 #pragma unroll
-  for (int e = 0; e < RC * RN; e += 4) {
-    f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int r = (e + q) / RN, j = (e + q) % RN;
-      if (k > 0 && i0 + RC * set + r < a.per && n0 + j < a.N)
-        v[q] = (a.hend + ((int64_t)(k - 1) * a.N + n0 + j) * a.cols)[col + r];
+    for (int j = 0; j < RN; ++j) {
+      if constexpr (RC == 2) {
+        const auto v = __builtin_amdgcn_raw_buffer_load_b64(b, (int)lane4, (int)(j * stride4), 0);
+        o[0][j] = __uint_as_float(v[0]);
+        o[1][j] = __uint_as_float(v[1]);
+      } else {
+        o[0][j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b, (int)lane4, (int)(j * stride4), 0));
+      }
     }
-    m.in[e / 4][lane] = v;
+  };
+  const int64_t chunk_rows = (int64_t)NT * a.cols;
+  if (k + 1 < a.chunks) tile(a.mu + (k + 1) * chunk_rows, col * 4u, mu);  // what the chunk to the right sends
+  if (k > 0) {
+    float in[RC][RN];
+    tile(a.hend + (k - 1) * chunk_rows, col * 4u, in);
+#pragma unroll
+    for (int e = 0; e < RC * RN; e += 4)
+      m.in[e / 4][lane] = (f32x4_t){in[e / RN][e % RN], in[e / RN][e % RN + 1], in[e / RN][e % RN + 2],
+                                    in[e / RN][e % RN + 3]};
   }
   float dD = 0.0f, dbias = 0.0f;
   constexpr float kLn2 = 0.6931471805599453f;
@@ -1003,24 +1009,29 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
   constexpr int kRaw = kScanKeep * 2 * NT / 64;
   uint32_t raw_bc[kRaw];
   float sum[RC];
+  // Lane e of 2 NT: state e of B, state e - NT of C.
+  const bool is_c = lane / NT % 2;
+  const uint32_t bc_stride = (uint32_t)(is_c ? a.Cs : a.Bs);
+  const uint16_t* const bc = (is_c ? a.Cm + t0 * a.Cs : a.B + t0 * a.Bs) + g * a.N + min(lane % NT, a.N - 1);
   auto request_block = [&](int32_t ib) {
     const int32_t i_first = ib * kScanKeep;
     const uint32_t at = here(col);
-    const int32_t N = here_uniform(a.N);
+    const uint32_t stride = here(bc_stride);
 #pragma unroll
     for (int u = 0; u < kRaw; ++u) {
-      const int32_t e = lane + 64 * u, n = min(e % NT, N - 1), i = min(i_first + e / (2 * NT), last);
-      const uint16_t* p = e / NT % 2 ? a.Cm + (int64_t)(t0 + i) * a.Cs : a.B + (int64_t)(t0 + i) * a.Bs;
-      raw_bc[u] = p[g * N + n];
+      if constexpr (NT < 64) {
+        const uint32_t i = (uint32_t)min(i_first + (lane + 64 * u) / (2 * NT), last);
+        raw_bc[u] = bc[(uint64_t)i * stride];
+      } else {  // a row of B or of C a wave
+        const int64_t i = t0 + min(i_first + u / 2, last);
+        raw_bc[u] = ((u % 2 ? a.Cm + i * a.Cs : a.B + i * a.Bs) + g * a.N)[min(lane, a.N - 1)];
+      }
     }
     if (ib > 0) {
-      const float* kept = a.keep + (int64_t)((t0 + i_first) / kScanKeep) * (N + 1) * a.cols;
+      const float* kept = a.keep + (int64_t)((t0 + i_first) / kScanKeep) * (NT + 1) * a.cols;
+      tile(kept, at * 4u, h);
 #pragma unroll
-      for (int r = 0; r < RC; ++r) {
-        sum[r] = (kept + (int64_t)N * a.cols)[at + r];
-#pragma unroll
-        for (int j = 0; j < RN; ++j) h[r][j] = (kept + (int64_t)min(n0 + j, N - 1) * a.cols)[at + r];
-      }
+      for (int r = 0; r < RC; ++r) sum[r] = (kept + chunk_rows)[at + r];
     }
   };
 
@@ -1216,15 +1227,14 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
       backward(s);
     }
   }
-  float* pp = a.pparam + (int64_t)k * (a.N + 2) * a.cols;
+  float* pp = a.pparam + (int64_t)k * (NT + 2) * a.cols;
 #pragma unroll
   for (int r = 0; r < RC; ++r)
 #pragma unroll
-    for (int j = 0; j < RN; ++j)
-      if (n0 + j < a.N) (pp + (int64_t)(n0 + j) * a.cols)[here(col) + r] = dA[r][j];
+    for (int j = 0; j < RN; ++j) (pp + (int64_t)j * a.cols)[(uint32_t)n0 * (uint32_t)a.cols + here(col) + r] = dA[r][j];
   if (part < RC) {
-    (pp + (int64_t)a.N * a.cols)[col + mine] = dD;
-    (pp + (int64_t)(a.N + 1) * a.cols)[col + mine] = dbias;
+    (pp + (int64_t)NT * a.cols)[col + mine] = dD;
+    (pp + (int64_t)(NT + 1) * a.cols)[col + mine] = dbias;
   }
 }
 
@@ -1232,8 +1242,9 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
 __device__ __forceinline__ void param_sum(const ScanArgs& a, int32_t col, int32_t n) {
   const int32_t g = col / (a.wpg * 64), i = col - g * a.wpg * 64;
   if (col >= a.cols || i >= a.per) return;
-  const float* p = a.pparam + (int64_t)n * a.cols + col;
-  const int64_t row = (int64_t)(a.N + 2) * a.cols;
+  // Rows: the states, then D and the bias behind the states that there is room for.
+  const float* p = a.pparam + (int64_t)(n < a.N ? n : a.rows + n - a.N) * a.cols + col;
+  const int64_t row = (int64_t)(a.rows + 2) * a.cols;
   double sum = 0.0;
   int32_t k = 0;
   for (; k + 16 <= a.chunks; k += 16) {  // 16 loads at once

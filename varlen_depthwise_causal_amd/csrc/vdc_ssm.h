@@ -61,6 +61,7 @@ struct ScanArgs {
   int32_t wpg;             // waves of 64 channels a group takes
   int32_t cols;            // G * wpg * 64
   int32_t chunk, chunks;   // tokens a chunk holds, chunks of the packed row
+  int32_t rows;            // states the workspace has room for: forward N, backward scan_states(N)
   float* state;            // [slots][C][N]
   const int32_t* index;
   const uint8_t* resume;
@@ -69,13 +70,13 @@ struct ScanArgs {
   uint16_t *dx, *ddt, *dz, *dB, *dC;
   void *dA, *dD, *dbias;
   // workspace
-  float* hend;             // [chunks][N][cols] state after each chunk
-  float* mu;               // [chunks][N][cols] gradient that leaves each chunk to its left
+  float* hend;             // [chunks][rows][cols] state after each chunk
+  float* mu;               // [chunks][rows][cols] gradient that leaves each chunk to its left
   float* sum;              // [chunks][cols] sum of the step sizes of each chunk
-  float* snap;             // [chunks][N][cols] state a resumed document began with
+  float* snap;             // [chunks][rows][cols] state a resumed document began with
   int32_t* flags;          // [chunks] bit 0: a document starts at the chunk's first token, 1: inside
-  float* keep;             // [chunks * chunk / kScanKeep][N + 1][cols]
-  float* pparam;           // [chunks][N + 2][cols] partial dA, dD, ddt_bias
+  float* keep;             // [chunks * chunk / kScanKeep][rows + 1][cols]
+  float* pparam;           // [chunks][rows + 2][cols] partial dA, dD, ddt_bias
   float* pbc;              // [G * bpg][S][2][NT] partial dB, dC
 };
 

@@ -188,7 +188,8 @@ struct ScanPlan {
 
 bool scan_plan(int dir, int64_t S, int64_t C, int64_t N, int64_t G, ScanPlan* out) {
   const int64_t per = C / G, wpg = ceil_div(per, 64), waves = G * wpg;
-  if (waves * 64 > INT32_MAX / 4) return false;
+  // Rows of states of a chunk are addressed by 32-bit offsets in bytes.
+  if (waves * 64 * scan_states(N) > INT32_MAX / 4) return false;
   const int64_t blocks = dir == VDC_BWD ? G * ceil_div(per, scan_bwd_channels(N)) : waves;
   const int64_t want = std::max<int64_t>(1, kScanWaves / blocks);
   int64_t low = ceil_div(std::max<int64_t>(S, 1), want);
@@ -229,7 +230,9 @@ size_t scan_layout(int dir, int64_t S, int64_t N, const ScanPlan& p, char* base,
     at += (elems * 4 + 255) / 256 * 256;
     return reinterpret_cast<float*>(r);
   };
-  const size_t cols = p.cols, rows = (size_t)p.chunks * N * cols;
+  // The backward's kernels read and write whole vectors of states.
+  a->rows = (int32_t)(dir == VDC_BWD ? scan_states(N) : N);
+  const size_t cols = p.cols, rows = (size_t)p.chunks * a->rows * cols;
   if (dir == VDC_FWD && p.chunks == 1) return 0;
   a->hend = take(rows);
   a->sum = take((size_t)p.chunks * cols);
@@ -239,8 +242,8 @@ size_t scan_layout(int dir, int64_t S, int64_t N, const ScanPlan& p, char* base,
     return at;
   }
   a->mu = take(rows);
-  a->keep = take((size_t)p.chunks * (p.chunk / kScanKeep) * (N + 1) * cols);
-  a->pparam = take((size_t)p.chunks * (N + 2) * cols);
+  a->keep = take((size_t)p.chunks * (p.chunk / kScanKeep) * (a->rows + 1) * cols);
+  a->pparam = take((size_t)p.chunks * (a->rows + 2) * cols);
   a->pbc = take((size_t)p.blocks * S * 2 * scan_states(N));
   return at;
 }
