@@ -122,6 +122,11 @@ __device__ __forceinline__ u32x4_t conv_row(const Taps8& t, bool bias, const Row
 // output and the inputs moved up by one.  A wave has 64 vectors of eight
 // channels, keeps their weights and takes `rows` rows one after another, the
 // next row's loads requested before the current is computed.
+//
+// Bound by HBM and the last cache, 16 bytes a channel, and below some hundred
+// rows by the launch: 1000 rows of 8192 channels 21.6 us (6.1 TB/s), one row of
+// 2048 channels 3.2.  Loads and stores past the caches take 25 us there; where
+// 20 such layers take turns, 29 us against 31.
 __global__ __launch_bounds__(256) void conv_step_kernel(ConvStateArgs a, int32_t rows) {
   const int64_t nvec = a.C / 8, vblocks = (nvec + 63) / 64;
   const int64_t wave = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64u);
