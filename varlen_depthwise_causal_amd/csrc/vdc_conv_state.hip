@@ -175,7 +175,9 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvStateArgs a, int32_t
 // What a prompt's carried state changes after the packed forward has run
 // with zero history: the first three outputs of a resumed document, and the
 // document's last three inputs, which go to its slot.  A lane reads the slot
-// before it writes it, so the cache is updated in place.
+// before it writes it, so the cache is updated in place.  A launch of its own
+// leaves the packed forward as it is, for 2.3 us at 37 documents of 520 channels
+// and 4.5 at 22 of 4096 (behind a forward of 175 us).
 __global__ __launch_bounds__(64) void conv_edges_kernel(ConvStateArgs a) {
   const int64_t nvec = a.C / 8, per = (nvec + 63) / 64;
   const int64_t doc = blockIdx.x / per;
