@@ -12,7 +12,7 @@
 // a wave for 64 elements where an FP32 instruction takes 4 and an exponential 8,
 // that is 164 us for one pass over 16384 tokens of 4096 channels with 16 states
 // on 1024 SIMDs at 2.4 GHz; a step size, a gate and the conversions of a token
-// and channel come to as much again as 4 or 5 states.
+// and channel cost as much as 6 states more.
 //
 // Time is cut into chunks that run in parallel.  The states after each chunk
 // are found first with zero history (scan_local), joined in order
