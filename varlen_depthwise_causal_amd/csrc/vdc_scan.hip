@@ -897,7 +897,6 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
   const int32_t g = wb / bpg, i0 = (wb - g * bpg) * CB;
   const int32_t t0 = k * a.chunk;
   const int32_t t1 = (int32_t)min((int64_t)a.S, (int64_t)t0 + a.chunk);
-  const int32_t first_start = find_starts(a, m.starts, t0, t1);
   // The channel whose loads and per-channel terms are this lane's.  A channel
   // past the group reads zeros (out of the buffers' range): its x, g, h and
   // lambda stay zero and add nothing.
@@ -911,31 +910,6 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
   const uint32_t col = (uint32_t)(g * a.wpg * 64 + i0 + RC * set);
   const int32_t n0 = RN * part;
 
-  // A times log2(e); the sums with A are taken with it and scaled at their end.
-  // Loads without a condition, all under way at once: what is past the group or
-  // the states is read at the last of them and set to zero.
-  float A2[RC][RN], mu[RC][RN], dA[RC][RN];
-  auto decays = [&](auto* A) {
-#pragma unroll
-    for (int r = 0; r < RC; ++r) {
-      const uint32_t row = (uint32_t)(g * a.per + min(i0 + RC * set + r, a.per - 1)) * (uint32_t)a.N;
-#pragma unroll
-      for (int j = 0; j < RN; ++j) {
-        const auto v = A[row + (uint32_t)min(n0 + j, a.N - 1)];
-        if constexpr (sizeof(v) == 2) A2[r][j] = bf16_f32(v);
-        else A2[r][j] = v;
-      }
-    }
-  };
-  if (a.A_bf16) decays(static_cast<const uint16_t*>(a.A));
-  else decays(static_cast<const float*>(a.A));
-#pragma unroll
-  for (int r = 0; r < RC; ++r)
-#pragma unroll
-    for (int j = 0; j < RN; ++j) {
-      A2[r][j] = i0 + RC * set + r < a.per && n0 + j < a.N ? A2[r][j] * kLog2E : 0.0f;
-      mu[r][j] = dA[r][j] = 0.0f;
-    }
   // The lane's tile of NT rows of the workspace, whose states past the last and
   // columns past a group hold zeros; the host keeps the rows below 2^31 bytes.
   const uint32_t stride4 = (uint32_t)a.cols * 4u;
@@ -954,15 +928,6 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
     }
   };
   const int64_t chunk_rows = (int64_t)NT * a.cols;
-  if (k + 1 < a.chunks) tile(a.mu + (k + 1) * chunk_rows, col * 4u, mu);  // what the chunk to the right sends
-  if (k > 0) {
-    float in[RC][RN];
-    tile(a.hend + (k - 1) * chunk_rows, col * 4u, in);
-#pragma unroll
-    for (int e = 0; e < RC * RN; e += 4)
-      m.in[e / 4][lane] = (f32x4_t){in[e / RN][e % RN], in[e / RN][e % RN + 1], in[e / RN][e % RN + 2],
-                                    in[e / RN][e % RN + 3]};
-  }
   float dD = 0.0f, dbias = 0.0f;
   constexpr float kLn2 = 0.6931471805599453f;
 
@@ -1052,8 +1017,44 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
     }
   };
 
+  // The first block's loads before all the others that a wave begins with.
   request(last / kScanKeep * kScanKeep, last % kScanKeep < kSub);
   request_block(last / kScanKeep);
+  const int32_t first_start = find_starts(a, m.starts, t0, t1);
+  // A times log2(e); the sums with A are taken with it and scaled at their end.
+  // Loads without a condition, all under way at once: what is past the group or
+  // the states is read at the last of them and set to zero.
+  float A2[RC][RN], mu[RC][RN], dA[RC][RN];
+  auto decays = [&](auto* A) {
+#pragma unroll
+    for (int r = 0; r < RC; ++r) {
+      const uint32_t row = (uint32_t)(g * a.per + min(i0 + RC * set + r, a.per - 1)) * (uint32_t)a.N;
+#pragma unroll
+      for (int j = 0; j < RN; ++j) {
+        const auto v = A[row + (uint32_t)min(n0 + j, a.N - 1)];
+        if constexpr (sizeof(v) == 2) A2[r][j] = bf16_f32(v);
+        else A2[r][j] = v;
+      }
+    }
+  };
+  if (a.A_bf16) decays(static_cast<const uint16_t*>(a.A));
+  else decays(static_cast<const float*>(a.A));
+#pragma unroll
+  for (int r = 0; r < RC; ++r)
+#pragma unroll
+    for (int j = 0; j < RN; ++j) {
+      A2[r][j] = i0 + RC * set + r < a.per && n0 + j < a.N ? A2[r][j] * kLog2E : 0.0f;
+      mu[r][j] = dA[r][j] = 0.0f;
+    }
+  if (k + 1 < a.chunks) tile(a.mu + (k + 1) * chunk_rows, col * 4u, mu);  // what the chunk to the right sends
+  if (k > 0) {
+    float in[RC][RN];
+    tile(a.hend + (k - 1) * chunk_rows, col * 4u, in);
+#pragma unroll
+    for (int e = 0; e < RC * RN; e += 4)
+      m.in[e / 4][lane] = (f32x4_t){in[e / RN][e % RN], in[e / RN][e % RN + 1], in[e / RN][e % RN + 2],
+                                    in[e / RN][e % RN + 3]};
+  }
 #pragma unroll 1
   for (int32_t ib = last / kScanKeep; ib >= 0; --ib) {
     const int32_t i_first = ib * kScanKeep;
