@@ -116,18 +116,16 @@ inline uint32_t place_grid(int64_t work) {
 // ------------------------------------------- B and C of one token, uniform --
 //
 // Every lane of a wave needs the same N values of B and of C, so they live in
-// scalar registers.  kWide: the states are exactly NT and a row's values start
-// at a multiple of 4 bytes: scalar loads of whole dwords, split into FP32 by
-// the scalar unit.  Otherwise lane n loads state n and the values are read
-// out of the lanes, two VALU instructions a state and token more.
-
-template <int NT, bool kWide>
-struct Uniform;
+// scalar registers: scalar loads of whole dwords, split into FP32 by the scalar
+// unit.  That takes rows of NT states at multiples of 4 bytes; others are copied
+// to the workspace first, padded with zeros (scan_pad_kernel).  Loads by lanes and
+// reads out of them instead cost two VALU instructions a state and token: 359 us
+// against 229 with the copy for 8192 tokens, C = 4096, 13 states, forward.
 
 template <int NT>
-struct Uniform<NT, true> {
+struct Uniform {
   uint32_t v[NT / 2];
-  __device__ __forceinline__ void load(const uint16_t* row, int32_t) {
+  __device__ __forceinline__ void load(const uint16_t* row) {
     scalar_ptr p = (scalar_ptr)(uintptr_t)row;
 #pragma unroll
     for (int i = 0; i < NT / 2; ++i) v[i] = p[i];
@@ -142,18 +140,18 @@ struct Uniform<NT, true> {
   }
 };
 
-template <int NT>
-struct Uniform<NT, false> {
-  float v;
-  __device__ __forceinline__ void load(const uint16_t* row, int32_t N) {
-    const int32_t lane = (int32_t)(threadIdx.x & 63);
-    v = lane < N ? bf16_f32(row[lane]) : 0.0f;
-  }
-  __device__ __forceinline__ void pin() {}
-  __device__ __forceinline__ float get(int n) const {
-    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), n));
-  }
-};
+// B's and C's rows, one after another, with NT states a group: a lane has two.
+__global__ __launch_bounds__(256) void scan_pad_kernel(ScanArgs a, int32_t NT) {
+  const int64_t each = (int64_t)a.S * a.G * (NT / 2);
+  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (e >= 2 * each) return;
+  const bool is_c = e >= each;
+  const int64_t q = is_c ? e - each : e, row = q / (NT / 2), t = row / a.G;
+  const int32_t n = (int32_t)(q - row * (NT / 2)) * 2;
+  const uint16_t* p = (is_c ? a.Cm + t * a.Cs : a.B + t * a.Bs) + (row - t * a.G) * a.N;
+  const uint32_t lo = n < a.N ? p[n] : 0u, hi = n + 1 < a.N ? p[n + 1] : 0u;
+  a.pad[e] = lo | hi << 16;
+}
 
 // ---------------------------------------------- forward, lane = channel --
 
@@ -180,40 +178,36 @@ __device__ __forceinline__ Column column_of(const ScanArgs& a, int32_t wave) {
 typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 
-// A's row of a channel times log2(e); 0 past the last state.  kAll: there are
-// exactly NT states, which are then loaded by vectors.
-template <int NT, bool kAll>
+// A's row of a channel times log2(e); 0 past the last state.  Rows of exactly NT
+// states are loaded by vectors.
+template <int NT>
 __device__ __forceinline__ void load_decay(const ScanArgs& a, const Column& l, float (&A2)[NT]) {
   const int64_t at = (int64_t)l.c * a.N;
-  if (a.A_bf16) {
-    const uint16_t* p = static_cast<const uint16_t*>(a.A) + at;
-    if constexpr (kAll) {
+  const uint16_t* p2 = static_cast<const uint16_t*>(a.A) + at;
+  const float* p4 = static_cast<const float*>(a.A) + at;
+  if (a.N == NT && a.A_bf16) {
 #pragma unroll
-      for (int n = 0; n < NT; n += 8) {
-        const u32x4_any v = *reinterpret_cast<const u32x4_any*>(p + n);
+    for (int n = 0; n < NT; n += 8) {
+      const u32x4_any v = *reinterpret_cast<const u32x4_any*>(p2 + n);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) A2[n + 2 * j] = bf16_lo(v[j]), A2[n + 2 * j + 1] = bf16_hi(v[j]);
-      }
-    } else {
-#pragma unroll
-      for (int n = 0; n < NT; ++n) A2[n] = bf16_f32(p[min(n, a.N - 1)]);
+      for (int j = 0; j < 4; ++j) A2[n + 2 * j] = bf16_lo(v[j]), A2[n + 2 * j + 1] = bf16_hi(v[j]);
     }
+  } else if (a.N == NT) {
+#pragma unroll
+    for (int n = 0; n < NT; n += 4) {
+      const f32x4_any v = *reinterpret_cast<const f32x4_any*>(p4 + n);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) A2[n + j] = v[j];
+    }
+  } else if (a.A_bf16) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) A2[n] = bf16_f32(p2[min(n, a.N - 1)]);
   } else {
-    const float* p = static_cast<const float*>(a.A) + at;
-    if constexpr (kAll) {
 #pragma unroll
-      for (int n = 0; n < NT; n += 4) {
-        const f32x4_any v = *reinterpret_cast<const f32x4_any*>(p + n);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) A2[n + j] = v[j];
-      }
-    } else {
-#pragma unroll
-      for (int n = 0; n < NT; ++n) A2[n] = p[min(n, a.N - 1)];
-    }
+    for (int n = 0; n < NT; ++n) A2[n] = p4[min(n, a.N - 1)];
   }
 #pragma unroll
-  for (int n = 0; n < NT; ++n) A2[n] = kAll || n < a.N ? A2[n] * kLog2E : 0.0f;
+  for (int n = 0; n < NT; ++n) A2[n] = n < a.N ? A2[n] * kLog2E : 0.0f;
 }
 
 // A value the compiler must not compute addresses from ahead of its use: the
@@ -241,7 +235,7 @@ __device__ __forceinline__ int32_t here_uniform(int32_t v) {
 // anything, and B and C come from scalar registers, free of VALU instructions.
 // 16384 tokens, C = 4096, 16 states: 189 us without the outputs and 256 with
 // them, VALU busy 94 and 92% of the time; HBM moves 0.34 GB in the second.
-template <int NT, bool kOut, bool kWide>
+template <int NT, bool kOut>
 __global__ __launch_bounds__(64 * kWaves)
 __attribute__((amdgpu_waves_per_eu(NT <= 16 ? 4 : NT == 32 ? 2 : 1)))
 void scan_fwd_kernel(ScanArgs a, int32_t work) {
@@ -258,7 +252,7 @@ void scan_fwd_kernel(ScanArgs a, int32_t work) {
     return base + ((int64_t)chunk * a.N + n) * a.cols;
   };
   float A2[NT], h[NT];
-  load_decay<NT, kWide>(a, l, A2);
+  load_decay<NT>(a, l, A2);
   const float Dc = a.D ? param_at(a.D, a.D_bf16, l.c) : 0.0f;
   const StepBias bias = step_bias(a, l.c);
   const bool gated = kOut && a.z != nullptr;
@@ -341,8 +335,8 @@ void scan_fwd_kernel(ScanArgs a, int32_t work) {
   // Past a group's channels a lane's stores are out of the buffer's range,
   // which drops them.
   const uint32_t lane2 = l.c * 2u, put2 = l.active ? lane2 : 0x80000000u;
-  const uint16_t* pB = a.B + t0 * a.Bs + l.group * a.N;
-  const uint16_t* pC = a.Cm + t0 * a.Cs + l.group * a.N;
+  const uint16_t* pB = a.B + t0 * a.Bs + l.group * a.bn;
+  const uint16_t* pC = a.Cm + t0 * a.Cs + l.group * a.bn;
   int32_t left = t1 - t0;  // tokens not requested yet, and as many of B and C
   int32_t left_bc = left;
   auto request = [&]() {
@@ -357,12 +351,12 @@ void scan_fwd_kernel(ScanArgs a, int32_t work) {
     return r;
   };
   struct Rows {
-    Uniform<NT, kWide> B, C;
+    Uniform<NT> B, C;
   };
   auto request_bc = [&]() {
     Rows r;
-    r.B.load(pB, a.N);
-    if (kOut) r.C.load(pC, a.N);
+    r.B.load(pB);
+    if (kOut) r.C.load(pC);
     --left_bc;
     pB += left_bc > 0 ? a.Bs : 0;
     if (kOut) pC += left_bc > 0 ? a.Cs : 0;
@@ -372,14 +366,10 @@ void scan_fwd_kernel(ScanArgs a, int32_t work) {
   // scalar loads complete in no order, so the wait for `now` is placed before
   // `then` is requested, and nothing waits for `then` until its own token.
   auto token = [&](const Raw& r, const Rows& now, Rows& then) {
-    if (kWide) {
-      __builtin_amdgcn_sched_barrier(0);
-      __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
-      then = request_bc();
-      __builtin_amdgcn_sched_barrier(0);
-    } else {
-      then = request_bc();
-    }
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+    then = request_bc();
+    __builtin_amdgcn_sched_barrier(0);
     const float x = bf16_lo(r.x);
     const float d = step_size(a, bf16_lo(r.dt), bias);
     const float dx = d * x;
@@ -563,7 +553,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void scan_join_kernel(ScanArgs a) 
 // start, the gradient that leaves to the left is sum_t p[t] C[t] g[t] over the
 // tokens of the chunk's first document.  16384 tokens, C = 4096, 16 states: 341
 // us, VALU busy 87% of the time; it writes 0.59 GB, the kept states, meanwhile.
-template <int NT, bool kWide>
+template <int NT>
 __global__ __launch_bounds__(64 * kWaves)
 __attribute__((amdgpu_waves_per_eu(NT <= 16 ? 4 : NT == 32 ? 2 : 1)))
 void scan_bwd_local_kernel(ScanArgs a, int32_t work) {
@@ -577,7 +567,7 @@ void scan_bwd_local_kernel(ScanArgs a, int32_t work) {
   const int32_t t0 = k * a.chunk;
   const int32_t t1 = (int32_t)min((int64_t)a.S, (int64_t)t0 + a.chunk);
   float A2[NT], h[NT], mu[NT], p[NT];
-  load_decay<NT, kWide>(a, l, A2);
+  load_decay<NT>(a, l, A2);
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     h[n] = 0.0f, mu[n] = 0.0f, p[n] = 1.0f;
@@ -595,8 +585,8 @@ void scan_bwd_local_kernel(ScanArgs a, int32_t work) {
   bd.open(a.dt, t0, a.dts);
   bg.open(a.dy, t0, a.dys);
   bz.open(gated ? a.z : a.x, t0, gated ? a.zs : a.xs);  // without a gate nothing uses it
-  const uint16_t* pB = a.B + t0 * a.Bs + l.group * a.N;
-  const uint16_t* pC = a.Cm + t0 * a.Cs + l.group * a.N;
+  const uint16_t* pB = a.B + t0 * a.Bs + l.group * a.bn;
+  const uint16_t* pC = a.Cm + t0 * a.Cs + l.group * a.bn;
   // Past a group's channels a lane reads zeros (out of the buffers' range), and
   // its state and gradient, which the main pass reads, stay zero, as do those
   // past the last state.
@@ -616,26 +606,22 @@ void scan_bwd_local_kernel(ScanArgs a, int32_t work) {
     return r;
   };
   struct Rows {
-    Uniform<NT, kWide> B, C;
+    Uniform<NT> B, C;
   };
   auto request_bc = [&]() {
     Rows r;
-    r.B.load(pB, a.N);
-    r.C.load(pC, a.N);
+    r.B.load(pB);
+    r.C.load(pC);
     --left_bc;
     pB += left_bc > 0 ? a.Bs : 0;
     pC += left_bc > 0 ? a.Cs : 0;
     return r;
   };
   auto token = [&](const Raw& r, const Rows& now, Rows& then) {
-    if (kWide) {
-      __builtin_amdgcn_sched_barrier(0);
-      __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0), as in the forward
-      then = request_bc();
-      __builtin_amdgcn_sched_barrier(0);
-    } else {
-      then = request_bc();
-    }
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0), as in the forward
+    then = request_bc();
+    __builtin_amdgcn_sched_barrier(0);
     const float d = step_size(a, bf16_lo(r.dt), bias);
     const float dx = d * bf16_lo(r.x);
     sum += d;
@@ -1696,19 +1682,9 @@ void short_nl(const ScanArgs& a, hipStream_t s) {
   }
 }
 
-// Whether B's and C's rows can be read by whole dwords (see Uniform).
-bool wide_rows(const ScanArgs& a) {
-  const auto even = [](const uint16_t* p, int64_t stride) {
-    return reinterpret_cast<uintptr_t>(p) % 4 == 0 && stride % 2 == 0;
-  };
-  return a.N == scan_states(a.N) && even(a.B, a.Bs) && even(a.Cm, a.Cs);
-}
-
 template <int NT, bool kOut>
 void fwd_nt(const ScanArgs& a, int32_t work, hipStream_t s) {
-  const dim3 grid(place_grid(work)), block(64 * kWaves);
-  if (wide_rows(a)) hipLaunchKernelGGL((scan_fwd_kernel<NT, kOut, true>), grid, block, 0, s, a, work);
-  else hipLaunchKernelGGL((scan_fwd_kernel<NT, kOut, false>), grid, block, 0, s, a, work);
+  hipLaunchKernelGGL((scan_fwd_kernel<NT, kOut>), dim3(place_grid(work)), dim3(64 * kWaves), 0, s, a, work);
 }
 
 template <bool kOut>
@@ -1735,12 +1711,28 @@ template <int NT>
 void bwd_local_nt(const ScanArgs& a, hipStream_t s) {
   static_assert(Tile<NT>::CB == (NT <= 16 ? 64 : NT == 32 ? 32 : 16), "scan_bwd_channels");
   const int32_t work = a.G * a.wpg * a.chunks;
-  const dim3 grid(place_grid(work)), block(64 * kWaves);
-  if (wide_rows(a)) hipLaunchKernelGGL((scan_bwd_local_kernel<NT, true>), grid, block, 0, s, a, work);
-  else hipLaunchKernelGGL((scan_bwd_local_kernel<NT, false>), grid, block, 0, s, a, work);
+  hipLaunchKernelGGL((scan_bwd_local_kernel<NT>), dim3(place_grid(work)), dim3(64 * kWaves), 0, s, a, work);
 }
 
 }  // namespace
+
+bool scan_rows_fit(const ScanArgs& a) {
+  const auto even = [](const uint16_t* p, int64_t stride) {
+    return reinterpret_cast<uintptr_t>(p) % 4 == 0 && stride % 2 == 0;
+  };
+  return a.N == scan_states(a.N) && even(a.B, a.Bs) && even(a.Cm, a.Cs);
+}
+
+hipError_t launch_scan_pad(ScanArgs* a, hipStream_t s) {
+  const int32_t NT = scan_states(a->N);
+  const int64_t each = (int64_t)a->S * a->G * (NT / 2);
+  hipLaunchKernelGGL(scan_pad_kernel, dim3((uint32_t)((2 * each + 255) / 256)), dim3(256), 0, s, *a, NT);
+  a->B = reinterpret_cast<const uint16_t*>(a->pad);
+  a->Cm = reinterpret_cast<const uint16_t*>(a->pad + each);
+  a->Bs = a->Cs = (int64_t)a->G * NT;
+  a->bn = NT;
+  return hipGetLastError();
+}
 
 hipError_t launch_scan_local(const ScanArgs& a, hipStream_t s) { return fwd<false>(a, a.chunks - 1, s); }
 hipError_t launch_scan_out(const ScanArgs& a, hipStream_t s) { return fwd<true>(a, a.chunks, s); }

@@ -55,6 +55,7 @@ struct ScanArgs {
   const int32_t* cu;
   int32_t num_docs;
   int32_t S, C, N, G;
+  int32_t bn;              // elements between the groups of a row of B or C
   // Channels by waves of 64 within a group: column (g, i) of the workspace
   // rows is g * wpg * 64 + i, for channel g * per + i.
   int32_t per;             // C / G
@@ -73,6 +74,7 @@ struct ScanArgs {
   float* hend;             // [chunks][rows][cols] state after each chunk
   float* mu;               // [chunks][rows][cols] gradient that leaves each chunk to its left
   float* sum;              // [chunks][cols] sum of the step sizes of each chunk
+  uint32_t* pad;           // [2][S][G][scan_states(N)] BF16: B and C, where their rows do not fit
   float* snap;             // [chunks][rows][cols] state a resumed document began with
   int32_t* flags;          // [chunks] bit 0: a document starts at the chunk's first token, 1: inside
   float* keep;             // [chunks * chunk / kScanKeep][rows + 1][cols]
@@ -88,6 +90,10 @@ inline int scan_bwd_channels(int64_t N) {
   return nt <= 16 ? 64 : nt == 32 ? 32 : 16;
 }
 
+// Whether the forward and the backward's first pass can read B's and C's rows as
+// they are; launch_scan_pad copies them to the workspace and points `a` there.
+bool scan_rows_fit(const ScanArgs& a);
+hipError_t launch_scan_pad(ScanArgs* a, hipStream_t s);
 hipError_t launch_scan_local(const ScanArgs& a, hipStream_t s);
 hipError_t launch_scan_join(const ScanArgs& a, bool backward, hipStream_t s);
 hipError_t launch_scan_out(const ScanArgs& a, hipStream_t s);

@@ -212,6 +212,7 @@ bool scan_plan(int dir, int64_t S, int64_t C, int64_t N, int64_t G, ScanPlan* ou
   if (out->brief) chunk = scan_short(N);
   const int64_t chunks = std::max<int64_t>(1, ceil_div(S, chunk));
   if (chunk > INT32_MAX || (chunks * std::max(blocks, waves) + 64) * 64 > kMaxThreads) return false;
+  if (!out->brief && ceil_div(S * G * scan_states(N), 256) * 256 > kMaxThreads) return false;
   const int64_t params = ceil_div(waves * 64, 256) * (N + 2);
   if (dir == VDC_BWD && (G * ceil_div(S * scan_states(N) / 2, 256) + params) * 256 > kMaxThreads) return false;
   out->wpg = (int32_t)wpg;
@@ -223,7 +224,7 @@ bool scan_plan(int dir, int64_t S, int64_t C, int64_t N, int64_t G, ScanPlan* ou
 }
 
 // Places the workspace's arrays (base may be null: the size alone).
-size_t scan_layout(int dir, int64_t S, int64_t N, const ScanPlan& p, char* base, ScanArgs* a) {
+size_t scan_layout(int dir, int64_t S, int64_t N, int64_t G, const ScanPlan& p, char* base, ScanArgs* a) {
   size_t at = 0;
   auto take = [&](size_t elems) {
     char* r = base ? base + at : nullptr;
@@ -233,7 +234,9 @@ size_t scan_layout(int dir, int64_t S, int64_t N, const ScanPlan& p, char* base,
   // The backward's kernels read and write whole vectors of states.
   a->rows = (int32_t)(dir == VDC_BWD ? scan_states(N) : N);
   const size_t cols = p.cols, rows = (size_t)p.chunks * a->rows * cols;
-  if (dir == VDC_FWD && p.chunks == 1) return 0;
+  if (p.brief) return 0;
+  a->pad = reinterpret_cast<uint32_t*>(take(S * G * scan_states(N)));
+  if (dir == VDC_FWD && p.chunks == 1) return at;
   a->hend = take(rows);
   a->sum = take((size_t)p.chunks * cols);
   a->flags = reinterpret_cast<int32_t*>(take(p.chunks));
@@ -300,6 +303,7 @@ int scan_common(const vdc_scan* v, bool prompt, ScanArgs* a) {
   a->C = (int32_t)v->C;
   a->N = (int32_t)v->N;
   a->G = (int32_t)v->groups;
+  a->bn = (int32_t)v->N;
   a->per = (int32_t)(v->C / v->groups);
   a->state = v->state;
   a->slots = v->slots;
@@ -347,7 +351,7 @@ extern "C" size_t selective_scan_workspace_bytes(int direction, int64_t S, int64
   if ((direction != VDC_FWD && direction != VDC_BWD) || scan_sizes(S, C, N, groups) != VDC_OK ||
       S == 0 || !scan_plan(direction, S, C, N, groups, &p))
     return 0;
-  return scan_layout(direction, S, N, p, nullptr, &a);
+  return scan_layout(direction, S, N, groups, p, nullptr, &a);
 }
 
 extern "C" int selective_scan_fwd(const vdc_scan* v, void* y, void* workspace, size_t ws_bytes,
@@ -362,7 +366,7 @@ extern "C" int selective_scan_fwd(const vdc_scan* v, void* y, void* workspace, s
   if (!aligned(y, 2)) return VDC_EALIGN;
   const Span out{y, (size_t)v->S * v->C * 2}, st = state_span(v);
   if (hits_input(v, out, true) || hits_input(v, st, true) || overlaps(out, st)) return VDC_EINVAL;
-  const size_t need = scan_layout(VDC_FWD, v->S, v->N, p, static_cast<char*>(workspace), &a);
+  const size_t need = scan_layout(VDC_FWD, v->S, v->N, v->groups, p, static_cast<char*>(workspace), &a);
   if (need) {
     if (!workspace || ws_bytes < need) return VDC_EWORKSPACE;
     if (!aligned(workspace, 16)) return VDC_EALIGN;
@@ -374,6 +378,7 @@ extern "C" int selective_scan_fwd(const vdc_scan* v, void* y, void* workspace, s
   a.cols = p.cols;
   a.chunk = p.chunk;
   a.chunks = p.chunks;
+  if (!p.brief && !scan_rows_fit(a) && (rc = done(launch_scan_pad(&a, stream)))) return rc;
   if (p.chunks > 1) {
     if ((rc = done(launch_scan_local(a, stream)))) return rc;
     if ((rc = done(launch_scan_join(a, false, stream)))) return rc;
@@ -402,7 +407,7 @@ extern "C" int selective_scan_bwd(const vdc_scan* v, const void* dy, int64_t dy_
       (ddt_bias && !aligned(ddt_bias, dtype_bytes(v->dt_bias_dtype))))
     return VDC_EALIGN;
   const size_t act = (size_t)v->S * v->C * 2, bc = (size_t)v->S * v->groups * v->N * 2;
-  const size_t need = v->S ? scan_layout(VDC_BWD, v->S, v->N, p, static_cast<char*>(workspace), &a) : 0;
+  const size_t need = v->S ? scan_layout(VDC_BWD, v->S, v->N, v->groups, p, static_cast<char*>(workspace), &a) : 0;
   if (need) {
     if (!workspace || ws_bytes < need) return VDC_EWORKSPACE;
     if (!aligned(workspace, 16)) return VDC_EALIGN;
@@ -431,7 +436,9 @@ extern "C" int selective_scan_bwd(const vdc_scan* v, const void* dy, int64_t dy_
   a.chunk = p.chunk;
   a.chunks = v->S ? p.chunks : 0;  // no tokens: sums over no partial rows
   if (v->S > 0) {
-    if ((rc = done(launch_scan_bwd_local(a, stream)))) return rc;
+    ScanArgs first = a;
+    if (!scan_rows_fit(a) && (rc = done(launch_scan_pad(&first, stream)))) return rc;
+    if ((rc = done(launch_scan_bwd_local(first, stream)))) return rc;
     if (p.chunks > 1 && (rc = done(launch_scan_join(a, true, stream)))) return rc;
     if ((rc = done(launch_scan_bwd_main(a, stream)))) return rc;
   }
