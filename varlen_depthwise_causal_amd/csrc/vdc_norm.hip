@@ -21,16 +21,14 @@
 namespace vdc {
 namespace {
 
-// ------------------------------------------------------ groups in registers --
-//
-// Groups of a multiple of 8 channels on rows aligned to 16 bytes: L lanes a
-// group (within a wave, or 256: a whole workgroup), K vectors of 8 channels a
-// lane.  A workgroup keeps its channels and takes tokens one after another,
-// the next one's vectors requested before the current is computed; within a
-// wave, the four waves of a workgroup have the same channels and different
-// tokens.
-
-constexpr int kThreads = 256;
+// L lanes have a group (within a wave, or a whole workgroup of 256 or 512), K
+// vectors of 8 channels a lane.  A workgroup keeps its channels and takes tokens
+// one after another, the next one's vectors requested before the current is
+// computed; within a wave, the four waves of a workgroup have the same channels
+// and different tokens.  kWhole: groups of a multiple of 8 channels on rows
+// aligned to 16 bytes; others end in a part of a vector and are read at any
+// address.  16384 tokens, C = 520 in 8 groups, with a gate: forward 27 us,
+// backward 49; three times over a row with a channel a lane takes 54 and 190.
 
 struct Vec8 {
   float v[8];
@@ -47,14 +45,40 @@ __device__ __forceinline__ u32x4_t pack8(const Vec8& a) {
   for (int i = 0; i < 4; ++i) r[i] = bf16_pack2(a.v[2 * i], a.v[2 * i + 1]);
   return r;
 }
-__device__ __forceinline__ u32x4_t load8(const uint16_t* p) { return *reinterpret_cast<const u32x4_t*>(p); }
-__device__ __forceinline__ void store8(uint16_t* p, u32x4_t v) {
+// At any address that holds BF16 values.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+
+// Eight values, of which there are `count`; the others are zeros.
+template <bool kWhole>
+__device__ __forceinline__ u32x4_t load8(const uint16_t* p, int32_t count) {
+  if (kWhole || count >= 8) {
+    if (kWhole) return *reinterpret_cast<const u32x4_t*>(p);
+    const u32x4_any v = *reinterpret_cast<const u32x4_any*>(p);
+    return (u32x4_t){v[0], v[1], v[2], v[3]};
+  }
+  u32x4_t r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = 2 * i < count ? p[2 * i] : 0u, hi = 2 * i + 1 < count ? p[2 * i + 1] : 0u;
+    r[i] = lo | hi << 16;
+  }
+  return r;
+}
+template <bool kWhole>
+__device__ __forceinline__ void store8(uint16_t* p, u32x4_t v, int32_t count) {
   // Every output byte is written once and not read here.
-  __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(p));
+  if (kWhole) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(p));
+  else if (count >= 8) *reinterpret_cast<u32x4_any*>(p) = (u32x4_any){v[0], v[1], v[2], v[3]};
+  else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < count) p[i] = (uint16_t)(v[i / 2] >> (i % 2 * 16));
+  }
 }
 
-template <int L, int K>
+template <int L, int K, bool kWhole>
 struct Place {
+  static constexpr int kThreads = L > 64 ? L : 256;
   static constexpr bool kWide = L > 64;            // a workgroup has one group
   static constexpr int kTokens = kWide ? 1 : 4;    // tokens a workgroup has at a time
   static constexpr int kGroups = kWide ? 1 : 64 / L;
@@ -75,9 +99,13 @@ struct Place {
   // Channel of vector k within the group, and whether it is one.
   __device__ __forceinline__ int32_t at(int k) const { return (k * L + li) * 8; }
   __device__ __forceinline__ bool has(const NormArgs& a, int k) const { return active && at(k) < a.per; }
+  __device__ __forceinline__ int32_t count(const NormArgs& a, int k) const { return a.per - at(k); }
+  __device__ __forceinline__ bool has(const NormArgs& a, int k, int i) const {
+    return active && at(k) + (kWhole ? 0 : i) < a.per;
+  }
 };
 
-// Sum over a team; `lds` has four floats for each call between barriers.
+// Sum over a team; `lds` has a float a wave for each call between barriers.
 template <int L>
 __device__ __forceinline__ float team_sum(float v, float* lds) {
   if constexpr (L <= 64) {
@@ -86,38 +114,39 @@ __device__ __forceinline__ float team_sum(float v, float* lds) {
     v = lanes_sum<64>(v);
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x / 64] = v;
     __syncthreads();
-    return (lds[0] + lds[1]) + (lds[2] + lds[3]);
+    const float four = (lds[0] + lds[1]) + (lds[2] + lds[3]);
+    return L == 256 ? four : four + ((lds[4] + lds[5]) + (lds[6] + lds[7]));
   }
 }
 
 template <int K>
 struct Affine {
   Vec8 w[K], b[K];
-  template <int L>
-  __device__ __forceinline__ void load(const NormArgs& a, const Place<L, K>& p) {
+  template <class P>
+  __device__ __forceinline__ void load(const NormArgs& a, const P& p) {
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int64_t c = p.c0 + p.at(k) + i;
-        w[k].v[i] = p.has(a, k) ? param_at(a.w, a.w_bf16, c) : 0.0f;
-        b[k].v[i] = p.has(a, k) && a.b ? param_at(a.b, a.b_bf16, c) : 0.0f;
+        w[k].v[i] = p.has(a, k, i) ? param_at(a.w, a.w_bf16, c) : 0.0f;
+        b[k].v[i] = p.has(a, k, i) && a.b ? param_at(a.b, a.b_bf16, c) : 0.0f;
       }
   }
 };
 
-template <int L, int K>
-__device__ __forceinline__ void request(const NormArgs& a, const Place<L, K>& p, const uint16_t* t,
+template <int L, int K, bool kWhole>
+__device__ __forceinline__ void request(const NormArgs& a, const Place<L, K, kWhole>& p, const uint16_t* t,
                                         int64_t stride, int64_t token, u32x4_t (&r)[K]) {
   const int64_t row = token < a.S ? token : a.S - 1;
 #pragma unroll
   for (int k = 0; k < K; ++k)
-    r[k] = p.has(a, k) ? load8(t + row * stride + p.c0 + p.at(k)) : (u32x4_t){0u, 0u, 0u, 0u};
+    r[k] = p.has(a, k) ? load8<kWhole>(t + row * stride + p.c0 + p.at(k), p.count(a, k)) : (u32x4_t){0u, 0u, 0u, 0u};
 }
 
 // Differences from the mean, and 1 / sqrt(var + eps).
-template <int L, int K>
-__device__ __forceinline__ float centre(const NormArgs& a, const Place<L, K>& p, const u32x4_t (&r)[K],
+template <int L, int K, bool kWhole>
+__device__ __forceinline__ float centre(const NormArgs& a, const Place<L, K, kWhole>& p, const u32x4_t (&r)[K],
                                         Vec8 (&d)[K], float* lds) {
   const float inv = 1.0f / (float)a.per;
   float s = 0.0f;
@@ -133,16 +162,16 @@ __device__ __forceinline__ float centre(const NormArgs& a, const Place<L, K>& p,
   for (int k = 0; k < K; ++k)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      d[k].v[i] = p.has(a, k) ? d[k].v[i] - mean : 0.0f;
+      d[k].v[i] = p.has(a, k, i) ? d[k].v[i] - mean : 0.0f;
       q = __builtin_fmaf(d[k].v[i], d[k].v[i], q);
     }
-  return 1.0f / __builtin_sqrtf(team_sum<L>(q, lds + 4) * inv + a.eps);
+  return 1.0f / __builtin_sqrtf(team_sum<L>(q, lds + 8) * inv + a.eps);
 }
 
-template <int L, int K, bool kGate>
-__global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs a, int32_t rows) {
-  __shared__ float lds[2][8];
-  const Place<L, K> p(a, rows);
+template <int L, int K, bool kWhole, bool kGate>
+__global__ __launch_bounds__(L > 64 ? L : 256) void norm_fwd_kernel(NormArgs a, int32_t rows) {
+  __shared__ float lds[2][16];
+  const Place<L, K, kWhole> p(a, rows);
   Affine<K> f;
   f.load(a, p);
   u32x4_t x[K], z[K];
@@ -167,18 +196,23 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs a, int32_t 
         const float v = __builtin_fmaf(d[k].v[i] * rstd, f.w[k].v[i], f.b[k].v[i]);
         y.v[i] = kGate ? v * (zk.v[i] * sigmoid_f32(zk.v[i])) : v * sigmoid_f32(v);
       }
-      if (p.has(a, k)) store8(a.y + t * a.C + p.c0 + p.at(k), pack8(y));
+      if (p.has(a, k)) store8<kWhole>(a.y + t * a.C + p.c0 + p.at(k), pack8(y), p.count(a, k));
     }
   }
 }
 
-template <int L, int K, bool kGate>
-__global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs a, int32_t rows) {
-  typedef Place<L, K> P;
-  __shared__ float lds[2][16];
+template <int L, int K, bool kWhole, bool kGate>
+__global__ __launch_bounds__(L > 64 ? L : 256) void norm_bwd_kernel(NormArgs a, int32_t rows) {
+  typedef Place<L, K, kWhole> P;
+  __shared__ float lds[2][32];
   __shared__ float sums[P::kWide ? 1 : 3][P::kWide ? 1 : 2 * K * 8][64];
   const P p(a, rows);
   const float inv = 1.0f / (float)a.per;
+  // Eight waves a workgroup, two a SIMD, have no registers for the next token
+  // (and with a gate some 30 too few even so, which go to scratch memory: 400 us
+  // for 4096 tokens of one group of 16384 channels, against 3360 by going over
+  // each row three times).
+  constexpr bool kAhead = L <= 256;
   Affine<K> f;
   f.load(a, p);
   Vec8 dw[K], db[K];
@@ -187,18 +221,20 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs a, int32_t 
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[k].v[i] = db[k].v[i] = 0.0f;
   u32x4_t x[K], z[K], dy[K];
-  request(a, p, a.x, a.xs, p.token, x);
-  request(a, p, a.dy, a.dys, p.token, dy);
-  if (kGate) request(a, p, a.z, a.zs, p.token, z);
+  auto fetch = [&](int64_t t) {
+    request(a, p, a.x, a.xs, t, x);
+    request(a, p, a.dy, a.dys, t, dy);
+    if (kGate) request(a, p, a.z, a.zs, t, z);
+  };
+  if (kAhead) fetch(p.token);
   int turn = 0;
 #pragma unroll 1
   for (int64_t t = p.token; t < a.S; t += p.step, turn ^= 1) {
+    if (!kAhead) fetch(t);
     u32x4_t xc[K], zc[K], dc[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) xc[k] = x[k], dc[k] = dy[k], zc[k] = kGate ? z[k] : x[k];
-    request(a, p, a.x, a.xs, t + p.step, x);
-    request(a, p, a.dy, a.dys, t + p.step, dy);
-    if (kGate) request(a, p, a.z, a.zs, t + p.step, z);
+    if (kAhead) fetch(t + p.step);
     Vec8 d[K], q[K];
     const float rstd = centre(a, p, xc, d, lds[turn]);
     float s1 = 0.0f, s2 = 0.0f;
@@ -220,16 +256,16 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs a, int32_t 
         s1 += q[k].v[i];
         s2 = __builtin_fmaf(q[k].v[i], xh, s2);
       }
-      if (kGate && p.has(a, k)) store8(a.dz + t * a.C + p.c0 + p.at(k), pack8(dz));
+      if (kGate && p.has(a, k)) store8<kWhole>(a.dz + t * a.C + p.c0 + p.at(k), pack8(dz), p.count(a, k));
     }
-    s1 = team_sum<L>(s1, lds[turn] + 8) * inv;
-    s2 = team_sum<L>(s2, lds[turn] + 12) * inv;
+    s1 = team_sum<L>(s1, lds[turn] + 16) * inv;
+    s2 = team_sum<L>(s2, lds[turn] + 24) * inv;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       Vec8 o;
 #pragma unroll
       for (int i = 0; i < 8; ++i) o.v[i] = rstd * __builtin_fmaf(-d[k].v[i], s2, q[k].v[i] - s1);
-      if (p.has(a, k)) store8(a.dx + t * a.C + p.c0 + p.at(k), pack8(o));
+      if (p.has(a, k)) store8<kWhole>(a.dx + t * a.C + p.c0 + p.at(k), pack8(o), p.count(a, k));
     }
   }
   // The workgroup's partial row: its waves' sums in order.
@@ -262,90 +298,12 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs a, int32_t 
   for (int k = 0; k < K; ++k)
     if (p.has(a, k)) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        part[p.at(k) + i] = dw[k].v[i];
-        part[a.C + p.at(k) + i] = db[k].v[i];
-      }
+      for (int i = 0; i < 8; ++i)
+        if (p.has(a, k, i)) {
+          part[p.at(k) + i] = dw[k].v[i];
+          part[a.C + p.at(k) + i] = db[k].v[i];
+        }
     }
-}
-
-// ------------------------------------------------- any group, any alignment --
-//
-// A wave has one group of a token and goes over it three times, from L2 after
-// the first.
-
-struct Stats {
-  float mean, rstd;
-};
-
-__device__ __forceinline__ Stats stats_of(const NormArgs& a, const uint16_t* x) {
-  const int lane = threadIdx.x & 63;
-  float s = 0.0f;
-  for (int i = lane; i < a.per; i += 64) s += bf16_f32(x[i]);
-  const float mean = lanes_sum<64>(s) / (float)a.per;
-  float q = 0.0f;
-  for (int i = lane; i < a.per; i += 64) {
-    const float d = bf16_f32(x[i]) - mean;
-    q = __builtin_fmaf(d, d, q);
-  }
-  return Stats{mean, 1.0f / __builtin_sqrtf(lanes_sum<64>(q) / (float)a.per + a.eps)};
-}
-
-__global__ __launch_bounds__(256) void norm_fwd_any_kernel(NormArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int64_t step = (int64_t)gridDim.x * 4;
-  for (int64_t e = (int64_t)blockIdx.x * 4 + threadIdx.x / 64; e < a.S * a.G; e += step) {
-    const int64_t t = e / a.G, c0 = (e - t * a.G) * a.per;
-    const uint16_t* x = a.x + t * a.xs + c0;
-    const Stats st = stats_of(a, x);
-    for (int i = lane; i < a.per; i += 64) {
-      const float xh = (bf16_f32(x[i]) - st.mean) * st.rstd;
-      const float v = __builtin_fmaf(xh, param_at(a.w, a.w_bf16, c0 + i),
-                                     a.b ? param_at(a.b, a.b_bf16, c0 + i) : 0.0f);
-      const float u = a.z ? bf16_f32(a.z[t * a.zs + c0 + i]) : v;
-      a.y[t * a.C + c0 + i] = bf16_of(v * (a.z ? u * sigmoid_f32(u) : sigmoid_f32(v)));
-    }
-  }
-}
-
-// A wave takes one group of every prows-th token and keeps its sums for dw
-// and db in its own partial row.
-__global__ __launch_bounds__(64) void norm_bwd_any_kernel(NormArgs a) {
-  const int64_t row = blockIdx.x / a.G, c0 = (blockIdx.x - row * a.G) * (int64_t)a.per;
-  const int lane = threadIdx.x;
-  float* pw = a.part + row * 2 * a.C + c0;
-  float* pb = pw + a.C;
-  for (int i = lane; i < a.per; i += 64) pw[i] = pb[i] = 0.0f;
-  const float inv = 1.0f / (float)a.per;
-  for (int64_t t = row; t < a.S; t += a.prows) {
-    const uint16_t* x = a.x + t * a.xs + c0;
-    const Stats st = stats_of(a, x);
-    // Channel i's xhat, and w times its dv.
-    auto terms = [&](int i, float& xh, float& v, float& u, float& s, float& dy, float& dv) {
-      xh = (bf16_f32(x[i]) - st.mean) * st.rstd;
-      v = __builtin_fmaf(xh, param_at(a.w, a.w_bf16, c0 + i), a.b ? param_at(a.b, a.b_bf16, c0 + i) : 0.0f);
-      dy = bf16_f32(a.dy[t * a.dys + c0 + i]);
-      u = a.z ? bf16_f32(a.z[t * a.zs + c0 + i]) : v;
-      s = sigmoid_f32(u);
-      dv = dy * (a.z ? u * s : dsilu_f32(u, s));
-      return dv * param_at(a.w, a.w_bf16, c0 + i);
-    };
-    float xh, v, u, s, dy, dv, s1 = 0.0f, s2 = 0.0f;
-    for (int i = lane; i < a.per; i += 64) {
-      const float q = terms(i, xh, v, u, s, dy, dv);
-      if (a.z) a.dz[t * a.C + c0 + i] = bf16_of(dy * v * dsilu_f32(u, s));
-      pw[i] = __builtin_fmaf(dv, xh, pw[i]);
-      pb[i] += dv;
-      s1 += q;
-      s2 = __builtin_fmaf(q, xh, s2);
-    }
-    s1 = lanes_sum<64>(s1) * inv;
-    s2 = lanes_sum<64>(s2) * inv;
-    for (int i = lane; i < a.per; i += 64) {
-      const float q = terms(i, xh, v, u, s, dy, dv);
-      a.dx[t * a.C + c0 + i] = bf16_of(st.rstd * __builtin_fmaf(-xh, s2, q - s1));
-    }
-  }
 }
 
 // The partial rows of dw and db in order, summed in FP64, 16 loads at once.
@@ -372,12 +330,10 @@ bool vectors(const uint16_t* p, int64_t stride) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % 8 == 0;
 }
 
-// Whether the groups go to registers: whole vectors on aligned rows, at most
-// 4 a lane of a workgroup (8 would spill the backward's sums).
-bool in_registers(const NormArgs& a) {
-  return a.per % 8 == 0 && a.per <= kThreads * 8 * 4 && a.C % 8 == 0 && vectors(a.x, a.xs) &&
-         (!a.z || vectors(a.z, a.zs)) && (!a.dy || vectors(a.dy, a.dys)) &&
-         vectors(a.y, 8) && vectors(a.dx, 8) && vectors(a.dz, 8);
+// Whether all vectors are whole and aligned (kWhole above).
+bool whole(const NormArgs& a) {
+  return a.per % 8 == 0 && a.C % 8 == 0 && vectors(a.x, a.xs) && (!a.z || vectors(a.z, a.zs)) &&
+         (!a.dy || vectors(a.dy, a.dys)) && vectors(a.y, 8) && vectors(a.dx, 8) && vectors(a.dz, 8);
 }
 
 // Lanes of a team and vectors of a lane for groups of `per` channels; one
@@ -393,40 +349,52 @@ Shape shape_of(int64_t per) {
   if (n <= 32) return {32, 1};
   if (n <= 64) return {64, 1};
   if (n <= 128) return {64, 2};
-  return {256, n <= 512 ? 2 : 4};
+  if (n <= 1024) return {256, n <= 512 ? 2 : 4};
+  return {512, 4};  // eight vectors a lane of 256 would spill the backward's sums
 }
 
-template <int L, int K>
+template <int L, int K, bool kWhole>
 void launch_vec(const NormArgs& a, bool back, hipStream_t s) {
-  const int64_t sets = (a.G + Place<L, K>::kGroups - 1) / Place<L, K>::kGroups;
-  const int64_t turns = (a.S + Place<L, K>::kTokens - 1) / Place<L, K>::kTokens;
+  typedef Place<L, K, kWhole> P;
+  const int64_t sets = (a.G + P::kGroups - 1) / P::kGroups;
+  const int64_t turns = (a.S + P::kTokens - 1) / P::kTokens;
   int64_t rows = back ? a.prows : turns;
-  if (!back) rows = rows * sets > 4096 ? (4096 + sets - 1) / sets : rows;
-  const dim3 grid((uint32_t)(rows * sets)), block(kThreads);
+  // A workgroup reads its weights once: the larger they are, the more tokens it
+  // takes.  Forward, one group of 16384 channels, 4096 tokens: 512 workgroups 97
+  // us, 4096 282; of 4096 channels, 8192 tokens: 1024 41 us, 4096 69.
+  const int64_t most = L <= 64 ? 4096 : K == 2 ? 1024 : 512;
+  if (!back) rows = rows * sets > most ? (most + sets - 1) / sets : rows;
+  const dim3 grid((uint32_t)(rows * sets)), block(P::kThreads);
   if (back) {
-    if (a.z) hipLaunchKernelGGL((norm_bwd_kernel<L, K, true>), grid, block, 0, s, a, (int32_t)rows);
-    else hipLaunchKernelGGL((norm_bwd_kernel<L, K, false>), grid, block, 0, s, a, (int32_t)rows);
+    if (a.z) hipLaunchKernelGGL((norm_bwd_kernel<L, K, kWhole, true>), grid, block, 0, s, a, (int32_t)rows);
+    else hipLaunchKernelGGL((norm_bwd_kernel<L, K, kWhole, false>), grid, block, 0, s, a, (int32_t)rows);
   } else {
-    if (a.z) hipLaunchKernelGGL((norm_fwd_kernel<L, K, true>), grid, block, 0, s, a, (int32_t)rows);
-    else hipLaunchKernelGGL((norm_fwd_kernel<L, K, false>), grid, block, 0, s, a, (int32_t)rows);
+    if (a.z) hipLaunchKernelGGL((norm_fwd_kernel<L, K, kWhole, true>), grid, block, 0, s, a, (int32_t)rows);
+    else hipLaunchKernelGGL((norm_fwd_kernel<L, K, kWhole, false>), grid, block, 0, s, a, (int32_t)rows);
   }
 }
 
+template <bool kWhole>
 void launch_shape(const NormArgs& a, bool back, hipStream_t s) {
   const Shape h = shape_of(a.per);
-  if (h.lanes == 8) launch_vec<8, 1>(a, back, s);
-  else if (h.lanes == 16) launch_vec<16, 1>(a, back, s);
-  else if (h.lanes == 32) launch_vec<32, 1>(a, back, s);
-  else if (h.lanes == 64 && h.vecs == 1) launch_vec<64, 1>(a, back, s);
-  else if (h.lanes == 64) launch_vec<64, 2>(a, back, s);
-  else if (h.vecs == 2) launch_vec<256, 2>(a, back, s);
-  else launch_vec<256, 4>(a, back, s);
+  if (h.lanes == 8) launch_vec<8, 1, kWhole>(a, back, s);
+  else if (h.lanes == 16) launch_vec<16, 1, kWhole>(a, back, s);
+  else if (h.lanes == 32) launch_vec<32, 1, kWhole>(a, back, s);
+  else if (h.lanes == 64 && h.vecs == 1) launch_vec<64, 1, kWhole>(a, back, s);
+  else if (h.lanes == 64) launch_vec<64, 2, kWhole>(a, back, s);
+  else if (h.lanes == 256 && h.vecs == 2) launch_vec<256, 2, kWhole>(a, back, s);
+  else if (h.lanes == 256) launch_vec<256, 4, kWhole>(a, back, s);
+  else launch_vec<512, 4, kWhole>(a, back, s);
+}
+
+hipError_t launch(const NormArgs& a, bool back, hipStream_t s) {
+  if (whole(a)) launch_shape<true>(a, back, s);
+  else launch_shape<false>(a, back, s);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-// Partial rows of the backward: about 1024 workgroups, four on each CU, by
-// the shape that aligned rows take.
 int norm_bwd_rows(int64_t S, int64_t C, int64_t G) {
   const Shape h = shape_of(C / G);
   const int64_t groups = h.lanes > 64 ? 1 : 64 / h.lanes, tokens = h.lanes > 64 ? 1 : 4;
@@ -435,21 +403,8 @@ int norm_bwd_rows(int64_t S, int64_t C, int64_t G) {
   return (int)(turns < want ? turns : want);
 }
 
-hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t s) {
-  if (in_registers(a)) launch_shape(a, false, s);
-  else {
-    const int64_t blocks = (a.S * a.G + 3) / 4;
-    hipLaunchKernelGGL(norm_fwd_any_kernel, dim3((uint32_t)(blocks < 65536 ? blocks : 65536)), dim3(256), 0,
-                       s, a);
-  }
-  return hipGetLastError();
-}
-
-hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s) {
-  if (in_registers(a)) launch_shape(a, true, s);
-  else hipLaunchKernelGGL(norm_bwd_any_kernel, dim3((uint32_t)((int64_t)a.prows * a.G)), dim3(64), 0, s, a);
-  return hipGetLastError();
-}
+hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t s) { return launch(a, false, s); }
+hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s) { return launch(a, true, s); }
 
 hipError_t launch_norm_bwd_sum(const NormArgs& a, hipStream_t s) {
   hipLaunchKernelGGL(norm_bwd_sum_kernel, dim3((uint32_t)((2 * a.C + 63) / 64)), dim3(64), 0, s, a);
