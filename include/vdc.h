@@ -332,8 +332,8 @@ typedef struct vdc_scan {
 } vdc_scan;
 
 /* selective_scan_workspace_bytes - workspace of selective_scan_fwd
- * (VDC_FWD) or selective_scan_bwd (VDC_BWD); 0 for invalid sizes.  Its
- * contents need not start at zero. */
+ * (VDC_FWD) or selective_scan_bwd (VDC_BWD); 0 for invalid sizes, and for
+ * the forward of short rows.  Its contents need not start at zero. */
 size_t selective_scan_workspace_bytes(int direction, int64_t S, int64_t C, int64_t N,
                                       int64_t groups);
 
