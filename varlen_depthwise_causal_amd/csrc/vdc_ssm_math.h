@@ -55,7 +55,8 @@ __device__ __forceinline__ float dsilu_f32(float z, float s) {
 //
 // P the polynomial of degree 4 nearest to 2 atanh(s) / s in relative error
 // (8e-9).  The exponent v log2(e) is rounded once more than v itself, at most
-// |v| 2^-24 of e.  max(v, 0) is taken as (v + |v|) / 2, which keeps a NaN.
+// |v| 2^-24 of e.  A step of -inf has the size 0: e is 0 then, and so is
+// max(v, 0).  That maximum drops a NaN, which s brings back.
 __device__ __forceinline__ float softplus_f32(float p, float q, float q2) {
   const float v = p + q;
   const float e = __builtin_amdgcn_exp2f(-__builtin_fabsf(__builtin_fmaf(p, kLog2E, q2)));
@@ -66,7 +67,7 @@ __device__ __forceinline__ float softplus_f32(float p, float q, float q2) {
   r = __builtin_fmaf(r, u, 0.4002491f);
   r = __builtin_fmaf(r, u, 0.66666317f);
   r = __builtin_fmaf(r, u, 2.0f);
-  return __builtin_fmaf(0.5f, v + __builtin_fabsf(v), s * r);
+  return __builtin_fmaf(s, r, __builtin_fmaxf(v, 0.0f));
 }
 
 // The value of the lane that the DPP control kCtrl names.
