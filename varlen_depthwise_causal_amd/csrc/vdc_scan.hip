@@ -285,8 +285,10 @@ void scan_fwd_kernel(ScanArgs a, int32_t work) {
       if (slot >= 0) {
         // The chunk that ends a document writes its slot while others may
         // still have to read it: a document that runs past its first chunk
-        // has its start copied by the first pass and read from there.
-        const bool past = next > t1;
+        // has its start copied by the first pass and read from there.  The
+        // first pass leaves the last chunk out: an end past the last token,
+        // which only malformed prefix sums have, must not ask for a copy.
+        const bool past = next > t1 && t1 < a.S;
         const uint32_t col = here(l.col);
         const int32_t kk = here_uniform(k), N = here_uniform(a.N);
         if (kOut && past) {
@@ -1556,8 +1558,9 @@ __global__ __launch_bounds__(64 * kShortWaves) void scan_short_kernel(ScanArgs a
       const int64_t slot = slot_of(a.index, d, a.slots);
       if (slot < 0) return;
       // The wave that ends the document writes its slot while this one is at
-      // its second pass: that pass has the state from the first.
-      const bool past = next > t1;
+      // its second pass: that pass has the state from the first, which the
+      // row's last part does not make.
+      const bool past = next > t1 && t1 < a.S;
       const float* s = a.state + slot * a.C * a.N + h0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
