@@ -1034,7 +1034,10 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
       A2[r][j] = i0 + RC * set + r < a.per && n0 + j < a.N ? A2[r][j] * kLog2E : 0.0f;
       mu[r][j] = dA[r][j] = 0.0f;
     }
-  if (k + 1 < a.chunks) tile(a.mu + (k + 1) * chunk_rows, col * 4u, mu);  // what the chunk to the right sends
+  // What the chunk to the right sends; nothing where a document starts with it.
+  // (The join clears such a chunk's rows, but for states past the last and
+  // columns past the group, where 0 times an infinity may have left a NaN.)
+  if (k + 1 < a.chunks && !(starts_from(m.starts, t1 - t0) & 1u)) tile(a.mu + (k + 1) * chunk_rows, col * 4u, mu);
   if (k > 0) {
     float in[RC][RN];
     tile(a.hend + (k - 1) * chunk_rows, col * 4u, in);
