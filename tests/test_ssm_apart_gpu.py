@@ -1,6 +1,7 @@
-"""Infinities and NaN of one document do not reach another through what the
-scan's kernels share: chunks of the packed row that a document's start cuts,
-states past the last of a channel and columns past the last of a group."""
+"""Infinities and NaN of one document do not reach another, nor the tokens that
+the formulas keep from them, through what the scan's kernels share: chunks of the
+packed row that a document's start cuts, states past the last of a channel and
+columns past the last of a group."""
 import pytest
 import torch
 
@@ -62,3 +63,19 @@ def test_gradients_of_the_documents_around(vdc, C, N, G, value, which):
     assert torch.equal(y[out], clean[out])
     for name, i in TOKENS.items():
         assert torch.equal(got[i][out], cleang[i][out]), name
+
+
+@pytest.mark.parametrize("C,N,G", SIZES)
+@pytest.mark.parametrize("t", [128, 133])
+def test_an_endless_step_cuts_its_document(vdc, C, N, G, t):
+    """A step of +inf forgets all that was: the gradients of the tokens before
+    it are those of a document that ends there."""
+    lengths, dy = [96, 104, 24], Maker(512, DEV).normal(224, C)
+    k, _, cu = scan_inputs(511, lengths, C, N, G, device=DEV)
+    cut = torch.tensor([0, 96, t, 200, 224], dtype=torch.int32, device=DEV)
+    want = vdc.selective_scan_bwd(*_head(k), cut, dy, **_rest(k))
+    k["dt"] = k["dt"].clone()
+    k["dt"][t] = INF
+    got = vdc.selective_scan_bwd(*_head(k), cu, dy, **_rest(k))
+    for name, i in TOKENS.items():
+        assert torch.equal(got[i][:t], want[i][:t]), name

@@ -178,8 +178,12 @@ __device__ __forceinline__ Column column_of(const ScanArgs& a, int32_t wave) {
 typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 
-// A's row of a channel times log2(e); 0 past the last state.  Rows of exactly NT
-// states are loaded by vectors.
+// The decay of a state past the last: any finite step leaves its zero as it is,
+// and so does an infinite one, for which a decay of 0 would make a NaN.
+constexpr float kNoState = -FLT_MIN;
+
+// A's row of a channel times log2(e); kNoState past the last state.  Rows of
+// exactly NT states are loaded by vectors.
 template <int NT>
 __device__ __forceinline__ void load_decay(const ScanArgs& a, const Column& l, float (&A2)[NT]) {
   const int64_t at = (int64_t)l.c * a.N;
@@ -207,7 +211,7 @@ __device__ __forceinline__ void load_decay(const ScanArgs& a, const Column& l, f
     for (int n = 0; n < NT; ++n) A2[n] = p4[min(n, a.N - 1)];
   }
 #pragma unroll
-  for (int n = 0; n < NT; ++n) A2[n] = n < a.N ? A2[n] * kLog2E : 0.0f;
+  for (int n = 0; n < NT; ++n) A2[n] = n < a.N ? A2[n] * kLog2E : kNoState;
 }
 
 // A value the compiler must not compute addresses from ahead of its use: the
@@ -1011,7 +1015,7 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
   const int32_t first_start = find_starts(a, m.starts, t0, t1);
   // A times log2(e); the sums with A are taken with it and scaled at their end.
   // Loads without a condition, all under way at once: what is past the group or
-  // the states is read at the last of them and set to zero.
+  // the states is read at the last of them and not used.
   float A2[RC][RN], mu[RC][RN], dA[RC][RN];
   auto decays = [&](auto* A) {
 #pragma unroll
@@ -1031,7 +1035,7 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
   for (int r = 0; r < RC; ++r)
 #pragma unroll
     for (int j = 0; j < RN; ++j) {
-      A2[r][j] = i0 + RC * set + r < a.per && n0 + j < a.N ? A2[r][j] * kLog2E : 0.0f;
+      A2[r][j] = i0 + RC * set + r < a.per && n0 + j < a.N ? A2[r][j] * kLog2E : kNoState;
       mu[r][j] = dA[r][j] = 0.0f;
     }
   // What the chunk to the right sends; nothing where a document starts with it.
