@@ -119,3 +119,19 @@ def test_nan_steps_stay(vdc):
     y = vdc.selective_scan_fwd(*_head(k), cu, **_rest(k))
     bad = torch.isnan(y)
     assert bool(bad[25:, 7].all()) and int(bad.sum()) == 25
+
+
+@pytest.mark.parametrize("S,at", [(700, 64), (2500, 192)])
+def test_states_that_vanish_and_decays_past_the_range(vdc, S, at):
+    """Steps of either sign (dt_softplus off): 32 tokens that take the state to
+    nothing are followed by 32 whose decay alone is past FP32's range.  What
+    follows is finite, and as the definition has it."""
+    C, N = 64, 8
+    k, docs, cu = scan_inputs(521, [S], C, N, device=DEV, softplus=False, gate=False)
+    k["A"] = torch.full((C, N), -1.0, device=DEV)
+    k["x"], k["dt"] = k["x"].clone(), k["dt"].clone()
+    k["x"][at:at + 64] = 0.0
+    k["dt"][at:at + 32], k["dt"][at + 32:at + 64] = 40.0, -12.0
+    ref = R.Scan(*_head(k), docs, k["D"], softplus_on=False)
+    y = vdc.selective_scan_fwd(*_head(k), cu, D=k["D"], dt_softplus=False)
+    R.close("y", y, ref.y, ref.ey)

@@ -507,7 +507,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void scan_join_kernel(ScanArgs a) 
     const int32_t s = s0 + w * kJoin;
     const Batch now = next;
     if (s0 + kJoin * kJoinWaves < steps) next = load(s + kJoin * kJoinWaves);
-    float decay[kJoin], all = 1.0f, own = 0.0f;
+    float decay[kJoin], sums = 0.0f, own = 0.0f;
     int32_t apart = 0;
     auto step = [&](int j, float in) {
       const int32_t f = now.flags[j];
@@ -518,11 +518,13 @@ __global__ __launch_bounds__(64 * kJoinWaves) void scan_join_kernel(ScanArgs a) 
     for (int j = 0; j < kJoin; ++j) {
       decay[j] = __builtin_amdgcn_exp2f(A2 * now.sum[j]);
       own = step(j, own);
-      all *= decay[j];
+      sums += now.sum[j];
       apart |= now.flags[j];
     }
     Piece* const p = pieces[turn];
-    p[w].decay[lane] = all;
+    // Of the sum and not a product: with steps of either sign one chunk's decay
+    // may be 0 and the next one's infinite, whose product is no number.
+    p[w].decay[lane] = __builtin_amdgcn_exp2f(A2 * sums);
     p[w].own[lane] = own;
     if (lane == 0) p[w].apart = apart;
     __syncthreads();
