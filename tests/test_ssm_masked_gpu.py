@@ -135,3 +135,26 @@ def test_states_that_vanish_and_decays_past_the_range(vdc, S, at):
     ref = R.Scan(*_head(k), docs, k["D"], softplus_on=False)
     y = vdc.selective_scan_fwd(*_head(k), cu, D=k["D"], dt_softplus=False)
     R.close("y", y, ref.y, ref.ey)
+
+
+@pytest.mark.parametrize("S", [100, 1200])
+@pytest.mark.parametrize("step", [False, True])
+def test_steps_of_a_bias_that_cancels(vdc, S, step):
+    """Step sizes near softplus(0) from a dt and a bias some hundred times as
+    large: with x = B = 1 a first token's state is the step size, in FP32."""
+    C = 64
+    m = Maker(441, DEV)
+    bias = -m.uniform(C, lo=2.0, hi=400.0)
+    raw = m.normal(S, C, std=8.0, dtype=F32).clamp(-40, 40)
+    dt = (raw - bias).to(BF)
+    one = torch.ones(S, 1, dtype=BF, device=DEV)
+    x = torch.ones(S, C, dtype=BF, device=DEV)
+    A = torch.full((C, 1), -1.0, device=DEV)
+    state = torch.zeros(S, C, 1, device=DEV)
+    if step:
+        vdc.selective_update(x, dt, A, one, one, state, dt_bias=bias)
+    else:
+        cu = torch.arange(S + 1, dtype=torch.int32, device=DEV)
+        vdc.selective_scan_fwd(x, dt, A, one, one, cu, dt_bias=bias, state=state)
+    want, rel = R.softplus(dt.double() + bias.double())
+    R.close("step size", state[:, :, 0], want, want * rel)

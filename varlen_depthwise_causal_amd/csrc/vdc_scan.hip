@@ -62,17 +62,13 @@ __device__ __forceinline__ int32_t first_at_least(const int32_t* cu, int32_t n, 
   return __builtin_amdgcn_readfirstlane((int32_t)lo);
 }
 
-// The bias of a channel's step size, and times log2(e).
-struct StepBias {
-  float b, b2;
-};
-__device__ __forceinline__ StepBias step_bias(const ScanArgs& a, int64_t c) {
-  const float b = a.bias ? param_at(a.bias, a.bias_bf16, c) : 0.0f;
-  return StepBias{b, b * kLog2E};
+// The bias of a channel's step size.
+__device__ __forceinline__ float step_bias(const ScanArgs& a, int64_t c) {
+  return a.bias ? param_at(a.bias, a.bias_bf16, c) : 0.0f;
 }
-__device__ __forceinline__ float step_size(const ScanArgs& a, float dt, const StepBias& b) {
-  const float s = softplus_f32(dt, b.b, b.b2);
-  return a.softplus ? s : dt + b.b;
+__device__ __forceinline__ float step_size(const ScanArgs& a, float dt, float bias) {
+  const float v = dt + bias, s = softplus_f32(v);
+  return a.softplus ? s : v;
 }
 
 // One BF16 row of activations after another, addressed by a buffer resource
@@ -258,7 +254,7 @@ void scan_fwd_kernel(ScanArgs a, int32_t work) {
   float A2[NT], h[NT];
   load_decay<NT>(a, l, A2);
   const float Dc = a.D ? param_at(a.D, a.D_bf16, l.c) : 0.0f;
-  const StepBias bias = step_bias(a, l.c);
+  const float bias = step_bias(a, l.c);
   const bool gated = kOut && a.z != nullptr;
   float sum = 0.0f;
   int32_t flags = 0;
@@ -581,7 +577,7 @@ void scan_bwd_local_kernel(ScanArgs a, int32_t work) {
     h[n] = 0.0f, mu[n] = 0.0f, p[n] = 1.0f;
     A2[n] = l.active ? A2[n] : 0.0f;
   }
-  const StepBias bias = l.active ? step_bias(a, l.c) : StepBias{0.0f, 0.0f};
+  const float bias = l.active ? step_bias(a, l.c) : 0.0f;
   const bool gated = a.z != nullptr;
   float sum = 0.0f;
 
@@ -899,8 +895,8 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
   const bool active = i0 + RC * set + mine < a.per;
   const uint32_t c = (uint32_t)(g * a.per + (active ? i0 + RC * set + mine : 0));
   const float Dc = active && a.D ? param_at(a.D, a.D_bf16, c) : 0.0f;
-  StepBias bias = step_bias(a, c);
-  if (!active) bias = StepBias{0.0f, 0.0f};
+  float bias = step_bias(a, c);
+  if (!active) bias = 0.0f;
   const uint32_t col = (uint32_t)(g * a.wpg * 64 + i0 + RC * set);
   const int32_t n0 = RN * part;
 
@@ -1204,7 +1200,7 @@ void scan_bwd_main_kernel(ScanArgs a, int32_t work) {
         reset_if((starts >> at) & 1u, mu);
         const float slb = set_sum<P, RC>(lb, odd), sva = set_sum<P, RC>(va, odd) * kLn2;
         float ddt = __builtin_fmaf(x, slb, sva);
-        if (a.softplus) ddt *= sigmoid_f32(bf16_lo(v[i].dt) + bias.b);
+        if (a.softplus) ddt *= sigmoid_f32(bf16_lo(v[i].dt) + bias);
         dD = __builtin_fmaf(gy, x, dD);
         dbias += real ? ddt : 0.0f;
         put(ox, tok, __builtin_fmaf(Dc, gy, own[i] * slb));
@@ -1353,7 +1349,7 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs a, int32_t rows
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     A2[j] = n0 + j < a.N ? param_at(a.A, a.A_bf16, (int64_t)c * a.N + n0 + j) * kLog2E : 0.0f;
-  const StepBias bias = step_bias(a, c);
+  const float bias = step_bias(a, c);
   const float Dc = a.D ? param_at(a.D, a.D_bf16, c) : 0.0f;
   const uint32_t bc0 = c / (uint32_t)a.per * (uint32_t)a.N + n0;
   const uint32_t h0 = c * (uint32_t)a.N + n0;
@@ -1490,7 +1486,7 @@ __global__ __launch_bounds__(64 * kShortWaves) void scan_short_kernel(ScanArgs a
     A2[j] = n0 + j < a.N ? param_at(a.A, a.A_bf16, (int64_t)c * a.N + n0 + j) * kLog2E : 0.0f;
     h[j] = 0.0f;
   }
-  const StepBias bias = step_bias(a, c);
+  const float bias = step_bias(a, c);
   const float Dc = a.D ? param_at(a.D, a.D_bf16, c) : 0.0f;
   const uint32_t bc0 = c / (uint32_t)a.per * (uint32_t)a.N + (some ? n0 : 0);
   const uint32_t h0 = c * (uint32_t)a.N + n0;

@@ -47,19 +47,20 @@ __device__ __forceinline__ float dsilu_f32(float z, float s) {
   return s * __builtin_fmaf(z, 1.0f - s, 1.0f);
 }
 
-// log(1 + exp(v)), v = (p + q) with q2 = q log2(e) at hand, with a small
-// relative error on all of its range: the result is a step size, which may be
-// many orders below 1.  With e = exp(-|v|) <= 1 and s = e / (2 + e) <= 1/3,
+// log(1 + exp(v)) with a small relative error on all of its range: the result
+// is a step size, which may be many orders below 1.  With e = exp(-|v|) <= 1 and
+// s = e / (2 + e) <= 1/3,
 //
 //   log1p(e) = 2 atanh(s) = s P(s^2),
 //
 // P the polynomial of degree 4 nearest to 2 atanh(s) / s in relative error
-// (8e-9).  The exponent v log2(e) is rounded once more than v itself, at most
-// |v| 2^-24 of e.  A step of -inf has the size 0: e is 0 then, and so is
-// max(v, 0).  That maximum drops a NaN, which s brings back.
-__device__ __forceinline__ float softplus_f32(float p, float q, float q2) {
-  const float v = p + q;
-  const float e = __builtin_amdgcn_exp2f(-__builtin_fabsf(__builtin_fmaf(p, kLog2E, q2)));
+// (8e-9).  The exponent v log2(e) is rounded once, with a constant that is
+// rounded too: at most 1.23 |v| 2^-24 of e.  It is taken from v, the sum of an
+// input and its bias, and not from the two of them, whose own roundings do not
+// get smaller where they cancel.  A step of -inf has the size 0: e is 0 then, and
+// so is max(v, 0).  That maximum drops a NaN, which s brings back.
+__device__ __forceinline__ float softplus_f32(float v) {
+  const float e = __builtin_amdgcn_exp2f(-__builtin_fabsf(v * kLog2E));
   const float s = e * __builtin_amdgcn_rcpf(2.0f + e);
   const float u = s * s;
   float r = 0.28178334f;
