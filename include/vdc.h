@@ -254,6 +254,20 @@ uint64_t conv1d_launch_count(void);
  * NULL: sequence i has slot i); a sequence whose index lies outside
  * [0, slots) has no slot, and two sequences of one call must not share one
  * (unspecified results).
+ *
+ * Beside the limits of each argument, sizes whose launches would need 2^32
+ * lanes are refused (VDC_EINVAL).  With M = N rounded up to 8, 16, 32 or 64:
+ *
+ *   conv1d_prefill      num_docs * ceil(C / 512) from 2^26 on
+ *   conv1d_update       rows * ceil(C / 512) from 2^26 on
+ *   selective_update    S * ceil(C * M / 256) from 2^26 on
+ *   selective_scan_*    K * groups * ceil(C / groups / w) from 2^26 on: K chunks
+ *                       of up to 2048 tokens (2^28 / C where that is less) by
+ *                       w = 64 channels (backward 32 for M = 32, 16 for M = 64)
+ *   selective_scan_bwd  S * groups * M from 2^33 on
+ *
+ * and selective_scan_* where a row of states, groups * ceil(C / groups / 64)
+ * * 64 * M of them, has 2^31 bytes.
  * ------------------------------------------------------------------------ */
 
 /*

@@ -21,6 +21,7 @@
 // Everything between documents is assigned, never multiplied by zero, so
 // that an infinity or a NaN stays in its document.
 
+#include <algorithm>
 #include <cfloat>
 #include <type_traits>
 
@@ -136,17 +137,19 @@ struct Uniform {
   }
 };
 
-// B's and C's rows, one after another, with NT states a group: a lane has two.
+// B's and C's rows, one after another, with NT states a group: a lane has two,
+// and of very long rows more in turn (a launch has less than 2^32 lanes).
+constexpr int64_t kPadBlocks = int64_t(1) << 22;
 __global__ __launch_bounds__(256) void scan_pad_kernel(ScanArgs a, int32_t NT) {
   const int64_t each = (int64_t)a.S * a.G * (NT / 2);
-  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (e >= 2 * each) return;
-  const bool is_c = e >= each;
-  const int64_t q = is_c ? e - each : e, row = q / (NT / 2), t = row / a.G;
-  const int32_t n = (int32_t)(q - row * (NT / 2)) * 2;
-  const uint16_t* p = (is_c ? a.Cm + t * a.Cs : a.B + t * a.Bs) + (row - t * a.G) * a.N;
-  const uint32_t lo = n < a.N ? p[n] : 0u, hi = n + 1 < a.N ? p[n + 1] : 0u;
-  a.pad[e] = lo | hi << 16;
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < 2 * each; e += kPadBlocks * 256) {
+    const bool is_c = e >= each;
+    const int64_t q = is_c ? e - each : e, row = q / (NT / 2), t = row / a.G;
+    const int32_t n = (int32_t)(q - row * (NT / 2)) * 2;
+    const uint16_t* p = (is_c ? a.Cm + t * a.Cs : a.B + t * a.Bs) + (row - t * a.G) * a.N;
+    const uint32_t lo = n < a.N ? p[n] : 0u, hi = n + 1 < a.N ? p[n + 1] : 0u;
+    a.pad[e] = lo | hi << 16;
+  }
 }
 
 // ---------------------------------------------- forward, lane = channel --
@@ -1734,7 +1737,8 @@ bool scan_rows_fit(const ScanArgs& a) {
 hipError_t launch_scan_pad(ScanArgs* a, hipStream_t s) {
   const int32_t NT = scan_states(a->N);
   const int64_t each = (int64_t)a->S * a->G * (NT / 2);
-  hipLaunchKernelGGL(scan_pad_kernel, dim3((uint32_t)((2 * each + 255) / 256)), dim3(256), 0, s, *a, NT);
+  const int64_t blocks = std::min((2 * each + 255) / 256, kPadBlocks);
+  hipLaunchKernelGGL(scan_pad_kernel, dim3((uint32_t)blocks), dim3(256), 0, s, *a, NT);
   a->B = reinterpret_cast<const uint16_t*>(a->pad);
   a->Cm = reinterpret_cast<const uint16_t*>(a->pad + each);
   a->Bs = a->Cs = (int64_t)a->G * NT;

@@ -212,7 +212,6 @@ bool scan_plan(int dir, int64_t S, int64_t C, int64_t N, int64_t G, ScanPlan* ou
   if (out->brief) chunk = scan_short(N);
   const int64_t chunks = std::max<int64_t>(1, ceil_div(S, chunk));
   if (chunk > INT32_MAX || (chunks * std::max(blocks, waves) + 64) * 64 > kMaxThreads) return false;
-  if (!out->brief && ceil_div(S * G * scan_states(N), 256) * 256 > kMaxThreads) return false;
   const int64_t params = ceil_div(waves * 64, 256) * (N + 2);
   if (dir == VDC_BWD && (G * ceil_div(S * scan_states(N) / 2, 256) + params) * 256 > kMaxThreads) return false;
   out->wpg = (int32_t)wpg;
