@@ -260,7 +260,8 @@ uint64_t conv1d_launch_count(void);
  *
  *   conv1d_prefill      num_docs * ceil(C / 512) from 2^26 on
  *   conv1d_update       rows * ceil(C / 512) from 2^26 on
- *   selective_update    S * ceil(C * M / 256) from 2^26 on
+ *   selective_update    S * ceil(C / 64) from 2^30 on for N <= 4, S * C * M
+ *                       from 2^38 on for more states
  *   selective_scan_*    K * groups * ceil(C / groups / w) from 2^26 on: K chunks
  *                       of up to 2048 tokens (2^28 / C where that is less) by
  *                       w = 64 channels (backward 32 for M = 32, 16 for M = 64)

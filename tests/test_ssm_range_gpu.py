@@ -1,5 +1,5 @@
 """The state space layer's operators at sizes past 2^32 threads of a lane a
-value: long packed rows with many states."""
+value: long packed rows with many states, and many rows of single tokens."""
 import pytest
 import torch
 
@@ -44,3 +44,24 @@ def test_scan_fwd_of_a_row_past_2_28_tokens(vdc, N):
         ref = R.Scan(x[t], dt[t], k["A"], B[t], Cm[t], docs, k["D"], z[t], k["dt_bias"])
         R.close("y", y[t], ref.y, ref.ey)
     assert bool(torch.isfinite(y).all())
+
+
+def test_update_of_rows_past_2_18(vdc):
+    """262147 rows of 4096 channels, three of them with a slot."""
+    rows, C, N = 2 ** 18 + 3, 4096, 16
+    real = [0, 2 ** 18 - 1, rows - 1]
+    k, _, _ = scan_inputs(611, [3], C, N, device=DEV)
+    state = Maker(612, DEV).normal(4, C, N, dtype=F32)
+    small = state[:3].clone()
+    index = torch.full((rows,), -1, dtype=torch.int32, device=DEV)
+    wide = {n: torch.zeros((rows,) + tuple(k[n].shape[1:]), dtype=BF, device=DEV) for n in ("x", "dt", "B", "C")}
+    for i, r in enumerate(real):
+        index[r] = i
+        for n in wide:
+            wide[n][r] = k[n][i]
+    y = vdc.selective_update(wide["x"], wide["dt"], k["A"], wide["B"], wide["C"], state, D=k["D"],
+                             dt_bias=k["dt_bias"], state_index=index)
+    want = vdc.selective_update(k["x"], k["dt"], k["A"], k["B"], k["C"], small, D=k["D"], dt_bias=k["dt_bias"])
+    assert torch.equal(y[real], want) and torch.equal(state[:3], small)
+    y[real] = 0
+    assert int(torch.count_nonzero(y)) == 0

@@ -1431,13 +1431,8 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs a, int32_t rows
 
 template <int NL>
 void step_nl(const ScanArgs& a, hipStream_t s) {
-  constexpr int kChannels = 64 / NL;
-  const int64_t cblocks = (a.C + kChannels - 1) / kChannels;
-  // Rows a wave takes: as many as leave eight waves a SIMD, at most 16.
-  int64_t rows = cblocks * a.S / 8192;
-  rows = rows < 1 ? 1 : rows > 16 ? 16 : rows;
-  const int64_t waves = cblocks * ((a.S + rows - 1) / rows);
-  const dim3 grid((uint32_t)((waves + 3) / 4)), block(256);
+  const int64_t rows = scan_step_rows(a.S, a.C, a.N);
+  const dim3 grid((uint32_t)(scan_step_threads(a.S, a.C, a.N) / 256)), block(256);
   const bool vec = a.N % 4 == 0 && reinterpret_cast<uintptr_t>(a.state) % 16 == 0;
   if (a.z) {
     if (vec) hipLaunchKernelGGL((scan_step_kernel<NL, true, true>), grid, block, 0, s, a, (int32_t)rows);
@@ -1795,11 +1790,13 @@ hipError_t launch_scan_short(const ScanArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_scan_step(const ScanArgs& a, hipStream_t s) {
-  if (a.N <= 4) step_nl<1>(a, s);
-  else if (a.N <= 8) step_nl<2>(a, s);
-  else if (a.N <= 16) step_nl<4>(a, s);
-  else if (a.N <= 32) step_nl<8>(a, s);
-  else step_nl<16>(a, s);
+  switch (scan_step_lanes(a.N)) {
+    case 1: step_nl<1>(a, s); break;
+    case 2: step_nl<2>(a, s); break;
+    case 4: step_nl<4>(a, s); break;
+    case 8: step_nl<8>(a, s); break;
+    default: step_nl<16>(a, s); break;
+  }
   return hipGetLastError();
 }
 

@@ -90,6 +90,19 @@ inline int scan_bwd_channels(int64_t N) {
   return nt <= 16 ? 64 : nt == 32 ? 32 : 16;
 }
 
+// Single tokens: lanes that hold a channel's states, four each, and the rows that
+// a wave takes one after another, as many as leave eight waves a SIMD, at most 16.
+inline int scan_step_lanes(int64_t N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
+inline int64_t scan_step_blocks(int64_t C, int64_t N) { return (C * scan_step_lanes(N) + 63) / 64; }
+inline int64_t scan_step_rows(int64_t S, int64_t C, int64_t N) {
+  const int64_t rows = scan_step_blocks(C, N) * S / 8192;
+  return rows < 1 ? 1 : rows > 16 ? 16 : rows;
+}
+inline int64_t scan_step_threads(int64_t S, int64_t C, int64_t N) {
+  const int64_t rows = scan_step_rows(S, C, N), waves = scan_step_blocks(C, N) * ((S + rows - 1) / rows);
+  return (waves + 3) / 4 * 256;
+}
+
 // Whether the forward and the backward's first pass can read B's and C's rows as
 // they are; launch_scan_pad copies them to the workspace and points `a` there.
 bool scan_rows_fit(const ScanArgs& a);

@@ -452,7 +452,7 @@ extern "C" int selective_update(const vdc_scan* v, void* y, hipStream_t stream) 
   if (!y || (!v->state && v->slots > 0)) return VDC_EINVAL;
   if (!v->state_index && v->S > v->slots) return VDC_EINVAL;
   if (!aligned(y, 2)) return VDC_EALIGN;
-  if (v->S * ceil_div(v->C * scan_states(v->N) / 4, 64) * 64 > kMaxThreads) return VDC_EINVAL;
+  if (scan_step_threads(v->S, v->C, v->N) > kMaxThreads) return VDC_EINVAL;
   const Span out{y, (size_t)v->S * v->C * 2}, st = state_span(v);
   if (hits_input(v, out, false) || hits_input(v, st, false) || overlaps(out, st)) return VDC_EINVAL;
   a.y = static_cast<uint16_t*>(y);
