@@ -318,7 +318,8 @@ int conv1d_update(const void *x, int64_t x_stride, const void *weight, int w_dty
  *   y[t,c]   = (sum_n Cm[t,group,n] h[t,c,n] + D[c] x[t,c]) silu(z[t,c])
  *
  * in FP32, y rounded to bf16 once.  h before a document's first token is
- * zero, or its slot's state where the document resumes.
+ * zero, or its slot's state where the document resumes.  softplus(-inf) is
+ * 0: with dt or dt_bias at -inf a token leaves the state as it is.
  */
 typedef struct vdc_scan {
     int64_t S;        /* tokens, at most 2^31 - 4096; for selective_update

@@ -208,10 +208,10 @@ __global__ __launch_bounds__(L > 64 ? L : 256) void norm_bwd_kernel(NormArgs a, 
   __shared__ float sums[P::kWide ? 1 : 3][P::kWide ? 1 : 2 * K * 8][64];
   const P p(a, rows);
   const float inv = 1.0f / (float)a.per;
-  // Eight waves a workgroup, two a SIMD, have no registers for the next token
-  // (and with a gate some 30 too few even so, which go to scratch memory: 400 us
-  // for 4096 tokens of one group of 16384 channels, against 3360 by going over
-  // each row three times).
+  // Eight waves a workgroup, two a SIMD, have no registers for the next token.
+  // Even so some go to scratch memory: 32 with a gate on aligned rows, on others
+  // 79 with one and 31 without.  4096 tokens of one group of 16384 channels with
+  // a gate, aligned: 400 us, against 3360 by going over each row three times.
   constexpr bool kAhead = L <= 256;
   Affine<K> f;
   f.load(a, p);

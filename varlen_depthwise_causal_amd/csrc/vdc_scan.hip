@@ -236,8 +236,8 @@ __device__ __forceinline__ int32_t here_uniform(int32_t v) {
 // outputs, from the joined states.  A lane has a channel with all its states, so
 // that the step size, the gate and the sum over states cost no other lane
 // anything, and B and C come from scalar registers, free of VALU instructions.
-// 16384 tokens, C = 4096, 16 states: 188 us without the outputs and 252 with
-// them, VALU busy 94 and 92% of the time; HBM moves 0.34 GB in the second.
+// 16384 tokens, C = 4096, 16 states: 187 us without the outputs and 251 with
+// them, VALU busy 93 and 91% of the time; HBM moves 0.55 GB in the second.
 template <int NT, bool kOut>
 __global__ __launch_bounds__(64 * kWaves)
 __attribute__((amdgpu_waves_per_eu(NT <= 16 ? 4 : NT == 32 ? 2 : 1)))
@@ -559,7 +559,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void scan_join_kernel(ScanArgs a) 
 // Forward over a chunk from zero history.  With p the decay since the chunk's
 // start, the gradient that leaves to the left is sum_t p[t] C[t] g[t] over the
 // tokens of the chunk's first document.  16384 tokens, C = 4096, 16 states: 336
-// us, VALU busy 87% of the time; it writes 0.59 GB, the kept states, meanwhile.
+// us, VALU busy 86% of the time; it writes 0.59 GB, the kept states, meanwhile.
 template <int NT>
 __global__ __launch_bounds__(64 * kWaves)
 __attribute__((amdgpu_waves_per_eu(NT <= 16 ? 4 : NT == 32 ? 2 : 1)))
@@ -860,7 +860,7 @@ __device__ __forceinline__ void zero_if(uint32_t bit, float& a, float& b, float&
 // States kept every 8 tokens are 1/8 of all of them: 0.55 GB written and read at
 // 16384 tokens, C = 4096, 16 states, behind the arithmetic.  Kept every 2 they
 // would save the first of the two ways forward, 14% of this kernel, and move 2.1
-// GB each way, which takes as long.  That size takes 926 us: 424 VALU instructions
+// GB each way, which takes as long.  That size takes 936 us: 424 VALU instructions
 // a token and 64 channels, of which the formulas above are 240, VALU busy 88% of
 // the time.
 //

@@ -257,7 +257,8 @@ def selective_scan_fwd(x, dt, A, B, C, cu_seqlens, *, D=None, z=None, dt_bias=No
 
     x, dt, z: BF16 [S, C]; B, C: BF16 [S, groups, N] or [S, N]; A: [C, N], D and
     dt_bias: [C], each FP32 or BF16.  The step size is softplus(dt + dt_bias),
-    or their sum without dt_softplus; y is gated by silu(z) where z is given.
+    0 at -inf (a masked token), or their sum without dt_softplus; y is gated by
+    silu(z) where z is given.
     state: FP32 [slots, C, N], where every document leaves its last state;
     state_index and resume as in conv1d_prefill."""
     a, S, width, N, groups, dev, xs = _scan_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, cu_seqlens,
