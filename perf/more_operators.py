@@ -335,8 +335,8 @@ def _plain_park(s):
     v[:, :E] = state[leave].float().reshape(n, E)
     v = v.view(n, blocks, BLOCK)
     e4m3 = s["codes"].dtype == torch.float8_e4m3fn
-    scale = v.abs().amax(-1) / (448.0 if e4m3 else 127.0)
-    # quotients next to the border of two codes
+    # rounded once, and quotients next to the border of two codes
+    scale = (v.abs().amax(-1).double() / (448.0 if e4m3 else 127.0)).float()
     t = v.double() / torch.where(scale > 0, scale, torch.ones_like(scale)).double()[..., None]
     if e4m3:
         # three bits after the first one, none of them below 2^-9
