@@ -335,8 +335,10 @@ def _plain_park(s):
     v[:, :E] = state[leave].float().reshape(n, E)
     v = v.view(n, blocks, BLOCK)
     e4m3 = s["codes"].dtype == torch.float8_e4m3fn
-    # rounded once, and quotients next to the border of two codes
-    scale = (v.abs().amax(-1).double() / (448.0 if e4m3 else 127.0)).float()
+    # rounded once, and quotients next to the border of two codes; a block with
+    # nothing of 2^-64 or more is zeros
+    most = v.abs().amax(-1)
+    scale = torch.where(most < 2.0 ** -64, 0.0, (most.double() / (448.0 if e4m3 else 127.0)).float())
     t = v.double() / torch.where(scale > 0, scale, torch.ones_like(scale)).double()[..., None]
     if e4m3:
         # three bits after the first one, none of them below 2^-9
@@ -453,10 +455,11 @@ def _exact_park(s):
             n = (part.numel() + BLOCK - 1) // BLOCK
             v = torch.cat([part, part.new_zeros(n * BLOCK - part.numel())]).view(n, BLOCK)
             one = (v.abs().amax(1) / codes[-1]).float().double()       # a scale is held in 32 bits
+            one[v.abs().amax(1) < 2.0 ** -64] = 0
             t = v.abs() / torch.where(one > 0, one, torch.ones_like(one))[:, None]
             k = torch.searchsorted(middle, t)                          # middles below t
             tie = (t == middle[k.clamp(max=middle.numel() - 1)]) & (k % 2 == 1)
-            q = codes[k + tie] * torch.sign(v)
+            q = codes[k + tie] * torch.sign(v) * (one > 0)[:, None]
             back[lo:lo + part.numel()] = (q * one[:, None]).view(-1)[:part.numel()]
             scales[p, lo // BLOCK:lo // BLOCK + n] = one
         state[b] = back.view(state.shape[1:])
