@@ -1,9 +1,11 @@
 /*
  * vdc.h - packed variable-length width-4 depthwise causal convolution
  * followed by SiLU, training forward and backward, on AMD Instinct MI355X
- * (gfx950), and the operators of the state space layer around it: the
+ * (gfx950), the operators of the state space layer around it: the
  * convolution with a carried state, the selective scan and the gated group
- * norm (second half of this file).  C ABI of libvdc.so.
+ * norm (second half of this file), and those of a recurrent layer: the gated
+ * linear recurrence, the layer norm on a residual stream and carried states
+ * put aside in 8 bits (its end).  C ABI of libvdc.so.
  *
  * The convolution is the one documented on the pages of
  * flashinfer.cake_causal_conv1d_train:
@@ -419,6 +421,161 @@ int group_norm_silu_bwd(const void *x, int64_t x_stride, const void *weight, int
                         int64_t S, int64_t C, int64_t groups, float eps,
                         void *dx, void *dweight, void *dbias, void *dz,
                         void *workspace, size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * A recurrent layer around the convolution.
+ *
+ * The rules of the state space layer hold here too: row strides, dense
+ * outputs, caches updated in place, sequences without a slot, and sizes whose
+ * launches would need 2^32 lanes refused (VDC_EINVAL):
+ *
+ *   gated_recurrence_*  ceil(S / 64) * ceil(C / 128) from 2^23 on
+ *   layer_norm_*        never
+ *   state_quantize, state_dequantize
+ *                       rows * ceil(E / 4096) from 2^24 on
+ * ------------------------------------------------------------------------ */
+
+/*
+ * The gated linear recurrence.  For token t and channel c, with
+ * u = 2 scale softplus(decay[c]) sigmoid(r[t,c]):
+ *
+ *   a[t,c] = exp(-u / 2),   m[t,c] = sqrt(1 - exp(-u))
+ *   h[t,c] = a[t,c] h[t-1,c] + m[t,c] sigmoid(i[t,c]) x[t,c]
+ *   y[t,c] = h[t,c] silu(z[t,c]),  or h[t,c] without a gate z
+ *
+ * in FP32, y rounded to bf16 once.  h before a document's first token is
+ * zero, or its slot's state where the document resumes.  A token with u = 0
+ * (r of -inf or the lowest finite number: a masked token) leaves the state
+ * exactly as it is, whatever x and i hold.
+ */
+typedef struct vdc_recurrence {
+    int64_t S;        /* tokens, at most 2^31 - 4096; for
+                         gated_recurrence_update rows, one token each        */
+    int64_t C;        /* channels, 1 .. 2^20                                 */
+    const void *x;    /* bf16 [S][C]                                         */
+    const void *r;    /* bf16 [S][C], the decay's gate                       */
+    const void *i;    /* bf16 [S][C], the input's gate                       */
+    const void *z;    /* bf16 [S][C], or NULL: no gate at the output         */
+    int64_t x_stride, r_stride, i_stride, z_stride; /* C .. 2^31             */
+    const void *decay; /* [C]                                                */
+    int decay_dtype;
+    float scale;      /* at least 0, finite                                  */
+    const int32_t *cu_seqlens; /* int32 [num_docs + 1]; unused by gated_recurrence_update */
+    int64_t num_docs;
+    float *state;     /* FP32 [slots][C], in place; forward: or NULL         */
+    int64_t slots;
+    const int32_t *state_index; /* one per document (row), or NULL           */
+    const uint8_t *resume;      /* per document, or NULL: none resumes       */
+} vdc_recurrence;
+
+/* gated_recurrence_keep_rows - rows of the states a training forward keeps
+ * for its backward, one for every 64 tokens; 0 for invalid S. */
+int64_t gated_recurrence_keep_rows(int64_t S);
+
+/* gated_recurrence_workspace_bytes - workspace of gated_recurrence_fwd
+ * (VDC_FWD) or gated_recurrence_bwd (VDC_BWD); 0 for invalid sizes, and for
+ * the forward of short rows.  Its contents need not start at zero. */
+size_t gated_recurrence_workspace_bytes(int direction, int64_t S, int64_t C);
+
+/*
+ * gated_recurrence_fwd - prompts, and the training forward.
+ *
+ * y bf16 [S][C].  keep FP32 [gated_recurrence_keep_rows(S)][C] or NULL:
+ * receives the states that gated_recurrence_bwd starts from; it takes no
+ * state beside it (VDC_EINVAL).  With a state, every document leaves the state
+ * after its last token in its slot; an empty one leaves zeros, or its slot as
+ * it is where it resumes.  Activations are 2-byte aligned, decay by its dtype,
+ * state and keep 4-byte, the workspace 16-byte.
+ */
+int gated_recurrence_fwd(const vdc_recurrence *args, void *y, float *keep,
+                         void *workspace, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * gated_recurrence_bwd - gradients of the training forward (every document
+ * from zero history; args->state must be NULL), from its inputs and what it
+ * kept.
+ *
+ * dy             bf16 [S][C], dy_stride elements between rows.
+ * keep           what gated_recurrence_fwd left of the same arguments.
+ * dx, dr, di, dz bf16 [S][C] outputs; dz NULL exactly where z is.
+ * ddecay         [C] output of decay's dtype.
+ * Sums are taken in an order that depends on the sizes only: results are
+ * bitwise reproducible.  S == 0 sets ddecay to zero.
+ */
+int gated_recurrence_bwd(const vdc_recurrence *args, const void *dy, int64_t dy_stride,
+                         const float *keep, void *dx, void *dr, void *di, void *ddecay,
+                         void *dz, void *workspace, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * gated_recurrence_update - one token of each of args->S sequences: the
+ * state of its slot is read and replaced.  A row without a slot is padding:
+ * its y is zero, nothing else is touched.  args->state is required.
+ */
+int gated_recurrence_update(const vdc_recurrence *args, void *y, hipStream_t stream);
+
+/*
+ * layer_norm_fwd - the norm of each token's channels, on a residual stream:
+ *
+ *   s = bf16(x + residual),  or x without a residual
+ *   y = bf16(weight (s - mean) / sqrt(var + eps) + bias),  var the biased variance
+ *
+ * x, residual bf16 [S][C] with row strides, C at most 16384; y bf16 [S][C];
+ * stream_out bf16 [S][C], the sum s; NULL exactly where residual is.  2-byte
+ * aligned.  weight, bias [C] of their dtypes; bias may be NULL.  eps >= 0.
+ */
+int layer_norm_fwd(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
+                   const void *weight, int w_dtype, const void *bias, int b_dtype,
+                   int64_t S, int64_t C, float eps, void *y, void *stream_out,
+                   hipStream_t stream);
+
+/* layer_norm_workspace_bytes - workspace of layer_norm_bwd. */
+size_t layer_norm_workspace_bytes(int64_t S, int64_t C);
+
+/*
+ * layer_norm_bwd - its gradients.  s is what was normalised (x, or the sum);
+ * dstream bf16 [S][C] or NULL is the gradient that reaches the sum from
+ * behind, past the norm, and is added to dx before its one rounding.  dx is
+ * the gradient of x and of the residual alike.  dweight [C] of weight's
+ * dtype; dbias [C] of dtype b_dtype, or NULL.  Reproducible; S == 0 sets
+ * dweight and dbias to zero.
+ */
+int layer_norm_bwd(const void *s, int64_t s_stride, const void *weight, int w_dtype,
+                   const void *dy, int64_t dy_stride, const void *dstream, int64_t dstream_stride,
+                   int64_t S, int64_t C, float eps, void *dx, void *dweight, void *dbias,
+                   int b_dtype, void *workspace, size_t ws_bytes, hipStream_t stream);
+
+/* Codes of a state put aside. */
+enum vdc_code {
+    VDC_INT8 = 0, /* -127 .. 127                                           */
+    VDC_E4M3 = 1  /* 8-bit floating point, largest value 448               */
+};
+
+/*
+ * state_quantize - carried states put aside: `rows` states leave a cache
+ * for a pool of codes, 8 bits a value and an FP32 scale for every 64 values.
+ *
+ * state   [slots][E] of dtype VDC_F32 or VDC_BF16: a cache of any of the
+ *         operators above, each state as E values in a row, E at most 2^28.
+ * codes   [pool][E] bytes; scales FP32 [pool][ceil(E / 64)].
+ * state_index, pool_index: int32 [rows] or NULL (row i has slot or place i).
+ *         A row whose slot or place lies outside its cache is left out.  No
+ *         place may be named twice (unspecified results).
+ *
+ * For each block of 64 values (the last may be shorter), with L = 127 or 448:
+ *   scale = fp32(max |v| / L),   code = the code nearest to v / scale, ties to
+ * the even one.  A block without a magnitude of 2^-64 or more has the scale 0
+ * and codes of 0, one with an infinity or a NaN the scale NaN and codes of 0.
+ * state, codes and scales are aligned to their elements.
+ */
+int state_quantize(const void *state, int dtype, int64_t slots, int64_t E,
+                   const int32_t *state_index, void *codes, int code, float *scales,
+                   int64_t pool, const int32_t *pool_index, int64_t rows, hipStream_t stream);
+
+/* state_dequantize - taken back: state = code * scale in FP32, rounded to the
+ * cache's dtype.  No slot may be named twice; rows left out as above. */
+int state_dequantize(const void *codes, int code, const float *scales, int64_t pool,
+                     const int32_t *pool_index, void *state, int dtype, int64_t slots, int64_t E,
+                     const int32_t *state_index, int64_t rows, hipStream_t stream);
 
 #ifdef __cplusplus
 }

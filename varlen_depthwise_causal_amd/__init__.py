@@ -11,8 +11,9 @@ dy are BF16 [S, C] or [1, S, C]; weight FP32 or BF16 [C, 4]; bias FP32 or BF16
 [C]; cu_seqlens int32 [num_docs + 1] on the device.
 
 The state space layer around the convolution (the convolution with a carried
-state, the selective scan, the gated group norm) is in module ssm; its calls
-are exported here too.
+state, the selective scan, the gated group norm) is in module ssm, a recurrent
+layer (the gated linear recurrence, the layer norm on a residual stream, carried
+states put aside in 8 bits) in module layer; their calls are exported here too.
 """
 from __future__ import annotations
 
@@ -34,17 +35,21 @@ __all__ = ["conv1d_fwd", "conv1d_bwd", "conv1d_bwd_noalloc", "workspace_bytes",
            "noalloc_scratch_bytes", "conv1d_plan", "conv1d_launch_count", "VdcError",
            "conv1d_prefill", "conv1d_update", "selective_scan_fwd", "selective_scan_bwd",
            "selective_scan_workspace_bytes", "selective_update", "group_norm_silu_fwd",
-           "group_norm_silu_bwd", "group_norm_silu_workspace_bytes"]
+           "group_norm_silu_bwd", "group_norm_silu_workspace_bytes", "gated_recurrence_fwd",
+           "gated_recurrence_bwd", "gated_recurrence_keep_rows", "gated_recurrence_workspace_bytes",
+           "gated_recurrence_update", "layer_norm_fwd", "layer_norm_bwd", "layer_norm_workspace_bytes",
+           "state_quantize", "state_dequantize"]
 
 _POLICIES = {"bf16": VDC_SILU_GRAD_BF16, "fp32": VDC_SILU_GRAD_FP32}
 
 
 def __getattr__(name):
-    # The state space layer's calls (module ssm) import torch; the rest of
-    # the package does so only when called.
+    # The state space layer's calls (module ssm) and the recurrent layer's
+    # (module layer) import torch; the rest of the package does so only when
+    # called.
     if name in __all__:
-        from . import ssm
-        globals()[name] = value = getattr(ssm, name)
+        from . import layer, ssm
+        globals()[name] = value = getattr(layer if name in layer.__all__ else ssm, name)
         return value
     raise AttributeError("module %r has no attribute %r" % (__name__, name))
 

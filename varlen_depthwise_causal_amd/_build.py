@@ -20,8 +20,8 @@ DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
                 "-ffp-contract=off"]
 COMMON = ["-O3", "-std=c++17", "-fPIC", "--offload-arch=" + ARCH, "-I", INCLUDE, "-I", CSRC]
 
-SOURCES = ("vdc_kernels.hip", "vdc_conv_state.hip", "vdc_scan.hip", "vdc_norm.hip", "vdc_api.cpp",
-           "vdc_ssm_api.cpp")
+SOURCES = ("vdc_kernels.hip", "vdc_conv_state.hip", "vdc_scan.hip", "vdc_norm.hip", "vdc_recurrence.hip",
+           "vdc_layer_norm.hip", "vdc_pool.hip", "vdc_api.cpp", "vdc_ssm_api.cpp", "vdc_layer_api.cpp")
 
 
 def hipcc() -> str:

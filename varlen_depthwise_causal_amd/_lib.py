@@ -10,6 +10,7 @@ from ._build import LIBRARY
 VDC_F32, VDC_BF16 = 0, 1
 VDC_SILU_GRAD_BF16, VDC_SILU_GRAD_FP32 = 0, 1
 VDC_FWD, VDC_BWD = 0, 1
+VDC_INT8, VDC_E4M3 = 0, 1
 (VDC_OK, VDC_EINVAL, VDC_EDTYPE, VDC_EALIGN, VDC_EWORKSPACE, VDC_ENOBIAS, VDC_EHIP,
  VDC_ESCRATCH) = range(8)
 STATUS = {VDC_OK: "VDC_OK", VDC_EINVAL: "VDC_EINVAL", VDC_EDTYPE: "VDC_EDTYPE",
@@ -28,6 +29,18 @@ class VdcScan(ctypes.Structure):
                 + [(n, ctypes.c_void_p) for n in ("A", "D", "dt_bias")]
                 + [(n, ctypes.c_int) for n in ("A_dtype", "D_dtype", "dt_bias_dtype", "dt_softplus")]
                 + [("cu_seqlens", ctypes.c_void_p), ("num_docs", ctypes.c_int64),
+                   ("state", ctypes.c_void_p), ("slots", ctypes.c_int64),
+                   ("state_index", ctypes.c_void_p), ("resume", ctypes.c_void_p)])
+
+
+class VdcRecurrence(ctypes.Structure):
+    """struct vdc_recurrence of include/vdc.h."""
+
+    _fields_ = ([(n, ctypes.c_int64) for n in ("S", "C")]
+                + [(n, ctypes.c_void_p) for n in ("x", "r", "i", "z")]
+                + [(n, ctypes.c_int64) for n in ("x_stride", "r_stride", "i_stride", "z_stride")]
+                + [("decay", ctypes.c_void_p), ("decay_dtype", ctypes.c_int), ("scale", ctypes.c_float),
+                   ("cu_seqlens", ctypes.c_void_p), ("num_docs", ctypes.c_int64),
                    ("state", ctypes.c_void_p), ("slots", ctypes.c_int64),
                    ("state_index", ctypes.c_void_p), ("resume", ctypes.c_void_p)])
 
@@ -75,7 +88,7 @@ def load(path: str | None = None):
         lib.conv1d_status_string.restype = ctypes.c_char_p
         lib.conv1d_plan.argtypes = [i32, i64, i64, i32, ctypes.POINTER(i64)]
         lib.conv1d_plan.restype = i32
-        # a VdcScan by reference, or its bytes
+        # a VdcScan or VdcRecurrence by reference, or its bytes
         scan, size_t, f32 = vp, ctypes.c_size_t, ctypes.c_float
         for name, restype, argtypes in (
                 ("conv1d_prefill", i32, [vp, vp, i32, vp, i32, vp, i64, i64, i64, vp, i64, vp, vp, vp,
@@ -89,7 +102,18 @@ def load(path: str | None = None):
                                               vp, vp]),
                 ("group_norm_silu_workspace_bytes", size_t, [i64, i64, i64]),
                 ("group_norm_silu_bwd", i32, [vp, i64, vp, i32, vp, i32, vp, i64, vp, i64, i64, i64,
-                                              i64, f32, vp, vp, vp, vp, vp, size_t, vp])):
+                                              i64, f32, vp, vp, vp, vp, vp, size_t, vp]),
+                ("gated_recurrence_keep_rows", i64, [i64]),
+                ("gated_recurrence_workspace_bytes", size_t, [i32, i64, i64]),
+                ("gated_recurrence_fwd", i32, [vp, vp, vp, vp, size_t, vp]),
+                ("gated_recurrence_bwd", i32, [vp, vp, i64] + [vp] * 7 + [size_t, vp]),
+                ("gated_recurrence_update", i32, [vp, vp, vp]),
+                ("layer_norm_fwd", i32, [vp, i64, vp, i64, vp, i32, vp, i32, i64, i64, f32, vp, vp, vp]),
+                ("layer_norm_workspace_bytes", size_t, [i64, i64]),
+                ("layer_norm_bwd", i32, [vp, i64, vp, i32, vp, i64, vp, i64, i64, i64, f32, vp, vp, vp, i32,
+                                         vp, size_t, vp]),
+                ("state_quantize", i32, [vp, i32, i64, i64, vp, vp, i32, vp, i64, vp, i64, vp]),
+                ("state_dequantize", i32, [vp, i32, vp, i64, vp, vp, i32, i64, i64, vp, i64, vp])):
             fn = getattr(lib, name)
             fn.restype, fn.argtypes = restype, argtypes
         lib.conv1d_launch_count.argtypes = []

@@ -11,7 +11,8 @@ Every step runs in libvdc.so's kernels through conv1d_fwd / conv1d_bwd.
 
 selective_scan and group_norm_silu wrap the other operators of a state space
 layer in the same way: the inputs alone are saved, their backward passes
-compute the rest again.
+compute the rest again.  So do gated_recurrence, which keeps one state in 64
+tokens beside them, and layer_norm, which saves what it normalised.
 """
 from __future__ import annotations
 
@@ -21,14 +22,19 @@ from torch.autograd.function import once_differentiable
 from . import (
     conv1d_bwd,
     conv1d_fwd,
+    gated_recurrence_bwd,
+    gated_recurrence_fwd,
     group_norm_silu_bwd,
     group_norm_silu_fwd,
+    layer_norm_bwd,
+    layer_norm_fwd,
     selective_scan_bwd,
     selective_scan_fwd,
 )
 
 __all__ = ["CausalConv1dFunction", "causal_conv1d_silu", "SelectiveScanFunction", "selective_scan",
-           "GroupNormSiluFunction", "group_norm_silu"]
+           "GroupNormSiluFunction", "group_norm_silu", "GatedRecurrenceFunction", "gated_recurrence",
+           "LayerNormFunction", "layer_norm"]
 
 
 def _dense(grad):
@@ -123,3 +129,58 @@ def group_norm_silu(x, weight, groups, bias=None, z=None, eps=1e-5):
     """Differentiable gated group norm: returns y, BF16 [S, C].  Arguments as
     in group_norm_silu_fwd."""
     return GroupNormSiluFunction.apply(x, weight, groups, bias, z, eps)
+
+
+class GatedRecurrenceFunction(torch.autograd.Function):
+    """gated_recurrence_fwd without a carried state, with the backward of
+    gated_recurrence_bwd.  ddecay comes in the parameter's dtype."""
+
+    @staticmethod
+    def forward(ctx, x, r, i, decay, cu_seqlens, z=None, scale=8.0):
+        y, keep = gated_recurrence_fwd(x, r, i, decay, cu_seqlens, z=z, scale=scale, keep=True)
+        ctx.save_for_backward(x, r, i, decay, cu_seqlens, z, keep)
+        ctx.scale = scale
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_y):
+        x, r, i, decay, cu_seqlens, z, keep = ctx.saved_tensors
+        dx, dr, di, ddecay, dz = gated_recurrence_bwd(x, r, i, decay, cu_seqlens, _dense(grad_y), keep, z=z,
+                                                      scale=ctx.scale)
+        return _needed(ctx, (dx, dr, di, ddecay, None, dz, None))
+
+
+def gated_recurrence(x, r, i, decay, cu_seqlens, z=None, scale=8.0):
+    """Differentiable gated linear recurrence over packed documents, each from
+    a zero state: returns y, BF16 [S, C].  Arguments as in gated_recurrence_fwd."""
+    return GatedRecurrenceFunction.apply(x, r, i, decay, cu_seqlens, z, scale)
+
+
+class LayerNormFunction(torch.autograd.Function):
+    """layer_norm_fwd with the backward of layer_norm_bwd.  x and the residual
+    have one gradient, in which the stream's own joins the norm's."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias=None, residual=None, eps=1e-5):
+        y, stream = layer_norm_fwd(x, weight, bias=bias, residual=residual, eps=eps)
+        ctx.save_for_backward(stream, weight, bias)
+        ctx.eps, ctx.sum = eps, residual is not None
+        ctx.set_materialize_grads(False)
+        return (y, stream) if ctx.sum else y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_y, grad_stream=None):
+        stream, weight, bias = ctx.saved_tensors
+        if grad_y is None:  # only the stream goes on
+            return _needed(ctx, (grad_stream, None, None, grad_stream, None))
+        dstream = None if grad_stream is None else _dense(grad_stream)
+        dx, dweight, dbias = layer_norm_bwd(stream, weight, _dense(grad_y), bias=bias, dstream=dstream, eps=ctx.eps)
+        return _needed(ctx, (dx, dweight, dbias, dx if ctx.sum else None, None))
+
+
+def layer_norm(x, weight, bias=None, residual=None, eps=1e-5):
+    """Differentiable layer norm: returns y, BF16 [S, C], or (y, stream) where
+    a residual is added first.  Arguments as in layer_norm_fwd."""
+    return LayerNormFunction.apply(x, weight, bias, residual, eps)

@@ -1,0 +1,85 @@
+// Internal interface between the host entry points (vdc_layer_api.cpp) and the
+// kernels of the recurrent layer (vdc_recurrence.hip, vdc_layer_norm.hip,
+// vdc_pool.hip).  Not installed; include/vdc.h is the ABI.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include <hip/hip_runtime_api.h>
+
+namespace vdc {
+
+// ---------------------------------------------- gated linear recurrence --
+
+// Tokens between two states that a training forward keeps.
+constexpr int kRecurKeep = 64;
+
+struct RecurArgs {
+  const uint16_t *x, *r, *i, *z, *dy;
+  int64_t xs, rs, is, zs, dys;  // elements between rows
+  const void* decay;            // [C]
+  int32_t decay_bf16;
+  float scale;
+  const int32_t* cu;
+  int32_t num_docs;
+  int32_t S, C;
+  float* state;                 // [slots][C]
+  const int32_t* index;
+  const uint8_t* resume;
+  int64_t slots;
+  uint16_t* y;
+  float* keep;                  // [ceil(S / kRecurKeep)][C] or null; backward: read
+  uint16_t *dx, *dr, *di, *dz;
+  void* ddecay;
+  // workspace
+  float* h;                     // backward: [kRecurKeep][C]
+};
+
+hipError_t launch_recur_fwd(const RecurArgs& a, hipStream_t s);
+hipError_t launch_recur_bwd(const RecurArgs& a, hipStream_t s);
+hipError_t launch_recur_step(const RecurArgs& a, hipStream_t s);
+
+// ------------------------------------------------------------ layer norm --
+
+// Widest row, in channels.
+constexpr int kLayerNormMaxC = 16384;
+
+struct LayerNormArgs {
+  const uint16_t *x, *res, *dy, *dstream;  // backward: x is the stream
+  int64_t xs, ress, dys, dss;
+  const void *w, *b;
+  int32_t w_bf16, b_bf16;
+  int64_t S;
+  int32_t C;
+  float eps;
+  uint16_t *y, *stream, *dx;
+  void *dw, *db;
+  float* part;                             // [prows][2][C]
+  int32_t prows;
+};
+
+hipError_t launch_layer_norm_fwd(const LayerNormArgs& a, hipStream_t s);
+hipError_t launch_layer_norm_bwd(const LayerNormArgs& a, hipStream_t s);
+hipError_t launch_layer_norm_bwd_sum(const LayerNormArgs& a, hipStream_t s);
+// Partial rows of dweight and dbias, one for each workgroup of the backward.
+int layer_norm_bwd_rows(int64_t S, int64_t C);
+
+// ------------------------------------------------------ states put aside --
+
+// Values that share a scale.
+constexpr int kPoolBlock = 64;
+
+struct PoolArgs {
+  void* state;            // [slots][E]
+  uint8_t* codes;         // [pool][E]
+  float* scales;          // [pool][blocks]
+  const int32_t *state_index, *pool_index;
+  int64_t slots, pool, rows, E;
+  int32_t bf16, e4m3;     // the state's dtype, the code
+};
+
+hipError_t launch_pool_quantize(const PoolArgs& a, hipStream_t s);
+hipError_t launch_pool_dequantize(const PoolArgs& a, hipStream_t s);
+
+}  // namespace vdc

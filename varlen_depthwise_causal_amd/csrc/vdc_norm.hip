@@ -30,52 +30,6 @@ namespace {
 // address.  16384 tokens, C = 520 in 8 groups, with a gate: forward 27 us,
 // backward 49; three times over a row with a channel a lane takes 54 and 190.
 
-struct Vec8 {
-  float v[8];
-};
-__device__ __forceinline__ Vec8 unpack8(u32x4_t r) {
-  Vec8 o;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o.v[2 * i] = bf16_lo(r[i]), o.v[2 * i + 1] = bf16_hi(r[i]);
-  return o;
-}
-__device__ __forceinline__ u32x4_t pack8(const Vec8& a) {
-  u32x4_t r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = bf16_pack2(a.v[2 * i], a.v[2 * i + 1]);
-  return r;
-}
-// At any address that holds BF16 values.
-typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
-
-// Eight values, of which there are `count`; the others are zeros.
-template <bool kWhole>
-__device__ __forceinline__ u32x4_t load8(const uint16_t* p, int32_t count) {
-  if (kWhole || count >= 8) {
-    if (kWhole) return *reinterpret_cast<const u32x4_t*>(p);
-    const u32x4_any v = *reinterpret_cast<const u32x4_any*>(p);
-    return (u32x4_t){v[0], v[1], v[2], v[3]};
-  }
-  u32x4_t r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t lo = 2 * i < count ? p[2 * i] : 0u, hi = 2 * i + 1 < count ? p[2 * i + 1] : 0u;
-    r[i] = lo | hi << 16;
-  }
-  return r;
-}
-template <bool kWhole>
-__device__ __forceinline__ void store8(uint16_t* p, u32x4_t v, int32_t count) {
-  // Every output byte is written once and not read here.
-  if (kWhole) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(p));
-  else if (count >= 8) *reinterpret_cast<u32x4_any*>(p) = (u32x4_any){v[0], v[1], v[2], v[3]};
-  else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < count) p[i] = (uint16_t)(v[i / 2] >> (i % 2 * 16));
-  }
-}
-
 template <int L, int K, bool kWhole>
 struct Place {
   static constexpr int kThreads = L > 64 ? L : 256;

@@ -1,5 +1,6 @@
-// Device helpers shared by the state space layer's kernels (the convolution
-// with carried state, the selective scan and the gated group norm).
+// Device helpers shared by the kernels of the state space layer (the convolution
+// with carried state, the selective scan and the gated group norm) and of the
+// recurrent layer (the gated recurrence, the layer norm, states put aside).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -97,6 +98,53 @@ __device__ __forceinline__ float lanes_sum(float v) {
     v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
   }
   return v;
+}
+
+// Eight channels of a row.
+struct Vec8 {
+  float v[8];
+};
+__device__ __forceinline__ Vec8 unpack8(u32x4_t r) {
+  Vec8 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o.v[2 * i] = bf16_lo(r[i]), o.v[2 * i + 1] = bf16_hi(r[i]);
+  return o;
+}
+__device__ __forceinline__ u32x4_t pack8(const Vec8& a) {
+  u32x4_t r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = bf16_pack2(a.v[2 * i], a.v[2 * i + 1]);
+  return r;
+}
+// At any address that holds BF16 values.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+
+// Eight values, of which there are `count`; the others are zeros.
+template <bool kWhole>
+__device__ __forceinline__ u32x4_t load8(const uint16_t* p, int32_t count) {
+  if (kWhole || count >= 8) {
+    if (kWhole) return *reinterpret_cast<const u32x4_t*>(p);
+    const u32x4_any v = *reinterpret_cast<const u32x4_any*>(p);
+    return (u32x4_t){v[0], v[1], v[2], v[3]};
+  }
+  u32x4_t r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = 2 * i < count ? p[2 * i] : 0u, hi = 2 * i + 1 < count ? p[2 * i + 1] : 0u;
+    r[i] = lo | hi << 16;
+  }
+  return r;
+}
+template <bool kWhole>
+__device__ __forceinline__ void store8(uint16_t* p, u32x4_t v, int32_t count) {
+  // Every output byte is written once and not read here.
+  if (kWhole) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(p));
+  else if (count >= 8) *reinterpret_cast<u32x4_any*>(p) = (u32x4_any){v[0], v[1], v[2], v[3]};
+  else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < count) p[i] = (uint16_t)(v[i / 2] >> (i % 2 * 16));
+  }
 }
 
 typedef const __attribute__((address_space(4))) uint32_t* scalar_ptr;
