@@ -429,7 +429,7 @@ int group_norm_silu_bwd(const void *x, int64_t x_stride, const void *weight, int
  * outputs, caches updated in place, sequences without a slot, and sizes whose
  * launches would need 2^32 lanes refused (VDC_EINVAL):
  *
- *   gated_recurrence_*  ceil(S / 64) * ceil(C / 128) from 2^23 on
+ *   gated_recurrence_*  ceil(S / 64) * ceil(C / 64) from 2^23 on
  *   layer_norm_*        never
  *   state_quantize, state_dequantize
  *                       rows * ceil(E / 4096) from 2^24 on

@@ -98,7 +98,7 @@ def test_gated_recurrence_sizes(lib):
         assert lib.gated_recurrence_workspace_bytes(FWD, S, C) == 0
     assert lib.gated_recurrence_workspace_bytes(7, 8, 8) == 0
     assert lib.gated_recurrence_workspace_bytes(BWD, 8, 8) > 0
-    # 2^23 tiles of 64 tokens and 128 channels
+    # 2^23 tiles of 64 tokens and 64 channels or more
     wide = dict(C=2 ** 20, x_stride=2 ** 20, r_stride=2 ** 20, i_stride=2 ** 20, z_stride=2 ** 20, state=None)
     assert fwd(lib, S=65536, **wide) == EINVAL and bwd(lib, S=65536, dys=2 ** 20, **wide) == EINVAL
 

@@ -12,8 +12,12 @@ namespace vdc {
 
 // ---------------------------------------------- gated linear recurrence --
 
+// A workgroup has a tile of kRecurCols channels by tokens: waves one behind
+// another in time, each with a run of tokens.
+constexpr int kRecurCols = 64, kRecurWaves = 8, kRecurFwdRun = 16, kRecurBwdRun = 8;
+constexpr int kRecurFwdTile = kRecurWaves * kRecurFwdRun, kRecurBwdTile = kRecurWaves * kRecurBwdRun;
 // Tokens between two states that a training forward keeps.
-constexpr int kRecurKeep = 64;
+constexpr int kRecurKeep = kRecurBwdTile;
 
 struct RecurArgs {
   const uint16_t *x, *r, *i, *z, *dy;
@@ -24,6 +28,7 @@ struct RecurArgs {
   const int32_t* cu;
   int32_t num_docs;
   int32_t S, C;
+  int32_t tiles, blocks;        // of tokens and of channels
   float* state;                 // [slots][C]
   const int32_t* index;
   const uint8_t* resume;
@@ -33,11 +38,21 @@ struct RecurArgs {
   uint16_t *dx, *dr, *di, *dz;
   void* ddecay;
   // workspace
-  float* h;                     // backward: [kRecurKeep][C]
+  uint32_t* ticket;             // tiles that have begun; the words follow it
+  uint64_t* words;              // [tiles][blocks * kRecurCols] what a tile hands on
+  float* part;                  // backward: [tiles][C] partial ddecay
 };
 
+// Bytes of a call's ticket and words, none for one tile.
+inline size_t recur_words_bytes(int64_t tiles, int64_t blocks) {
+  return tiles > 1 ? 256 + (size_t)tiles * blocks * kRecurCols * 8 : 0;
+}
+
+// The ticket and the words as a call finds them.
+hipError_t launch_recur_clear(const RecurArgs& a, hipStream_t s);
 hipError_t launch_recur_fwd(const RecurArgs& a, hipStream_t s);
 hipError_t launch_recur_bwd(const RecurArgs& a, hipStream_t s);
+hipError_t launch_recur_bwd_sum(const RecurArgs& a, hipStream_t s);
 hipError_t launch_recur_step(const RecurArgs& a, hipStream_t s);
 
 // ------------------------------------------------------------ layer norm --

@@ -21,7 +21,7 @@ constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 4096;
 
 int recur_sizes(int64_t S, int64_t C) {
   if (S < 0 || S > kMaxTokens || C < 1 || C > kMaxC) return VDC_EINVAL;
-  return ceil_div(S, kRecurKeep) * ceil_div(C, 128) >= (int64_t(1) << 23) ? VDC_EINVAL : VDC_OK;
+  return ceil_div(S, kRecurBwdTile) * ceil_div(C, kRecurCols) >= (int64_t(1) << 23) ? VDC_EINVAL : VDC_OK;
 }
 
 // The checks that fwd, bwd and update share, and the kernels' arguments.
@@ -92,10 +92,17 @@ Span state_span(const vdc_recurrence* v) {
   return {v->state, v->state ? (size_t)v->slots * v->C * 4 : 0};
 }
 
+// Places the workspace's arrays (base may be null: the size alone).
 size_t recur_layout(int dir, int64_t S, int64_t C, char* base, RecurArgs* a) {
-  if (dir == VDC_FWD) return 0;
-  a->h = reinterpret_cast<float*>(base);
-  return (size_t)kRecurKeep * C * 4;
+  const int64_t tiles = ceil_div(S, dir == VDC_FWD ? kRecurFwdTile : kRecurBwdTile);
+  const int64_t blocks = ceil_div(C, kRecurCols);
+  const size_t words = recur_words_bytes(tiles, blocks);
+  a->tiles = (int32_t)tiles;
+  a->blocks = (int32_t)blocks;
+  a->ticket = reinterpret_cast<uint32_t*>(base);
+  a->words = reinterpret_cast<uint64_t*>(base + 256);
+  a->part = reinterpret_cast<float*>(base + words);
+  return words + (dir == VDC_BWD ? (size_t)tiles * C * 4 : 0);
 }
 
 }  // namespace
@@ -122,7 +129,7 @@ extern "C" int gated_recurrence_fwd(const vdc_recurrence* v, void* y, float* kee
   if (v->S == 0 && (!v->state || v->num_docs == 0)) return VDC_OK;
   if (v->S > 0 && !y) return VDC_EINVAL;
   if (!aligned(y, 2) || !aligned(keep, 4)) return VDC_EALIGN;
-  const size_t need = v->S ? recur_layout(VDC_FWD, v->S, v->C, static_cast<char*>(workspace), &a) : 0;
+  const size_t need = recur_layout(VDC_FWD, v->S, v->C, static_cast<char*>(workspace), &a);
   if (need) {
     if (!workspace || ws_bytes < need) return VDC_EWORKSPACE;
     if (!aligned(workspace, 16)) return VDC_EALIGN;
@@ -136,6 +143,7 @@ extern "C" int gated_recurrence_fwd(const vdc_recurrence* v, void* y, float* kee
   }
   a.y = static_cast<uint16_t*>(y);
   a.keep = keep;
+  if (a.tiles > 1 && (rc = done(launch_recur_clear(a, stream)))) return rc;
   return done(launch_recur_fwd(a, stream));
 }
 
@@ -151,7 +159,7 @@ extern "C" int gated_recurrence_bwd(const vdc_recurrence* v, const void* dy, int
   if (!aligned(dy, 2) || !aligned(keep, 4) || !aligned(dx, 2) || !aligned(dr, 2) || !aligned(di, 2) ||
       !aligned(dz, 2) || !aligned(ddecay, dtype_bytes(v->decay_dtype)))
     return VDC_EALIGN;
-  const size_t need = v->S ? recur_layout(VDC_BWD, v->S, v->C, static_cast<char*>(workspace), &a) : 0;
+  const size_t need = recur_layout(VDC_BWD, v->S, v->C, static_cast<char*>(workspace), &a);
   if (need) {
     if (!workspace || ws_bytes < need) return VDC_EWORKSPACE;
     if (!aligned(workspace, 16)) return VDC_EALIGN;
@@ -174,7 +182,9 @@ extern "C" int gated_recurrence_bwd(const vdc_recurrence* v, const void* dy, int
   a.di = static_cast<uint16_t*>(di);
   a.dz = static_cast<uint16_t*>(dz);
   a.ddecay = ddecay;
-  return done(launch_recur_bwd(a, stream));
+  if (a.tiles > 1 && (rc = done(launch_recur_clear(a, stream)))) return rc;
+  if (v->S > 0 && (rc = done(launch_recur_bwd(a, stream)))) return rc;
+  return done(launch_recur_bwd_sum(a, stream));
 }
 
 extern "C" int gated_recurrence_update(const vdc_recurrence* v, void* y, hipStream_t stream) {

@@ -25,7 +25,6 @@
 #include <cfloat>
 #include <type_traits>
 
-#include "vdc_search.h"
 #include "vdc_ssm.h"
 #include "vdc_ssm_math.h"
 
@@ -48,19 +47,6 @@ __device__ __forceinline__ bool resumes(const ScanArgs& a, int32_t d) {
 }
 __device__ __forceinline__ int64_t doc_slot(const ScanArgs& a, int32_t d) {
   return slot_of(a.index, d, a.slots);
-}
-
-// First index i in [0, n) with cu[i] >= v (n if none), by a whole wave.
-__device__ __forceinline__ int32_t first_at_least(const int32_t* cu, int32_t n, int32_t v) {
-  const int lane = (int)(threadIdx.x & 63);
-  int64_t lo = 0, hi = n;
-  while (lo < hi) {
-    const int64_t step = search_step(lo, hi);
-    const int64_t idx = search_probe(lo, hi, step, lane);
-    const uint64_t ball = __ballot(idx >= 0 && cu[idx] < v);
-    search_narrow(lo, hi, step, ~ball == 0 ? 64 : (int)__builtin_ctzll(~ball));
-  }
-  return __builtin_amdgcn_readfirstlane((int32_t)lo);
 }
 
 // The bias of a channel's step size.

@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "vdc.h"
+#include "vdc_search.h"
 
 namespace vdc {
 
@@ -160,6 +161,19 @@ __device__ __forceinline__ int32_t uniform_at(const int32_t* p, int64_t i) {
 __device__ __forceinline__ int64_t slot_of(const int32_t* index, int64_t i, int64_t slots) {
   const int64_t s = index ? (int64_t)uniform_at(index, i) : i;
   return s >= 0 && s < slots ? s : -1;
+}
+
+// First index i in [0, n) with cu[i] >= v (n if none), by a whole wave.
+__device__ __forceinline__ int32_t first_at_least(const int32_t* cu, int32_t n, int32_t v) {
+  const int lane = (int)(threadIdx.x & 63);
+  int64_t lo = 0, hi = n;
+  while (lo < hi) {
+    const int64_t step = search_step(lo, hi);
+    const int64_t idx = search_probe(lo, hi, step, lane);
+    const uint64_t ball = __ballot(idx >= 0 && cu[idx] < v);
+    search_narrow(lo, hi, step, ~ball == 0 ? 64 : (int)__builtin_ctzll(~ball));
+  }
+  return __builtin_amdgcn_readfirstlane((int32_t)lo);
 }
 
 }  // namespace vdc
