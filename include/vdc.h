@@ -456,7 +456,7 @@ typedef struct vdc_recurrence {
     const void *r;    /* bf16 [S][C], the decay's gate                       */
     const void *i;    /* bf16 [S][C], the input's gate                       */
     const void *z;    /* bf16 [S][C], or NULL: no gate at the output         */
-    int64_t x_stride, r_stride, i_stride, z_stride; /* C .. 2^31             */
+    int64_t x_stride, r_stride, i_stride, z_stride; /* C .. 2^25             */
     const void *decay; /* [C]                                                */
     int decay_dtype;
     float scale;      /* at least 0, finite                                  */
@@ -495,7 +495,7 @@ int gated_recurrence_fwd(const vdc_recurrence *args, void *y, float *keep,
  * from zero history; args->state must be NULL), from its inputs and what it
  * kept.
  *
- * dy             bf16 [S][C], dy_stride elements between rows.
+ * dy             bf16 [S][C], dy_stride (up to 2^25) elements between rows.
  * keep           what gated_recurrence_fwd left of the same arguments.
  * dx, dr, di, dz bf16 [S][C] outputs; dz NULL exactly where z is.
  * ddecay         [C] output of decay's dtype.

@@ -41,7 +41,7 @@ def recur(**change):
 
 
 RECUR_BAD = [({"C": 0}, EINVAL), ({"C": 2 ** 20 + 1}, EINVAL), ({"S": -1}, EINVAL), ({"S": 2 ** 31 - 4095}, EINVAL),
-             ({"x_stride": 63}, EINVAL), ({"r_stride": 63}, EINVAL), ({"i_stride": 2 ** 31 + 1}, EINVAL),
+             ({"x_stride": 63}, EINVAL), ({"r_stride": 63}, EINVAL), ({"i_stride": 2 ** 25 + 1}, EINVAL),
              ({"z_stride": 0}, EINVAL), ({"x": None}, EINVAL), ({"r": None}, EINVAL), ({"i": None}, EINVAL),
              ({"decay": None}, EINVAL), ({"scale": -1.0}, EINVAL), ({"scale": float("nan")}, EINVAL),
              ({"scale": float("inf")}, EINVAL), ({"decay_dtype": 2}, EDTYPE), ({"x": at(0) + 1}, EALIGN),

@@ -12,10 +12,8 @@ namespace vdc {
 
 // ---------------------------------------------- gated linear recurrence --
 
-// A workgroup has a tile of kRecurCols channels by tokens: waves one behind
-// another in time, each with a run of tokens.
-constexpr int kRecurCols = 64, kRecurWaves = 8, kRecurFwdRun = 16, kRecurBwdRun = 8;
-constexpr int kRecurFwdTile = kRecurWaves * kRecurFwdRun, kRecurBwdTile = kRecurWaves * kRecurBwdRun;
+// Tokens of the tiles that a row of tokens is cut into.
+constexpr int kRecurFwdTile = 128, kRecurBwdTile = 64;
 // Tokens between two states that a training forward keeps.
 constexpr int kRecurKeep = kRecurBwdTile;
 
@@ -28,7 +26,9 @@ struct RecurArgs {
   const int32_t* cu;
   int32_t num_docs;
   int32_t S, C;
-  int32_t tiles, blocks;        // of tokens and of channels
+  int32_t tiles;                // of tokens
+  int32_t blocks;               // workgroups that share a tile of tokens
+  int32_t cols;                 // words of a tile: C rounded up to 128
   float* state;                 // [slots][C]
   const int32_t* index;
   const uint8_t* resume;
@@ -39,13 +39,13 @@ struct RecurArgs {
   void* ddecay;
   // workspace
   uint32_t* ticket;             // tiles that have begun; the words follow it
-  uint64_t* words;              // [tiles][blocks * kRecurCols] what a tile hands on
+  uint64_t* words;              // [tiles][cols] what a tile hands on
   float* part;                  // backward: [tiles][C] partial ddecay
 };
 
 // Bytes of a call's ticket and words, none for one tile.
-inline size_t recur_words_bytes(int64_t tiles, int64_t blocks) {
-  return tiles > 1 ? 256 + (size_t)tiles * blocks * kRecurCols * 8 : 0;
+inline size_t recur_words_bytes(int64_t tiles, int64_t cols) {
+  return tiles > 1 ? 256 + (size_t)tiles * cols * 8 : 0;
 }
 
 // The ticket and the words as a call finds them.

@@ -19,9 +19,12 @@ namespace {
 // The kernels count tokens, and a few past the last, in 32 bits.
 constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 4096;
 
+// Largest row stride of x, r, i, z and dy: a run of tokens stays below 2^31 bytes.
+constexpr int64_t kRecurMaxStride = int64_t(1) << 25;
+
 int recur_sizes(int64_t S, int64_t C) {
   if (S < 0 || S > kMaxTokens || C < 1 || C > kMaxC) return VDC_EINVAL;
-  return ceil_div(S, kRecurBwdTile) * ceil_div(C, kRecurCols) >= (int64_t(1) << 23) ? VDC_EINVAL : VDC_OK;
+  return ceil_div(S, kRecurBwdTile) * ceil_div(C, 64) >= (int64_t(1) << 23) ? VDC_EINVAL : VDC_OK;
 }
 
 // The checks that fwd, bwd and update share, and the kernels' arguments.
@@ -33,7 +36,7 @@ int recur_common(const vdc_recurrence* v, bool prompt, RecurArgs* a) {
   if (!(v->scale >= 0.0f) || std::isinf(v->scale)) return VDC_EINVAL;
   const int64_t strides[4] = {v->x_stride, v->r_stride, v->i_stride, v->z ? v->z_stride : v->C};
   for (int64_t s : strides)
-    if (s < v->C || s > kMaxStride) return VDC_EINVAL;
+    if (s < v->C || s > kRecurMaxStride) return VDC_EINVAL;
   if (prompt) {
     if (v->num_docs < 0 || v->num_docs > kMaxS - 1 || (v->S > 0 && v->num_docs < 1)) return VDC_EINVAL;
     if (v->num_docs > 0 && !v->cu_seqlens) return VDC_EINVAL;
@@ -95,10 +98,10 @@ Span state_span(const vdc_recurrence* v) {
 // Places the workspace's arrays (base may be null: the size alone).
 size_t recur_layout(int dir, int64_t S, int64_t C, char* base, RecurArgs* a) {
   const int64_t tiles = ceil_div(S, dir == VDC_FWD ? kRecurFwdTile : kRecurBwdTile);
-  const int64_t blocks = ceil_div(C, kRecurCols);
-  const size_t words = recur_words_bytes(tiles, blocks);
+  const int64_t cols = ceil_div(C, 128) * 128;
+  const size_t words = recur_words_bytes(tiles, cols);
   a->tiles = (int32_t)tiles;
-  a->blocks = (int32_t)blocks;
+  a->cols = (int32_t)cols;
   a->ticket = reinterpret_cast<uint32_t*>(base);
   a->words = reinterpret_cast<uint64_t*>(base + 256);
   a->part = reinterpret_cast<float*>(base + words);
@@ -153,7 +156,7 @@ extern "C" int gated_recurrence_bwd(const vdc_recurrence* v, const void* dy, int
   RecurArgs a{};
   int rc = recur_common(v, true, &a);
   if (rc) return rc;
-  if (v->state || !ddecay || dy_stride < v->C || dy_stride > kMaxStride) return VDC_EINVAL;
+  if (v->state || !ddecay || dy_stride < v->C || dy_stride > kRecurMaxStride) return VDC_EINVAL;
   if (v->S > 0 && (!dy || !keep || !dx || !dr || !di || (dz == nullptr) != (v->z == nullptr)))
     return VDC_EINVAL;
   if (!aligned(dy, 2) || !aligned(keep, 4) || !aligned(dx, 2) || !aligned(dr, 2) || !aligned(di, 2) ||
@@ -194,7 +197,6 @@ extern "C" int gated_recurrence_update(const vdc_recurrence* v, void* y, hipStre
   if (v->S == 0) return VDC_OK;
   if (!y || (!v->state && v->slots > 0)) return VDC_EINVAL;
   if (!v->state_index && v->S > v->slots) return VDC_EINVAL;
-  if (v->S * ceil_div(v->C, 64) * 64 > kMaxThreads) return VDC_EINVAL;
   if (!aligned(y, 2)) return VDC_EALIGN;
   const Span out{y, (size_t)v->S * v->C * 2}, st = state_span(v);
   if (hits_input(v, out, false) || hits_input(v, st, false) || overlaps(out, st)) return VDC_EINVAL;

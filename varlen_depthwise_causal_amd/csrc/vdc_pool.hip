@@ -34,82 +34,158 @@ __device__ __forceinline__ float odd_quotient(float v, float s) {
   return __uint_as_float(b);
 }
 
-__device__ __forceinline__ float max64(float v) {
+// V values a lane, 64 / V lanes a block.  V = 8: states of a multiple of 64 values, as
+// long as vectors of them and of their codes are aligned; else V = 1.
+template <int V, bool kBf16>
+__device__ __forceinline__ void state_load(const PoolArgs& a, int64_t at, float (&v)[V]) {
+  if constexpr (V == 1) {
+    v[0] = kBf16 ? bf16_f32(static_cast<const uint16_t*>(a.state)[at]) : static_cast<const float*>(a.state)[at];
+  } else if constexpr (kBf16) {
+    const u32x4_t w = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(a.state) + at));
 #pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v = __builtin_fmaxf(v, __shfl_xor(v, d, 64));
-  return v;
+    for (int k = 0; k < 4; ++k) v[2 * k] = bf16_lo(w[k]), v[2 * k + 1] = bf16_hi(w[k]);
+  } else {
+    const f32x4_t* p = reinterpret_cast<const f32x4_t*>(static_cast<const float*>(a.state) + at);
+    const f32x4_t lo = __builtin_nontemporal_load(p), hi = __builtin_nontemporal_load(p + 1);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = lo[k], v[4 + k] = hi[k];
+  }
+}
+template <int V, bool kBf16>
+__device__ __forceinline__ void state_store(const PoolArgs& a, int64_t at, const float (&v)[V]) {
+  if constexpr (V == 1) {
+    if (kBf16) static_cast<uint16_t*>(a.state)[at] = bf16_of(v[0]);
+    else static_cast<float*>(a.state)[at] = v[0];
+  } else if constexpr (kBf16) {
+    u32x4_t w;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = bf16_pack2(v[2 * k], v[2 * k + 1]);
+    __builtin_nontemporal_store(w, reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(a.state) + at));
+  } else {
+    f32x4_t* p = reinterpret_cast<f32x4_t*>(static_cast<float*>(a.state) + at);
+    __builtin_nontemporal_store((f32x4_t){v[0], v[1], v[2], v[3]}, p);
+    __builtin_nontemporal_store((f32x4_t){v[4], v[5], v[6], v[7]}, p + 1);
+  }
 }
 
-template <bool kBf16, bool kE4m3>
+template <bool kE4m3>
+__device__ __forceinline__ uint32_t code_of(float t) {
+  if (kE4m3) return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(t, t, 0, false) & 0xffu;
+  return (uint32_t)(int32_t)__builtin_rintf(t) & 0xffu;
+}
+
+// A workgroup has a part of 4096 values of one state.
+template <int V, bool kBf16, bool kE4m3>
 __global__ __launch_bounds__(256) void pool_quantize_kernel(PoolArgs a, int32_t parts) {
-  const int64_t row = blockIdx.x / parts;
-  const int64_t part = blockIdx.x - row * parts;
+  const int64_t row = blockIdx.x / parts, part = blockIdx.x - row * parts;
   int64_t slot, place;
   if (!pool_row(a, row, &slot, &place)) return;
   const int64_t blocks = (a.E + kPoolBlock - 1) / kPoolBlock;
-  const int lane = threadIdx.x & 63;
-#pragma unroll 1
-  for (int k = threadIdx.x / 64; k < kPoolValues / kPoolBlock; k += 4) {
-    const int64_t block = part * (kPoolValues / kPoolBlock) + k, at = block * kPoolBlock + lane;
-    if (block >= blocks) return;
-    float v = 0.0f;
-    if (at < a.E)
-      v = kBf16 ? bf16_f32(static_cast<const uint16_t*>(a.state)[slot * a.E + at])
-                : static_cast<const float*>(a.state)[slot * a.E + at];
-    const float most = max64(__builtin_fabsf(v));
-    // a maximum drops a NaN
-    const bool bad = __ballot(!(__builtin_fabsf(v) < __builtin_inff())) != 0;
-    const bool none = bad || most < 0x1p-64f;
-    const float scale = bad ? __builtin_nanf("") : none ? 0.0f : most / (kE4m3 ? 448.0f : 127.0f);
-    const float t = none ? 0.0f : odd_quotient(v, scale);
-    uint32_t code;
-    if (kE4m3) code = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(t, t, 0, false) & 0xffu;
-    else code = (uint32_t)(int32_t)__builtin_rintf(t) & 0xffu;
-    if (at < a.E) a.codes[place * a.E + at] = (uint8_t)code;
-    if (lane == 0) a.scales[place * blocks + block] = scale;
+  constexpr int kTurns = kPoolValues / (256 * V), kLanes = kPoolBlock / V;
+  const int64_t at0 = part * kPoolValues + (int64_t)threadIdx.x * V;
+  float v[kTurns][V];
+#pragma unroll
+  for (int k = 0; k < kTurns; ++k) {
+    const int64_t at = at0 + k * 256 * V;
+#pragma unroll
+    for (int q = 0; q < V; ++q) v[k][q] = 0.0f;
+    if (at < a.E) state_load<V, kBf16>(a, slot * a.E + at, v[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < kTurns; ++k) {
+    const int64_t at = at0 + k * 256 * V;
+    // a maximum drops a NaN, a sum of products with 0 keeps that of an infinity too
+    float most = 0.0f, bad = 0.0f;
+#pragma unroll
+    for (int q = 0; q < V; ++q) {
+      most = __builtin_fmaxf(most, __builtin_fabsf(v[k][q]));
+      bad = __builtin_fmaf(v[k][q], 0.0f, bad);
+    }
+    most = lanes_max<kLanes>(most);
+    bad = lanes_sum<kLanes>(bad);
+    const bool none = !(most >= 0x1p-64f) || bad != bad;
+    const float scale = bad != bad ? __builtin_nanf("") : none ? 0.0f : most / (kE4m3 ? 448.0f : 127.0f);
+    uint32_t code[V];
+#pragma unroll
+    for (int q = 0; q < V; ++q) code[q] = code_of<kE4m3>(none ? 0.0f : odd_quotient(v[k][q], scale));
+    if (at >= a.E) continue;
+    uint8_t* out = a.codes + place * a.E + at;
+    if constexpr (V == 1) {
+      *out = (uint8_t)code[0];
+    } else {
+      u32x2_t w = {0, 0};
+#pragma unroll
+      for (int q = 0; q < V; ++q) w[q / 4] |= code[q] << (q % 4 * 8);
+      __builtin_nontemporal_store(w, reinterpret_cast<u32x2_t*>(out));
+    }
+    if (threadIdx.x % kLanes == 0) a.scales[place * blocks + at / kPoolBlock] = scale;
   }
 }
 
-template <bool kBf16, bool kE4m3>
+template <int V, bool kBf16, bool kE4m3>
 __global__ __launch_bounds__(256) void pool_dequantize_kernel(PoolArgs a, int32_t parts) {
-  const int64_t row = blockIdx.x / parts;
-  const int64_t part = blockIdx.x - row * parts;
+  const int64_t row = blockIdx.x / parts, part = blockIdx.x - row * parts;
   int64_t slot, place;
   if (!pool_row(a, row, &slot, &place)) return;
   const int64_t blocks = (a.E + kPoolBlock - 1) / kPoolBlock;
-#pragma unroll 1
-  for (int k = threadIdx.x; k < kPoolValues; k += 256) {
-    const int64_t at = part * kPoolValues + k;
-    if (at >= a.E) return;
-    const uint32_t code = a.codes[place * a.E + at];
-    const float scale = a.scales[place * blocks + at / kPoolBlock];
-    const float q = kE4m3 ? __builtin_amdgcn_cvt_f32_fp8((int)code, 0) : (float)(int8_t)code;
-    const float v = q * scale;
-    if (kBf16) static_cast<uint16_t*>(a.state)[slot * a.E + at] = bf16_of(v);
-    else static_cast<float*>(a.state)[slot * a.E + at] = v;
+  constexpr int kTurns = kPoolValues / (256 * V);
+  const int64_t at0 = part * kPoolValues + (int64_t)threadIdx.x * V;
+  uint32_t code[kTurns][(V + 3) / 4];
+  float scale[kTurns];
+#pragma unroll
+  for (int k = 0; k < kTurns; ++k) {
+    const int64_t at = at0 + k * 256 * V;
+    if (at >= a.E) continue;
+    const uint8_t* in = a.codes + place * a.E + at;
+    if constexpr (V == 1) {
+      code[k][0] = *in;
+    } else {
+      const u32x2_t w = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(in));
+      code[k][0] = w[0], code[k][1] = w[1];
+    }
+    scale[k] = a.scales[place * blocks + at / kPoolBlock];
   }
+#pragma unroll
+  for (int k = 0; k < kTurns; ++k) {
+    const int64_t at = at0 + k * 256 * V;
+    if (at >= a.E) continue;
+    float v[V];
+#pragma unroll
+    for (int q = 0; q < V; ++q) {
+      const uint32_t b = code[k][q / 4] >> (q % 4 * 8) & 0xffu;
+      v[q] = (kE4m3 ? __builtin_amdgcn_cvt_f32_fp8((int)b, 0) : (float)(int8_t)b) * scale[k];
+    }
+    state_store<V, kBf16>(a, slot * a.E + at, v);
+  }
+}
+
+template <int V, bool kBf16, bool kE4m3>
+void launch_as(const PoolArgs& a, bool back, hipStream_t s) {
+  const int32_t parts = (int32_t)((a.E + kPoolValues - 1) / kPoolValues);
+  const dim3 grid((uint32_t)(a.rows * parts)), block(256);
+  if (back) hipLaunchKernelGGL((pool_dequantize_kernel<V, kBf16, kE4m3>), grid, block, 0, s, a, parts);
+  else hipLaunchKernelGGL((pool_quantize_kernel<V, kBf16, kE4m3>), grid, block, 0, s, a, parts);
+}
+
+template <int V>
+void launch_values(const PoolArgs& a, bool back, hipStream_t s) {
+  if (a.bf16 && a.e4m3) launch_as<V, true, true>(a, back, s);
+  else if (a.bf16) launch_as<V, true, false>(a, back, s);
+  else if (a.e4m3) launch_as<V, false, true>(a, back, s);
+  else launch_as<V, false, false>(a, back, s);
+}
+
+hipError_t launch(const PoolArgs& a, bool back, hipStream_t s) {
+  const bool vectors = a.E % kPoolBlock == 0 && reinterpret_cast<uintptr_t>(a.state) % 16 == 0 &&
+                       reinterpret_cast<uintptr_t>(a.codes) % 8 == 0;
+  if (vectors) launch_values<8>(a, back, s);
+  else launch_values<1>(a, back, s);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_pool_quantize(const PoolArgs& a, hipStream_t s) {
-  const int32_t parts = (int32_t)((a.E + kPoolValues - 1) / kPoolValues);
-  const dim3 grid((uint32_t)(a.rows * parts)), block(256);
-  if (a.bf16 && a.e4m3) hipLaunchKernelGGL((pool_quantize_kernel<true, true>), grid, block, 0, s, a, parts);
-  else if (a.bf16) hipLaunchKernelGGL((pool_quantize_kernel<true, false>), grid, block, 0, s, a, parts);
-  else if (a.e4m3) hipLaunchKernelGGL((pool_quantize_kernel<false, true>), grid, block, 0, s, a, parts);
-  else hipLaunchKernelGGL((pool_quantize_kernel<false, false>), grid, block, 0, s, a, parts);
-  return hipGetLastError();
-}
-
-hipError_t launch_pool_dequantize(const PoolArgs& a, hipStream_t s) {
-  const int32_t parts = (int32_t)((a.E + kPoolValues - 1) / kPoolValues);
-  const dim3 grid((uint32_t)(a.rows * parts)), block(256);
-  if (a.bf16 && a.e4m3) hipLaunchKernelGGL((pool_dequantize_kernel<true, true>), grid, block, 0, s, a, parts);
-  else if (a.bf16) hipLaunchKernelGGL((pool_dequantize_kernel<true, false>), grid, block, 0, s, a, parts);
-  else if (a.e4m3) hipLaunchKernelGGL((pool_dequantize_kernel<false, true>), grid, block, 0, s, a, parts);
-  else hipLaunchKernelGGL((pool_dequantize_kernel<false, false>), grid, block, 0, s, a, parts);
-  return hipGetLastError();
-}
+hipError_t launch_pool_quantize(const PoolArgs& a, hipStream_t s) { return launch(a, false, s); }
+hipError_t launch_pool_dequantize(const PoolArgs& a, hipStream_t s) { return launch(a, true, s); }
 
 }  // namespace vdc

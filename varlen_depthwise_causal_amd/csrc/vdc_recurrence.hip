@@ -32,6 +32,7 @@
 // Everything between documents is assigned, never multiplied by zero, so that
 // an infinity or a NaN stays in its document.
 
+#include <algorithm>
 #include <cfloat>
 #include <climits>
 
@@ -41,103 +42,134 @@
 namespace vdc {
 namespace {
 
-constexpr int kW = kRecurWaves;
-
-// u / sigmoid(r) of a channel.
+// u / sigmoid(r) of a channel, at most 2^126: no product of it is an infinity, which
+// a decay of 0 would make a NaN.
 __device__ __forceinline__ float decay_rate(const RecurArgs& a, int64_t c) {
-  return 2.0f * a.scale * softplus_f32(param_at(a.decay, a.decay_bf16, c));
+  const float rate = 2.0f * a.scale * softplus_f32(param_at(a.decay, a.decay_bf16, c));
+  return rate > 0x1p126f ? 0x1p126f : rate;  // a NaN stays
 }
 
-// What the decay's gate makes of a token.
-struct Decay {
-  float u, a;   // the decay exp(-u / 2)
-  float rm, m;  // 1 / sqrt(1 - exp(-u)) and its inverse; both 0 without a step
-};
-
-// 1 - a^2 cancels where a is near 1: below u = 1/4 it is the series of 1 - exp(-u),
-// whose first term left out is less than u^6 / 5040 of it, 2^-24.  A token whose u
-// is below the normal numbers has no step.
-__device__ __forceinline__ float decay_step(float rate, float sr) {
-  const float u = rate * sr;
-  return u > 256.0f ? 256.0f : u;  // no infinity times zero; a NaN stays
-}
+// The decay exp(-u / 2).
 __device__ __forceinline__ float decay_of(float u) { return __builtin_amdgcn_exp2f(u * (-0.5f * kLog2E)); }
-__device__ __forceinline__ Decay decay_from(float u, float a) {
-  Decay g;
-  g.u = u;
-  g.a = a;
-  float s = __builtin_fmaf(u, -1.0f / 720.0f, 1.0f / 120.0f);
-  s = __builtin_fmaf(u, -s, 1.0f / 24.0f);
-  s = __builtin_fmaf(u, -s, 1.0f / 6.0f);
-  s = __builtin_fmaf(u, -s, 0.5f);
-  s = __builtin_fmaf(u, -s, 1.0f);
-  const float v = u < 0.25f ? u * s : __builtin_fmaf(-a, a, 1.0f);
-  g.rm = v < FLT_MIN ? 0.0f : __builtin_amdgcn_rsqf(v);
-  g.m = v * g.rm;
-  return g;
+
+// m = sqrt(1 - exp(-u)), with a = exp(-u / 2).  1 - a^2 cancels where a is near 1:
+// below u = 1/4 it is u (1 - u q(u)), q the polynomial of degree 3 that makes that
+// nearest in relative error (6e-9).
+__device__ __forceinline__ float input_scale(float u, float a) {
+  float q = -0.007534402422606945f;
+  q = __builtin_fmaf(q, u, 0.04150218889117241f);
+  q = __builtin_fmaf(q, u, -0.16665320098400116f);
+  q = __builtin_fmaf(q, u, 0.49999964237213135f);
+  const float small = u * __builtin_fmaf(-q, u, 1.0f);
+  return __builtin_amdgcn_sqrtf(u < 0.25f ? small : __builtin_fmaf(-a, a, 1.0f));
 }
-// What a token adds to the state: nothing without a step, whatever x holds.
-__device__ __forceinline__ float input_of(const Decay& g, float si, float x) {
-  return g.rm == 0.0f ? 0.0f : g.m * (si * x);
-}
+
+// a b, and 0 where either is 0: a token without a step adds nothing, whatever its
+// input holds.
+extern "C" __device__ float vdc_fmul_legacy(float, float) __asm("llvm.amdgcn.fmul.legacy");
+__device__ __forceinline__ float gated(float a, float b) { return vdc_fmul_legacy(a, b); }
 
 // ------------------------------------------------------------------- tiles --
 
-// A lane's channel; lanes past the last one go by the first one's addresses and
-// store nothing.
-struct Col {
+// The V channels of a lane, two where they are one aligned word in every row, else
+// one.  Lanes past the last channel read the first one's values and store nothing.
+template <int V>
+struct Cols {
   uint32_t c;
   bool has;
+  __device__ __forceinline__ Cols(const RecurArgs& a, int32_t block) {
+    c = ((uint32_t)block * 64u + (threadIdx.x & 63u)) * V;
+    has = c < (uint32_t)a.C;
+    if (!has) c = 0;
+  }
 };
-__device__ __forceinline__ Col col_of(const RecurArgs& a, int32_t block) {
-  const uint32_t c = (uint32_t)block * kRecurCols + (threadIdx.x & 63u);
-  const bool has = c < (uint32_t)a.C;
-  return {has ? c : 0u, has};
-}
 
-// Rows t0 .. t0 + N - 1; past the last token the last one again.
-template <int N>
-__device__ __forceinline__ void rows(Col c, const uint16_t* t, int64_t stride, int32_t t0, int32_t S,
-                                     uint16_t (&v)[N]) {
+// A run's rows of BF16, addressed by a buffer resource at the first of them: the
+// lane's byte and a scalar offset per row, no address arithmetic in the lanes.  Rows
+// past the last token are out of the resource's range, as are lanes past the last
+// channel when they store: they read as zeros, and a store there is dropped.  The
+// host keeps offsets below 2^31.
+struct Run {
+  __amdgpu_buffer_rsrc_t r;
+  uint32_t stride;  // bytes
+  int32_t left;     // rows from the first to the last token
+  __device__ __forceinline__ Run(const uint16_t* base, int64_t stride_, int32_t t0, int32_t S)
+      : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base + (int64_t)t0 * stride_), (short)0, 0x7fffffff,
+                                            0x00020000)),
+        stride((uint32_t)stride_ * 2u), left(S - t0) {}
+  __device__ __forceinline__ int row(int j) const { return (int)(j < left ? (uint32_t)j * stride : 0x7fffffffu); }
+  template <int V>
+  __device__ __forceinline__ uint32_t get(const Cols<V>& c, int j) const {
+    if (V == 2) return __builtin_amdgcn_raw_buffer_load_b32(r, (int)(c.c * 2u), row(j), kOnce);
+    return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)(c.c * 2u), row(j), kOnce);
+  }
+  template <int V>
+  __device__ __forceinline__ void put(const Cols<V>& c, int j, const float (&v)[V]) const {
+    const int at = (int)(c.has ? c.c * 2u : 0x80000000u);
+    if (V == 2) __builtin_amdgcn_raw_buffer_store_b32(bf16_pack2(v[0], v[V - 1]), r, at, row(j), kOnce);
+    else __builtin_amdgcn_raw_buffer_store_b16(bf16_of(v[0]), r, at, row(j), kOnce);
+  }
+  // Nothing is read or written twice: loads and stores do not stay in the caches.
+  static constexpr int kOnce = 2;
+};
+
+template <int N, int V>
+__device__ __forceinline__ void rows(const Cols<V>& c, const uint16_t* t, int64_t stride, int32_t t0, int32_t S,
+                                     uint32_t (&v)[N]) {
+  const Run b(t, stride, t0, S);
 #pragma unroll
-  for (int j = 0; j < N; ++j) v[j] = (t + (int64_t)min(t0 + j, S - 1) * stride)[c.c];
+  for (int j = 0; j < N; ++j) v[j] = b.get(c, j);
+}
+// Channel v of a lane's word.
+template <int V>
+__device__ __forceinline__ float channel(uint32_t w, int v) {
+  return V == 2 && v ? bf16_hi(w) : bf16_lo(w);
 }
 
 // The documents that start or end among a tile's tokens.
 template <int T, bool kState>
 struct Starts {
-  uint32_t mask[T / 32 + 1];       // bit j: a document starts at token j of the tile
-  int32_t first[kState ? T + 1 : 1];  // the last entry of cu_seqlens that is token j: the document that starts there
-  int32_t last[kState ? T + 1 : 1];   // the first one; the document before it ends there
+  uint32_t mask[T / 32 + 1];          // bit j: a document starts at token j of the tile, or the last one ends before it
+  int32_t from[kState ? T + 1 : 1];   // the slot whose state the document that starts there goes on from, or -1
+  int32_t to[kState ? T + 1 : 1];     // the slot of the document that ends before it, or -1
 };
 
-template <int T, bool kState>
+template <int W, int T, bool kState>
 __device__ __forceinline__ void clear_starts(Starts<T, kState>& s) {
-  for (int i = threadIdx.x; i <= T; i += 64 * kW) {
+  for (int i = threadIdx.x; i <= T; i += 64 * W) {
     if (i <= T / 32) s.mask[i] = 0;
-    if (kState) s.first[i] = -1, s.last[i] = INT_MAX;
+    if (kState) s.from[i] = s.to[i] = -1;
   }
 }
 
-// All threads of the workgroup; the masks are complete after the next barrier.
-template <int T, bool kState>
+// All threads of the workgroup, an entry of cu_seqlens each and all its loads at
+// once; the result is complete after the next barrier.
+template <int W, int T, bool kState>
 __device__ __forceinline__ void find_starts(const RecurArgs& a, int32_t t0, Starts<T, kState>& s) {
   const int32_t entries = a.num_docs + 1;
-  int32_t e = entries > 64 * kW ? first_at_least(a.cu, entries, t0) : 0;
+  int32_t e = entries > 64 * W ? first_at_least(a.cu, entries, t0) : 0;
   e += threadIdx.x;
   while (true) {
-    int32_t v = INT_MAX;
+    int32_t v = INT_MAX, next = INT_MAX, past = INT_MAX, from = -1, to = -1;
     if (e < entries) v = a.cu[e];
+    if (kState && e < a.num_docs) {
+      next = a.cu[e + 1];
+      if (a.resume && a.resume[e]) from = a.index ? a.index[e] : e;
+    }
+    if (kState && e > 0 && e < entries) {
+      past = a.cu[e - 1];
+      to = a.index ? a.index[e - 1] : e - 1;
+    }
     const int64_t j = (int64_t)v - t0;
     if (v <= a.S && j >= 0 && j <= T) {
       atomicOr(&s.mask[j / 32], 1u << (j % 32));
-      if (kState) {
-        atomicMax(&s.first[j], e);
-        atomicMin(&s.last[j], e);
-      }
+      // Of the entries at one token the last is that of the document which starts
+      // there, and the first follows the one that ends; others are empty ones'.
+      if (kState && e < a.num_docs && next > v && from >= 0 && from < a.slots) s.from[j] = from;
+      if (kState && past < v && to >= 0 && to < a.slots) s.to[j] = to;
     }
     if (__ballot(e < entries && j <= T) == 0) return;
-    e += 64 * kW;
+    e += 64 * W;
   }
 }
 
@@ -154,6 +186,9 @@ constexpr uint32_t kEmpty = 0xffffffffu, kKnown = 0xfffffffeu;
 // Reads of a word before its reader gives up: about a second.  Only two calls that
 // share a workspace come here.
 constexpr int kPolls = 1 << 18;
+// How often a tile looks at the next W words for a known one, before it waits for
+// one.
+constexpr int kLooks = 2;
 
 __device__ __forceinline__ uint64_t word_of(float P, float H) {
   const uint32_t p = P != P ? 0x7fc00000u : __float_as_uint(P);
@@ -162,44 +197,90 @@ __device__ __forceinline__ uint64_t word_of(float P, float H) {
 __device__ __forceinline__ uint64_t known(float H) { return (uint64_t)kKnown << 32 | __float_as_uint(H); }
 __device__ __forceinline__ uint32_t mark(uint64_t w) { return (uint32_t)(w >> 32); }
 
-__device__ __forceinline__ void hand_on(uint64_t* p, uint64_t v) {
-  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+template <int V>
+__device__ __forceinline__ void hand_on(uint64_t* p, const uint64_t (&w)[V]) {
+#pragma unroll
+  for (int v = 0; v < V; ++v) __hip_atomic_store(p + v, w[v], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 // A wave's words once all of them are there, or once all are known.
-template <bool kAll>
-__device__ __forceinline__ uint64_t take(uint64_t* p) {
-  uint64_t v = 0;
+template <bool kAll, int V>
+__device__ __forceinline__ void take(uint64_t* p, uint64_t (&w)[V]) {
   for (int n = 0; n < kPolls; ++n) {
-    v = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (__ballot(kAll ? mark(v) != kKnown : mark(v) == kEmpty) == 0) break;
+    bool wait = false;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      w[v] = __hip_atomic_load(p + v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      wait |= kAll ? mark(w[v]) != kKnown : mark(w[v]) == kEmpty;
+    }
+    if (__ballot(wait) == 0) break;
     __builtin_amdgcn_s_sleep(1);
   }
-  return v;
 }
+
+// The words of the tiles before this one, W at a time, and which lanes have found a
+// known one among those of each time.
+template <int W, int V>
+struct Seen {
+  uint64_t w[kLooks * W][64][V];
+  uint64_t known[kLooks][V][W];
+};
 
 // What reaches this tile from those of lower numbers, `far` tiles of which there
 // are; `step` leads from a tile's words to those of the next lower number.  All
 // waves call it and have the result.
-__device__ __forceinline__ float look_back(uint64_t* words, int64_t step, int32_t far, uint64_t (&seen)[kW][64]) {
+template <int W, int V>
+__device__ __forceinline__ void look_back(uint64_t* words, int64_t step, int32_t far, Seen<W, V>& seen,
+                                          float (&carry)[V]) {
   const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64u), lane = threadIdx.x & 63;
-  seen[wave][lane] = wave < far ? take<false>(words + (wave + 1) * step) : known(0.0f);
-  __syncthreads();
-  bool found = false;
+  uint64_t missing[V];
 #pragma unroll
-  for (int w = 0; w < kW; ++w) found |= mark(seen[w][lane]) == kKnown;
-  if (__ballot(!found) != 0) {  // the same in all waves; there are more than eight tiles
+  for (int v = 0; v < V; ++v) missing[v] = ~(uint64_t)0;
+  int32_t looks = 0;
+  bool all = false;  // the same in all waves
+#pragma unroll 1
+  while (looks < kLooks && !all) {
+    const int32_t d = looks * W + wave;
+    uint64_t w[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) w[v] = known(0.0f);
+    if (d < far) take<false>(words + (int64_t)(d + 1) * step, w);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      seen.w[d][lane][v] = w[v];
+      seen.known[looks][v][wave] = __ballot(mark(w[v]) == kKnown);
+    }
     __syncthreads();
-    if (wave == kW - 1) seen[wave][lane] = take<true>(words + kW * step);
+    all = true;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      uint64_t k = seen.known[looks][v][lane % W];
+#pragma unroll
+      for (int i = 1; i < W; i <<= 1) k |= __shfl_xor(k, i, 64);
+      missing[v] &= ~k;
+      all &= __builtin_amdgcn_readfirstlane((uint32_t)missing[v] | (uint32_t)(missing[v] >> 32)) == 0;
+    }
+    ++looks;
+  }
+  if (!all) {  // so there are more than kLooks * W of them
+    __syncthreads();
+    if (wave == W - 1) {
+      uint64_t w[V];
+      take<true>(words + (int64_t)(kLooks * W) * step, w);
+#pragma unroll
+      for (int v = 0; v < V; ++v) seen.w[kLooks * W - 1][lane][v] = w[v];
+    }
     __syncthreads();
   }
-  float carry = 0.0f;
 #pragma unroll
-  for (int w = kW - 1; w >= 0; --w) {
-    const uint64_t v = seen[w][lane];
-    const float H = __uint_as_float((uint32_t)v), P = __uint_as_float(mark(v));
-    carry = mark(v) == kKnown ? H : __builtin_fmaf(P, carry, H);
-  }
-  return carry;
+  for (int v = 0; v < V; ++v) carry[v] = 0.0f;
+#pragma unroll 4
+  for (int d = looks * W - 1; d >= 0; --d)
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const uint64_t w = seen.w[d][lane][v];
+      const float H = __uint_as_float((uint32_t)w), P = __uint_as_float(mark(w));
+      carry[v] = mark(w) == kKnown ? H : __builtin_fmaf(P, carry[v], H);
+    }
 }
 
 // The tile of this workgroup: its number and channel block.
@@ -217,16 +298,19 @@ __device__ __forceinline__ Place place_of(const RecurArgs& a, uint32_t* lds) {
 
 // Documents without tokens leave zeros, or their slot as it is where they resume;
 // part `k` of `parts`.
-__device__ __forceinline__ void empty_documents(const RecurArgs& a, int32_t k, int32_t parts, Col c) {
+template <int W, int V>
+__device__ __forceinline__ void empty_documents(const RecurArgs& a, int32_t k, int32_t parts, const Cols<V>& c) {
   const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64u), lane = threadIdx.x & 63;
   const int64_t per = ((int64_t)a.num_docs + parts - 1) / parts, end = min((k + 1) * per, (int64_t)a.num_docs);
-  for (int64_t d0 = k * per + wave * 64; d0 < end; d0 += 64 * kW) {
+  for (int64_t d0 = k * per + wave * 64; d0 < end; d0 += 64 * W) {
     const int64_t d = d0 + lane;
     bool empty = false;
     if (d < end) empty = a.cu[d] == a.cu[d + 1] && !(a.resume && a.resume[d]);
     for (uint64_t m = __ballot(empty); m; m &= m - 1) {
       const int64_t slot = slot_of(a.index, d0 + __builtin_ctzll(m), a.slots);
-      if (slot >= 0 && c.has) a.state[slot * a.C + c.c] = 0.0f;
+      if (slot >= 0 && c.has)
+#pragma unroll
+        for (int v = 0; v < V; ++v) a.state[slot * a.C + c.c + v] = 0.0f;
     }
   }
 }
@@ -238,238 +322,355 @@ __global__ __launch_bounds__(256) void recur_clear_kernel(RecurArgs a, int64_t w
 }
 
 // No tokens, but documents that leave their states.
-__global__ __launch_bounds__(64 * kW) void recur_empty_kernel(RecurArgs a) {
-  empty_documents(a, 0, 1, col_of(a, blockIdx.x));
+__global__ __launch_bounds__(512) void recur_empty_kernel(RecurArgs a) {
+  empty_documents<8>(a, 0, 1, Cols<1>(a, blockIdx.x));
 }
 
-// Runs of a tile for which `bit` says so, as a mask.
-template <int N, class F>
-__device__ __forceinline__ uint32_t runs(const uint32_t* mask, F bit) {
-  uint32_t m = 0;
+// The runs of a tile that have any of the bits kFrom .. kTo of theirs set, as a mask.
+template <int N, int W, int kFrom, int kTo>
+__device__ __forceinline__ uint32_t runs_with(const uint32_t* mask) {
+  uint32_t w[W * N / 32 + 1], m = 0;
 #pragma unroll
-  for (int w = 0; w < kW; ++w) m |= bit(bits_at<N>(mask, w * N)) ? 1u << w : 0u;
+  for (int k = 0; k <= W * N / 32; ++k) w[k] = __builtin_amdgcn_readfirstlane(mask[k]);
+#pragma unroll
+  for (int k = 0; k < W; ++k) {
+    const int at = k * N;
+    constexpr uint32_t low = ((kTo < N ? 2u << kTo : 1u << N) - 1u) & ~((1u << kFrom) - 1u);
+    bool any = (w[at / 32] >> (at % 32) & low) != 0;
+    if (kTo == N) any |= (w[(at + N) / 32] >> ((at + N) % 32) & 1u) != 0;
+    m |= any ? 1u << k : 0u;
+  }
   return m;
 }
 
-template <bool kGate, bool kState>
-__global__ __launch_bounds__(64 * kW) __attribute__((amdgpu_waves_per_eu(4)))
+// V channels a lane, W waves with a run of N tokens each.  Everything between the
+// loads and the stores is in registers: with more of them than 128 a second workgroup
+// does not fit on a CU, and fewer tokens a tile make more words to hand on.
+template <int V, int N, int W, bool kGate, bool kState>
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4)))
 void recur_fwd_kernel(RecurArgs a) {
-  constexpr int N = kRecurFwdRun, T = kRecurFwdTile;
+  constexpr int T = N * W;
+  static_assert(T == kRecurFwdTile && kRecurKeep % N == 0, "");
   __shared__ Starts<T, kState> docs;
-  __shared__ float2 sums[kW][64];  // P and H of the waves' runs
-  __shared__ uint64_t seen[kW][64];
+  __shared__ float2 sums[W][64][V];  // P and H of the waves' runs
+  __shared__ Seen<W, V> seen;
   __shared__ uint32_t ticket;
-  clear_starts(docs);
+  clear_starts<W>(docs);
   const Place p = place_of(a, &ticket);
   const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64u), lane = threadIdx.x & 63;
   const int32_t tile0 = p.n * T, t0 = tile0 + wave * N;
-  const Col c = col_of(a, p.block);
-  uint16_t x[N], r[N], i[N], z[N];
+  const Cols<V> c(a, p.block);
+  uint32_t x[N], r[N], i[N], z[N];
   rows(c, a.r, a.rs, t0, a.S, r);
   rows(c, a.i, a.is, t0, a.S, i);
   rows(c, a.x, a.xs, t0, a.S, x);
   if (kGate) rows(c, a.z, a.zs, t0, a.S, z);
-  const float rate = decay_rate(a, c.c);
-  find_starts(a, tile0, docs);
-  if (kState) empty_documents(a, p.n, a.tiles, c);
+  float rate[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) rate[v] = decay_rate(a, c.c + v);
+  find_starts<W>(a, tile0, docs);
+  if (kState) empty_documents<W>(a, p.n, a.tiles, c);
   __syncthreads();
   const uint32_t bits = bits_at<N>(docs.mask, wave * N), own = bits & ((1u << N) - 1u);
 
-  float A[N], B[N];
+  float A[N][V], B[N][V];
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    const float u = decay_step(rate, sigmoid_f32(bf16_f32(r[j])));
-    const Decay g = decay_from(u, decay_of(u));
-    A[j] = g.a;
-    B[j] = input_of(g, sigmoid_f32(bf16_f32(i[j])), bf16_f32(x[j]));
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float u = rate[v] * sigmoid_f32(channel<V>(r[j], v));
+      A[j][v] = decay_of(u);
+      B[j][v] = gated(input_scale(u, A[j][v]), sigmoid_f32(channel<V>(i[j], v)) * channel<V>(x[j], v));
+    }
+    if (j % 2) __builtin_amdgcn_sched_barrier(0);  // no more tokens side by side than registers hold
   }
   // A resumed document goes on from its slot's state.
   if (kState && a.resume && own) {
 #pragma unroll
     for (int j = 0; j < N; ++j)
       if (own >> j & 1u) {
-        const int32_t d = __builtin_amdgcn_readfirstlane(docs.first[wave * N + j]);
-        const bool go_on = d >= 0 && d < a.num_docs && __builtin_amdgcn_readfirstlane((int32_t)a.resume[d]) != 0;
-        const int64_t slot = go_on ? slot_of(a.index, d, a.slots) : -1;
-        if (slot >= 0) B[j] = __builtin_fmaf(A[j], a.state[slot * a.C + c.c], B[j]);
+        const int64_t slot = __builtin_amdgcn_readfirstlane(docs.from[wave * N + j]);
+        if (slot >= 0)
+#pragma unroll
+          for (int v = 0; v < V; ++v) B[j][v] = __builtin_fmaf(A[j][v], a.state[slot * a.C + c.c + v], B[j][v]);
       }
   }
-  float P = 1.0f, H = 0.0f;
 #pragma unroll
-  for (int j = 0; j < N; ++j) {
-    P *= A[j];
-    H = own >> j & 1u ? B[j] : __builtin_fmaf(A[j], H, B[j]);
+  for (int v = 0; v < V; ++v) {
+    float P = 1.0f, H = 0.0f;
+    if (own == 0) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) P *= A[j][v], H = __builtin_fmaf(A[j][v], H, B[j][v]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) H = own >> j & 1u ? B[j][v] : __builtin_fmaf(A[j][v], H, B[j][v]);
+    }
+    sums[wave][lane][v] = {P, H};
   }
-  sums[wave][lane] = {P, H};
   __syncthreads();
 
-  const uint32_t starts = runs<N>(docs.mask, [](uint32_t b) { return (b & ((1u << N) - 1u)) != 0; });
-  uint64_t* const mine = a.words + ((int64_t)p.n * a.blocks + p.block) * kRecurCols + lane;
-  const bool waits = p.n > 0 && (docs.mask[0] & 1u) == 0;  // on what comes from the left
-  const bool cut = !waits || starts != 0;                  // the tile's last state does not go by it
+  const uint32_t starts = runs_with<N, W, 0, N - 1>(docs.mask);
+  uint64_t* const mine = a.words + (int64_t)p.n * a.cols + (p.block * 64 + lane) * V;
+  const bool waits = p.n > 0 && (__builtin_amdgcn_readfirstlane(docs.mask[0]) & 1u) == 0;  // on what comes from the left
+  const bool cut = !waits || starts != 0;  // the tile's last state does not go by it
   const bool hands = wave == 0 && p.n + 1 < a.tiles;
-  float tp = 1.0f, th = 0.0f;
+  float tp[V], th[V];
   if (hands) {
+    uint64_t w[V];
 #pragma unroll
-    for (int w = 0; w < kW; ++w) {
-      const float2 s = sums[w][lane];
-      th = starts >> w & 1u ? s.y : __builtin_fmaf(s.x, th, s.y);
-      tp *= s.x;
-    }
-    hand_on(mine, cut ? known(th) : word_of(tp, th));
+    for (int v = 0; v < V; ++v) tp[v] = 1.0f, th[v] = 0.0f;
+#pragma unroll 2
+    for (int k = 0; k < W; ++k)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float2 s = sums[k][lane][v];
+        th[v] = starts >> k & 1u ? s.y : __builtin_fmaf(s.x, th[v], s.y);
+        tp[v] *= s.x;
+      }
+#pragma unroll
+    for (int v = 0; v < V; ++v) w[v] = cut ? known(th[v]) : word_of(tp[v], th[v]);
+    hand_on(mine, w);
   }
-  float h = 0.0f;
+  float h[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) h[v] = 0.0f;
   if (waits) {
-    h = look_back(mine, -(int64_t)a.blocks * kRecurCols, p.n, seen);
-    if (hands && !cut) hand_on(mine, known(__builtin_fmaf(tp, h, th)));
+    look_back(mine, -(int64_t)a.cols, p.n, seen, h);
+    if (hands && !cut) {
+      uint64_t w[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) w[v] = known(__builtin_fmaf(tp[v], h[v], th[v]));
+      hand_on(mine, w);
+    }
   }
-  for (int w = 0; w < wave; ++w) {
-    const float2 s = sums[w][lane];
-    h = starts >> w & 1u ? s.y : __builtin_fmaf(s.x, h, s.y);
-  }
-  if (a.keep && t0 % kRecurKeep == 0 && t0 < a.S && c.has) a.keep[(int64_t)(t0 / kRecurKeep) * a.C + c.c] = h;
+#pragma unroll 2
+  for (int k = 0; k < wave; ++k)
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float2 s = sums[k][lane][v];
+      h[v] = starts >> k & 1u ? s.y : __builtin_fmaf(s.x, h[v], s.y);
+    }
+  if (a.keep && t0 % kRecurKeep == 0 && t0 < a.S && c.has)
+#pragma unroll
+    for (int v = 0; v < V; ++v) a.keep[(int64_t)(t0 / kRecurKeep) * a.C + c.c + v] = h[v];
 
 #pragma unroll
+  for (int v = 0; v < V; ++v) {
+    if (own == 0) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) h[v] = B[j][v] = __builtin_fmaf(A[j][v], h[v], B[j][v]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        h[v] = B[j][v] = own >> j & 1u ? B[j][v] : __builtin_fmaf(A[j][v], h[v], B[j][v]);
+    }
+  }
+  const Run y(a.y, a.C, t0, a.S);
+#pragma unroll
   for (int j = 0; j < N; ++j) {
-    h = own >> j & 1u ? B[j] : __builtin_fmaf(A[j], h, B[j]);
-    float y = h;
-    if (kGate) {
-      const float zj = bf16_f32(z[j]);
-      y *= zj * sigmoid_f32(zj);
+    float o[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float zj = kGate ? channel<V>(z[j], v) : 0.0f;
+      o[v] = kGate ? B[j][v] * (zj * sigmoid_f32(zj)) : B[j][v];
     }
-    if (t0 + j < a.S && c.has) (a.y + (int64_t)(t0 + j) * a.C)[c.c] = bf16_of(y);
-    if (kState && bits >> (j + 1) & 1u) {
-      const int32_t d = __builtin_amdgcn_readfirstlane(docs.last[wave * N + j + 1]) - 1;
-      const int64_t slot = d >= 0 && d < a.num_docs ? slot_of(a.index, d, a.slots) : -1;
-      if (slot >= 0 && c.has) a.state[slot * a.C + c.c] = h;
-    }
+    y.put(c, j, o);
+  }
+  // Documents that end leave their states.
+  if (kState && bits >> 1) {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (bits >> (j + 1) & 1u) {
+        const int64_t slot = __builtin_amdgcn_readfirstlane(docs.to[wave * N + j + 1]);
+        if (slot >= 0 && c.has)
+#pragma unroll
+          for (int v = 0; v < V; ++v) a.state[slot * a.C + c.c + v] = B[j][v];
+      }
   }
 }
 
-template <bool kGate>
-__global__ __launch_bounds__(64 * kW) __attribute__((amdgpu_waves_per_eu(4)))
+// dy silu'(z) waits for the states in LDS: with it in registers two workgroups fit on
+// a CU instead of three.
+template <int V, int N, int W, bool kGate>
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(3)))
 void recur_bwd_kernel(RecurArgs a) {
-  constexpr int N = kRecurBwdRun, T = kRecurBwdTile;
+  constexpr int T = N * W;
+  static_assert(T == kRecurBwdTile, "");
   __shared__ Starts<T, false> docs;
-  __shared__ float2 sums[kW][64];  // P and H of the waves' runs
-  __shared__ float sent[kW][64];   // what a run sends to its left without any from its right
-  __shared__ uint64_t seen[kW][64];
+  __shared__ float2 sums[W][64][V];  // P and H of the waves' runs
+  __shared__ float sent[W][64][V];   // what a run sends to its left without any from its right
+  __shared__ Seen<W, V> seen;
+  __shared__ float gate[kGate ? W : 1][N][V][64];
   __shared__ uint32_t ticket;
-  clear_starts(docs);
+  clear_starts<W>(docs);
   const Place p = place_of(a, &ticket);
   const int32_t k = a.tiles - 1 - p.n;  // the last tile first
   const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64u), lane = threadIdx.x & 63;
   const int32_t tile0 = k * T, t0 = tile0 + wave * N;
-  const Col c = col_of(a, p.block);
-  uint16_t x[N], r[N], i[N], z[N], dy[N];
+  const Cols<V> c(a, p.block);
+  uint32_t x[N], r[N], i[N], zw[N], dy[N];
   rows(c, a.r, a.rs, t0, a.S, r);
   rows(c, a.i, a.is, t0, a.S, i);
   rows(c, a.x, a.xs, t0, a.S, x);
-  if (kGate) rows(c, a.z, a.zs, t0, a.S, z);
+  if (kGate) rows(c, a.z, a.zs, t0, a.S, zw);
   rows(c, a.dy, a.dys, t0, a.S, dy);
-  float h = a.keep[(int64_t)k * a.C + c.c];
-  const float rate = decay_rate(a, c.c);
-  find_starts(a, tile0, docs);
+  float h[V], rate[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    h[v] = a.keep[(int64_t)k * a.C + c.c + v];
+    rate[v] = decay_rate(a, c.c + v);
+  }
+  find_starts<W>(a, tile0, docs);
   __syncthreads();
   const uint32_t bits = bits_at<N>(docs.mask, wave * N);
 
-  float A[N], B[N], si[N], sr[N], g[N];
-  float P = 1.0f, H = 0.0f, M = 0.0f;
+  float A[N][V], B[N][V], m[N][V], sr[N][V], si[N][V], g[N][V];
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    sr[j] = sigmoid_f32(bf16_f32(r[j]));
-    si[j] = sigmoid_f32(bf16_f32(i[j]));
-    const float u = decay_step(rate, sr[j]);
-    const Decay d = decay_from(u, decay_of(u));
-    A[j] = d.a;
-    B[j] = input_of(d, si[j], bf16_f32(x[j]));
-    g[j] = bf16_f32(dy[j]);
-    if (kGate) {
-      const float zj = bf16_f32(z[j]);
-      g[j] *= zj * sigmoid_f32(zj);
-    }
-    if (t0 + j >= a.S) g[j] = 0.0f;  // rows past the last token send nothing
-    P *= A[j];
-    H = bits >> j & 1u ? B[j] : __builtin_fmaf(A[j], H, B[j]);
-  }
 #pragma unroll
-  for (int j = N - 1; j >= 0; --j) M = A[j] * (bits >> (j + 1) & 1u ? g[j] : g[j] + M);
-  sums[wave][lane] = {P, H};
-  sent[wave][lane] = M;
-  __syncthreads();
-
-  const uint32_t starts = runs<N>(docs.mask, [](uint32_t b) { return (b & ((1u << N) - 1u)) != 0; });
-  // Runs with a start behind their first token, up to the token after them: nothing
-  // from the right gets through.
-  const uint32_t shut = runs<N>(docs.mask, [](uint32_t b) { return b >> 1 != 0; });
-  uint64_t* const mine = a.words + ((int64_t)k * a.blocks + p.block) * kRecurCols + lane;
-  const bool waits = p.n > 0 && (docs.mask[T / 32] & 1u) == 0;
-  const bool cut = !waits || shut != 0;
-  const bool hands = wave == 0 && p.n + 1 < a.tiles;
-  float tp = 1.0f, tm = 0.0f;
-  if (hands) {
-#pragma unroll
-    for (int w = kW - 1; w >= 0; --w) {
-      const float s = sums[w][lane].x, m = sent[w][lane];
-      tm = shut >> w & 1u ? m : __builtin_fmaf(s, tm, m);
-      tp *= s;
-    }
-    hand_on(mine, cut ? known(tm) : word_of(tp, tm));
-  }
-  // The states before this run, from the one that the forward kept.
-  for (int w = 0; w < wave; ++w) {
-    const float2 s = sums[w][lane];
-    h = starts >> w & 1u ? s.y : __builtin_fmaf(s.x, h, s.y);
-  }
-#pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const float before = bits >> j & 1u ? 0.0f : h;
-    h = bits >> j & 1u ? B[j] : __builtin_fmaf(A[j], h, B[j]);
-    B[j] = before;  // from here on the state before the token
-    if (kGate) {
-      const float zj = bf16_f32(z[j]), dz = bf16_f32(dy[j]) * h * dsilu_f32(zj, sigmoid_f32(zj));
-      if (t0 + j < a.S && c.has) (a.dz + (int64_t)(t0 + j) * a.C)[c.c] = bf16_of(dz);
-    }
-  }
-
-  float m = 0.0f;
-  if (waits) {
-    m = look_back(mine, (int64_t)a.blocks * kRecurCols, p.n, seen);
-    if (hands && !cut) hand_on(mine, known(__builtin_fmaf(tp, m, tm)));
-  }
-  for (int w = kW - 1; w > wave; --w) {
-    const float o = sent[w][lane];
-    m = shut >> w & 1u ? o : __builtin_fmaf(sums[w][lane].x, m, o);
-  }
-  float sum = 0.0f;
-#pragma unroll
-  for (int j = N - 1; j >= 0; --j) {
-    const float l = bits >> (j + 1) & 1u ? g[j] : g[j] + m;
-    const Decay d = decay_from(decay_step(rate, sr[j]), A[j]);
-    const float xj = bf16_f32(x[j]), half = 0.5f * d.u;
-    m = d.a * l;
-    const float dx = l * d.m * si[j];
-    const float di = d.rm == 0.0f ? 0.0f : dx * xj * (1.0f - si[j]);
-    const float in = d.rm == 0.0f ? 0.0f : si[j] * xj * (d.a * d.a) * (half * d.rm);
-    const float E = l * __builtin_fmaf(-half * d.a, B[j], in);
-    if (t0 + j < a.S) {
-      sum += E;
-      if (c.has) {
-        const int64_t at = (int64_t)(t0 + j) * a.C;
-        (a.dx + at)[c.c] = bf16_of(dx);
-        (a.di + at)[c.c] = bf16_of(di);
-        (a.dr + at)[c.c] = bf16_of(E * (1.0f - sr[j]));
+    for (int v = 0; v < V; ++v) {
+      sr[j][v] = sigmoid_f32(channel<V>(r[j], v));
+      si[j][v] = sigmoid_f32(channel<V>(i[j], v));
+      const float u = rate[v] * sr[j][v];
+      A[j][v] = decay_of(u);
+      m[j][v] = input_scale(u, A[j][v]);
+      B[j][v] = gated(m[j][v], si[j][v] * channel<V>(x[j], v));
+      g[j][v] = channel<V>(dy[j], v);
+      if (kGate) {
+        // dy silu(z), the gradient at the state, and dy silu'(z), dz but for the state
+        const float zj = channel<V>(zw[j], v), s = sigmoid_f32(zj), dyj = g[j][v];
+        g[j][v] = dyj * (zj * s);
+        gate[wave][j][v][lane] = dyj * dsilu_f32(zj, s);
       }
     }
+    if (j % 2) __builtin_amdgcn_sched_barrier(0);
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    float P = 1.0f, H = 0.0f, M = 0.0f;
+    if (bits == 0) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) P *= A[j][v], H = __builtin_fmaf(A[j][v], H, B[j][v]);
+#pragma unroll
+      for (int j = N - 1; j >= 0; --j) M = A[j][v] * (g[j][v] + M);
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        P *= A[j][v];
+        H = bits >> j & 1u ? B[j][v] : __builtin_fmaf(A[j][v], H, B[j][v]);
+      }
+#pragma unroll
+      for (int j = N - 1; j >= 0; --j) M = A[j][v] * (bits >> (j + 1) & 1u ? g[j][v] : g[j][v] + M);
+    }
+    sums[wave][lane][v] = {P, H};
+    sent[wave][lane][v] = M;
+  }
+  __syncthreads();
+
+  const uint32_t starts = runs_with<N, W, 0, N - 1>(docs.mask);
+  // Runs with a start behind their first token, up to the token after them: nothing
+  // from the right gets through.
+  const uint32_t shut = runs_with<N, W, 1, N>(docs.mask);
+  uint64_t* const mine = a.words + (int64_t)k * a.cols + (p.block * 64 + lane) * V;
+  const bool waits = p.n > 0 && (__builtin_amdgcn_readfirstlane(docs.mask[T / 32]) & 1u) == 0;
+  const bool cut = !waits || shut != 0;
+  const bool hands = wave == 0 && p.n + 1 < a.tiles;
+  float tp[V], tm[V];
+  if (hands) {
+    uint64_t w[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) tp[v] = 1.0f, tm[v] = 0.0f;
+#pragma unroll 2
+    for (int q = W - 1; q >= 0; --q)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float s = sums[q][lane][v].x, o = sent[q][lane][v];
+        tm[v] = shut >> q & 1u ? o : __builtin_fmaf(s, tm[v], o);
+        tp[v] *= s;
+      }
+#pragma unroll
+    for (int v = 0; v < V; ++v) w[v] = cut ? known(tm[v]) : word_of(tp[v], tm[v]);
+    hand_on(mine, w);
+  }
+  // The states before this run, from the one that the forward kept.
+#pragma unroll 2
+  for (int q = 0; q < wave; ++q)
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float2 s = sums[q][lane][v];
+      h[v] = starts >> q & 1u ? s.y : __builtin_fmaf(s.x, h[v], s.y);
+    }
+  const Run dz(a.dz, a.C, t0, a.S);
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const bool first = bits >> j & 1u;
+    float o[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float before = first ? 0.0f : h[v];
+      h[v] = first ? B[j][v] : __builtin_fmaf(A[j][v], h[v], B[j][v]);
+      B[j][v] = before;  // from here on the state before the token
+      o[v] = kGate ? gate[wave][j][v][lane] * h[v] : 0.0f;
+    }
+    if (kGate) dz.put(c, j, o);
+  }
+
+  float l[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) l[v] = 0.0f;
+  if (waits) {
+    look_back(mine, (int64_t)a.cols, p.n, seen, l);
+    if (hands && !cut) {
+      uint64_t w[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) w[v] = known(__builtin_fmaf(tp[v], l[v], tm[v]));
+      hand_on(mine, w);
+    }
+  }
+#pragma unroll 2
+  for (int q = W - 1; q > wave; --q)
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float o = sent[q][lane][v];
+      l[v] = shut >> q & 1u ? o : __builtin_fmaf(sums[q][lane][v].x, l[v], o);
+    }
+  const Run dx(a.dx, a.C, t0, a.S), di(a.di, a.C, t0, a.S), dr(a.dr, a.C, t0, a.S);
+  float sum[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) sum[v] = 0.0f;
+#pragma unroll
+  for (int j = N - 1; j >= 0; --j) {
+    float ox[V], oi[V], orr[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float xj = channel<V>(x[j], v);
+      l[v] = bits >> (j + 1) & 1u ? g[j][v] : g[j][v] + l[v];
+      ox[v] = gated(m[j][v], l[v]) * si[j][v];
+      oi[v] = gated(ox[v], xj) * (1.0f - si[j][v]);
+      // u / 2 and u / (2 m): without a step the first is 0, or too small to matter
+      const float half = 0.5f * rate[v] * sr[j][v];
+      const float w = half * __builtin_amdgcn_rcpf(__builtin_fmaxf(m[j][v], 0x1p-60f));
+      const float E = l[v] * __builtin_fmaf(-half * A[j][v], B[j][v], gated(A[j][v] * A[j][v] * w, si[j][v] * xj));
+      sum[v] += E;
+      orr[v] = E * (1.0f - sr[j][v]);
+      l[v] *= A[j][v];
+    }
+    dx.put(c, j, ox);
+    di.put(c, j, oi);
+    dr.put(c, j, orr);
   }
   // The tile's partial sum: its waves' in order.
   __syncthreads();
-  sent[wave][lane] = sum;
+#pragma unroll
+  for (int v = 0; v < V; ++v) sent[wave][lane][v] = sum[v];
   __syncthreads();
   if (wave > 0 || !c.has) return;
 #pragma unroll
-  for (int w = 1; w < kW; ++w) sum += sent[w][lane];
-  a.part[(int64_t)k * a.C + c.c] = sum;
+  for (int v = 0; v < V; ++v) {
+#pragma unroll 4
+    for (int q = 1; q < W; ++q) sum[v] += sent[q][lane][v];
+    a.part[(int64_t)k * a.C + c.c + v] = sum[v];
+  }
 }
 
 // The tiles' sums of E in FP64, sixteen waves a part of the tiles each.
@@ -503,55 +704,141 @@ __global__ __launch_bounds__(1024) void recur_bwd_sum_kernel(RecurArgs a) {
 
 // ----------------------------------------------------------- single tokens --
 
-__global__ __launch_bounds__(64) void recur_step_kernel(RecurArgs a) {
-  const int64_t blocks = (a.C + 63) / 64, row = blockIdx.x / blocks;
-  const int64_t c = (blockIdx.x - row * blocks) * 64 + threadIdx.x;
-  const int64_t slot = slot_of(a.index, row, a.slots);
-  if (c >= a.C) return;
-  float y = 0.0f;
-  if (slot >= 0) {
-    const float u = decay_step(decay_rate(a, c), sigmoid_f32(bf16_f32(a.r[row * a.rs + c])));
-    const Decay g = decay_from(u, decay_of(u));
-    const float b = input_of(g, sigmoid_f32(bf16_f32(a.i[row * a.is + c])), bf16_f32(a.x[row * a.xs + c]));
-    float* p = a.state + slot * a.C + c;
-    y = __builtin_fmaf(g.a, *p, b);
-    *p = y;
-    if (a.z) {
-      const float z = bf16_f32(a.z[row * a.zs + c]);
-      y *= z * sigmoid_f32(z);
-    }
+// V channels a lane, kept over several rows, two of which are under way at a time:
+// their decay's rate is computed once.  Bound by HBM for many rows, 18 bytes a row and
+// channel with a gate, by the host for few.
+template <int V>
+struct StepRow {
+  int64_t slot;
+  uint32_t x[(V + 1) / 2], r[(V + 1) / 2], i[(V + 1) / 2], z[(V + 1) / 2];
+  float h[V];
+};
+// Two at a time; a state's values and the inputs are used once.
+template <int V>
+__device__ __forceinline__ void step_words(const uint16_t* p, uint32_t (&w)[(V + 1) / 2]) {
+  if constexpr (V == 4) {
+    const u32x2_t v = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(p));
+    w[0] = v[0], w[1] = v[1];
+  } else {
+    w[0] = *p;
   }
-  a.y[row * a.C + c] = bf16_of(y);
+}
+template <int V>
+__device__ __forceinline__ void step_load(const RecurArgs& a, int64_t row, int64_t c, StepRow<V>* s) {
+  s->slot = slot_of(a.index, row, a.slots);
+  if (s->slot < 0) return;
+  step_words<V>(a.x + row * a.xs + c, s->x);
+  step_words<V>(a.r + row * a.rs + c, s->r);
+  step_words<V>(a.i + row * a.is + c, s->i);
+  if (a.z) step_words<V>(a.z + row * a.zs + c, s->z);
+  const float* p = a.state + s->slot * a.C + c;
+  if constexpr (V == 4) {
+    const f32x4_t v = __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(p));
+#pragma unroll
+    for (int k = 0; k < V; ++k) s->h[k] = v[k];
+  } else {
+    s->h[0] = *p;
+  }
+}
+template <int V>
+__device__ __forceinline__ void step_row(const RecurArgs& a, int64_t row, int64_t c, const float (&rate)[V],
+                                         const StepRow<V>& s) {
+  float h[V], y[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    auto value = [&](const uint32_t* w) { return k % 2 ? bf16_hi(w[k / 2]) : bf16_lo(w[k / 2]); };
+    const float u = rate[k] * sigmoid_f32(value(s.r)), decay = decay_of(u);
+    h[k] = __builtin_fmaf(decay, s.h[k], gated(input_scale(u, decay), sigmoid_f32(value(s.i)) * value(s.x)));
+    y[k] = h[k];
+    if (a.z) {
+      const float z = value(s.z);
+      y[k] *= z * sigmoid_f32(z);
+    }
+    if (s.slot < 0) y[k] = 0.0f;
+  }
+  uint16_t* out = a.y + row * a.C + c;
+  float* p = a.state + s.slot * a.C + c;
+  if constexpr (V == 4) {
+    const u32x2_t w = {bf16_pack2(y[0], y[1]), bf16_pack2(y[2], y[3])};
+    __builtin_nontemporal_store(w, reinterpret_cast<u32x2_t*>(out));
+    if (s.slot >= 0) __builtin_nontemporal_store((f32x4_t){h[0], h[1], h[2], h[3]}, reinterpret_cast<f32x4_t*>(p));
+  } else {
+    *out = bf16_of(y[0]);
+    if (s.slot >= 0) *p = h[0];
+  }
+}
+
+template <int V>
+__global__ __launch_bounds__(256) void recur_step_kernel(RecurArgs a, int32_t rows) {
+  const int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64u);
+  const int64_t row0 = w / a.blocks * rows, c = ((w % a.blocks) * 64 + (threadIdx.x & 63)) * V;
+  const int64_t row1 = min(row0 + rows, (int64_t)a.S);
+  if (row0 >= a.S || c >= a.C) return;
+  float rate[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) rate[k] = decay_rate(a, c + k);
+  int64_t row = row0;
+#pragma unroll 1
+  for (; row + 2 <= row1; row += 2) {
+    StepRow<V> s, t;
+    step_load(a, row, c, &s);
+    step_load(a, row + 1, c, &t);
+    step_row(a, row, c, rate, s);
+    step_row(a, row + 1, c, rate, t);
+  }
+  if (row < row1) {
+    StepRow<V> s;
+    step_load(a, row, c, &s);
+    step_row(a, row, c, rate, s);
+  }
 }
 
 // ------------------------------------------------------------------ launch --
 
-dim3 tile_grid(const RecurArgs& a) { return dim3((uint32_t)((int64_t)a.tiles * a.blocks)); }
+bool pairs(const uint16_t* p, int64_t stride) {
+  return reinterpret_cast<uintptr_t>(p) % 4 == 0 && stride % 2 == 0;
+}
 
-template <bool kGate>
-void launch_fwd_gate(const RecurArgs& a, hipStream_t s) {
-  if (a.state) hipLaunchKernelGGL((recur_fwd_kernel<kGate, true>), tile_grid(a), dim3(64 * kW), 0, s, a);
-  else hipLaunchKernelGGL((recur_fwd_kernel<kGate, false>), tile_grid(a), dim3(64 * kW), 0, s, a);
+// Forward, whether a lane has two channels: they have to be one aligned word in every
+// row.  Lines of 256 bytes are faster to read (16384 tokens, C = 4096, a gate: 159
+// against 182 us), but of few channels a tile's way to the next one is longer
+// (65536 tokens, C = 100: 65 against 49).
+bool pairs(const RecurArgs& a) {
+  return a.C > 128 && a.C % 2 == 0 && pairs(a.x, a.xs) && pairs(a.r, a.rs) && pairs(a.i, a.is) &&
+         pairs(a.z, a.z ? a.zs : 0) && pairs(a.y, 0);
+}
+
+template <int V, bool kGate>
+void launch_fwd(RecurArgs a, hipStream_t s) {
+  a.blocks = (a.C + 64 * V - 1) / (64 * V);
+  const dim3 grid((uint32_t)((int64_t)a.tiles * a.blocks)), block(512);
+  if (a.state) hipLaunchKernelGGL((recur_fwd_kernel<V, 16, 8, kGate, true>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((recur_fwd_kernel<V, 16, 8, kGate, false>), grid, block, 0, s, a);
 }
 
 }  // namespace
 
 hipError_t launch_recur_clear(const RecurArgs& a, hipStream_t s) {
-  const int64_t words = (int64_t)a.tiles * a.blocks * kRecurCols;
+  const int64_t words = (int64_t)a.tiles * a.cols;
   hipLaunchKernelGGL(recur_clear_kernel, dim3((uint32_t)((words + 511) / 512)), dim3(256), 0, s, a, words);
   return hipGetLastError();
 }
 
 hipError_t launch_recur_fwd(const RecurArgs& a, hipStream_t s) {
-  if (a.S == 0) hipLaunchKernelGGL(recur_empty_kernel, dim3((uint32_t)a.blocks), dim3(64 * kW), 0, s, a);
-  else if (a.z) launch_fwd_gate<true>(a, s);
-  else launch_fwd_gate<false>(a, s);
+  if (a.S == 0) hipLaunchKernelGGL(recur_empty_kernel, dim3((uint32_t)((a.C + 63) / 64)), dim3(512), 0, s, a);
+  else if (pairs(a) && a.z) launch_fwd<2, true>(a, s);
+  else if (pairs(a)) launch_fwd<2, false>(a, s);
+  else if (a.z) launch_fwd<1, true>(a, s);
+  else launch_fwd<1, false>(a, s);
   return hipGetLastError();
 }
 
-hipError_t launch_recur_bwd(const RecurArgs& a, hipStream_t s) {
-  if (a.z) hipLaunchKernelGGL((recur_bwd_kernel<true>), tile_grid(a), dim3(64 * kW), 0, s, a);
-  else hipLaunchKernelGGL((recur_bwd_kernel<false>), tile_grid(a), dim3(64 * kW), 0, s, a);
+hipError_t launch_recur_bwd(const RecurArgs& args, hipStream_t s) {
+  RecurArgs a = args;
+  a.blocks = (a.C + 63) / 64;
+  const dim3 grid((uint32_t)((int64_t)a.tiles * a.blocks)), block(256);
+  if (a.z) hipLaunchKernelGGL((recur_bwd_kernel<1, 16, 4, true>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((recur_bwd_kernel<1, 16, 4, false>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 
@@ -560,8 +847,20 @@ hipError_t launch_recur_bwd_sum(const RecurArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_recur_step(const RecurArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL(recur_step_kernel, dim3((uint32_t)((int64_t)a.S * ((a.C + 63) / 64))), dim3(64), 0, s, a);
+hipError_t launch_recur_step(const RecurArgs& args, hipStream_t s) {
+  RecurArgs a = args;
+  // Four channels a lane where they are one aligned vector in every row.
+  auto fours = [](const void* p, int64_t stride) { return reinterpret_cast<uintptr_t>(p) % 8 == 0 && stride % 4 == 0; };
+  const bool vec = a.C % 4 == 0 && fours(a.x, a.xs) && fours(a.r, a.rs) && fours(a.i, a.is) && fours(a.z, a.z ? a.zs : 0) &&
+                   fours(a.y, 0) && reinterpret_cast<uintptr_t>(a.state) % 16 == 0;
+  const int64_t cols = vec ? 256 : 64;
+  a.blocks = (int32_t)((a.C + cols - 1) / cols);
+  // As many rows a wave as leave eight waves a SIMD, at most 16.
+  const int64_t rows = std::max<int64_t>(1, std::min<int64_t>(16, (int64_t)a.blocks * a.S / 8192));
+  const int64_t waves = a.blocks * ((a.S + rows - 1) / rows);
+  const dim3 grid((uint32_t)((waves + 3) / 4)), block(256);
+  if (vec) hipLaunchKernelGGL(recur_step_kernel<4>, grid, block, 0, s, a, (int32_t)rows);
+  else hipLaunchKernelGGL(recur_step_kernel<1>, grid, block, 0, s, a, (int32_t)rows);
   return hipGetLastError();
 }
 

@@ -101,6 +101,24 @@ __device__ __forceinline__ float lanes_sum(float v) {
   return v;
 }
 
+// Their largest value, in the same way; NaN are left out.
+template <int L>
+__device__ __forceinline__ float lanes_max(float v) {
+  if constexpr (L >= 2) v = __builtin_fmaxf(v, dpp<kXor1>(v));
+  if constexpr (L >= 4) v = __builtin_fmaxf(v, dpp<kXor2>(v));
+  if constexpr (L >= 8) v = __builtin_fmaxf(v, dpp<kHalfMirror>(v));
+  if constexpr (L >= 16) v = __builtin_fmaxf(v, dpp<kMirror>(v));
+  if constexpr (L >= 32) {
+    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __builtin_fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+  }
+  if constexpr (L >= 64) {
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __builtin_fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+  }
+  return v;
+}
+
 // Eight channels of a row.
 struct Vec8 {
   float v[8];
