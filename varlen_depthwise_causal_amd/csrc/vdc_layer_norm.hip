@@ -33,6 +33,7 @@ struct Team {
   static constexpr int kThreads = kWide ? L : 256;
   static constexpr int kTokens = kWide ? 1 : 256 / L;  // tokens a workgroup has at a time
   static constexpr int kWaves = kWide ? L / 64 : 1;    // waves of a team
+  static constexpr int kUnroll = kWaves > 8 ? 2 : kWaves;  // of loops over them: registers
   int32_t li, wave;  // lane and wave of the team
   int64_t token, step;
   float inv_own;  // 1 / channels of the wave
@@ -69,12 +70,29 @@ __device__ __forceinline__ void request(const LayerNormArgs& a, const Team<L, K,
     r[k] = p.has(a, k) ? load8<kWhole>(t + row * stride + p.at(k), p.count(a, k)) : (u32x4_t){0u, 0u, 0u, 0u};
 }
 
+// A lane's channels of a parameter, by vectors but for a part of one; zeros without
+// the parameter and past the last channel.
 template <int K, class P>
 __device__ __forceinline__ void params(const LayerNormArgs& a, const P& p, const void* t, int bf16, Vec8 (&o)[K]) {
+  typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 #pragma unroll
-  for (int k = 0; k < K; ++k)
+  for (int k = 0; k < K; ++k) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[k].v[i] = t && p.has(a, k, i) ? param_at(t, bf16, p.at(k) + i) : 0.0f;
+    for (int i = 0; i < 8; ++i) o[k].v[i] = 0.0f;
+    if (!t || !p.has(a, k)) continue;
+    if (bf16) {
+      o[k] = unpack8(load8<false>(static_cast<const uint16_t*>(t) + p.at(k), p.count(a, k)));
+    } else if (p.count(a, k) >= 8) {
+      const f32x4_any* q = reinterpret_cast<const f32x4_any*>(static_cast<const float*>(t) + p.at(k));
+      const f32x4_any lo = q[0], hi = q[1];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[k].v[i] = lo[i], o[k].v[4 + i] = hi[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (p.at(k) + i < a.C) o[k].v[i] = static_cast<const float*>(t)[p.at(k) + i];
+    }
+  }
 }
 
 // d = s - m_w, the differences from the wave's own mean m_w; returns m_w and the
@@ -104,10 +122,10 @@ template <class P>
 __device__ __forceinline__ void join(const LayerNormArgs& a, const float (*lds)[4], float* mean, float* rstd) {
   const float inv = 1.0f / (float)a.C;
   float s = 0.0f, q = 0.0f;
-#pragma unroll
+#pragma unroll P::kUnroll
   for (int w = 0; w < P::kWaves; ++w) s = __builtin_fmaf((float)P::channels(a, w), lds[w][0], s);
   *mean = s * inv;
-#pragma unroll
+#pragma unroll P::kUnroll
   for (int w = 0; w < P::kWaves; ++w) {
     const float off = lds[w][0] - *mean;
     q += __builtin_fmaf((float)P::channels(a, w) * off, off, lds[w][1]);
@@ -170,7 +188,7 @@ template <int L, int K, bool kWhole, bool kRes>
 __global__ __launch_bounds__(L > 64 ? L : 256) void layer_norm_bwd_kernel(LayerNormArgs a, int32_t rows) {
   typedef Team<L, K, kWhole> P;
   __shared__ float lds[2][P::kWaves][4];
-  __shared__ float sums[P::kWide ? 1 : 256][P::kWide ? 1 : 2 * K * 8 + 1];
+  __shared__ float sums[P::kWide ? 1 : P::kTokens][P::kWide ? 1 : 2 * K * 8][P::kWide ? 1 : L + 1];
   const P p(a, rows);
   const float inv = 1.0f / (float)a.C;
   Vec8 w[K], dw[K], db[K];
@@ -185,15 +203,18 @@ __global__ __launch_bounds__(L > 64 ? L : 256) void layer_norm_bwd_kernel(LayerN
     request(a, p, a.dy, a.dys, t, dy);
     if (kRes) request(a, p, a.dstream, a.dss, t, ds);
   };
-  fetch(p.token);
+  // Sixteen waves a workgroup, four a SIMD, have no registers for the next token.
+  constexpr bool kAhead = L < 1024;
+  if (kAhead) fetch(p.token);
   int turn = 0;
 #pragma unroll 1
   for (int64_t t = p.token; t < a.S; t += p.step, turn ^= 1) {
+    if (!kAhead) fetch(t);
     Vec8 d[K], g[K];
     u32x4_t dc[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) d[k] = unpack8(x[k]), g[k] = unpack8(dy[k]), dc[k] = kRes ? ds[k] : x[k];
-    fetch(t + p.step);
+    if (kAhead) fetch(t + p.step);
     float mean, square, rstd, off = 0.0f;
     centre(a, p, d, &mean, &square);
     float s1 = 0.0f, s2 = 0.0f;
@@ -219,7 +240,7 @@ __global__ __launch_bounds__(L > 64 ? L : 256) void layer_norm_bwd_kernel(LayerN
       join<P>(a, lds[turn], &all, &rstd);
       off = mean - all;
       s1 = s2 = 0.0f;
-#pragma unroll
+#pragma unroll P::kUnroll
       for (int v = 0; v < P::kWaves; ++v) {
         const float o = lds[turn][v][0] - all;
         s1 += lds[turn][v][2];
@@ -246,38 +267,33 @@ __global__ __launch_bounds__(L > 64 ? L : 256) void layer_norm_bwd_kernel(LayerN
     }
   }
   // The workgroup's partial row: its teams' sums in order.
-  if (!P::kWide) {
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        sums[threadIdx.x][k * 8 + i] = dw[k].v[i];
-        sums[threadIdx.x][(K + k) * 8 + i] = db[k].v[i];
-      }
-    __syncthreads();
-    if (threadIdx.x >= L) return;
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float u = 0.0f, v = 0.0f;
-        for (int o = 0; o < P::kTokens; ++o) {
-          u += sums[o * L + threadIdx.x][k * 8 + i];
-          v += sums[o * L + threadIdx.x][(K + k) * 8 + i];
-        }
-        dw[k].v[i] = u;
-        db[k].v[i] = v;
-      }
-  }
   float* part = a.part + (int64_t)blockIdx.x * 2 * a.C;
+  if (P::kWide) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (p.has(a, k) && p.has(a, k, i)) {
+          part[p.at(k) + i] = dw[k].v[i];
+          part[a.C + p.at(k) + i] = db[k].v[i];
+        }
+    return;
+  }
 #pragma unroll
   for (int k = 0; k < K; ++k)
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (p.has(a, k) && p.has(a, k, i)) {
-        part[p.at(k) + i] = dw[k].v[i];
-        part[a.C + p.at(k) + i] = db[k].v[i];
-      }
+    for (int i = 0; i < 8; ++i) {
+      sums[threadIdx.x / L][k * 8 + i][p.li] = dw[k].v[i];
+      sums[threadIdx.x / L][(K + k) * 8 + i][p.li] = db[k].v[i];
+    }
+  __syncthreads();
+  for (int32_t o = threadIdx.x; o < 2 * a.C; o += 256) {
+    const int32_t c = o < a.C ? o : o - a.C, q = c / (8 * L) * 8 + c % 8 + (o < a.C ? 0 : K * 8), l = c / 8 % L;
+    float s = 0.0f;
+#pragma unroll
+    for (int g = 0; g < P::kTokens; ++g) s += sums[g][q][l];
+    part[o] = s;
+  }
 }
 
 // The partial rows of dw and db, summed in FP64: sixteen waves take their part of
@@ -331,15 +347,15 @@ Shape shape_of(int64_t C) {
   if (n <= 32) return {32, 1};
   if (n <= 64) return {64, 1};
   if (n <= 128) return {64, 2};
-  if (n <= 1024) return {256, n <= 256 ? 1 : n <= 512 ? 2 : 4};
-  return {512, 4};
+  if (n <= 512) return {256, n <= 256 ? 1 : 2};
+  return {n <= 1024 ? 512 : 1024, 2};
 }
 
 template <int L, int K, bool kWhole>
 void launch_vec(const LayerNormArgs& a, bool back, hipStream_t s) {
   typedef Team<L, K, kWhole> P;
   const int64_t turns = (a.S + P::kTokens - 1) / P::kTokens;
-  const int64_t most = L <= 64 ? 4096 : K <= 2 ? 1024 : 512;
+  const int64_t most = L <= 64 ? 4096 : L == 256 ? 1024 : L == 512 ? 512 : 256;
   const int64_t rows = back ? a.prows : turns < most ? turns : most;
   const dim3 grid((uint32_t)rows), block(P::kThreads);
   if (back) {
@@ -360,9 +376,9 @@ void launch_shape(const LayerNormArgs& a, bool back, hipStream_t s) {
   else if (h.lanes == 64 && h.vecs == 1) launch_vec<64, 1, kWhole>(a, back, s);
   else if (h.lanes == 64) launch_vec<64, 2, kWhole>(a, back, s);
   else if (h.lanes == 256 && h.vecs == 1) launch_vec<256, 1, kWhole>(a, back, s);
-  else if (h.lanes == 256 && h.vecs == 2) launch_vec<256, 2, kWhole>(a, back, s);
-  else if (h.lanes == 256) launch_vec<256, 4, kWhole>(a, back, s);
-  else launch_vec<512, 4, kWhole>(a, back, s);
+  else if (h.lanes == 256) launch_vec<256, 2, kWhole>(a, back, s);
+  else if (h.lanes == 512) launch_vec<512, 2, kWhole>(a, back, s);
+  else launch_vec<1024, 2, kWhole>(a, back, s);
 }
 
 hipError_t launch(const LayerNormArgs& a, bool back, hipStream_t s) {
@@ -376,7 +392,8 @@ hipError_t launch(const LayerNormArgs& a, bool back, hipStream_t s) {
 int layer_norm_bwd_rows(int64_t S, int64_t C) {
   const Shape h = shape_of(C);
   const int64_t tokens = h.lanes > 64 ? 1 : 256 / h.lanes, turns = (S + tokens - 1) / tokens;
-  return (int)(turns < 512 ? turns : 512);
+  const int64_t most = h.lanes == 1024 ? 256 : 512;
+  return (int)(turns < most ? turns : most);
 }
 
 hipError_t launch_layer_norm_fwd(const LayerNormArgs& a, hipStream_t s) { return launch(a, false, s); }

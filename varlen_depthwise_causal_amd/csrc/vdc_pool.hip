@@ -34,8 +34,9 @@ __device__ __forceinline__ float odd_quotient(float v, float s) {
   return __uint_as_float(b);
 }
 
-// V values a lane, 64 / V lanes a block.  V = 8: states of a multiple of 64 values, as
-// long as vectors of them and of their codes are aligned; else V = 1.
+// V values a lane, 64 / V lanes a block: 16 bytes of a state (V = 4 or 8) where states
+// have a multiple of 64 values and vectors of them and of their codes are aligned,
+// else one value.
 template <int V, bool kBf16>
 __device__ __forceinline__ void state_load(const PoolArgs& a, int64_t at, float (&v)[V]) {
   if constexpr (V == 1) {
@@ -45,10 +46,9 @@ __device__ __forceinline__ void state_load(const PoolArgs& a, int64_t at, float 
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[2 * k] = bf16_lo(w[k]), v[2 * k + 1] = bf16_hi(w[k]);
   } else {
-    const f32x4_t* p = reinterpret_cast<const f32x4_t*>(static_cast<const float*>(a.state) + at);
-    const f32x4_t lo = __builtin_nontemporal_load(p), hi = __builtin_nontemporal_load(p + 1);
+    const f32x4_t w = __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(static_cast<const float*>(a.state) + at));
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = lo[k], v[4 + k] = hi[k];
+    for (int k = 0; k < 4; ++k) v[k] = w[k];
   }
 }
 template <int V, bool kBf16>
@@ -62,11 +62,30 @@ __device__ __forceinline__ void state_store(const PoolArgs& a, int64_t at, const
     for (int k = 0; k < 4; ++k) w[k] = bf16_pack2(v[2 * k], v[2 * k + 1]);
     __builtin_nontemporal_store(w, reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(a.state) + at));
   } else {
-    f32x4_t* p = reinterpret_cast<f32x4_t*>(static_cast<float*>(a.state) + at);
-    __builtin_nontemporal_store((f32x4_t){v[0], v[1], v[2], v[3]}, p);
-    __builtin_nontemporal_store((f32x4_t){v[4], v[5], v[6], v[7]}, p + 1);
+    __builtin_nontemporal_store((f32x4_t){v[0], v[1], v[2], v[3]},
+                                reinterpret_cast<f32x4_t*>(static_cast<float*>(a.state) + at));
   }
 }
+
+// V codes, four to a word.
+template <int V>
+struct Codes {
+  static constexpr int kWords = (V + 3) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const uint8_t* p) {
+    if constexpr (V == 1) w[0] = *p;
+    else if constexpr (V == 4) w[0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p));
+    else {
+      const u32x2_t v = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(p));
+      w[0] = v[0], w[1] = v[1];
+    }
+  }
+  __device__ __forceinline__ void store(uint8_t* p) const {
+    if constexpr (V == 1) *p = (uint8_t)w[0];
+    else if constexpr (V == 4) __builtin_nontemporal_store(w[0], reinterpret_cast<uint32_t*>(p));
+    else __builtin_nontemporal_store((u32x2_t){w[0], w[1]}, reinterpret_cast<u32x2_t*>(p));
+  }
+};
 
 template <bool kE4m3>
 __device__ __forceinline__ uint32_t code_of(float t) {
@@ -105,19 +124,12 @@ __global__ __launch_bounds__(256) void pool_quantize_kernel(PoolArgs a, int32_t 
     bad = lanes_sum<kLanes>(bad);
     const bool none = !(most >= 0x1p-64f) || bad != bad;
     const float scale = bad != bad ? __builtin_nanf("") : none ? 0.0f : most / (kE4m3 ? 448.0f : 127.0f);
-    uint32_t code[V];
+    Codes<V> codes = {};
 #pragma unroll
-    for (int q = 0; q < V; ++q) code[q] = code_of<kE4m3>(none ? 0.0f : odd_quotient(v[k][q], scale));
+    for (int q = 0; q < V; ++q)
+      codes.w[q / 4] |= code_of<kE4m3>(none ? 0.0f : odd_quotient(v[k][q], scale)) << (q % 4 * 8);
     if (at >= a.E) continue;
-    uint8_t* out = a.codes + place * a.E + at;
-    if constexpr (V == 1) {
-      *out = (uint8_t)code[0];
-    } else {
-      u32x2_t w = {0, 0};
-#pragma unroll
-      for (int q = 0; q < V; ++q) w[q / 4] |= code[q] << (q % 4 * 8);
-      __builtin_nontemporal_store(w, reinterpret_cast<u32x2_t*>(out));
-    }
+    codes.store(a.codes + place * a.E + at);
     if (threadIdx.x % kLanes == 0) a.scales[place * blocks + at / kPoolBlock] = scale;
   }
 }
@@ -130,19 +142,13 @@ __global__ __launch_bounds__(256) void pool_dequantize_kernel(PoolArgs a, int32_
   const int64_t blocks = (a.E + kPoolBlock - 1) / kPoolBlock;
   constexpr int kTurns = kPoolValues / (256 * V);
   const int64_t at0 = part * kPoolValues + (int64_t)threadIdx.x * V;
-  uint32_t code[kTurns][(V + 3) / 4];
+  Codes<V> codes[kTurns];
   float scale[kTurns];
 #pragma unroll
   for (int k = 0; k < kTurns; ++k) {
     const int64_t at = at0 + k * 256 * V;
     if (at >= a.E) continue;
-    const uint8_t* in = a.codes + place * a.E + at;
-    if constexpr (V == 1) {
-      code[k][0] = *in;
-    } else {
-      const u32x2_t w = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(in));
-      code[k][0] = w[0], code[k][1] = w[1];
-    }
+    codes[k].load(a.codes + place * a.E + at);
     scale[k] = a.scales[place * blocks + at / kPoolBlock];
   }
 #pragma unroll
@@ -152,7 +158,7 @@ __global__ __launch_bounds__(256) void pool_dequantize_kernel(PoolArgs a, int32_
     float v[V];
 #pragma unroll
     for (int q = 0; q < V; ++q) {
-      const uint32_t b = code[k][q / 4] >> (q % 4 * 8) & 0xffu;
+      const uint32_t b = codes[k].w[q / 4] >> (q % 4 * 8) & 0xffu;
       v[q] = (kE4m3 ? __builtin_amdgcn_cvt_f32_fp8((int)b, 0) : (float)(int8_t)b) * scale[k];
     }
     state_store<V, kBf16>(a, slot * a.E + at, v);
@@ -167,25 +173,24 @@ void launch_as(const PoolArgs& a, bool back, hipStream_t s) {
   else hipLaunchKernelGGL((pool_quantize_kernel<V, kBf16, kE4m3>), grid, block, 0, s, a, parts);
 }
 
-template <int V>
-void launch_values(const PoolArgs& a, bool back, hipStream_t s) {
-  if (a.bf16 && a.e4m3) launch_as<V, true, true>(a, back, s);
-  else if (a.bf16) launch_as<V, true, false>(a, back, s);
-  else if (a.e4m3) launch_as<V, false, true>(a, back, s);
-  else launch_as<V, false, false>(a, back, s);
-}
-
+template <bool kE4m3>
 hipError_t launch(const PoolArgs& a, bool back, hipStream_t s) {
   const bool vectors = a.E % kPoolBlock == 0 && reinterpret_cast<uintptr_t>(a.state) % 16 == 0 &&
                        reinterpret_cast<uintptr_t>(a.codes) % 8 == 0;
-  if (vectors) launch_values<8>(a, back, s);
-  else launch_values<1>(a, back, s);
+  if (vectors && a.bf16) launch_as<8, true, kE4m3>(a, back, s);
+  else if (vectors) launch_as<4, false, kE4m3>(a, back, s);
+  else if (a.bf16) launch_as<1, true, kE4m3>(a, back, s);
+  else launch_as<1, false, kE4m3>(a, back, s);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_pool_quantize(const PoolArgs& a, hipStream_t s) { return launch(a, false, s); }
-hipError_t launch_pool_dequantize(const PoolArgs& a, hipStream_t s) { return launch(a, true, s); }
+hipError_t launch_pool_quantize(const PoolArgs& a, hipStream_t s) {
+  return a.e4m3 ? launch<true>(a, false, s) : launch<false>(a, false, s);
+}
+hipError_t launch_pool_dequantize(const PoolArgs& a, hipStream_t s) {
+  return a.e4m3 ? launch<true>(a, true, s) : launch<false>(a, true, s);
+}
 
 }  // namespace vdc

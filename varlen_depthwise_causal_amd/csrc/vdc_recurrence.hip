@@ -109,6 +109,10 @@ struct Run {
     if (V == 2) __builtin_amdgcn_raw_buffer_store_b32(bf16_pack2(v[0], v[V - 1]), r, at, row(j), kOnce);
     else __builtin_amdgcn_raw_buffer_store_b16(bf16_of(v[0]), r, at, row(j), kOnce);
   }
+  __device__ __forceinline__ void put(const Cols<1>& c, int j, float v) const {
+    const float one[1] = {v};
+    put(c, j, one);
+  }
   // Nothing is read or written twice: loads and stores do not stay in the caches.
   static constexpr int kOnce = 2;
 };
@@ -489,188 +493,147 @@ void recur_fwd_kernel(RecurArgs a) {
   }
 }
 
-// dy silu'(z) waits for the states in LDS: with it in registers two workgroups fit on
-// a CU instead of three.
-template <int V, int N, int W, bool kGate>
+// N tokens a run, W runs a tile.  dy silu'(z) waits for the states in LDS: with it in
+// registers two workgroups fit on a CU instead of three.
+template <int N, int W, bool kGate>
 __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(3)))
 void recur_bwd_kernel(RecurArgs a) {
   constexpr int T = N * W;
   static_assert(T == kRecurBwdTile, "");
   __shared__ Starts<T, false> docs;
-  __shared__ float2 sums[W][64][V];  // P and H of the waves' runs
-  __shared__ float sent[W][64][V];   // what a run sends to its left without any from its right
-  __shared__ Seen<W, V> seen;
-  __shared__ float gate[kGate ? W : 1][N][V][64];
+  __shared__ float2 sums[W][64];  // P and H of the waves' runs
+  __shared__ float sent[W][64];   // what a run sends to its left without any from its right
+  __shared__ Seen<W, 1> seen;
+  __shared__ float gate[kGate ? W : 1][N][64];
   __shared__ uint32_t ticket;
   clear_starts<W>(docs);
   const Place p = place_of(a, &ticket);
   const int32_t k = a.tiles - 1 - p.n;  // the last tile first
   const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64u), lane = threadIdx.x & 63;
   const int32_t tile0 = k * T, t0 = tile0 + wave * N;
-  const Cols<V> c(a, p.block);
-  uint32_t x[N], r[N], i[N], zw[N], dy[N];
+  const Cols<1> c(a, p.block);
+  uint32_t x[N], r[N], i[N], z[N], dy[N];
   rows(c, a.r, a.rs, t0, a.S, r);
   rows(c, a.i, a.is, t0, a.S, i);
   rows(c, a.x, a.xs, t0, a.S, x);
-  if (kGate) rows(c, a.z, a.zs, t0, a.S, zw);
+  if (kGate) rows(c, a.z, a.zs, t0, a.S, z);
   rows(c, a.dy, a.dys, t0, a.S, dy);
-  float h[V], rate[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    h[v] = a.keep[(int64_t)k * a.C + c.c + v];
-    rate[v] = decay_rate(a, c.c + v);
-  }
+  float h = a.keep[(int64_t)k * a.C + c.c];
+  const float rate = decay_rate(a, c.c);
   find_starts<W>(a, tile0, docs);
   __syncthreads();
   const uint32_t bits = bits_at<N>(docs.mask, wave * N);
 
-  float A[N][V], B[N][V], m[N][V], sr[N][V], si[N][V], g[N][V];
+  float A[N], B[N], m[N], sr[N], si[N], g[N];
+  float P = 1.0f, H = 0.0f, M = 0.0f;
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      sr[j][v] = sigmoid_f32(channel<V>(r[j], v));
-      si[j][v] = sigmoid_f32(channel<V>(i[j], v));
-      const float u = rate[v] * sr[j][v];
-      A[j][v] = decay_of(u);
-      m[j][v] = input_scale(u, A[j][v]);
-      B[j][v] = gated(m[j][v], si[j][v] * channel<V>(x[j], v));
-      g[j][v] = channel<V>(dy[j], v);
-      if (kGate) {
-        // dy silu(z), the gradient at the state, and dy silu'(z), dz but for the state
-        const float zj = channel<V>(zw[j], v), s = sigmoid_f32(zj), dyj = g[j][v];
-        g[j][v] = dyj * (zj * s);
-        gate[wave][j][v][lane] = dyj * dsilu_f32(zj, s);
-      }
+    sr[j] = sigmoid_f32(channel<1>(r[j], 0));
+    si[j] = sigmoid_f32(channel<1>(i[j], 0));
+    const float u = rate * sr[j];
+    A[j] = decay_of(u);
+    m[j] = input_scale(u, A[j]);
+    B[j] = gated(m[j], si[j] * channel<1>(x[j], 0));
+    g[j] = channel<1>(dy[j], 0);
+    if (kGate) {
+      // dy silu(z), the gradient at the state, and dy silu'(z), dz but for the state
+      const float zj = channel<1>(z[j], 0), s = sigmoid_f32(zj);
+      gate[wave][j][lane] = g[j] * dsilu_f32(zj, s);
+      g[j] *= zj * s;
     }
-    if (j % 2) __builtin_amdgcn_sched_barrier(0);
+    if (j % 2) __builtin_amdgcn_sched_barrier(0);  // no more tokens side by side than registers hold
   }
+  if (bits == 0) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    float P = 1.0f, H = 0.0f, M = 0.0f;
-    if (bits == 0) {
+    for (int j = 0; j < N; ++j) P *= A[j], H = __builtin_fmaf(A[j], H, B[j]);
 #pragma unroll
-      for (int j = 0; j < N; ++j) P *= A[j][v], H = __builtin_fmaf(A[j][v], H, B[j][v]);
+    for (int j = N - 1; j >= 0; --j) M = A[j] * (g[j] + M);
+  } else {
 #pragma unroll
-      for (int j = N - 1; j >= 0; --j) M = A[j][v] * (g[j][v] + M);
-    } else {
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        P *= A[j][v];
-        H = bits >> j & 1u ? B[j][v] : __builtin_fmaf(A[j][v], H, B[j][v]);
-      }
-#pragma unroll
-      for (int j = N - 1; j >= 0; --j) M = A[j][v] * (bits >> (j + 1) & 1u ? g[j][v] : g[j][v] + M);
+    for (int j = 0; j < N; ++j) {
+      P *= A[j];
+      H = bits >> j & 1u ? B[j] : __builtin_fmaf(A[j], H, B[j]);
     }
-    sums[wave][lane][v] = {P, H};
-    sent[wave][lane][v] = M;
+#pragma unroll
+    for (int j = N - 1; j >= 0; --j) M = A[j] * (bits >> (j + 1) & 1u ? g[j] : g[j] + M);
   }
+  sums[wave][lane] = {P, H};
+  sent[wave][lane] = M;
   __syncthreads();
 
   const uint32_t starts = runs_with<N, W, 0, N - 1>(docs.mask);
   // Runs with a start behind their first token, up to the token after them: nothing
   // from the right gets through.
   const uint32_t shut = runs_with<N, W, 1, N>(docs.mask);
-  uint64_t* const mine = a.words + (int64_t)k * a.cols + (p.block * 64 + lane) * V;
+  uint64_t* const mine = a.words + (int64_t)k * a.cols + p.block * 64 + lane;
   const bool waits = p.n > 0 && (__builtin_amdgcn_readfirstlane(docs.mask[T / 32]) & 1u) == 0;
   const bool cut = !waits || shut != 0;
   const bool hands = wave == 0 && p.n + 1 < a.tiles;
-  float tp[V], tm[V];
+  float tp = 1.0f, tm = 0.0f;
   if (hands) {
-    uint64_t w[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) tp[v] = 1.0f, tm[v] = 0.0f;
 #pragma unroll 2
-    for (int q = W - 1; q >= 0; --q)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float s = sums[q][lane][v].x, o = sent[q][lane][v];
-        tm[v] = shut >> q & 1u ? o : __builtin_fmaf(s, tm[v], o);
-        tp[v] *= s;
-      }
-#pragma unroll
-    for (int v = 0; v < V; ++v) w[v] = cut ? known(tm[v]) : word_of(tp[v], tm[v]);
+    for (int q = W - 1; q >= 0; --q) {
+      const float s = sums[q][lane].x, o = sent[q][lane];
+      tm = shut >> q & 1u ? o : __builtin_fmaf(s, tm, o);
+      tp *= s;
+    }
+    const uint64_t w[1] = {cut ? known(tm) : word_of(tp, tm)};
     hand_on(mine, w);
   }
   // The states before this run, from the one that the forward kept.
 #pragma unroll 2
-  for (int q = 0; q < wave; ++q)
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float2 s = sums[q][lane][v];
-      h[v] = starts >> q & 1u ? s.y : __builtin_fmaf(s.x, h[v], s.y);
-    }
+  for (int q = 0; q < wave; ++q) {
+    const float2 s = sums[q][lane];
+    h = starts >> q & 1u ? s.y : __builtin_fmaf(s.x, h, s.y);
+  }
   const Run dz(a.dz, a.C, t0, a.S);
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     const bool first = bits >> j & 1u;
-    float o[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float before = first ? 0.0f : h[v];
-      h[v] = first ? B[j][v] : __builtin_fmaf(A[j][v], h[v], B[j][v]);
-      B[j][v] = before;  // from here on the state before the token
-      o[v] = kGate ? gate[wave][j][v][lane] * h[v] : 0.0f;
-    }
-    if (kGate) dz.put(c, j, o);
+    const float before = first ? 0.0f : h;
+    h = first ? B[j] : __builtin_fmaf(A[j], h, B[j]);
+    B[j] = before;  // from here on the state before the token
+    if (kGate) dz.put(c, j, gate[wave][j][lane] * h);
   }
 
-  float l[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) l[v] = 0.0f;
+  float l[1] = {0.0f};
   if (waits) {
     look_back(mine, (int64_t)a.cols, p.n, seen, l);
     if (hands && !cut) {
-      uint64_t w[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) w[v] = known(__builtin_fmaf(tp[v], l[v], tm[v]));
+      const uint64_t w[1] = {known(__builtin_fmaf(tp, l[0], tm))};
       hand_on(mine, w);
     }
   }
 #pragma unroll 2
-  for (int q = W - 1; q > wave; --q)
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float o = sent[q][lane][v];
-      l[v] = shut >> q & 1u ? o : __builtin_fmaf(sums[q][lane][v].x, l[v], o);
-    }
+  for (int q = W - 1; q > wave; --q) {
+    const float o = sent[q][lane];
+    l[0] = shut >> q & 1u ? o : __builtin_fmaf(sums[q][lane].x, l[0], o);
+  }
   const Run dx(a.dx, a.C, t0, a.S), di(a.di, a.C, t0, a.S), dr(a.dr, a.C, t0, a.S);
-  float sum[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) sum[v] = 0.0f;
+  float sum = 0.0f, left = l[0];
 #pragma unroll
   for (int j = N - 1; j >= 0; --j) {
-    float ox[V], oi[V], orr[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float xj = channel<V>(x[j], v);
-      l[v] = bits >> (j + 1) & 1u ? g[j][v] : g[j][v] + l[v];
-      ox[v] = gated(m[j][v], l[v]) * si[j][v];
-      oi[v] = gated(ox[v], xj) * (1.0f - si[j][v]);
-      // u / 2 and u / (2 m): without a step the first is 0, or too small to matter
-      const float half = 0.5f * rate[v] * sr[j][v];
-      const float w = half * __builtin_amdgcn_rcpf(__builtin_fmaxf(m[j][v], 0x1p-60f));
-      const float E = l[v] * __builtin_fmaf(-half * A[j][v], B[j][v], gated(A[j][v] * A[j][v] * w, si[j][v] * xj));
-      sum[v] += E;
-      orr[v] = E * (1.0f - sr[j][v]);
-      l[v] *= A[j][v];
-    }
-    dx.put(c, j, ox);
-    di.put(c, j, oi);
-    dr.put(c, j, orr);
+    const float xj = channel<1>(x[j], 0);
+    left = bits >> (j + 1) & 1u ? g[j] : g[j] + left;
+    const float lx = gated(m[j], left) * si[j];
+    dx.put(c, j, lx);
+    di.put(c, j, gated(lx, xj) * (1.0f - si[j]));
+    // u / 2 and u / (2 m): without a step the first is 0, or too small to matter
+    const float half = 0.5f * rate * sr[j];
+    const float w = half * __builtin_amdgcn_rcpf(__builtin_fmaxf(m[j], 0x1p-60f));
+    const float E = left * __builtin_fmaf(-half * A[j], B[j], gated(A[j] * A[j] * w, si[j] * xj));
+    sum += E;
+    dr.put(c, j, E * (1.0f - sr[j]));
+    left *= A[j];
   }
   // The tile's partial sum: its waves' in order.
   __syncthreads();
-#pragma unroll
-  for (int v = 0; v < V; ++v) sent[wave][lane][v] = sum[v];
+  sent[wave][lane] = sum;
   __syncthreads();
   if (wave > 0 || !c.has) return;
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-#pragma unroll 4
-    for (int q = 1; q < W; ++q) sum[v] += sent[q][lane][v];
-    a.part[(int64_t)k * a.C + c.c + v] = sum[v];
-  }
+  for (int q = 1; q < W; ++q) sum += sent[q][lane];
+  a.part[(int64_t)k * a.C + c.c] = sum;
 }
 
 // The tiles' sums of E in FP64, sixteen waves a part of the tiles each.
@@ -800,12 +763,13 @@ bool pairs(const uint16_t* p, int64_t stride) {
 }
 
 // Forward, whether a lane has two channels: they have to be one aligned word in every
-// row.  Lines of 256 bytes are faster to read (16384 tokens, C = 4096, a gate: 159
-// against 182 us), but of few channels a tile's way to the next one is longer
-// (65536 tokens, C = 100: 65 against 49).
+// row.  Rows of 256 bytes are faster to read (16384 tokens, C = 4096, a gate: 159
+// against 182 us), but a tile takes longer, which tells where there are few of them
+// (1543 tokens, C = 520: 13.2 against 10.8) or of few channels many in a row (65536
+// tokens, C = 100: 65 against 49).
 bool pairs(const RecurArgs& a) {
-  return a.C > 128 && a.C % 2 == 0 && pairs(a.x, a.xs) && pairs(a.r, a.rs) && pairs(a.i, a.is) &&
-         pairs(a.z, a.z ? a.zs : 0) && pairs(a.y, 0);
+  return a.C > 128 && a.tiles * ((a.C + 127) / 128) >= 256 && a.C % 2 == 0 && pairs(a.x, a.xs) && pairs(a.r, a.rs) &&
+         pairs(a.i, a.is) && pairs(a.z, a.z ? a.zs : 0) && pairs(a.y, 0);
 }
 
 template <int V, bool kGate>
@@ -837,8 +801,8 @@ hipError_t launch_recur_bwd(const RecurArgs& args, hipStream_t s) {
   RecurArgs a = args;
   a.blocks = (a.C + 63) / 64;
   const dim3 grid((uint32_t)((int64_t)a.tiles * a.blocks)), block(256);
-  if (a.z) hipLaunchKernelGGL((recur_bwd_kernel<1, 16, 4, true>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((recur_bwd_kernel<1, 16, 4, false>), grid, block, 0, s, a);
+  if (a.z) hipLaunchKernelGGL((recur_bwd_kernel<16, 4, true>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((recur_bwd_kernel<16, 4, false>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 

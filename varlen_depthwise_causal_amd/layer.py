@@ -10,19 +10,61 @@ are BF16 with dense rows (a slice of wider rows is fine), outputs are dense.
 from __future__ import annotations
 
 import ctypes
+import functools
 import struct
 
 import torch
 
 from ._lib import VDC_BWD, VDC_E4M3, VDC_FWD, VDC_INT8, VdcError, VdcRecurrence, load
-from .ssm import (_CODES, _activation, _at, _cache, _cu, _dense, _out, _param, _ptr, _rows, _stream, _workspace,
-                  _x_rows)
+from .ssm import _CODES, _at, _cache, _cu, _dense, _out, _param, _ptr, _rows, _stream, _workspace
 
 __all__ = ["gated_recurrence_fwd", "gated_recurrence_bwd", "gated_recurrence_keep_rows",
            "gated_recurrence_workspace_bytes", "gated_recurrence_update", "layer_norm_fwd", "layer_norm_bwd",
            "layer_norm_workspace_bytes", "state_quantize", "state_dequantize"]
 
 _F32, _BF16 = torch.float32, torch.bfloat16
+
+
+# As in module ssm the checks first ask whether a tensor is the usual one; most
+# of what a single token costs is the host's.
+
+def _act(t, what, shape, C, device):
+    """Row stride of a BF16 [S, C] activation whose rows are dense."""
+    if t.dtype is _BF16 and t.shape == shape and t.device == device:
+        stride, one = t.stride()
+        if one == 1 and C <= stride <= 1 << 25:
+            return stride
+    return _rows(t, what, shape, C, device)
+
+
+def _x_act(x):
+    """Sizes, device and row stride of the activation that gives them."""
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, C], got %s" % (list(x.shape),))
+    shape, device = x.shape, x.device
+    S, C = shape
+    stride = _act(x, "x", shape, C, device)
+    if not x.is_cuda:
+        raise ValueError("x must be a device tensor")
+    return shape, S, C, device, stride
+
+
+def _recur_cache(state, C, state_index, resume, sequences, device):
+    """Number of slots of an FP32 [slots, C] cache."""
+    if (state.dtype is _F32 and state.dim() == 2 and state.shape[1] == C and state.is_contiguous()
+            and state.device == device and state_index is not None and _list(state_index, torch.int32, sequences, device)
+            and (resume is None or _list(resume, torch.bool, sequences, device))):
+        return state.shape[0]
+    return _cache(state, "state", (C,), _F32, state_index, resume, sequences, device)
+
+
+def _list(t, dtype, n, device):
+    return t.dtype is dtype and t.shape == (n,) and t.is_contiguous() and t.device == device
+
+
+@functools.lru_cache(maxsize=1024)
+def _bytes(name, *sizes):
+    return int(getattr(load(), name)(*sizes))
 
 
 # The library launches on the device that is current, so a call for tensors on
@@ -49,16 +91,15 @@ assert _RECUR.size == ctypes.sizeof(VdcRecurrence)
 
 
 def _recur_args(x, r, i, decay, z, scale, cu_seqlens, state, state_index, resume):
-    S, C, dev = _activation(x)
-    shape = x.shape
-    xs, rs, is_ = _x_rows(x, C, dev), _rows(r, "r", shape, C, dev), _rows(i, "i", shape, C, dev)
-    zs = C if z is None else _rows(z, "z", shape, C, dev)
+    shape, S, C, dev, xs = _x_act(x)
+    rs, is_ = _act(r, "r", shape, C, dev), _act(i, "i", shape, C, dev)
+    zs = C if z is None else _act(z, "z", shape, C, dev)
     code = _param(decay, "decay", (C,), dev)
     sequences, docs, slots = S, 0, 0
     if cu_seqlens is not None:
         sequences = docs = _cu(cu_seqlens, dev)
     if state is not None:
-        slots = _cache(state, "state", (C,), _F32, state_index, resume, sequences, dev)
+        slots = _recur_cache(state, C, state_index, resume, sequences, dev)
     elif state_index is not None or resume is not None:
         raise ValueError("state_index and resume need a state")
     a = _RECUR.pack(S, C, x.data_ptr(), r.data_ptr(), i.data_ptr(), _at(z), xs, rs, is_, zs, decay.data_ptr(), code,
@@ -68,12 +109,12 @@ def _recur_args(x, r, i, decay, z, scale, cu_seqlens, state, state_index, resume
 
 def gated_recurrence_keep_rows(S: int) -> int:
     """Rows of the states that gated_recurrence_fwd keeps for its backward."""
-    return int(load().gated_recurrence_keep_rows(S))
+    return _bytes("gated_recurrence_keep_rows", S)
 
 
 def gated_recurrence_workspace_bytes(direction: str, S: int, C: int) -> int:
     """Workspace bytes of gated_recurrence_fwd ("fwd") / gated_recurrence_bwd ("bwd")."""
-    return int(load().gated_recurrence_workspace_bytes({"fwd": VDC_FWD, "bwd": VDC_BWD}[direction], S, C))
+    return _bytes("gated_recurrence_workspace_bytes", {"fwd": VDC_FWD, "bwd": VDC_BWD}[direction], S, C)
 
 
 def gated_recurrence_fwd(x, r, i, decay, cu_seqlens, *, z=None, scale=8.0, state=None, state_index=None, resume=None,
@@ -93,17 +134,16 @@ def gated_recurrence_fwd(x, r, i, decay, cu_seqlens, *, z=None, scale=8.0, state
     gated_recurrence_bwd starts from."""
     a, S, C, dev, xs = _recur_args(x, r, i, decay, z, scale, cu_seqlens, state, state_index, resume)
     out = _out(out, x, xs, x.shape, "out", dev)
-    lib = load()
     want = keep is not None and keep is not False
     if want:
         if state is not None:
             raise ValueError("keep is for the training forward, without a state")
-        shape = (lib.gated_recurrence_keep_rows(S), C)
+        shape = (gated_recurrence_keep_rows(S), C)
         if keep is True:
             keep = torch.empty(shape, dtype=_F32, device=dev)
         else:
             _dense(keep, "keep", _F32, shape, dev)
-    need = lib.gated_recurrence_workspace_bytes(VDC_FWD, S, C)
+    need = _bytes("gated_recurrence_workspace_bytes", VDC_FWD, S, C)
     ws, ws_n = None, 0
     if need or workspace is not None:
         workspace, ws_n = _workspace(need, workspace, dev)
@@ -117,14 +157,13 @@ def gated_recurrence_bwd(x, r, i, decay, cu_seqlens, dy, keep, *, z=None, scale=
     what it kept of them: (dx, dr, di, ddecay, dz), dz None without a gate.
     ddecay has decay's dtype, the others BF16."""
     a, S, C, dev, xs = _recur_args(x, r, i, decay, z, scale, cu_seqlens, None, None, None)
-    dy_stride = _rows(dy, "dy", x.shape, C, dev)
-    lib = load()
-    _dense(keep, "keep", _F32, (lib.gated_recurrence_keep_rows(S), C), dev)
+    dy_stride = _act(dy, "dy", x.shape, C, dev)
+    _dense(keep, "keep", _F32, (gated_recurrence_keep_rows(S), C), dev)
     dx = _out(None, x, xs, x.shape, "dx", dev)
     dr, di = torch.empty_like(dx), torch.empty_like(dx)
     dz = None if z is None else torch.empty_like(dx)
     ddecay = torch.empty_like(decay)
-    workspace, ws_n = _workspace(lib.gated_recurrence_workspace_bytes(VDC_BWD, S, C), workspace, dev)
+    workspace, ws_n = _workspace(_bytes("gated_recurrence_workspace_bytes", VDC_BWD, S, C), workspace, dev)
     _call("gated_recurrence_bwd", dev, a, dy.data_ptr(), dy_stride, keep.data_ptr(), dx.data_ptr(), dr.data_ptr(),
           di.data_ptr(), ddecay.data_ptr(), _ptr(dz), workspace.data_ptr(), ws_n, _stream(dev))
     return dx, dr, di, ddecay, dz
@@ -149,15 +188,14 @@ def layer_norm_fwd(x, weight, *, bias=None, residual=None, eps=1e-5, out=None, s
     bf16(x + residual), or x without one, y = weight * xhat(s) + bias.
     x, residual: BF16 [S, C], C at most 16384; weight, bias: FP32 or BF16 [C].
     Returns (y, s); s is x itself without a residual."""
-    S, C, dev = _activation(x)
-    xs = _x_rows(x, C, dev)
+    shape, S, C, dev, xs = _x_act(x)
     w_code = _param(weight, "weight", (C,), dev)
     b_code = 0 if bias is None else _param(bias, "bias", (C,), dev)
-    out = _out(out, x, xs, x.shape, "out", dev)
+    out = _out(out, x, xs, shape, "out", dev)
     rs = C
     if residual is not None:
-        rs = _rows(residual, "residual", x.shape, C, dev)
-        stream_out = _out(stream_out, x, xs, x.shape, "stream_out", dev)
+        rs = _act(residual, "residual", shape, C, dev)
+        stream_out = _out(stream_out, x, xs, shape, "stream_out", dev)
     elif stream_out is not None:
         raise ValueError("stream_out needs a residual")
     _call("layer_norm_fwd", dev, x.data_ptr(), xs, _ptr(residual), rs, weight.data_ptr(), w_code, _ptr(bias), b_code,
@@ -167,7 +205,7 @@ def layer_norm_fwd(x, weight, *, bias=None, residual=None, eps=1e-5, out=None, s
 
 def layer_norm_workspace_bytes(S: int, C: int) -> int:
     """Workspace bytes of layer_norm_bwd."""
-    return int(load().layer_norm_workspace_bytes(S, C))
+    return _bytes("layer_norm_workspace_bytes", S, C)
 
 
 def layer_norm_bwd(s, weight, dy, *, bias=None, dstream=None, eps=1e-5, workspace=None):
@@ -175,15 +213,15 @@ def layer_norm_bwd(s, weight, dy, *, bias=None, dstream=None, eps=1e-5, workspac
     dbias), dbias None without a bias.  dstream, BF16 [S, C]: the gradient that
     reaches the sum past the norm; dx has it added and is the gradient of x and
     of the residual alike."""
-    S, C, dev = _activation(s)
-    ss, dys = _x_rows(s, C, dev), _rows(dy, "dy", s.shape, C, dev)
+    shape, S, C, dev, ss = _x_act(s)
+    dys = _act(dy, "dy", shape, C, dev)
     w_code = _param(weight, "weight", (C,), dev)
     b_code = 0 if bias is None else _param(bias, "bias", (C,), dev)
-    dss = C if dstream is None else _rows(dstream, "dstream", s.shape, C, dev)
-    dx = _out(None, s, ss, s.shape, "dx", dev)
+    dss = C if dstream is None else _act(dstream, "dstream", shape, C, dev)
+    dx = _out(None, s, ss, shape, "dx", dev)
     dw = torch.empty_like(weight)
     db = None if bias is None else torch.empty_like(bias)
-    workspace, ws_n = _workspace(load().layer_norm_workspace_bytes(S, C), workspace, dev)
+    workspace, ws_n = _workspace(_bytes("layer_norm_workspace_bytes", S, C), workspace, dev)
     _call("layer_norm_bwd", dev, s.data_ptr(), ss, weight.data_ptr(), w_code, dy.data_ptr(), dys, _ptr(dstream), dss,
           S, C, eps, dx.data_ptr(), dw.data_ptr(), _ptr(db), b_code, workspace.data_ptr(), ws_n, _stream(dev))
     return dx, dw, db
