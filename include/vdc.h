@@ -446,7 +446,8 @@ int group_norm_silu_bwd(const void *x, int64_t x_stride, const void *weight, int
  * in FP32, y rounded to bf16 once.  h before a document's first token is
  * zero, or its slot's state where the document resumes.  A token with u = 0
  * (r of -inf or the lowest finite number: a masked token) leaves the state
- * exactly as it is, whatever x and i hold.
+ * exactly as it is, whatever x and i hold.  softplus(decay) and u count as 0 below
+ * the normal FP32 numbers, and 2 scale softplus(decay) is at most 2^126.
  */
 typedef struct vdc_recurrence {
     int64_t S;        /* tokens, at most 2^31 - 4096; for

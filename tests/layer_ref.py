@@ -21,6 +21,7 @@ class Recurrence:
         self.soft, self.es = softplus(decay)
         self.sr, self.er = sigmoid(r)
         self.si, self.ei = sigmoid(i)
+        self.er = torch.where(self.sr == 0, torch.zeros_like(self.er), self.er)  # no infinite error of a zero
         self.u = 2 * scale * self.soft * self.sr
         self.eu = self.es + self.er + 4 * U
         self.a = torch.exp(-self.u / 2)

@@ -615,9 +615,9 @@ void recur_bwd_kernel(RecurArgs a) {
   for (int j = N - 1; j >= 0; --j) {
     const float xj = channel<1>(x[j], 0);
     left = bits >> (j + 1) & 1u ? g[j] : g[j] + left;
-    const float lx = gated(m[j], left) * si[j];
+    const float lx = gated(m[j], left * si[j]);
     dx.put(c, j, lx);
-    di.put(c, j, gated(lx, xj) * (1.0f - si[j]));
+    di.put(c, j, gated(lx, xj * (1.0f - si[j])));
     // u / 2 and u / (2 m): without a step the first is 0, or too small to matter
     const float half = 0.5f * rate * sr[j];
     const float w = half * __builtin_amdgcn_rcpf(__builtin_fmaxf(m[j], 0x1p-60f));
