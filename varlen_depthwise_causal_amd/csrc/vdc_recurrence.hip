@@ -35,6 +35,7 @@
 #include <algorithm>
 #include <cfloat>
 #include <climits>
+#include <type_traits>
 
 #include "vdc_layer.h"
 #include "vdc_ssm_math.h"
@@ -96,7 +97,11 @@ struct Run {
   __device__ __forceinline__ Run(const uint16_t* base, int64_t stride_, int32_t t0, int32_t S)
       : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base + (int64_t)t0 * stride_), (short)0, 0x7fffffff,
                                             0x00020000)),
-        stride((uint32_t)stride_ * 2u), left(S - t0) {}
+        stride((uint32_t)stride_ * 2u), left(S - t0) {
+    // Known to this run alone: which rows are there would otherwise be kept in scalar
+    // registers for all of a tile's tensors, and these run out.
+    asm volatile("" : "+s"(left));
+  }
   __device__ __forceinline__ int row(int j) const { return (int)(j < left ? (uint32_t)j * stride : 0x7fffffffu); }
   template <int V>
   __device__ __forceinline__ uint32_t get(const Cols<V>& c, int j) const {
@@ -587,14 +592,20 @@ void recur_bwd_kernel(RecurArgs a) {
     h = starts >> q & 1u ? s.y : __builtin_fmaf(s.x, h, s.y);
   }
   const Run dz(a.dz, a.C, t0, a.S);
+  // B becomes the state before the token.
+  auto states = [&](auto plain) {
 #pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const bool first = bits >> j & 1u;
-    const float before = first ? 0.0f : h;
-    h = first ? B[j] : __builtin_fmaf(A[j], h, B[j]);
-    B[j] = before;  // from here on the state before the token
-    if (kGate) dz.put(c, j, gate[wave][j][lane] * h);
-  }
+    for (int j = 0; j < N; ++j) {
+      const bool first = !decltype(plain)::value && (bits >> j & 1u);
+      const float before = first ? 0.0f : h;
+      h = first ? B[j] : __builtin_fmaf(A[j], h, B[j]);
+      B[j] = before;
+      if (kGate) dz.put(c, j, gate[wave][j][lane] * h);
+      if (j % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  if (bits == 0) states(std::true_type());
+  else states(std::false_type());
 
   float l[1] = {0.0f};
   if (waits) {
@@ -620,7 +631,7 @@ void recur_bwd_kernel(RecurArgs a) {
     di.put(c, j, gated(lx, xj * (1.0f - si[j])));
     // u / 2 and u / (2 m): without a step the first is 0, or too small to matter
     const float half = 0.5f * rate * sr[j];
-    const float w = half * __builtin_amdgcn_rcpf(__builtin_fmaxf(m[j], 0x1p-60f));
+    const float w = half * __builtin_amdgcn_rcpf(m[j] < 0x1p-60f ? 0x1p-60f : m[j]);
     const float E = left * __builtin_fmaf(-half * A[j], B[j], gated(A[j] * A[j] * w, si[j] * xj));
     sum += E;
     dr.put(c, j, E * (1.0f - sr[j]));
