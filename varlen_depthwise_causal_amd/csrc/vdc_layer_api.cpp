@@ -95,17 +95,21 @@ Span state_span(const vdc_recurrence* v) {
   return {v->state, v->state ? (size_t)v->slots * v->C * 4 : 0};
 }
 
-// Places the workspace's arrays (base may be null: the size alone).
+// Places the workspace's arrays (base may be null: the size alone): the ticket and
+// the words, which one tile does without, then the backward's partial sums.
 size_t recur_layout(int dir, int64_t S, int64_t C, char* base, RecurArgs* a) {
   const int64_t tiles = ceil_div(S, dir == VDC_FWD ? kRecurFwdTile : kRecurBwdTile);
   const int64_t cols = ceil_div(C, 128) * 128;
-  const size_t words = recur_words_bytes(tiles, cols);
+  const size_t row = (size_t)tiles * cols * 8, words = tiles > 1 ? 256 + row : 0;
+  const bool few = recur_few(tiles, C);
   a->tiles = (int32_t)tiles;
   a->cols = (int32_t)cols;
   a->ticket = reinterpret_cast<uint32_t*>(base);
   a->words = reinterpret_cast<uint64_t*>(base + 256);
   a->part = reinterpret_cast<float*>(base + words);
-  return words + (dir == VDC_BWD ? (size_t)tiles * C * 4 : 0);
+  a->sums = dir == VDC_BWD && few ? reinterpret_cast<uint64_t*>(base + words) : nullptr;
+  if (dir == VDC_FWD) return words;
+  return few ? words + std::max<size_t>(row, 256) : words + (size_t)tiles * C * 4;
 }
 
 }  // namespace
@@ -162,7 +166,7 @@ extern "C" int gated_recurrence_bwd(const vdc_recurrence* v, const void* dy, int
   if (!aligned(dy, 2) || !aligned(keep, 4) || !aligned(dx, 2) || !aligned(dr, 2) || !aligned(di, 2) ||
       !aligned(dz, 2) || !aligned(ddecay, dtype_bytes(v->decay_dtype)))
     return VDC_EALIGN;
-  const size_t need = recur_layout(VDC_BWD, v->S, v->C, static_cast<char*>(workspace), &a);
+  const size_t need = v->S ? recur_layout(VDC_BWD, v->S, v->C, static_cast<char*>(workspace), &a) : 0;
   if (need) {
     if (!workspace || ws_bytes < need) return VDC_EWORKSPACE;
     if (!aligned(workspace, 16)) return VDC_EALIGN;
@@ -187,7 +191,7 @@ extern "C" int gated_recurrence_bwd(const vdc_recurrence* v, const void* dy, int
   a.ddecay = ddecay;
   if (a.tiles > 1 && (rc = done(launch_recur_clear(a, stream)))) return rc;
   if (v->S > 0 && (rc = done(launch_recur_bwd(a, stream)))) return rc;
-  return done(launch_recur_bwd_sum(a, stream));
+  return a.sums ? VDC_OK : done(launch_recur_bwd_sum(a, stream));
 }
 
 extern "C" int gated_recurrence_update(const vdc_recurrence* v, void* y, hipStream_t stream) {

@@ -498,6 +498,14 @@ void recur_fwd_kernel(RecurArgs a) {
   }
 }
 
+// The decay's gradient from the sum of E.  sigmoid / softplus tends to 1 where both
+// are too small to be told from 0.
+__device__ __forceinline__ void put_ddecay(const RecurArgs& a, int64_t c, double s) {
+  const float decay = param_at(a.decay, a.decay_bf16, c), soft = softplus_f32(decay);
+  const float ratio = soft > FLT_MIN ? sigmoid_f32(decay) / soft : 1.0f;
+  param_put(a.ddecay, a.decay_bf16, c, ratio * (float)s);
+}
+
 // N tokens a run, W runs a tile.  dy silu'(z) waits for the states in LDS: with it in
 // registers two workgroups fit on a CU instead of three.
 template <int N, int W, bool kGate>
@@ -641,10 +649,33 @@ void recur_bwd_kernel(RecurArgs a) {
   __syncthreads();
   sent[wave][lane] = sum;
   __syncthreads();
+  if (wave == 0) {
+#pragma unroll
+    for (int q = 1; q < W; ++q) sum += sent[q][lane];
+    if (!a.sums) {
+      if (c.has) a.part[(int64_t)k * a.C + c.c] = sum;
+    } else if (a.tiles > 1) {
+      const uint64_t w[1] = {known(sum)};
+      hand_on(a.sums + (int64_t)k * a.cols + p.block * 64 + lane, w);
+    }
+  }
+  if (!a.sums || p.n + 1 < a.tiles) return;
+  // Few tiles: the last one's workgroup adds them, in FP64, as their sums come.
+  __shared__ double total[W][64];
+  double s = a.tiles == 1 && wave == 0 ? sum : 0.0;
+  const int32_t per = (a.tiles + W - 1) / W;
+  if (a.tiles > 1)
+    for (int32_t q = wave * per; q < min((wave + 1) * per, a.tiles); ++q) {
+      uint64_t w[1];
+      take<true>(a.sums + (int64_t)q * a.cols + p.block * 64 + lane, w);
+      s += __uint_as_float((uint32_t)w[0]);
+    }
+  total[wave][lane] = s;
+  __syncthreads();
   if (wave > 0 || !c.has) return;
 #pragma unroll
-  for (int q = 1; q < W; ++q) sum += sent[q][lane];
-  a.part[(int64_t)k * a.C + c.c] = sum;
+  for (int q = 1; q < W; ++q) s += total[q][lane];
+  put_ddecay(a, c.c, s);
 }
 
 // The tiles' sums of E in FP64, sixteen waves a part of the tiles each.
@@ -670,10 +701,7 @@ __global__ __launch_bounds__(1024) void recur_bwd_sum_kernel(RecurArgs a) {
   if (wave > 0 || c >= a.C) return;
 #pragma unroll
   for (int w = 1; w < 16; ++w) s += lds[w][lane];
-  const float decay = param_at(a.decay, a.decay_bf16, c), soft = softplus_f32(decay);
-  // sigmoid / softplus, which tends to 1 where both are too small to be told from 0
-  const float ratio = soft > FLT_MIN ? sigmoid_f32(decay) / soft : 1.0f;
-  param_put(a.ddecay, a.decay_bf16, c, ratio * (float)s);
+  put_ddecay(a, c, s);
 }
 
 // ----------------------------------------------------------- single tokens --
@@ -794,7 +822,7 @@ void launch_fwd(RecurArgs a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_recur_clear(const RecurArgs& a, hipStream_t s) {
-  const int64_t words = (int64_t)a.tiles * a.cols;
+  const int64_t words = (int64_t)a.tiles * a.cols * (a.sums ? 2 : 1);
   hipLaunchKernelGGL(recur_clear_kernel, dim3((uint32_t)((words + 511) / 512)), dim3(256), 0, s, a, words);
   return hipGetLastError();
 }
