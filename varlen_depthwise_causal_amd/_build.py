@@ -1,9 +1,12 @@
-"""Ahead-of-time build of libvdc.so for gfx950 with hipcc (no JIT)."""
+"""Ahead-of-time build of libvdc.so for gfx950 with hipcc, and of the recurrent
+layer's binding (no JIT)."""
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -11,6 +14,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIBRARY = os.path.join(PKG, "libvdc.so")
+BINDING = os.path.join(PKG, "_vdc_torch.so")
 
 ARCH = "gfx950"
 # Packed FP32 instructions stay off: plain float code is scheduled on the
@@ -31,9 +35,27 @@ def hipcc() -> str:
     return path
 
 
+def _binding_commands(obj: str, out: str):
+    """Compiles csrc/vdc_torch.cpp against the installed torch and links it with
+    libvdc.so, which it finds beside itself, and torch's libraries, which are
+    loaded when it is."""
+    cxx = shutil.which("g++") or hipcc()
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    rocm = os.path.dirname(os.path.dirname(os.path.realpath(hipcc())))
+    compile_ = [cxx, "-O2", "-std=c++17", "-fPIC", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+                "-I", sysconfig.get_paths()["include"], "-I", os.path.join(torch, "include"),
+                "-I", os.path.join(rocm, "include"), "-I", INCLUDE, "-c", os.path.join(CSRC, "vdc_torch.cpp"), "-o", obj]
+    link = [cxx, "-shared", "-o", out, obj, "-L", PKG, "-lvdc", "-Wl,-rpath,$ORIGIN", "-L", os.path.join(torch, "lib"),
+            "-ltorch_python", "-ltorch_cpu", "-lc10_hip", "-lc10"]
+    return compile_, link
+
+
 def build(verbose: bool = False) -> str:
-    """Compile csrc/*.hip + csrc/*.cpp into libvdc.so (always rebuilds)."""
+    """Compile csrc/*.hip + csrc/*.cpp into libvdc.so, and the recurrent layer's
+    binding into _vdc_torch.so (always rebuilds)."""
     os.makedirs(BUILD_DIR, exist_ok=True)
+    binding_obj, binding_tmp = os.path.join(BUILD_DIR, "vdc_torch.o"), BINDING + ".tmp%d" % os.getpid()
+    binding, binding_link = _binding_commands(binding_obj, binding_tmp)
     cc = hipcc()
     objs, running = [], []
     for src in SOURCES:
@@ -44,6 +66,9 @@ def build(verbose: bool = False) -> str:
             print(" ".join(cmd), flush=True)
         running.append((cmd, subprocess.Popen(cmd)))
         objs.append(obj)
+    if verbose:
+        print(" ".join(binding), flush=True)
+    running.append((binding, subprocess.Popen(binding)))
     for cmd, p in running:
         if p.wait():
             raise subprocess.CalledProcessError(p.returncode, cmd)
@@ -53,6 +78,10 @@ def build(verbose: bool = False) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIBRARY)
+    if verbose:
+        print(" ".join(binding_link), flush=True)
+    subprocess.run(binding_link, check=True)
+    os.replace(binding_tmp, BINDING)
     return LIBRARY
 
 
