@@ -359,7 +359,7 @@ template <int V, int N, int W, bool kGate, bool kState>
 __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4)))
 void recur_fwd_kernel(RecurArgs a) {
   constexpr int T = N * W;
-  static_assert(T == kRecurFwdTile && kRecurKeep % N == 0, "");
+  static_assert(T <= kRecurFwdTile && kRecurKeep % N == 0, "");
   __shared__ Starts<T, kState> docs;
   __shared__ float2 sums[W][64][V];  // P and H of the waves' runs
   __shared__ Seen<W, V> seen;
@@ -369,6 +369,13 @@ void recur_fwd_kernel(RecurArgs a) {
   const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64u), lane = threadIdx.x & 63;
   const int32_t tile0 = p.n * T, t0 = tile0 + wave * N;
   const Cols<V> c(a, p.block);
+  if (a.tiles == 1 && t0 >= a.S) {  // no tokens, but a part in finding documents
+    find_starts<W>(a, tile0, docs);
+    if (kState) empty_documents<W>(a, p.n, a.tiles, c);
+    __syncthreads();
+    __syncthreads();
+    return;
+  }
   uint32_t x[N], r[N], i[N], z[N];
   rows(c, a.r, a.rs, t0, a.S, r);
   rows(c, a.i, a.is, t0, a.S, i);
@@ -512,12 +519,13 @@ template <int N, int W, bool kGate>
 __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(3)))
 void recur_bwd_kernel(RecurArgs a) {
   constexpr int T = N * W;
-  static_assert(T == kRecurBwdTile, "");
+  static_assert(T <= kRecurBwdTile, "");
   __shared__ Starts<T, false> docs;
   __shared__ float2 sums[W][64];  // P and H of the waves' runs
   __shared__ float sent[W][64];   // what a run sends to its left without any from its right
   __shared__ Seen<W, 1> seen;
   __shared__ float gate[kGate ? W : 1][N][64];
+  __shared__ double total[W][64];
   __shared__ uint32_t ticket;
   clear_starts<W>(docs);
   const Place p = place_of(a, &ticket);
@@ -525,6 +533,20 @@ void recur_bwd_kernel(RecurArgs a) {
   const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64u), lane = threadIdx.x & 63;
   const int32_t tile0 = k * T, t0 = tile0 + wave * N;
   const Cols<1> c(a, p.block);
+  if (a.tiles == 1 && t0 >= a.S) {  // no tokens
+    find_starts<W>(a, tile0, docs);
+    sums[wave][lane] = {1.0f, 0.0f};
+    sent[wave][lane] = 0.0f;  // nothing to the left, and nothing to the sum
+    __syncthreads();
+    __syncthreads();
+    __syncthreads();
+    __syncthreads();
+    if (a.sums) {
+      total[wave][lane] = 0.0;
+      __syncthreads();
+    }
+    return;
+  }
   uint32_t x[N], r[N], i[N], z[N], dy[N];
   rows(c, a.r, a.rs, t0, a.S, r);
   rows(c, a.i, a.is, t0, a.S, i);
@@ -661,7 +683,6 @@ void recur_bwd_kernel(RecurArgs a) {
   }
   if (!a.sums || p.n + 1 < a.tiles) return;
   // Few tiles: the last one's workgroup adds them, in FP64, as their sums come.
-  __shared__ double total[W][64];
   double s = a.tiles == 1 && wave == 0 ? sum : 0.0;
   const int32_t per = (a.tiles + W - 1) / W;
   if (a.tiles > 1)
@@ -811,12 +832,22 @@ bool pairs(const RecurArgs& a) {
          pairs(a.i, a.is) && pairs(a.z, a.z ? a.zs : 0) && pairs(a.y, 0);
 }
 
-template <int V, bool kGate>
+template <int V, int N, int W>
 void launch_fwd(RecurArgs a, hipStream_t s) {
   a.blocks = (a.C + 64 * V - 1) / (64 * V);
-  const dim3 grid((uint32_t)((int64_t)a.tiles * a.blocks)), block(512);
-  if (a.state) hipLaunchKernelGGL((recur_fwd_kernel<V, 16, 8, kGate, true>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((recur_fwd_kernel<V, 16, 8, kGate, false>), grid, block, 0, s, a);
+  const dim3 grid((uint32_t)((int64_t)a.tiles * a.blocks)), block(64 * W);
+  if (a.z && a.state) hipLaunchKernelGGL((recur_fwd_kernel<V, N, W, true, true>), grid, block, 0, s, a);
+  else if (a.z) hipLaunchKernelGGL((recur_fwd_kernel<V, N, W, true, false>), grid, block, 0, s, a);
+  else if (a.state) hipLaunchKernelGGL((recur_fwd_kernel<V, N, W, false, true>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((recur_fwd_kernel<V, N, W, false, false>), grid, block, 0, s, a);
+}
+
+template <int N, int W>
+void launch_bwd(RecurArgs a, hipStream_t s) {
+  a.blocks = (a.C + 63) / 64;
+  const dim3 grid((uint32_t)((int64_t)a.tiles * a.blocks)), block(64 * W);
+  if (a.z) hipLaunchKernelGGL((recur_bwd_kernel<N, W, true>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((recur_bwd_kernel<N, W, false>), grid, block, 0, s, a);
 }
 
 }  // namespace
@@ -829,19 +860,18 @@ hipError_t launch_recur_clear(const RecurArgs& a, hipStream_t s) {
 
 hipError_t launch_recur_fwd(const RecurArgs& a, hipStream_t s) {
   if (a.S == 0) hipLaunchKernelGGL(recur_empty_kernel, dim3((uint32_t)((a.C + 63) / 64)), dim3(512), 0, s, a);
-  else if (pairs(a) && a.z) launch_fwd<2, true>(a, s);
-  else if (pairs(a)) launch_fwd<2, false>(a, s);
-  else if (a.z) launch_fwd<1, true>(a, s);
-  else launch_fwd<1, false>(a, s);
+  else if (a.S <= 32) launch_fwd<1, 4, 8>(a, s);
+  else if (a.S <= 64) launch_fwd<1, 8, 8>(a, s);
+  else if (a.tiles == 1) launch_fwd<1, 8, 16>(a, s);
+  else if (pairs(a)) launch_fwd<2, 16, 8>(a, s);
+  else launch_fwd<1, 16, 8>(a, s);
   return hipGetLastError();
 }
 
-hipError_t launch_recur_bwd(const RecurArgs& args, hipStream_t s) {
-  RecurArgs a = args;
-  a.blocks = (a.C + 63) / 64;
-  const dim3 grid((uint32_t)((int64_t)a.tiles * a.blocks)), block(256);
-  if (a.z) hipLaunchKernelGGL((recur_bwd_kernel<16, 4, true>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((recur_bwd_kernel<16, 4, false>), grid, block, 0, s, a);
+hipError_t launch_recur_bwd(const RecurArgs& a, hipStream_t s) {
+  if (a.S <= 32) launch_bwd<4, 8>(a, s);
+  else if (a.S <= 64) launch_bwd<8, 8>(a, s);
+  else launch_bwd<16, 4>(a, s);
   return hipGetLastError();
 }
 
