@@ -12,8 +12,16 @@ namespace vdc {
 
 // ---------------------------------------------- gated linear recurrence --
 
-// Tokens of the tiles that a row of tokens is cut into.
+// Tokens of the tiles that a row is cut into: 128 forward and 64 backward, and 64
+// forward where that leaves a CU one tile or none (1543 tokens, C = 520, 225 tiles of
+// 64: 9.5 against 10.9 us; 8000 tokens, C = 256, 500 of them: 17.9 against 13.5), but
+// one tile as far as it goes, which needs no words (77 tokens, C = 2048: 7.5 against
+// 2.0 and 7.9).
 constexpr int kRecurFwdTile = 128, kRecurBwdTile = 64;
+inline int64_t recur_tiles_of_64(int64_t S, int64_t C) { return (S + 63) / 64 * ((C + 63) / 64); }
+inline int recur_fwd_tile(int64_t S, int64_t C) {
+  return S > kRecurFwdTile && recur_tiles_of_64(S, C) <= 256 ? 64 : kRecurFwdTile;
+}
 // Tokens between two states that a training forward keeps.
 constexpr int kRecurKeep = kRecurBwdTile;
 
@@ -26,7 +34,7 @@ struct RecurArgs {
   const int32_t* cu;
   int32_t num_docs;
   int32_t S, C;
-  int32_t tiles;                // of tokens
+  int32_t tiles, tile;          // of tokens, and how many each has
   int32_t blocks;               // workgroups that share a tile of tokens
   int32_t cols;                 // words of a tile: C rounded up to 128
   float* state;                 // [slots][C]
@@ -44,10 +52,10 @@ struct RecurArgs {
   uint64_t* sums;               // backward of few: [tiles][cols] of them as words, behind the others; else null
 };
 
-// Whether a backward's tiles add their partial sums of ddecay in the same launch: all
-// of them are at work at once then.  25 tiles, C = 520, with their forward: 34.3
-// against 36.6 us; 32 tiles, C = 4096: 85 against 83.
-inline bool recur_few(int64_t tiles, int64_t C) { return tiles <= 32 && tiles * ((C + 63) / 64) <= 512; }
+// Whether a backward's tiles add their partial sums of ddecay in the same launch.  25
+// tiles, C = 520, with their forward: 34.3 against 36.6 us; 32 tiles, C = 4096, which
+// are not at work at once: 85 against 83.
+inline bool recur_few(int64_t S, int64_t C) { return S <= 32 * kRecurBwdTile && recur_tiles_of_64(S, C) <= 512; }
 
 // The ticket and the words as a call finds them.
 hipError_t launch_recur_clear(const RecurArgs& a, hipStream_t s);
