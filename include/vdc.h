@@ -462,7 +462,7 @@ typedef struct vdc_recurrence {
     int decay_dtype;
     float scale;      /* at least 0, finite                                  */
     const int32_t *cu_seqlens; /* int32 [num_docs + 1]; unused by gated_recurrence_update */
-    int64_t num_docs;
+    int64_t num_docs; /* at most 2^31 - 4096                                 */
     float *state;     /* FP32 [slots][C], in place; forward: or NULL         */
     int64_t slots;
     const int32_t *state_index; /* one per document (row), or NULL           */

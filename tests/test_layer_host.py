@@ -47,7 +47,8 @@ RECUR_BAD = [({"C": 0}, EINVAL), ({"C": 2 ** 20 + 1}, EINVAL), ({"S": -1}, EINVA
              ({"scale": float("inf")}, EINVAL), ({"decay_dtype": 2}, EDTYPE), ({"x": at(0) + 1}, EALIGN),
              ({"r": at(1) + 1}, EALIGN), ({"i": at(2) + 1}, EALIGN), ({"z": at(3) + 1}, EALIGN),
              ({"decay": at(4) + 2}, EALIGN)]
-PROMPT_BAD = [({"num_docs": 0}, EINVAL), ({"num_docs": -1}, EINVAL), ({"cu_seqlens": None}, EINVAL),
+PROMPT_BAD = [({"num_docs": 0}, EINVAL), ({"num_docs": -1}, EINVAL), ({"num_docs": 2 ** 31 - 4095}, EINVAL),
+              ({"cu_seqlens": None}, EINVAL),
               ({"cu_seqlens": at(5) + 2}, EALIGN)]
 STATE_BAD = [({"slots": 2}, EINVAL), ({"slots": -1}, EINVAL), ({"state": at(6) + 2}, EALIGN),
              ({"state": at(0)}, EINVAL), ({"state": at(4)}, EINVAL), ({"state_index": at(6)}, EINVAL),
@@ -190,6 +191,28 @@ def test_the_binding_refuses_what_is_no_device_tensor():
         vdc.state_quantize(state, codes, scales)
     with pytest.raises(TypeError, match="float32 or bfloat16"):
         vdc.state_quantize(state.double(), codes, scales)
+
+
+def test_the_binding_is_required(monkeypatch):
+    """No fallback where the compiled calls are missing."""
+    from varlen_depthwise_causal_amd import layer
+    with pytest.raises(AttributeError):
+        layer._call.no_such_call
+    monkeypatch.setattr(layer, "BINDING", "/nowhere/_vdc_torch.so")
+    with pytest.raises(ImportError, match="not built"):
+        layer._Binding().norm_fwd
+
+
+def test_the_binding_refuses_arguments_of_other_types():
+    import varlen_depthwise_causal_amd as vdc
+    x = torch.zeros(4, 8, dtype=torch.bfloat16)
+    for call in (lambda: vdc.layer_norm_fwd(None, x), lambda: vdc.layer_norm_fwd(x, 3),
+                 lambda: vdc.gated_recurrence_fwd(x, x, x, [1.0], None),
+                 lambda: vdc.state_quantize("cache", x, x)):
+        with pytest.raises((TypeError, ValueError)):
+            call()
+    with pytest.raises(TypeError):
+        vdc.layer_norm_fwd(x, torch.zeros(8), eps="small")
 
 
 # ------------------------------------------------------- the definitions --

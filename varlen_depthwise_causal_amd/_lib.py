@@ -10,7 +10,6 @@ from ._build import LIBRARY
 VDC_F32, VDC_BF16 = 0, 1
 VDC_SILU_GRAD_BF16, VDC_SILU_GRAD_FP32 = 0, 1
 VDC_FWD, VDC_BWD = 0, 1
-VDC_INT8, VDC_E4M3 = 0, 1
 (VDC_OK, VDC_EINVAL, VDC_EDTYPE, VDC_EALIGN, VDC_EWORKSPACE, VDC_ENOBIAS, VDC_EHIP,
  VDC_ESCRATCH) = range(8)
 STATUS = {VDC_OK: "VDC_OK", VDC_EINVAL: "VDC_EINVAL", VDC_EDTYPE: "VDC_EDTYPE",

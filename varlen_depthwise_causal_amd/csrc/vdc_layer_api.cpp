@@ -16,7 +16,8 @@
 namespace vdc {
 namespace {
 
-// The kernels count tokens, and a few past the last, in 32 bits.
+// The kernels count tokens, and entries of cu_seqlens, and a few past the last of
+// them, in 32 bits.
 constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 4096;
 
 // Largest row stride of x, r, i, z and dy: a run of tokens stays below 2^31 bytes.
@@ -38,7 +39,7 @@ int recur_common(const vdc_recurrence* v, bool prompt, RecurArgs* a) {
   for (int64_t s : strides)
     if (s < v->C || s > kRecurMaxStride) return VDC_EINVAL;
   if (prompt) {
-    if (v->num_docs < 0 || v->num_docs > kMaxS - 1 || (v->S > 0 && v->num_docs < 1)) return VDC_EINVAL;
+    if (v->num_docs < 0 || v->num_docs > kMaxTokens || (v->S > 0 && v->num_docs < 1)) return VDC_EINVAL;
     if (v->num_docs > 0 && !v->cu_seqlens) return VDC_EINVAL;
   }
   const int64_t seqs = prompt ? v->num_docs : v->S;

@@ -306,14 +306,14 @@ __global__ __launch_bounds__(1024) void layer_norm_bwd_sum_kernel(LayerNormArgs 
   double s = 0.0;
   if (i < width) {
     int32_t r = r0;
-    // sixteen loads at once, past the end the last row again
-    for (; r < r1; r += 16) {
-      float v[16];
+    for (; r + 8 <= r1; r += 8) {
+      float v[8];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) v[j] = a.part[min(r + j, r1 - 1) * width + i];
+      for (int j = 0; j < 8; ++j) v[j] = a.part[(r + j) * width + i];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) s += r + j < r1 ? v[j] : 0.0f;
+      for (int j = 0; j < 8; ++j) s += v[j];
     }
+    for (; r < r1; ++r) s += a.part[r * width + i];
   }
   lds[wave][lane] = s;
   __syncthreads();

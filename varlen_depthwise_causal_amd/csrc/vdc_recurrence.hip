@@ -13,17 +13,17 @@
 //
 // Bound by HBM, where a token's inputs are read once: 8 bytes a token and channel
 // forward (10 with a gate), 14 (18) backward.  So both directions are one pass: a
-// workgroup has a tile of 64 channels by 128 (backward 64) tokens in registers,
-// finds what the tile makes of any state, h -> P h + H, hands that on, takes the
-// state that the tiles before it leave (backward: the gradient that the tiles
-// behind it send), and finishes.  Two passes over a long row would read 14 bytes
-// instead of 8.
+// workgroup has a tile of 64 or 128 channels by 128 (backward 64) tokens in
+// registers, finds what the tile makes of any state, h -> P h + H, hands that on,
+// takes the state that the tiles before it leave (backward: the gradient that the
+// tiles behind it send), and finishes.  Two passes over a long row would read 14
+// bytes instead of 8.
 //
 // What a tile hands on is one 64-bit word a channel: P and H, or, once the state
 // after the tile is known, that state and a mark in place of P.  A tile reads the
-// words of the eight before it and folds them in order from the nearest marked one.
-// A marked word is by its definition the fold of the word before it with its own P
-// and H, so where a fold begins makes no difference to its bits.
+// words of those before it, one a wave, and folds them in order from the nearest
+// marked one.  A marked word is by its definition the fold of the word before it with
+// its own P and H, so where a fold begins makes no difference to its bits.
 //
 // No wait is for ever: tiles are numbered by a ticket as their workgroups begin,
 // each waits for lower numbers alone, and those have begun.  A word is written and
