@@ -36,7 +36,7 @@ struct RecurArgs {
   int32_t S, C;
   int32_t tiles, tile;          // of tokens, and how many each has
   int32_t blocks;               // workgroups that share a tile of tokens
-  int32_t cols;                 // words of a tile: C rounded up to 128
+  int32_t cols;                 // words of a tile: C rounded up to 64
   float* state;                 // [slots][C]
   const int32_t* index;
   const uint8_t* resume;
@@ -46,7 +46,7 @@ struct RecurArgs {
   uint16_t *dx, *dr, *di, *dz;
   void* ddecay;
   // workspace
-  uint32_t* ticket;             // tiles that have begun; the words follow it
+  uint64_t* tickets;            // [cols] every 64th counts the tiles of its channels that have begun; the words follow
   uint64_t* words;              // [tiles][cols] what a tile hands on
   float* part;                  // backward of many tiles: [tiles][C] partial ddecay
   uint64_t* sums;               // backward of few: [tiles][cols] of them as words, behind the others; else null
@@ -57,7 +57,7 @@ struct RecurArgs {
 // are not at work at once: 85 against 83.
 inline bool recur_few(int64_t S, int64_t C) { return S <= 32 * kRecurBwdTile && recur_tiles_of_64(S, C) <= 512; }
 
-// The ticket and the words as a call finds them.
+// The tickets and the words as a call finds them.
 hipError_t launch_recur_clear(const RecurArgs& a, hipStream_t s);
 hipError_t launch_recur_fwd(const RecurArgs& a, hipStream_t s);
 hipError_t launch_recur_bwd(const RecurArgs& a, hipStream_t s);

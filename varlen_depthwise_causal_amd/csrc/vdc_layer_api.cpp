@@ -96,19 +96,19 @@ Span state_span(const vdc_recurrence* v) {
   return {v->state, v->state ? (size_t)v->slots * v->C * 4 : 0};
 }
 
-// Places the workspace's arrays (base may be null: the size alone): the ticket and
-// the words, which one tile does without, then the backward's partial sums.
+// Places the workspace's arrays (base may be null: the size alone): the tickets
+// and the words, which one tile does without, then the backward's partial sums.
 size_t recur_layout(int dir, int64_t S, int64_t C, char* base, RecurArgs* a) {
   const int tile = dir == VDC_FWD ? recur_fwd_tile(S, C) : kRecurBwdTile;
   const int64_t tiles = ceil_div(S, tile);
-  const int64_t cols = ceil_div(C, 128) * 128;
-  const size_t row = (size_t)tiles * cols * 8, words = tiles > 1 ? 256 + row : 0;
+  const int64_t cols = ceil_div(C, 64) * 64;
+  const size_t row = (size_t)tiles * cols * 8, words = tiles > 1 ? cols * 8 + row : 0;
   const bool few = recur_few(S, C);
   a->tiles = (int32_t)tiles;
   a->tile = tile;
   a->cols = (int32_t)cols;
-  a->ticket = reinterpret_cast<uint32_t*>(base);
-  a->words = reinterpret_cast<uint64_t*>(base + 256);
+  a->tickets = reinterpret_cast<uint64_t*>(base);
+  a->words = a->tickets + cols;
   a->part = reinterpret_cast<float*>(base + words);
   a->sums = dir == VDC_BWD && few ? reinterpret_cast<uint64_t*>(base + words) : nullptr;
   if (dir == VDC_FWD) return words;

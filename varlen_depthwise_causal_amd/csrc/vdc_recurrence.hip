@@ -25,8 +25,8 @@
 // marked one.  A marked word is by its definition the fold of the word before it with
 // its own P and H, so where a fold begins makes no difference to its bits.
 //
-// No wait is for ever: tiles are numbered by a ticket as their workgroups begin,
-// each waits for lower numbers alone, and those have begun.  A word is written and
+// No wait is for ever: a block of channels' tiles are numbered as their workgroups
+// begin, each waits for lower numbers alone, and those have begun.  A word is written and
 // read whole and holds all that its reader needs, so no fence is needed either.
 //
 // Everything between documents is assigned, never multiplied by zero, so that
@@ -72,14 +72,13 @@ __device__ __forceinline__ float gated(float a, float b) { return vdc_fmul_legac
 
 // ------------------------------------------------------------------- tiles --
 
-// The V channels of a lane, two where they are one aligned word in every row, else
-// one.  Lanes past the last channel read the first one's values and store nothing.
-template <int V>
-struct Cols {
+// A lane's channel.  Lanes past the last one read the first one's values and store
+// nothing.
+struct Col {
   uint32_t c;
   bool has;
-  __device__ __forceinline__ Cols(const RecurArgs& a, int32_t block) {
-    c = ((uint32_t)block * 64u + (threadIdx.x & 63u)) * V;
+  __device__ __forceinline__ Col(const RecurArgs& a, int32_t block) {
+    c = (uint32_t)block * 64u + (threadIdx.x & 63u);
     has = c < (uint32_t)a.C;
     if (!has) c = 0;
   }
@@ -103,36 +102,22 @@ struct Run {
     asm volatile("" : "+s"(left));
   }
   __device__ __forceinline__ int row(int j) const { return (int)(j < left ? (uint32_t)j * stride : 0x7fffffffu); }
-  template <int V>
-  __device__ __forceinline__ uint32_t get(const Cols<V>& c, int j) const {
-    if (V == 2) return __builtin_amdgcn_raw_buffer_load_b32(r, (int)(c.c * 2u), row(j), kOnce);
+  __device__ __forceinline__ uint32_t get(const Col& c, int j) const {
     return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)(c.c * 2u), row(j), kOnce);
   }
-  template <int V>
-  __device__ __forceinline__ void put(const Cols<V>& c, int j, const float (&v)[V]) const {
-    const int at = (int)(c.has ? c.c * 2u : 0x80000000u);
-    if (V == 2) __builtin_amdgcn_raw_buffer_store_b32(bf16_pack2(v[0], v[V - 1]), r, at, row(j), kOnce);
-    else __builtin_amdgcn_raw_buffer_store_b16(bf16_of(v[0]), r, at, row(j), kOnce);
-  }
-  __device__ __forceinline__ void put(const Cols<1>& c, int j, float v) const {
-    const float one[1] = {v};
-    put(c, j, one);
+  __device__ __forceinline__ void put(const Col& c, int j, float v) const {
+    __builtin_amdgcn_raw_buffer_store_b16(bf16_of(v), r, (int)(c.has ? c.c * 2u : 0x80000000u), row(j), kOnce);
   }
   // Nothing is read or written twice: loads and stores do not stay in the caches.
   static constexpr int kOnce = 2;
 };
 
-template <int N, int V>
-__device__ __forceinline__ void rows(const Cols<V>& c, const uint16_t* t, int64_t stride, int32_t t0, int32_t S,
+template <int N>
+__device__ __forceinline__ void rows(const Col& c, const uint16_t* t, int64_t stride, int32_t t0, int32_t S,
                                      uint32_t (&v)[N]) {
   const Run b(t, stride, t0, S);
 #pragma unroll
   for (int j = 0; j < N; ++j) v[j] = b.get(c, j);
-}
-// Channel v of a lane's word.
-template <int V>
-__device__ __forceinline__ float channel(uint32_t w, int v) {
-  return V == 2 && v ? bf16_hi(w) : bf16_lo(w);
 }
 
 // The documents that start or end among a tile's tokens.
@@ -206,109 +191,90 @@ __device__ __forceinline__ uint64_t word_of(float P, float H) {
 __device__ __forceinline__ uint64_t known(float H) { return (uint64_t)kKnown << 32 | __float_as_uint(H); }
 __device__ __forceinline__ uint32_t mark(uint64_t w) { return (uint32_t)(w >> 32); }
 
-template <int V>
-__device__ __forceinline__ void hand_on(uint64_t* p, const uint64_t (&w)[V]) {
-#pragma unroll
-  for (int v = 0; v < V; ++v) __hip_atomic_store(p + v, w[v], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+__device__ __forceinline__ void hand_on(uint64_t* p, uint64_t w) {
+  __hip_atomic_store(p, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 // A wave's words once all of them are there, or once all are known.
-template <bool kAll, int V>
-__device__ __forceinline__ void take(uint64_t* p, uint64_t (&w)[V]) {
+template <bool kAll>
+__device__ __forceinline__ uint64_t take(uint64_t* p) {
+  uint64_t w = 0;
   for (int n = 0; n < kPolls; ++n) {
-    bool wait = false;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      w[v] = __hip_atomic_load(p + v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      wait |= kAll ? mark(w[v]) != kKnown : mark(w[v]) == kEmpty;
-    }
-    if (__ballot(wait) == 0) break;
+    w = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (__ballot(kAll ? mark(w) != kKnown : mark(w) == kEmpty) == 0) break;
     __builtin_amdgcn_s_sleep(1);
   }
+  return w;
 }
 
 // The words of the tiles before this one, W at a time, and which lanes have found a
 // known one among those of each time.
-template <int W, int V>
+template <int W>
 struct Seen {
-  uint64_t w[kLooks * W][64][V];
-  uint64_t known[kLooks][V][W];
+  uint64_t w[kLooks * W][64];
+  uint64_t known[kLooks][W];
 };
 
 // What reaches this tile from those of lower numbers, `far` tiles of which there
 // are; `step` leads from a tile's words to those of the next lower number.  All
 // waves call it and have the result.
-template <int W, int V>
-__device__ __forceinline__ void look_back(uint64_t* words, int64_t step, int32_t far, Seen<W, V>& seen,
-                                          float (&carry)[V]) {
+template <int W>
+__device__ __forceinline__ float look_back(uint64_t* words, int64_t step, int32_t far, Seen<W>& seen) {
   const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64u), lane = threadIdx.x & 63;
-  uint64_t missing[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) missing[v] = ~(uint64_t)0;
+  uint64_t missing = ~(uint64_t)0;
   int32_t looks = 0;
   bool all = false;  // the same in all waves
 #pragma unroll 1
   while (looks < kLooks && !all) {
     const int32_t d = looks * W + wave;
-    uint64_t w[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) w[v] = known(0.0f);
-    if (d < far) take<false>(words + (int64_t)(d + 1) * step, w);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      seen.w[d][lane][v] = w[v];
-      seen.known[looks][v][wave] = __ballot(mark(w[v]) == kKnown);
-    }
+    const uint64_t w = d < far ? take<false>(words + (int64_t)(d + 1) * step) : known(0.0f);
+    seen.w[d][lane] = w;
+    seen.known[looks][wave] = __ballot(mark(w) == kKnown);
     __syncthreads();
-    all = true;
+    uint64_t k = seen.known[looks][lane % W];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      uint64_t k = seen.known[looks][v][lane % W];
-#pragma unroll
-      for (int i = 1; i < W; i <<= 1) k |= __shfl_xor(k, i, 64);
-      missing[v] &= ~k;
-      all &= __builtin_amdgcn_readfirstlane((uint32_t)missing[v] | (uint32_t)(missing[v] >> 32)) == 0;
-    }
+    for (int i = 1; i < W; i <<= 1) k |= __shfl_xor(k, i, 64);
+    missing &= ~k;
+    all = __builtin_amdgcn_readfirstlane((uint32_t)missing | (uint32_t)(missing >> 32)) == 0;
     ++looks;
   }
   if (!all) {  // so there are more than kLooks * W of them
     __syncthreads();
-    if (wave == W - 1) {
-      uint64_t w[V];
-      take<true>(words + (int64_t)(kLooks * W) * step, w);
-#pragma unroll
-      for (int v = 0; v < V; ++v) seen.w[kLooks * W - 1][lane][v] = w[v];
-    }
+    if (wave == W - 1) seen.w[kLooks * W - 1][lane] = take<true>(words + (int64_t)(kLooks * W) * step);
     __syncthreads();
   }
-#pragma unroll
-  for (int v = 0; v < V; ++v) carry[v] = 0.0f;
+  float carry = 0.0f;
 #pragma unroll 4
-  for (int d = looks * W - 1; d >= 0; --d)
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const uint64_t w = seen.w[d][lane][v];
-      const float H = __uint_as_float((uint32_t)w), P = __uint_as_float(mark(w));
-      carry[v] = mark(w) == kKnown ? H : __builtin_fmaf(P, carry[v], H);
-    }
+  for (int d = looks * W - 1; d >= 0; --d) {
+    const uint64_t w = seen.w[d][lane];
+    const float H = __uint_as_float((uint32_t)w), P = __uint_as_float(mark(w));
+    carry = mark(w) == kKnown ? H : __builtin_fmaf(P, carry, H);
+  }
+  return carry;
 }
 
-// The tile of this workgroup: its number and channel block.
+// The tile of this workgroup: its number, of its channel block, and that block.  Each
+// block of channels has a counter of its own, 512 bytes apart: one for all of them hands
+// its numbers out one after the other (1543 tokens, C = 520, 225 tiles, forward and
+// backward: 26.2 against 22.5 us; 8192 tokens, C = 2048, forward: 48.4 against 43.4).
 struct Place {
   int32_t n, block;
 };
 __device__ __forceinline__ Place place_of(const RecurArgs& a, uint32_t* lds) {
-  if (a.tiles > 1 && threadIdx.x == 0) *lds = atomicAdd(a.ticket, 1u);
+  const uint32_t blocks = (uint32_t)a.blocks;
+  // Of `blocks` workgroups each has another block, and a block's are on all XCDs in turn
+  // (on one XCD each: 16384 tokens, C = 4096, forward and backward 446 against 416 us).
+  const uint32_t block = (blockIdx.x + blockIdx.x / blocks) % blocks;
+  if (a.tiles > 1 && threadIdx.x == 0) *lds = atomicAdd(reinterpret_cast<uint32_t*>(a.tickets + block * 64), 1u) + 1u;
   __syncthreads();
-  const uint32_t t = a.tiles > 1 ? __builtin_amdgcn_readfirstlane(*lds) : blockIdx.x;
   // Two calls that share a workspace run past the last.
-  const uint32_t n = min(t / (uint32_t)a.blocks, (uint32_t)a.tiles - 1u);
-  return {(int32_t)n, (int32_t)(t % (uint32_t)a.blocks)};
+  const uint32_t n = a.tiles > 1 ? min(__builtin_amdgcn_readfirstlane(*lds), (uint32_t)a.tiles - 1u) : 0;
+  return {(int32_t)n, (int32_t)block};
 }
 
 // Documents without tokens leave zeros, or their slot as it is where they resume;
 // part `k` of `parts`.
-template <int W, int V>
-__device__ __forceinline__ void empty_documents(const RecurArgs& a, int32_t k, int32_t parts, const Cols<V>& c) {
+template <int W>
+__device__ __forceinline__ void empty_documents(const RecurArgs& a, int32_t k, int32_t parts, const Col& c) {
   const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64u), lane = threadIdx.x & 63;
   const int64_t per = ((int64_t)a.num_docs + parts - 1) / parts, end = min((k + 1) * per, (int64_t)a.num_docs);
   for (int64_t d0 = k * per + wave * 64; d0 < end; d0 += 64 * W) {
@@ -317,22 +283,19 @@ __device__ __forceinline__ void empty_documents(const RecurArgs& a, int32_t k, i
     if (d < end) empty = a.cu[d] == a.cu[d + 1] && !(a.resume && a.resume[d]);
     for (uint64_t m = __ballot(empty); m; m &= m - 1) {
       const int64_t slot = slot_of(a.index, d0 + __builtin_ctzll(m), a.slots);
-      if (slot >= 0 && c.has)
-#pragma unroll
-        for (int v = 0; v < V; ++v) a.state[slot * a.C + c.c + v] = 0.0f;
+      if (slot >= 0 && c.has) a.state[slot * a.C + c.c] = 0.0f;
     }
   }
 }
 
-__global__ __launch_bounds__(256) void recur_clear_kernel(RecurArgs a, int64_t words) {
+__global__ __launch_bounds__(256) void recur_clear_kernel(uint64_t* words, int64_t n) {
   const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 2;
-  if (i == 0) *a.ticket = 0;
-  if (i < words) *reinterpret_cast<u32x4_t*>(a.words + i) = (u32x4_t){kEmpty, kEmpty, kEmpty, kEmpty};
+  if (i < n) *reinterpret_cast<u32x4_t*>(words + i) = (u32x4_t){kEmpty, kEmpty, kEmpty, kEmpty};
 }
 
 // No tokens, but documents that leave their states.
 __global__ __launch_bounds__(512) void recur_empty_kernel(RecurArgs a) {
-  empty_documents<8>(a, 0, 1, Cols<1>(a, blockIdx.x));
+  empty_documents<8>(a, 0, 1, Col(a, blockIdx.x));
 }
 
 // The runs of a tile that have any of the bits kFrom .. kTo of theirs set, as a mask.
@@ -352,23 +315,22 @@ __device__ __forceinline__ uint32_t runs_with(const uint32_t* mask) {
   return m;
 }
 
-// V channels a lane, W waves with a run of N tokens each.  Everything between the
-// loads and the stores is in registers: with more of them than 128 a second workgroup
-// does not fit on a CU, and fewer tokens a tile make more words to hand on.
-template <int V, int N, int W, bool kGate, bool kState>
-__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4)))
+// W waves with a run of N tokens each.  Everything between the loads and the stores is
+// in registers: 80 of them leave room for three workgroups of runs of 16 on a CU.
+template <int N, int W, bool kGate, bool kState>
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(6)))
 void recur_fwd_kernel(RecurArgs a) {
   constexpr int T = N * W;
   static_assert(T <= kRecurFwdTile && kRecurKeep % N == 0, "");
   __shared__ Starts<T, kState> docs;
-  __shared__ float2 sums[W][64][V];  // P and H of the waves' runs
-  __shared__ Seen<W, V> seen;
+  __shared__ float2 sums[W][64];  // P and H of the waves' runs
+  __shared__ Seen<W> seen;
   __shared__ uint32_t ticket;
   clear_starts<W>(docs);
   const Place p = place_of(a, &ticket);
   const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64u), lane = threadIdx.x & 63;
   const int32_t tile0 = p.n * T, t0 = tile0 + wave * N;
-  const Cols<V> c(a, p.block);
+  const Col c(a, p.block);
   if (a.tiles == 1 && t0 >= a.S) {  // no tokens, but a part in finding documents
     find_starts<W>(a, tile0, docs);
     if (kState) empty_documents<W>(a, p.n, a.tiles, c);
@@ -380,24 +342,19 @@ void recur_fwd_kernel(RecurArgs a) {
   rows(c, a.r, a.rs, t0, a.S, r);
   rows(c, a.i, a.is, t0, a.S, i);
   rows(c, a.x, a.xs, t0, a.S, x);
-  if (kGate) rows(c, a.z, a.zs, t0, a.S, z);
-  float rate[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) rate[v] = decay_rate(a, c.c + v);
+  const float rate = decay_rate(a, c.c);
   find_starts<W>(a, tile0, docs);
   if (kState) empty_documents<W>(a, p.n, a.tiles, c);
+  if (kGate) rows(c, a.z, a.zs, t0, a.S, z);  // needed last; before the documents it takes 88 registers
   __syncthreads();
   const uint32_t bits = bits_at<N>(docs.mask, wave * N), own = bits & ((1u << N) - 1u);
 
-  float A[N][V], B[N][V];
+  float A[N], B[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float u = rate[v] * sigmoid_f32(channel<V>(r[j], v));
-      A[j][v] = decay_of(u);
-      B[j][v] = gated(input_scale(u, A[j][v]), sigmoid_f32(channel<V>(i[j], v)) * channel<V>(x[j], v));
-    }
+    const float u = rate * sigmoid_f32(bf16_lo(r[j]));
+    A[j] = decay_of(u);
+    B[j] = gated(input_scale(u, A[j]), sigmoid_f32(bf16_lo(i[j])) * bf16_lo(x[j]));
     if (j % 2) __builtin_amdgcn_sched_barrier(0);  // no more tokens side by side than registers hold
   }
   // A resumed document goes on from its slot's state.
@@ -406,91 +363,59 @@ void recur_fwd_kernel(RecurArgs a) {
     for (int j = 0; j < N; ++j)
       if (own >> j & 1u) {
         const int64_t slot = __builtin_amdgcn_readfirstlane(docs.from[wave * N + j]);
-        if (slot >= 0)
-#pragma unroll
-          for (int v = 0; v < V; ++v) B[j][v] = __builtin_fmaf(A[j][v], a.state[slot * a.C + c.c + v], B[j][v]);
+        if (slot >= 0) B[j] = __builtin_fmaf(A[j], a.state[slot * a.C + c.c], B[j]);
       }
   }
+  float P = 1.0f, H = 0.0f;
+  if (own == 0) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    float P = 1.0f, H = 0.0f;
-    if (own == 0) {
+    for (int j = 0; j < N; ++j) P *= A[j], H = __builtin_fmaf(A[j], H, B[j]);
+  } else {
 #pragma unroll
-      for (int j = 0; j < N; ++j) P *= A[j][v], H = __builtin_fmaf(A[j][v], H, B[j][v]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < N; ++j) H = own >> j & 1u ? B[j][v] : __builtin_fmaf(A[j][v], H, B[j][v]);
-    }
-    sums[wave][lane][v] = {P, H};
+    for (int j = 0; j < N; ++j) H = own >> j & 1u ? B[j] : __builtin_fmaf(A[j], H, B[j]);
   }
+  sums[wave][lane] = {P, H};
   __syncthreads();
 
   const uint32_t starts = runs_with<N, W, 0, N - 1>(docs.mask);
-  uint64_t* const mine = a.words + (int64_t)p.n * a.cols + (p.block * 64 + lane) * V;
+  uint64_t* const mine = a.words + (int64_t)p.n * a.cols + p.block * 64 + lane;
   const bool waits = p.n > 0 && (__builtin_amdgcn_readfirstlane(docs.mask[0]) & 1u) == 0;  // on what comes from the left
   const bool cut = !waits || starts != 0;  // the tile's last state does not go by it
   const bool hands = wave == 0 && p.n + 1 < a.tiles;
-  float tp[V], th[V];
+  float tp = 1.0f, th = 0.0f;
   if (hands) {
-    uint64_t w[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) tp[v] = 1.0f, th[v] = 0.0f;
 #pragma unroll 2
-    for (int k = 0; k < W; ++k)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float2 s = sums[k][lane][v];
-        th[v] = starts >> k & 1u ? s.y : __builtin_fmaf(s.x, th[v], s.y);
-        tp[v] *= s.x;
-      }
-#pragma unroll
-    for (int v = 0; v < V; ++v) w[v] = cut ? known(th[v]) : word_of(tp[v], th[v]);
-    hand_on(mine, w);
+    for (int k = 0; k < W; ++k) {
+      const float2 s = sums[k][lane];
+      th = starts >> k & 1u ? s.y : __builtin_fmaf(s.x, th, s.y);
+      tp *= s.x;
+    }
+    hand_on(mine, cut ? known(th) : word_of(tp, th));
   }
-  float h[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) h[v] = 0.0f;
+  float h = 0.0f;
   if (waits) {
-    look_back(mine, -(int64_t)a.cols, p.n, seen, h);
-    if (hands && !cut) {
-      uint64_t w[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) w[v] = known(__builtin_fmaf(tp[v], h[v], th[v]));
-      hand_on(mine, w);
-    }
+    h = look_back(mine, -(int64_t)a.cols, p.n, seen);
+    if (hands && !cut) hand_on(mine, known(__builtin_fmaf(tp, h, th)));
   }
 #pragma unroll 2
-  for (int k = 0; k < wave; ++k)
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float2 s = sums[k][lane][v];
-      h[v] = starts >> k & 1u ? s.y : __builtin_fmaf(s.x, h[v], s.y);
-    }
-  if (a.keep && t0 % kRecurKeep == 0 && t0 < a.S && c.has)
-#pragma unroll
-    for (int v = 0; v < V; ++v) a.keep[(int64_t)(t0 / kRecurKeep) * a.C + c.c + v] = h[v];
+  for (int k = 0; k < wave; ++k) {
+    const float2 s = sums[k][lane];
+    h = starts >> k & 1u ? s.y : __builtin_fmaf(s.x, h, s.y);
+  }
+  if (a.keep && t0 % kRecurKeep == 0 && t0 < a.S && c.has) a.keep[(int64_t)(t0 / kRecurKeep) * a.C + c.c] = h;
 
+  if (own == 0) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    if (own == 0) {
+    for (int j = 0; j < N; ++j) h = B[j] = __builtin_fmaf(A[j], h, B[j]);
+  } else {
 #pragma unroll
-      for (int j = 0; j < N; ++j) h[v] = B[j][v] = __builtin_fmaf(A[j][v], h[v], B[j][v]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < N; ++j)
-        h[v] = B[j][v] = own >> j & 1u ? B[j][v] : __builtin_fmaf(A[j][v], h[v], B[j][v]);
-    }
+    for (int j = 0; j < N; ++j) h = B[j] = own >> j & 1u ? B[j] : __builtin_fmaf(A[j], h, B[j]);
   }
   const Run y(a.y, a.C, t0, a.S);
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    float o[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float zj = kGate ? channel<V>(z[j], v) : 0.0f;
-      o[v] = kGate ? B[j][v] * (zj * sigmoid_f32(zj)) : B[j][v];
-    }
-    y.put(c, j, o);
+    const float zj = kGate ? bf16_lo(z[j]) : 0.0f;
+    y.put(c, j, kGate ? B[j] * (zj * sigmoid_f32(zj)) : B[j]);
   }
   // Documents that end leave their states.
   if (kState && bits >> 1) {
@@ -498,9 +423,7 @@ void recur_fwd_kernel(RecurArgs a) {
     for (int j = 0; j < N; ++j)
       if (bits >> (j + 1) & 1u) {
         const int64_t slot = __builtin_amdgcn_readfirstlane(docs.to[wave * N + j + 1]);
-        if (slot >= 0 && c.has)
-#pragma unroll
-          for (int v = 0; v < V; ++v) a.state[slot * a.C + c.c + v] = B[j][v];
+        if (slot >= 0 && c.has) a.state[slot * a.C + c.c] = B[j];
       }
   }
 }
@@ -523,7 +446,7 @@ void recur_bwd_kernel(RecurArgs a) {
   __shared__ Starts<T, false> docs;
   __shared__ float2 sums[W][64];  // P and H of the waves' runs
   __shared__ float sent[W][64];   // what a run sends to its left without any from its right
-  __shared__ Seen<W, 1> seen;
+  __shared__ Seen<W> seen;
   __shared__ float gate[kGate ? W : 1][N][64];
   __shared__ double total[W][64];
   __shared__ uint32_t ticket;
@@ -532,7 +455,7 @@ void recur_bwd_kernel(RecurArgs a) {
   const int32_t k = a.tiles - 1 - p.n;  // the last tile first
   const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64u), lane = threadIdx.x & 63;
   const int32_t tile0 = k * T, t0 = tile0 + wave * N;
-  const Cols<1> c(a, p.block);
+  const Col c(a, p.block);
   if (a.tiles == 1 && t0 >= a.S) {  // no tokens
     find_starts<W>(a, tile0, docs);
     sums[wave][lane] = {1.0f, 0.0f};
@@ -563,16 +486,16 @@ void recur_bwd_kernel(RecurArgs a) {
   float P = 1.0f, H = 0.0f, M = 0.0f;
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    sr[j] = sigmoid_f32(channel<1>(r[j], 0));
-    si[j] = sigmoid_f32(channel<1>(i[j], 0));
+    sr[j] = sigmoid_f32(bf16_lo(r[j]));
+    si[j] = sigmoid_f32(bf16_lo(i[j]));
     const float u = rate * sr[j];
     A[j] = decay_of(u);
     m[j] = input_scale(u, A[j]);
-    B[j] = gated(m[j], si[j] * channel<1>(x[j], 0));
-    g[j] = channel<1>(dy[j], 0);
+    B[j] = gated(m[j], si[j] * bf16_lo(x[j]));
+    g[j] = bf16_lo(dy[j]);
     if (kGate) {
       // dy silu(z), the gradient at the state, and dy silu'(z), dz but for the state
-      const float zj = channel<1>(z[j], 0), s = sigmoid_f32(zj);
+      const float zj = bf16_lo(z[j]), s = sigmoid_f32(zj);
       gate[wave][j][lane] = g[j] * dsilu_f32(zj, s);
       g[j] *= zj * s;
     }
@@ -612,8 +535,7 @@ void recur_bwd_kernel(RecurArgs a) {
       tm = shut >> q & 1u ? o : __builtin_fmaf(s, tm, o);
       tp *= s;
     }
-    const uint64_t w[1] = {cut ? known(tm) : word_of(tp, tm)};
-    hand_on(mine, w);
+    hand_on(mine, cut ? known(tm) : word_of(tp, tm));
   }
   // The states before this run, from the one that the forward kept.
 #pragma unroll 2
@@ -637,24 +559,21 @@ void recur_bwd_kernel(RecurArgs a) {
   if (bits == 0) states(std::true_type());
   else states(std::false_type());
 
-  float l[1] = {0.0f};
+  float left = 0.0f;  // l, and a l once a token is done
   if (waits) {
-    look_back(mine, (int64_t)a.cols, p.n, seen, l);
-    if (hands && !cut) {
-      const uint64_t w[1] = {known(__builtin_fmaf(tp, l[0], tm))};
-      hand_on(mine, w);
-    }
+    left = look_back(mine, (int64_t)a.cols, p.n, seen);
+    if (hands && !cut) hand_on(mine, known(__builtin_fmaf(tp, left, tm)));
   }
 #pragma unroll 2
   for (int q = W - 1; q > wave; --q) {
     const float o = sent[q][lane];
-    l[0] = shut >> q & 1u ? o : __builtin_fmaf(sums[q][lane].x, l[0], o);
+    left = shut >> q & 1u ? o : __builtin_fmaf(sums[q][lane].x, left, o);
   }
   const Run dx(a.dx, a.C, t0, a.S), di(a.di, a.C, t0, a.S), dr(a.dr, a.C, t0, a.S);
-  float sum = 0.0f, left = l[0];
+  float sum = 0.0f;
 #pragma unroll
   for (int j = N - 1; j >= 0; --j) {
-    const float xj = channel<1>(x[j], 0);
+    const float xj = bf16_lo(x[j]);
     left = bits >> (j + 1) & 1u ? g[j] : g[j] + left;
     const float lx = gated(m[j], left * si[j]);
     dx.put(c, j, lx);
@@ -677,8 +596,7 @@ void recur_bwd_kernel(RecurArgs a) {
     if (!a.sums) {
       if (c.has) a.part[(int64_t)k * a.C + c.c] = sum;
     } else if (a.tiles > 1) {
-      const uint64_t w[1] = {known(sum)};
-      hand_on(a.sums + (int64_t)k * a.cols + p.block * 64 + lane, w);
+      hand_on(a.sums + (int64_t)k * a.cols + p.block * 64 + lane, known(sum));
     }
   }
   if (!a.sums || p.n + 1 < a.tiles) return;
@@ -686,11 +604,8 @@ void recur_bwd_kernel(RecurArgs a) {
   double s = a.tiles == 1 && wave == 0 ? sum : 0.0;
   const int32_t per = (a.tiles + W - 1) / W;
   if (a.tiles > 1)
-    for (int32_t q = wave * per; q < min((wave + 1) * per, a.tiles); ++q) {
-      uint64_t w[1];
-      take<true>(a.sums + (int64_t)q * a.cols + p.block * 64 + lane, w);
-      s += __uint_as_float((uint32_t)w[0]);
-    }
+    for (int32_t q = wave * per; q < min((wave + 1) * per, a.tiles); ++q)
+      s += __uint_as_float((uint32_t)take<true>(a.sums + (int64_t)q * a.cols + p.block * 64 + lane));
   total[wave][lane] = s;
   __syncthreads();
   if (wave > 0 || !c.has) return;
@@ -818,28 +733,14 @@ __global__ __launch_bounds__(256) void recur_step_kernel(RecurArgs a, int32_t ro
 
 // ------------------------------------------------------------------ launch --
 
-bool pairs(const uint16_t* p, int64_t stride) {
-  return reinterpret_cast<uintptr_t>(p) % 4 == 0 && stride % 2 == 0;
-}
-
-// Forward, whether a lane has two channels: they have to be one aligned word in every
-// row.  Rows of 256 bytes are faster to read (16384 tokens, C = 4096, a gate: 159
-// against 182 us), but a tile takes longer, which tells where there are few of them
-// (1543 tokens, C = 520: 13.2 against 10.8) or of few channels many in a row (65536
-// tokens, C = 100: 65 against 49).
-bool pairs(const RecurArgs& a) {
-  return a.C > 128 && a.tiles * ((a.C + 127) / 128) >= 256 && a.C % 2 == 0 && pairs(a.x, a.xs) && pairs(a.r, a.rs) &&
-         pairs(a.i, a.is) && pairs(a.z, a.z ? a.zs : 0) && pairs(a.y, 0);
-}
-
-template <int V, int N, int W>
+template <int N, int W>
 void launch_fwd(RecurArgs a, hipStream_t s) {
-  a.blocks = (a.C + 64 * V - 1) / (64 * V);
+  a.blocks = (a.C + 63) / 64;
   const dim3 grid((uint32_t)((int64_t)a.tiles * a.blocks)), block(64 * W);
-  if (a.z && a.state) hipLaunchKernelGGL((recur_fwd_kernel<V, N, W, true, true>), grid, block, 0, s, a);
-  else if (a.z) hipLaunchKernelGGL((recur_fwd_kernel<V, N, W, true, false>), grid, block, 0, s, a);
-  else if (a.state) hipLaunchKernelGGL((recur_fwd_kernel<V, N, W, false, true>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((recur_fwd_kernel<V, N, W, false, false>), grid, block, 0, s, a);
+  if (a.z && a.state) hipLaunchKernelGGL((recur_fwd_kernel<N, W, true, true>), grid, block, 0, s, a);
+  else if (a.z) hipLaunchKernelGGL((recur_fwd_kernel<N, W, true, false>), grid, block, 0, s, a);
+  else if (a.state) hipLaunchKernelGGL((recur_fwd_kernel<N, W, false, true>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((recur_fwd_kernel<N, W, false, false>), grid, block, 0, s, a);
 }
 
 template <int N, int W>
@@ -853,20 +754,20 @@ void launch_bwd(RecurArgs a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_recur_clear(const RecurArgs& a, hipStream_t s) {
-  const int64_t words = (int64_t)a.tiles * a.cols * (a.sums ? 2 : 1);
-  hipLaunchKernelGGL(recur_clear_kernel, dim3((uint32_t)((words + 511) / 512)), dim3(256), 0, s, a, words);
+  const int64_t n = (1 + (int64_t)a.tiles * (a.sums ? 2 : 1)) * a.cols;
+  hipLaunchKernelGGL(recur_clear_kernel, dim3((uint32_t)((n + 511) / 512)), dim3(256), 0, s, a.tickets, n);
   return hipGetLastError();
 }
 
 hipError_t launch_recur_fwd(const RecurArgs& a, hipStream_t s) {
   if (a.S == 0) hipLaunchKernelGGL(recur_empty_kernel, dim3((uint32_t)((a.C + 63) / 64)), dim3(512), 0, s, a);
-  // A tile of one takes the longer the more tokens a wave has: 20 tokens, C = 2048 5.0
-  // us in runs of 4 and 8.1 in runs of 16, 50 tokens, C = 1000 6.6 in runs of 8 and 8.3.
-  else if (a.S <= 32) launch_fwd<1, 4, 8>(a, s);
-  else if (a.S <= 64 || a.tile == 64) launch_fwd<1, 8, 8>(a, s);
-  else if (a.tiles == 1) launch_fwd<1, 8, 16>(a, s);
-  else if (pairs(a)) launch_fwd<2, 16, 8>(a, s);
-  else launch_fwd<1, 16, 8>(a, s);
+  // A tile of one takes the longer the more tokens a wave has: 20 tokens, C = 2048 4.2
+  // us in runs of 4 and 4.5 in runs of 8, 50 tokens, C = 1000 5.7 with eight waves and
+  // 5.9 with sixteen.
+  else if (a.S <= 32) launch_fwd<4, 8>(a, s);
+  else if (a.S <= 64 || a.tile == 64) launch_fwd<8, 8>(a, s);
+  else if (a.tiles == 1) launch_fwd<8, 16>(a, s);
+  else launch_fwd<16, 8>(a, s);
   return hipGetLastError();
 }
 
