@@ -514,3 +514,20 @@ def test_states_at_any_alignment(vdc, shift):
             assert torch.equal(back, torch.stack([L.take_back(codes[j].float(), scales[j], dtype) for j in range(6)]))
             assert not bool(raw[:shift].any()) and not bool(raw[shift + 6 * E:].any())
         assert not bool(flat[:shift].any()) and not bool(flat[shift + 6 * E:].any())
+
+
+def test_memory_that_is_not_there_is_its_own_error(vdc):
+    """An output that does not fit raises what torch raises, and the next call works."""
+    x = torch.randn(4096, 4096, device=DEV).bfloat16()
+    w = torch.ones(4096, device=DEV)
+    want = vdc.layer_norm_fwd(x, w)[0]
+    torch.cuda.empty_cache()
+    total = torch.cuda.mem_get_info()[1]
+    torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (1 << 20)) / total)
+    try:
+        with pytest.raises(torch.cuda.OutOfMemoryError):
+            held = [vdc.layer_norm_fwd(x, w)[0] for _ in range(64)]  # reserved memory has room for some
+            del held
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert torch.equal(vdc.layer_norm_fwd(x, w)[0], want)

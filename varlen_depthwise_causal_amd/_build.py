@@ -46,7 +46,7 @@ def _binding_commands(obj: str, out: str):
                 "-I", sysconfig.get_paths()["include"], "-I", os.path.join(torch, "include"),
                 "-I", os.path.join(rocm, "include"), "-I", INCLUDE, "-c", os.path.join(CSRC, "vdc_torch.cpp"), "-o", obj]
     link = [cxx, "-shared", "-o", out, obj, "-L", PKG, "-lvdc", "-Wl,-rpath,$ORIGIN", "-L", os.path.join(torch, "lib"),
-            "-ltorch_python", "-ltorch_cpu", "-lc10_hip", "-lc10"]
+            "-ltorch_python", "-ltorch_hip", "-ltorch_cpu", "-lc10_hip", "-lc10"]
     return compile_, link
 
 

@@ -14,9 +14,9 @@ namespace vdc {
 
 // Tokens of the tiles that a row is cut into: 128 forward and 64 backward, and 64
 // forward where that leaves a CU one tile or none (1543 tokens, C = 520, 225 tiles of
-// 64: 9.5 against 10.9 us; 8000 tokens, C = 256, 500 of them: 17.9 against 13.5), but
-// one tile as far as it goes, which needs no words (77 tokens, C = 2048: 7.5 against
-// 2.0 and 7.9).
+// 64: 8.8 against 10.6 us; 8000 tokens, C = 256, 500 of them: 14.4 against 12.5), but
+// one tile as far as it goes, which needs no words (77 tokens, C = 2048: 7.5 us against
+// 2.0 for the words and 7.9).
 constexpr int kRecurFwdTile = 128, kRecurBwdTile = 64;
 inline int64_t recur_tiles_of_64(int64_t S, int64_t C) { return (S + 63) / 64 * ((C + 63) / 64); }
 inline int recur_fwd_tile(int64_t S, int64_t C) {
@@ -53,9 +53,9 @@ struct RecurArgs {
 };
 
 // Whether a backward's tiles add their partial sums of ddecay in the same launch.  25
-// tiles, C = 520, with their forward: 34.3 against 36.6 us; 32 tiles, C = 4096, which
-// are not at work at once: 85 against 83.
-inline bool recur_few(int64_t S, int64_t C) { return S <= 32 * kRecurBwdTile && recur_tiles_of_64(S, C) <= 512; }
+// tiles, C = 520, with their forward: 22.6 against 23.9 us; 125 tiles, C = 1024, whose
+// last one has more words to read than its neighbours: 81 against 75.
+inline bool recur_few(int64_t S) { return S <= 32 * kRecurBwdTile; }
 
 // The tickets and the words as a call finds them.
 hipError_t launch_recur_clear(const RecurArgs& a, hipStream_t s);

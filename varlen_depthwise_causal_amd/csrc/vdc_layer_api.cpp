@@ -103,7 +103,7 @@ size_t recur_layout(int dir, int64_t S, int64_t C, char* base, RecurArgs* a) {
   const int64_t tiles = ceil_div(S, tile);
   const int64_t cols = ceil_div(C, 64) * 64;
   const size_t row = (size_t)tiles * cols * 8, words = tiles > 1 ? cols * 8 + row : 0;
-  const bool few = recur_few(S, C);
+  const bool few = recur_few(S);
   a->tiles = (int32_t)tiles;
   a->tile = tile;
   a->cols = (int32_t)cols;

@@ -773,9 +773,9 @@ hipError_t launch_recur_fwd(const RecurArgs& a, hipStream_t s) {
 
 hipError_t launch_recur_bwd(const RecurArgs& a, hipStream_t s) {
   // Runs of 16 tokens make the fewest instructions a token, shorter ones more waves:
-  // 8000 tokens, C = 256, 500 tiles: 19.5 against 21.5 us, 1543 tokens, C = 520: 12.6
-  // against 13.3, 20 tokens, C = 2048: 5.5 against 7.6; 16384 tokens, C = 4096: 302
-  // against 267.
+  // 8000 tokens, C = 256, 500 tiles: 16.3 us in runs of 8 and 18.7 in runs of 16, 20
+  // tokens, C = 2048: 5.9 in runs of 4 and 6.4 in runs of 8; 16384 tokens, C = 512: 49.9
+  // in runs of 8 and 45.0 in runs of 16, C = 4096: 379 and 286.
   if (a.S <= 32) launch_bwd<4, 8>(a, s);
   else if (recur_tiles_of_64(a.S, a.C) <= 512) launch_bwd<8, 8>(a, s);
   else launch_bwd<16, 4>(a, s);

@@ -7,7 +7,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -111,14 +111,19 @@ int64_t documents(const Tensor& cu, Device dev) {
   return cu.numel() - 1;
 }
 
+// A new tensor, past the dispatcher, which takes 0.25 us of a call's 4 to 10.
+Tensor fresh(c10::IntArrayRef sizes, ScalarType type, Device dev) {
+  return Tensor(at::detail::empty_cuda(sizes, type, dev, std::nullopt));
+}
+Tensor fresh_as(const Tensor& t) { return fresh(t.sizes(), t.scalar_type(), t.device()); }
+
 // The caller's output, or a new one.
 Tensor output(PyObject* o, const char* what, int64_t S, int64_t C, Device dev) {
-  if (o == Py_None) return at::empty({S, C}, at::TensorOptions().dtype(ScalarType::BFloat16).device(dev));
+  if (o == Py_None) return fresh({S, C}, ScalarType::BFloat16, dev);
   const Tensor& t = tensor(o, what);
   dense(t, what, ScalarType::BFloat16, {S, C}, dev);
   return t;
 }
-Tensor empty_as(const Tensor& t) { return at::empty(t.sizes(), t.options()); }
 
 struct Workspace {
   Tensor t;
@@ -130,7 +135,7 @@ struct Workspace {
       if (t.device() != dev || !t.is_contiguous())
         value_error("workspace must be a contiguous device tensor on " + dev.str());
     } else if (need) {
-      t = at::empty({(int64_t)need}, at::TensorOptions().dtype(ScalarType::Byte).device(dev));
+      t = fresh({(int64_t)need}, ScalarType::Byte, dev);
     } else {
       return;
     }
@@ -166,6 +171,13 @@ void check(int rc, const char* what) {
   if (rc) throw Status{rc, what};
 }
 
+PyObject* attribute(const char* module, const char* name) {
+  PyObject* m = PyImport_ImportModule(module);
+  PyObject* a = m ? PyObject_GetAttrString(m, name) : nullptr;
+  Py_XDECREF(m);
+  return a;
+}
+
 template <class F>
 PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F f) {
   if (n != want) {
@@ -177,14 +189,18 @@ PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F f) {
   } catch (const Refused& r) {
     PyErr_SetString(r.type, r.text.c_str());
   } catch (const Status& s) {
-    PyObject* lib = PyImport_ImportModule("varlen_depthwise_causal_amd._lib");
-    PyObject* cls = lib ? PyObject_GetAttrString(lib, "VdcError") : nullptr;
-    PyObject* err = cls ? PyObject_CallFunction(cls, "is", s.rc, s.what) : nullptr;
-    if (err) PyErr_SetObject(cls, err);
-    Py_XDECREF(err);
-    Py_XDECREF(cls);
-    Py_XDECREF(lib);
-  } catch (const std::exception& e) {  // an allocation that failed
+    if (PyObject* cls = attribute("varlen_depthwise_causal_amd._lib", "VdcError")) {
+      PyObject* err = PyObject_CallFunction(cls, "is", s.rc, s.what);
+      if (err) PyErr_SetObject(cls, err);
+      Py_XDECREF(err);
+      Py_DECREF(cls);
+    }
+  } catch (const c10::OutOfMemoryError& e) {
+    if (PyObject* cls = attribute("torch", "OutOfMemoryError")) {
+      PyErr_SetString(cls, e.what_without_backtrace());
+      Py_DECREF(cls);
+    }
+  } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
   } catch (...) {
     if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, "unknown error");
@@ -260,7 +276,7 @@ PyObject* recurrence_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (state) value_error("keep is for the training forward, without a state");
       const int64_t kept = gated_recurrence_keep_rows(x.S);
       if (a[10] == Py_True) {
-        keep = at::empty({kept, x.C}, at::TensorOptions().dtype(ScalarType::Float).device(x.dev));
+        keep = fresh({kept, x.C}, ScalarType::Float, x.dev);
       } else {
         keep = tensor(a[10], "keep");
         dense(keep, "keep", ScalarType::Float, {kept, x.C}, x.dev);
@@ -286,9 +302,9 @@ PyObject* recurrence_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     v.cu_seqlens = static_cast<const int32_t*>(ptr(cu));
     const int64_t dys = rows(dy, "dy", x.S, x.C, x.dev);
     dense(keep, "keep", ScalarType::Float, {gated_recurrence_keep_rows(x.S), x.C}, x.dev);
-    const Tensor dx = output(Py_None, "dx", x.S, x.C, x.dev), dr = empty_as(dx), di = empty_as(dx),
-                 ddecay = empty_as(tensor(a[3], "decay"));
-    const Tensor dz = v.z || a[4] != Py_None ? empty_as(dx) : Tensor();
+    const Tensor dx = output(Py_None, "dx", x.S, x.C, x.dev), dr = fresh_as(dx), di = fresh_as(dx),
+                 ddecay = fresh_as(tensor(a[3], "decay"));
+    const Tensor dz = v.z || a[4] != Py_None ? fresh_as(dx) : Tensor();
     const Tensor* gate = dz.defined() ? &dz : nullptr;
     const Workspace ws(a[9], gated_recurrence_workspace_bytes(VDC_BWD, x.S, x.C), x.dev);
     const c10::DeviceGuard guard(x.dev);
@@ -344,7 +360,7 @@ PyObject* norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t dys = rows(dy, "dy", s.S, s.C, s.dev), dss = ds ? rows(*ds, "dstream", s.S, s.C, s.dev) : s.C;
     const int wd = param(w, "weight", s.C, s.dev), bd = b ? param(*b, "bias", s.C, s.dev) : 0;
     const float eps = number(a[5]);
-    const Tensor dx = output(Py_None, "dx", s.S, s.C, s.dev), dw = empty_as(w), db = b ? empty_as(*b) : Tensor();
+    const Tensor dx = output(Py_None, "dx", s.S, s.C, s.dev), dw = fresh_as(w), db = b ? fresh_as(*b) : Tensor();
     const Tensor* dbias = b ? &db : nullptr;
     const Workspace ws(a[6], layer_norm_workspace_bytes(s.S, s.C), s.dev);
     const c10::DeviceGuard guard(s.dev);
