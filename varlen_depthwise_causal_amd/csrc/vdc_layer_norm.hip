@@ -70,11 +70,12 @@ __device__ __forceinline__ void request(const LayerNormArgs& a, const Team<L, K,
     r[k] = p.has(a, k) ? load8<kWhole>(t + row * stride + p.at(k), p.count(a, k)) : (u32x4_t){0u, 0u, 0u, 0u};
 }
 
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+
 // A lane's channels of a parameter, by vectors but for a part of one; zeros without
 // the parameter and past the last channel.
 template <int K, class P>
 __device__ __forceinline__ void params(const LayerNormArgs& a, const P& p, const void* t, int bf16, Vec8 (&o)[K]) {
-  typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 #pragma unroll
   for (int k = 0; k < K; ++k) {
 #pragma unroll
@@ -184,6 +185,20 @@ __global__ __launch_bounds__(L > 64 ? L : 256) void layer_norm_fwd_kernel(LayerN
   }
 }
 
+// A lane's part of a partial row, `count` values of 8 or more: by words its lanes' would
+// be 32 bytes apart.
+__device__ __forceinline__ void part_put(float* p, const Vec8& v, int32_t count) {
+  if (count >= 8) {
+#pragma unroll
+    for (int h = 0; h < 8; h += 4)
+      *reinterpret_cast<f32x4_any*>(p + h) = (f32x4_any){v.v[h], v.v[h + 1], v.v[h + 2], v.v[h + 3]};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < count) p[i] = v.v[i];
+  }
+}
+
 template <int L, int K, bool kWhole, bool kRes>
 __global__ __launch_bounds__(L > 64 ? L : 256) void layer_norm_bwd_kernel(LayerNormArgs a, int32_t rows) {
   typedef Team<L, K, kWhole> P;
@@ -270,13 +285,11 @@ __global__ __launch_bounds__(L > 64 ? L : 256) void layer_norm_bwd_kernel(LayerN
   float* part = a.part + (int64_t)blockIdx.x * 2 * a.C;
   if (P::kWide) {
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (p.has(a, k) && p.has(a, k, i)) {
-          part[p.at(k) + i] = dw[k].v[i];
-          part[a.C + p.at(k) + i] = db[k].v[i];
-        }
+    for (int k = 0; k < K; ++k) {
+      if (!p.has(a, k)) continue;
+      part_put(part + p.at(k), dw[k], p.count(a, k));
+      part_put(part + a.C + p.at(k), db[k], p.count(a, k));
+    }
     return;
   }
 #pragma unroll
@@ -340,6 +353,11 @@ bool whole(const LayerNormArgs& a) {
 struct Shape {
   int lanes, vecs;
 };
+// The fewest lanes that hold a row in one or two vectors each, whole waves alone past 64:
+// exchanges between waves cost more than idle lanes.  16384 tokens, C = 1000, forward and
+// backward 21.4 and 24.1 us by a wave, 23.5 and 53.4 by four; C = 4096 101 and 114 by four
+// waves, 94 and 169 by eight; 8192 tokens, C = 8192 96 and 129 by eight, 130 and 177 by
+// sixteen.
 Shape shape_of(int64_t C) {
   const int64_t n = (C + 7) / 8;
   if (n <= 8) return {8, 1};
@@ -351,12 +369,23 @@ Shape shape_of(int64_t C) {
   return {n <= 1024 ? 512 : 1024, 2};
 }
 
+// The forward's workgroups: sixteen waves a SIMD of single waves' tokens, and of wider
+// ones as many as are at work at once, but half of those where they have four tokens or
+// more each, whose requests are under way before they are needed: 16384 tokens, C = 4096
+// and a residual 92 against 101 us, 8192 tokens, C = 8192 92 against 96; 700 tokens, C =
+// 4096 6.6 against 5.4.
+template <int L>
+int64_t forward_rows(int64_t turns) {
+  constexpr int64_t full = L <= 64 ? 4096 : L == 256 ? 1024 : L == 512 ? 512 : 256;
+  if (L > 64 && L < 1024 && turns >= 4 * full) return full / 2;
+  return turns < full ? turns : full;
+}
+
 template <int L, int K, bool kWhole>
 void launch_vec(const LayerNormArgs& a, bool back, hipStream_t s) {
   typedef Team<L, K, kWhole> P;
   const int64_t turns = (a.S + P::kTokens - 1) / P::kTokens;
-  const int64_t most = L <= 64 ? 4096 : L == 256 ? 1024 : L == 512 ? 512 : 256;
-  const int64_t rows = back ? a.prows : turns < most ? turns : most;
+  const int64_t rows = back ? a.prows : forward_rows<L>(turns);
   const dim3 grid((uint32_t)rows), block(P::kThreads);
   if (back) {
     if (a.dstream) hipLaunchKernelGGL((layer_norm_bwd_kernel<L, K, kWhole, true>), grid, block, 0, s, a, (int32_t)rows);
@@ -389,11 +418,18 @@ hipError_t launch(const LayerNormArgs& a, bool back, hipStream_t s) {
 
 }  // namespace
 
+// A row costs its writing and reading, too few leave the machine idle.  Forward and
+// backward of 16384 tokens, C = 520 and a residual: 39 us with 512 rows, 47 with 256, 43
+// with 1024; backward, C = 2048: 32768 tokens 105 with 1024 and 129 with 512, 1500
+// tokens 11.4 and 9.9; C = 4096, 16384 tokens: 107 with 512, 120 with 1024, 142 with 256;
+// C = 8192, 8192 tokens: 113 with 256, 128 with 512.  No more of them than take the same
+// number of turns.
 int layer_norm_bwd_rows(int64_t S, int64_t C) {
   const Shape h = shape_of(C);
   const int64_t tokens = h.lanes > 64 ? 1 : 256 / h.lanes, turns = (S + tokens - 1) / tokens;
-  const int64_t most = h.lanes == 1024 ? 256 : 512;
-  return (int)(turns < most ? turns : most);
+  const int64_t most = h.lanes >= 512 ? 256 : h.lanes == 256 && h.vecs == 1 && turns >= 4096 ? 1024 : 512;
+  const int64_t each = (turns + most - 1) / most;
+  return each ? (int)((turns + each - 1) / each) : 0;
 }
 
 hipError_t launch_layer_norm_fwd(const LayerNormArgs& a, hipStream_t s) { return launch(a, false, s); }
