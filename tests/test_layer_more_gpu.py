@@ -531,3 +531,17 @@ def test_memory_that_is_not_there_is_its_own_error(vdc):
     finally:
         torch.cuda.set_per_process_memory_fraction(1.0)
     assert torch.equal(vdc.layer_norm_fwd(x, w)[0], want)
+
+
+def test_more_rows_than_one_launch_has_waves_for(vdc):
+    """2^24 rows and some of one channel, in turns of 2^24: each row is its own sequence."""
+    rows = (1 << 24) + 77
+    x = torch.randn(rows, 1, device=DEV).bfloat16()
+    r, i = torch.randn(rows, 1, device=DEV).bfloat16(), torch.randn(rows, 1, device=DEV).bfloat16()
+    decay = torch.full((1,), 0.5, device=DEV)
+    state = torch.randn(rows, 1, device=DEV)
+    at = torch.cat([torch.arange(200, device=DEV), torch.arange(rows - 200, rows, device=DEV)])
+    some = state[at].clone()
+    want = vdc.gated_recurrence_update(x[at], r[at], i[at], decay, some)
+    got = vdc.gated_recurrence_update(x, r, i, decay, state)
+    assert torch.equal(got[at], want) and torch.equal(state[at], some)

