@@ -481,6 +481,11 @@ size_t gated_recurrence_workspace_bytes(int direction, int64_t S, int64_t C);
 /*
  * gated_recurrence_fwd - prompts, and the training forward.
  *
+ * The workspace is the call's own until its work has ended, as the backward's is: the
+ * tiles of a row hand their states on through it.  Two calls in flight that share one
+ * have unspecified results; a tile that waits there in vain gives up after a bounded
+ * time, and what depends on it is NaN.
+ *
  * y bf16 [S][C].  keep FP32 [gated_recurrence_keep_rows(S)][C] or NULL:
  * receives the states that gated_recurrence_bwd starts from; it takes no
  * state beside it (VDC_EINVAL).  With a state, every document leaves the state

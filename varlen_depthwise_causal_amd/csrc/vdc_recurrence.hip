@@ -32,7 +32,8 @@
 //
 // No wait is for ever: a block of channels' tiles are numbered as their workgroups
 // begin, each waits for lower numbers alone, and those have begun.  A word is written and
-// read whole and holds all that its reader needs, so no fence is needed either.
+// read whole and holds all that its reader needs, so no fence is needed either.  The words
+// and their folds are vdc_words.h's.
 //
 // Everything between documents is assigned, never multiplied by zero, so that
 // an infinity or a NaN stays in its document.
@@ -44,6 +45,7 @@
 
 #include "vdc_layer.h"
 #include "vdc_ssm_math.h"
+#include "vdc_words.h"
 
 namespace vdc {
 namespace {
@@ -179,36 +181,26 @@ __device__ __forceinline__ uint32_t bits_at(const uint32_t* mask, int at) {
   return __builtin_amdgcn_readfirstlane(lo | hi << N);
 }
 
-// Words.  The upper half is P, or one of two marks, which no P is: a product of
-// decays is at least 0, and a NaN is written as the usual one.
-constexpr uint32_t kEmpty = 0xffffffffu, kKnown = 0xfffffffeu;
-// Reads of a word before its reader gives up: about a second.  Only two calls that
-// share a workspace come here.
-constexpr int kPolls = 1 << 18;
+// Reads of a word before its reader gives up and has a NaN in its place: 0.6 s, at 0.14
+// us each.
+constexpr int kPolls = 1 << 22;
 // How often a tile looks at the next W words for a known one, before it waits for
 // one.
 constexpr int kLooks = 2;
 
-__device__ __forceinline__ uint64_t word_of(float P, float H) {
-  const uint32_t p = P != P ? 0x7fc00000u : __float_as_uint(P);
-  return (uint64_t)p << 32 | __float_as_uint(H);
-}
-__device__ __forceinline__ uint64_t known(float H) { return (uint64_t)kKnown << 32 | __float_as_uint(H); }
-__device__ __forceinline__ uint32_t mark(uint64_t w) { return (uint32_t)(w >> 32); }
-
 __device__ __forceinline__ void hand_on(uint64_t* p, uint64_t w) {
   __hip_atomic_store(p, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-// A wave's words once all of them are there, or once all are known.
+// A wave's words once all of them are there, or once all are known (kAll).
 template <bool kAll>
 __device__ __forceinline__ uint64_t take(uint64_t* p) {
   uint64_t w = 0;
   for (int n = 0; n < kPolls; ++n) {
     w = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (__ballot(kAll ? mark(w) != kKnown : mark(w) == kEmpty) == 0) break;
+    if (__ballot(!there<kAll>(w)) == 0) break;
     __builtin_amdgcn_s_sleep(1);
   }
-  return w;
+  return taken<kAll>(w);
 }
 
 // The words of the tiles before this one, W at a time, and which lanes have found a
@@ -249,11 +241,7 @@ __device__ __forceinline__ float look_back(uint64_t* words, int64_t step, int32_
   }
   float carry = 0.0f;
 #pragma unroll 4
-  for (int d = looks * W - 1; d >= 0; --d) {
-    const uint64_t w = seen.w[d][lane];
-    const float H = __uint_as_float((uint32_t)w), P = __uint_as_float(mark(w));
-    carry = mark(w) == kKnown ? H : __builtin_fmaf(P, carry, H);
-  }
+  for (int d = looks * W - 1; d >= 0; --d) carry = folded(seen.w[d][lane], carry);
   return carry;
 }
 
@@ -611,7 +599,7 @@ void recur_bwd_kernel(RecurArgs a) {
   const int32_t per = (a.tiles + W - 1) / W;
   if (a.tiles > 1)
     for (int32_t q = wave * per; q < min((wave + 1) * per, a.tiles); ++q)
-      s += __uint_as_float((uint32_t)take<true>(a.sums + (int64_t)q * a.cols + p.block * 64 + lane));
+      s += word_value(take<true>(a.sums + (int64_t)q * a.cols + p.block * 64 + lane));
   total[wave][lane] = s;
   __syncthreads();
   if (wave > 0 || !c.has) return;
