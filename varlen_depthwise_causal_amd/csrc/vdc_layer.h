@@ -37,6 +37,7 @@ struct RecurArgs {
   int32_t tiles, tile;          // of tokens, and how many each has
   int32_t blocks;               // workgroups that share a tile of tokens
   int32_t cols;                 // words of a tile: C rounded up to 64
+  int32_t docs_each;            // documents that a tile looks through for empty ones
   float* state;                 // [slots][C]
   const int32_t* index;
   const uint8_t* resume;

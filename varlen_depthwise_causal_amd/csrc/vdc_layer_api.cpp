@@ -153,6 +153,7 @@ extern "C" int gated_recurrence_fwd(const vdc_recurrence* v, void* y, float* kee
   }
   a.y = static_cast<uint16_t*>(y);
   a.keep = keep;
+  a.docs_each = (int32_t)ceil_div(v->num_docs, std::max(a.tiles, 1));
   if (a.tiles > 1 && (rc = done(launch_recur_clear(a, stream)))) return rc;
   return done(launch_recur_fwd(a, stream));
 }

@@ -144,11 +144,26 @@ __device__ __forceinline__ void clear_starts(Starts<T, kState>& s) {
 }
 
 // All threads of the workgroup, an entry of cu_seqlens each and all its loads at
-// once; the result is complete after the next barrier.
+// once; the result is complete after the next barrier.  Where the tile's tokens have
+// more than sixteen entries a thread, nearly all of them are empty documents'; a search
+// for each token passes them, so that a tile has its word after some 50 us at most, while
+// others wait for it.
 template <int W, int T, bool kState>
 __device__ __forceinline__ void find_starts(const RecurArgs& a, int32_t t0, Starts<T, kState>& s) {
   const int32_t entries = a.num_docs + 1;
   int32_t e = entries > 64 * W ? first_at_least(a.cu, entries, t0) : 0;
+  constexpr int32_t kMany = 16 * 64 * W;
+  if (entries > kMany && e < entries - kMany && a.cu[e + kMany] <= t0 + T) {
+    const int32_t* const cu = a.cu;
+    for (int j = threadIdx.x; j <= T && t0 + j <= a.S; j += 64 * W) {
+      const TokenDocs d = token_docs([cu](int64_t i) { return cu[i]; }, entries, t0 + j);
+      if (!d.any) continue;
+      atomicOr(&s.mask[j / 32], 1u << (j % 32));
+      if (kState && d.starts >= 0 && a.resume && a.resume[d.starts]) s.from[j] = (int32_t)slot_of(a.index, d.starts, a.slots);
+      if (kState && d.ends >= 0) s.to[j] = (int32_t)slot_of(a.index, d.ends, a.slots);
+    }
+    return;
+  }
   e += threadIdx.x;
   while (true) {
     int32_t v = INT_MAX, next = INT_MAX, past = INT_MAX, from = -1, to = -1;
@@ -182,7 +197,8 @@ __device__ __forceinline__ uint32_t bits_at(const uint32_t* mask, int at) {
 }
 
 // Reads of a word before its reader gives up and has a NaN in its place: 0.6 s, at 0.14
-// us each.
+// us each, while a tile's word is there within a fraction of a millisecond of the tile's
+// beginning and those of all tiles before it.  Only calls that share a workspace come here.
 constexpr int kPolls = 1 << 22;
 // How often a tile looks at the next W words for a known one, before it waits for
 // one.
@@ -264,22 +280,34 @@ __device__ __forceinline__ Place place_of(const RecurArgs& a, uint32_t* lds) {
   return {(int32_t)n, (int32_t)block};
 }
 
-// Documents without tokens leave zeros, or their slot as it is where they resume;
-// part `k` of `parts`.
+// Documents without tokens leave zeros, or their slot as it is where they resume: those of
+// [first, end).
 template <int W>
-__device__ __forceinline__ void empty_documents(const RecurArgs& a, int32_t k, int32_t parts, const Col& c) {
+__device__ __forceinline__ void empty_documents(const RecurArgs& a, int32_t first, int32_t end, const Col& c) {
   const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64u), lane = threadIdx.x & 63;
-  const int64_t per = ((int64_t)a.num_docs + parts - 1) / parts, end = min((k + 1) * per, (int64_t)a.num_docs);
-  for (int64_t d0 = k * per + wave * 64; d0 < end; d0 += 64 * W) {
-    const int64_t d = d0 + lane;
-    bool empty = false;
-    if (d < end) empty = a.cu[d] == a.cu[d + 1] && !(a.resume && a.resume[d]);
-    for (uint64_t m = __ballot(empty); m; m &= m - 1) {
-      const int64_t slot = slot_of(a.index, d0 + __builtin_ctzll(m), a.slots);
-      if (slot >= 0 && c.has) a.state[slot * a.C + c.c] = 0.0f;
+  for (int32_t d0 = first + wave * 64; d0 < end; d0 += 64 * W) {
+    const int32_t d = d0 + lane;
+    int32_t slot = -1;
+    if (d < end && a.cu[d] == a.cu[d + 1] && !(a.resume && a.resume[d])) slot = (int32_t)slot_of(a.index, d, a.slots);
+    for (uint64_t m = __ballot(slot >= 0); m; m &= m - 1) {
+      const int64_t s = __builtin_amdgcn_readlane(slot, __builtin_ctzll(m));
+      if (c.has) a.state[s * a.C + c.c] = 0.0f;
     }
   }
 }
+
+// A tile's part of the documents that it looks through for empty ones: the first of them,
+// a thread's each, beside its loads, the others at its end.  Many of them take longer than
+// the tiles behind this one wait for its word.
+template <int W>
+struct Part {
+  int32_t first, then, end;
+  __device__ __forceinline__ Part(const RecurArgs& a, int32_t k) {
+    first = (int32_t)min((int64_t)k * a.docs_each, (int64_t)a.num_docs);
+    end = first + min(a.docs_each, a.num_docs - first);
+    then = first + min(64 * W, end - first);
+  }
+};
 
 // 16 bytes a lane: 2 us for few words, 8.2 for 65536 tokens, C = 4096 (17 MB).
 __global__ __launch_bounds__(256) void recur_clear_kernel(uint64_t* words, int64_t n) {
@@ -289,7 +317,7 @@ __global__ __launch_bounds__(256) void recur_clear_kernel(uint64_t* words, int64
 
 // No tokens, but documents that leave their states.
 __global__ __launch_bounds__(512) void recur_empty_kernel(RecurArgs a) {
-  empty_documents<8>(a, 0, 1, Col(a, blockIdx.x));
+  empty_documents<8>(a, 0, a.num_docs, Col(a, blockIdx.x));
 }
 
 // The runs of a tile that have any of the bits kFrom .. kTo of theirs set, as a mask.
@@ -327,7 +355,7 @@ void recur_fwd_kernel(RecurArgs a) {
   const Col c(a, p.block);
   if (a.tiles == 1 && t0 >= a.S) {  // no tokens, but a part in finding documents
     find_starts<W>(a, tile0, docs);
-    if (kState) empty_documents<W>(a, p.n, a.tiles, c);
+    if (kState) empty_documents<W>(a, 0, a.num_docs, c);
     __syncthreads();
     __syncthreads();
     return;
@@ -338,7 +366,8 @@ void recur_fwd_kernel(RecurArgs a) {
   rows(c, a.x, a.xs, t0, a.S, x);
   const float rate = decay_rate(a, c.c);
   find_starts<W>(a, tile0, docs);
-  if (kState) empty_documents<W>(a, p.n, a.tiles, c);
+  const Part<W> part(a, kState ? p.n : 0);
+  if (kState) empty_documents<W>(a, part.first, part.then, c);
   if (kGate) rows(c, a.z, a.zs, t0, a.S, z);  // needed last; before the documents it takes 88 registers
   __syncthreads();
   const uint32_t bits = bits_at<N>(docs.mask, wave * N), own = bits & ((1u << N) - 1u);
@@ -420,6 +449,7 @@ void recur_fwd_kernel(RecurArgs a) {
         if (slot >= 0 && c.has) a.state[slot * a.C + c.c] = B[j];
       }
   }
+  if (kState) empty_documents<W>(a, part.then, part.end, c);
 }
 
 // The decay's gradient from the sum of E.  sigmoid / softplus tends to 1 where both

@@ -36,4 +36,33 @@ VDC_HD inline void search_narrow(int64_t& lo, int64_t& hi, int64_t step, int c) 
   lo = nlo;
 }
 
+// The first index i in [0, n) with at(i) >= v (n if none), by one thread: 31 probes at
+// most.  Contents in no order give some index in [0, n].
+template <class At>
+VDC_HD inline int64_t search_alone(const At& at, int64_t n, int64_t v) {
+  int64_t lo = 0, hi = n;
+  while (lo < hi) {
+    const int64_t mid = lo + (hi - lo) / 2;
+    if ((int64_t)at(mid) < v) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// The documents around token v of n entries of cu_seqlens, by one thread.
+struct TokenDocs {
+  int64_t ends;    // the document that ends before the token, or -1
+  int64_t starts;  // the one that starts at it, or -1 (behind the last one, too)
+  bool any;        // whether there is an entry at the token
+};
+template <class At>
+VDC_HD inline TokenDocs token_docs(const At& at, int64_t n, int64_t v) {
+  // Of the entries at one token the first follows the document that ends and the last
+  // is that of the one that starts there; others are empty ones'.
+  const int64_t first = search_alone(at, n, v);
+  if (first == n || (int64_t)at(first) != v) return {-1, -1, false};
+  const int64_t last = search_alone(at, n, v + 1) - 1;
+  return {first - 1, last >= first && last < n - 1 ? last : -1, true};
+}
+
 }  // namespace vdc
