@@ -35,12 +35,11 @@ def hipcc() -> str:
     return path
 
 
-def _binding_commands(obj: str, out: str):
-    """Compiles csrc/vdc_torch.cpp against the installed torch and links it with
-    libvdc.so, which it finds beside itself, and torch's libraries, which are
-    loaded when it is."""
+def _binding_commands(torch: str, obj: str, out: str):
+    """Compiles csrc/vdc_torch.cpp against the torch installed in that folder and
+    links it with libvdc.so, which it finds beside itself, and torch's libraries,
+    which are loaded when it is."""
     cxx = shutil.which("g++") or hipcc()
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
     rocm = os.path.dirname(os.path.dirname(os.path.realpath(hipcc())))
     compile_ = [cxx, "-O2", "-std=c++17", "-fPIC", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
                 "-I", sysconfig.get_paths()["include"], "-I", os.path.join(torch, "include"),
@@ -52,36 +51,43 @@ def _binding_commands(obj: str, out: str):
 
 def build(verbose: bool = False) -> str:
     """Compile csrc/*.hip + csrc/*.cpp into libvdc.so, and the recurrent layer's
-    binding into _vdc_torch.so (always rebuilds)."""
+    binding into _vdc_torch.so (always rebuilds).  libvdc.so needs hipcc alone and
+    is in place before the binding can fail; without torch there is no binding,
+    and the calls of module layer raise ImportError."""
+    def start(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        return cmd, subprocess.Popen(cmd)
+
+    def finish(cmd, process):
+        if process.wait():
+            raise subprocess.CalledProcessError(process.returncode, cmd)
+
+    def link(cmd, tmp, out):
+        finish(*start(cmd))
+        os.replace(tmp, out)
+
     os.makedirs(BUILD_DIR, exist_ok=True)
-    binding_obj, binding_tmp = os.path.join(BUILD_DIR, "vdc_torch.o"), BINDING + ".tmp%d" % os.getpid()
-    binding, binding_link = _binding_commands(binding_obj, binding_tmp)
     cc = hipcc()
     objs, running = [], []
     for src in SOURCES:
         obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
         extra = DEVICE_FLAGS if src.endswith(".hip") else []
-        cmd = [cc, *COMMON, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        running.append((cmd, subprocess.Popen(cmd)))
+        running.append(start([cc, *COMMON, *extra, "-c", os.path.join(CSRC, src), "-o", obj]))
         objs.append(obj)
-    if verbose:
-        print(" ".join(binding), flush=True)
-    running.append((binding, subprocess.Popen(binding)))
-    for cmd, p in running:
-        if p.wait():
-            raise subprocess.CalledProcessError(p.returncode, cmd)
-    tmp = LIBRARY + ".tmp%d" % os.getpid()
-    cmd = [cc, "-shared", "-fPIC", "--offload-arch=" + ARCH, "-o", tmp, *objs]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, LIBRARY)
-    if verbose:
-        print(" ".join(binding_link), flush=True)
-    subprocess.run(binding_link, check=True)
-    os.replace(binding_tmp, BINDING)
+    torch, tmp = importlib.util.find_spec("torch"), ".tmp%d" % os.getpid()
+    if torch:
+        binding_compile, binding_link = _binding_commands(os.path.dirname(torch.origin),
+                                                          os.path.join(BUILD_DIR, "vdc_torch.o"), BINDING + tmp)
+        binding = start(binding_compile)
+    for job in running:
+        finish(*job)
+    link([cc, "-shared", "-fPIC", "--offload-arch=" + ARCH, "-o", LIBRARY + tmp, *objs], LIBRARY + tmp, LIBRARY)
+    if torch:
+        finish(*binding)
+        link(binding_link, BINDING + tmp, BINDING)
+    else:
+        print("torch not found: libvdc.so alone, without the binding of module layer", flush=True)
     return LIBRARY
 
 
