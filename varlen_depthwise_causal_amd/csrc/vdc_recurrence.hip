@@ -51,9 +51,10 @@ namespace vdc {
 namespace {
 
 // u / sigmoid(r) of a channel, at most 2^126: no product of it is an infinity, which
-// a decay of 0 would make a NaN.
+// a decay of 0 would make a NaN.  The scale is not doubled first: where that is an
+// infinity, a softplus of 0 would make a NaN too.
 __device__ __forceinline__ float decay_rate(const RecurArgs& a, int64_t c) {
-  const float rate = 2.0f * a.scale * softplus_f32(param_at(a.decay, a.decay_bf16, c));
+  const float rate = 2.0f * (a.scale * softplus_f32(param_at(a.decay, a.decay_bf16, c)));
   return rate > 0x1p126f ? 0x1p126f : rate;  // a NaN stays
 }
 
