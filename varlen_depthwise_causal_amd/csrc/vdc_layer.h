@@ -87,7 +87,7 @@ struct LayerNormArgs {
 hipError_t launch_layer_norm_fwd(const LayerNormArgs& a, hipStream_t s);
 hipError_t launch_layer_norm_bwd(const LayerNormArgs& a, hipStream_t s);
 hipError_t launch_layer_norm_bwd_sum(const LayerNormArgs& a, hipStream_t s);
-// Partial rows of dweight and dbias, one for each workgroup of the backward.
+// Partial rows of dweight and dbias, one or more for each workgroup of the backward.
 int layer_norm_bwd_rows(int64_t S, int64_t C);
 
 // ------------------------------------------------------ states put aside --

@@ -23,6 +23,8 @@
 // forward 80 us, 6.7 TB/s, the last cache's part in it.  Few tokens are latency: 33 tokens,
 // C = 520 3.9 us; 1543 tokens of 1001 channels 5.0 forward, 8.3 and 4.7 backward.
 
+#include <algorithm>
+
 #include "vdc_layer.h"
 #include "vdc_ssm_math.h"
 
@@ -205,7 +207,8 @@ __device__ __forceinline__ void part_put(float* p, const Vec8& v, int32_t count)
 }
 
 template <int L, int K, bool kWhole, bool kRes>
-__global__ __launch_bounds__(L > 64 ? L : 256) void layer_norm_bwd_kernel(LayerNormArgs a, int32_t rows) {
+__global__ __launch_bounds__(L > 64 ? L : 256) void layer_norm_bwd_kernel(LayerNormArgs a, int32_t rows,
+                                                                          int32_t turns, int32_t parts) {
   typedef Team<L, K, kWhole> P;
   __shared__ float lds[2][P::kWaves][4];
   __shared__ float sums[P::kWide ? 1 : P::kTokens][P::kWide ? 1 : 2 * K * 8][P::kWide ? 1 : L + 1];
@@ -213,10 +216,6 @@ __global__ __launch_bounds__(L > 64 ? L : 256) void layer_norm_bwd_kernel(LayerN
   const float inv = 1.0f / (float)a.C;
   Vec8 w[K], dw[K], db[K];
   params<K>(a, p, a.w, a.w_bf16, w);
-#pragma unroll
-  for (int k = 0; k < K; ++k)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) dw[k].v[i] = db[k].v[i] = 0.0f;
   u32x4_t x[K], dy[K], ds[K];
   auto fetch = [&](int64_t t) {
     request(a, p, a.x, a.xs, t, x);
@@ -227,90 +226,100 @@ __global__ __launch_bounds__(L > 64 ? L : 256) void layer_norm_bwd_kernel(LayerN
   constexpr bool kAhead = L < 1024;
   if (kAhead) fetch(p.token);
   int turn = 0;
+  int64_t t = p.token, end = 0;
 #pragma unroll 1
-  for (int64_t t = p.token; t < a.S; t += p.step, turn ^= 1) {
-    if (!kAhead) fetch(t);
-    Vec8 d[K], g[K];
-    u32x4_t dc[K];
+  for (int64_t part = 0; part < parts; ++part) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) d[k] = unpack8(x[k]), g[k] = unpack8(dy[k]), dc[k] = kRes ? ds[k] : x[k];
-    if (kAhead) fetch(t + p.step);
-    float mean, square, rstd, off = 0.0f;
-    centre(a, p, d, &mean, &square);
-    float s1 = 0.0f, s2 = 0.0f;
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) dw[k].v[i] = db[k].v[i] = 0.0f;
+    end = min(a.S, end + turns * p.step);
+#pragma unroll 1
+    for (; t < end; t += p.step, turn ^= 1) {
+      if (!kAhead) fetch(t);
+      Vec8 d[K], g[K];
+      u32x4_t dc[K];
+#pragma unroll
+      for (int k = 0; k < K; ++k) d[k] = unpack8(x[k]), g[k] = unpack8(dy[k]), dc[k] = kRes ? ds[k] : x[k];
+      if (kAhead) fetch(t + p.step);
+      float mean, square, rstd, off = 0.0f;
+      centre(a, p, d, &mean, &square);
+      float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float q = g[k].v[i] * w[k].v[i];
+          s1 += q;
+          s2 = __builtin_fmaf(q, d[k].v[i], s2);
+        }
+      s1 = lanes_sum<L < 64 ? L : 64>(s1);
+      s2 = lanes_sum<L < 64 ? L : 64>(s2);
+      if (P::kWide) {
+        if ((threadIdx.x & 63) == 0) {
+          lds[turn][p.wave][0] = mean;
+          lds[turn][p.wave][1] = square;
+          lds[turn][p.wave][2] = s1;
+          lds[turn][p.wave][3] = s2;
+        }
+        __syncthreads();
+        float all;
+        join<P>(a, lds[turn], &all, &rstd);
+        off = mean - all;
+        s1 = s2 = 0.0f;
+#pragma unroll P::kUnroll
+        for (int v = 0; v < P::kWaves; ++v) {
+          const float o = lds[turn][v][0] - all;
+          s1 += lds[turn][v][2];
+          s2 += __builtin_fmaf(o, lds[turn][v][2], lds[turn][v][3]);
+        }
+      } else {
+        rstd = 1.0f / __builtin_sqrtf(square * p.inv_own + a.eps);
+      }
+      s1 *= inv;
+      s2 *= inv * rstd;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        Vec8 o;
+        const Vec8 e = unpack8(dc[k]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float xh = (d[k].v[i] + off) * rstd, q = g[k].v[i] * w[k].v[i];
+          dw[k].v[i] = __builtin_fmaf(g[k].v[i], xh, dw[k].v[i]);
+          db[k].v[i] += g[k].v[i];
+          o.v[i] = rstd * __builtin_fmaf(-xh, s2, q - s1);
+          if (kRes) o.v[i] += e.v[i];
+        }
+        if (p.has(a, k)) store8<kWhole>(a.dx + t * a.C + p.at(k), pack8(o), p.count(a, k));
+      }
+    }
+    // The workgroup's partial row: its teams' sums in order.
+    float* row = a.part + (part * rows + blockIdx.x) * 2 * a.C;
+    if (P::kWide) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (!p.has(a, k)) continue;
+        part_put(row + p.at(k), dw[k], p.count(a, k));
+        part_put(row + a.C + p.at(k), db[k], p.count(a, k));
+      }
+      continue;
+    }
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float q = g[k].v[i] * w[k].v[i];
-        s1 += q;
-        s2 = __builtin_fmaf(q, d[k].v[i], s2);
+        sums[threadIdx.x / L][k * 8 + i][p.li] = dw[k].v[i];
+        sums[threadIdx.x / L][(K + k) * 8 + i][p.li] = db[k].v[i];
       }
-    s1 = lanes_sum<L < 64 ? L : 64>(s1);
-    s2 = lanes_sum<L < 64 ? L : 64>(s2);
-    if (P::kWide) {
-      if ((threadIdx.x & 63) == 0) {
-        lds[turn][p.wave][0] = mean;
-        lds[turn][p.wave][1] = square;
-        lds[turn][p.wave][2] = s1;
-        lds[turn][p.wave][3] = s2;
-      }
-      __syncthreads();
-      float all;
-      join<P>(a, lds[turn], &all, &rstd);
-      off = mean - all;
-      s1 = s2 = 0.0f;
-#pragma unroll P::kUnroll
-      for (int v = 0; v < P::kWaves; ++v) {
-        const float o = lds[turn][v][0] - all;
-        s1 += lds[turn][v][2];
-        s2 += __builtin_fmaf(o, lds[turn][v][2], lds[turn][v][3]);
-      }
-    } else {
-      rstd = 1.0f / __builtin_sqrtf(square * p.inv_own + a.eps);
+    __syncthreads();
+    for (int32_t o = threadIdx.x; o < 2 * a.C; o += 256) {
+      const int32_t c = o < a.C ? o : o - a.C, q = c / (8 * L) * 8 + c % 8 + (o < a.C ? 0 : K * 8), l = c / 8 % L;
+      float s = 0.0f;
+#pragma unroll
+      for (int g = 0; g < P::kTokens; ++g) s += sums[g][q][l];
+      row[o] = s;
     }
-    s1 *= inv;
-    s2 *= inv * rstd;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      Vec8 o;
-      const Vec8 e = unpack8(dc[k]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float xh = (d[k].v[i] + off) * rstd, q = g[k].v[i] * w[k].v[i];
-        dw[k].v[i] = __builtin_fmaf(g[k].v[i], xh, dw[k].v[i]);
-        db[k].v[i] += g[k].v[i];
-        o.v[i] = rstd * __builtin_fmaf(-xh, s2, q - s1);
-        if (kRes) o.v[i] += e.v[i];
-      }
-      if (p.has(a, k)) store8<kWhole>(a.dx + t * a.C + p.at(k), pack8(o), p.count(a, k));
-    }
-  }
-  // The workgroup's partial row: its teams' sums in order.
-  float* part = a.part + (int64_t)blockIdx.x * 2 * a.C;
-  if (P::kWide) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      if (!p.has(a, k)) continue;
-      part_put(part + p.at(k), dw[k], p.count(a, k));
-      part_put(part + a.C + p.at(k), db[k], p.count(a, k));
-    }
-    return;
-  }
-#pragma unroll
-  for (int k = 0; k < K; ++k)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      sums[threadIdx.x / L][k * 8 + i][p.li] = dw[k].v[i];
-      sums[threadIdx.x / L][(K + k) * 8 + i][p.li] = db[k].v[i];
-    }
-  __syncthreads();
-  for (int32_t o = threadIdx.x; o < 2 * a.C; o += 256) {
-    const int32_t c = o < a.C ? o : o - a.C, q = c / (8 * L) * 8 + c % 8 + (o < a.C ? 0 : K * 8), l = c / 8 % L;
-    float s = 0.0f;
-#pragma unroll
-    for (int g = 0; g < P::kTokens; ++g) s += sums[g][q][l];
-    part[o] = s;
+    if (part + 1 < parts) __syncthreads();  // the sums have been read
   }
 }
 
@@ -386,16 +395,42 @@ int64_t forward_rows(int64_t turns) {
   return turns < full ? turns : full;
 }
 
+// The backward's workgroups and their partial rows.  A row costs its writing and reading,
+// too few leave the machine idle.  Forward and backward of 16384 tokens, C = 520 and a
+// residual: 39 us with 512 rows, 47 with 256, 43 with 1024; backward, C = 2048: 32768
+// tokens 105 with 1024 and 129 with 512, 1500 tokens 11.4 and 9.9; C = 4096, 16384
+// tokens: 107 with 512, 120 with 1024, 142 with 256; C = 8192, 8192 tokens: 113 with 256,
+// 128 with 512.  No more of them than take the same number of turns.
+//
+// A team adds its turns up in FP32, and the rows are added in FP64: what FP32 loses grows
+// with the turns where terms are alike, so a row has 256 at most, and a workgroup of a long
+// input several rows, one part of the tokens after the other.  1048577 tokens of the same
+// values, C = 4096: dw off by 1.4e-5 in rows of 2048 turns, by 1.9e-6 so.
+struct Rows {
+  int64_t groups, turns, parts;
+};
+Rows backward_rows(int64_t S, int64_t C) {
+  const Shape h = shape_of(C);
+  const int64_t tokens = h.lanes > 64 ? 1 : 256 / h.lanes, turns = (S + tokens - 1) / tokens;
+  const int64_t most = h.lanes >= 512 ? 256 : h.lanes == 256 && h.vecs == 1 && turns >= 4096 ? 1024 : 512;
+  const int64_t each = (turns + most - 1) / most;
+  if (each == 0) return {0, 0, 0};
+  const int64_t parts = (each + 255) / 256;
+  return {(turns + each - 1) / each, (each + parts - 1) / parts, parts};
+}
+
 template <int L, int K, bool kWhole>
 void launch_vec(const LayerNormArgs& a, bool back, hipStream_t s) {
   typedef Team<L, K, kWhole> P;
-  const int64_t turns = (a.S + P::kTokens - 1) / P::kTokens;
-  const int64_t rows = back ? a.prows : forward_rows<L>(turns);
-  const dim3 grid((uint32_t)rows), block(P::kThreads);
   if (back) {
-    if (a.dstream) hipLaunchKernelGGL((layer_norm_bwd_kernel<L, K, kWhole, true>), grid, block, 0, s, a, (int32_t)rows);
-    else hipLaunchKernelGGL((layer_norm_bwd_kernel<L, K, kWhole, false>), grid, block, 0, s, a, (int32_t)rows);
+    const Rows r = backward_rows(a.S, a.C);
+    const dim3 grid((uint32_t)r.groups), block(P::kThreads);
+    const int32_t rows = (int32_t)r.groups, turns = (int32_t)r.turns, parts = (int32_t)r.parts;
+    if (a.dstream) hipLaunchKernelGGL((layer_norm_bwd_kernel<L, K, kWhole, true>), grid, block, 0, s, a, rows, turns, parts);
+    else hipLaunchKernelGGL((layer_norm_bwd_kernel<L, K, kWhole, false>), grid, block, 0, s, a, rows, turns, parts);
   } else {
+    const int64_t rows = forward_rows<L>((a.S + P::kTokens - 1) / P::kTokens);
+    const dim3 grid((uint32_t)rows), block(P::kThreads);
     if (a.res) hipLaunchKernelGGL((layer_norm_fwd_kernel<L, K, kWhole, true>), grid, block, 0, s, a, (int32_t)rows);
     else hipLaunchKernelGGL((layer_norm_fwd_kernel<L, K, kWhole, false>), grid, block, 0, s, a, (int32_t)rows);
   }
@@ -423,18 +458,9 @@ hipError_t launch(const LayerNormArgs& a, bool back, hipStream_t s) {
 
 }  // namespace
 
-// A row costs its writing and reading, too few leave the machine idle.  Forward and
-// backward of 16384 tokens, C = 520 and a residual: 39 us with 512 rows, 47 with 256, 43
-// with 1024; backward, C = 2048: 32768 tokens 105 with 1024 and 129 with 512, 1500
-// tokens 11.4 and 9.9; C = 4096, 16384 tokens: 107 with 512, 120 with 1024, 142 with 256;
-// C = 8192, 8192 tokens: 113 with 256, 128 with 512.  No more of them than take the same
-// number of turns.
 int layer_norm_bwd_rows(int64_t S, int64_t C) {
-  const Shape h = shape_of(C);
-  const int64_t tokens = h.lanes > 64 ? 1 : 256 / h.lanes, turns = (S + tokens - 1) / tokens;
-  const int64_t most = h.lanes >= 512 ? 256 : h.lanes == 256 && h.vecs == 1 && turns >= 4096 ? 1024 : 512;
-  const int64_t each = (turns + most - 1) / most;
-  return each ? (int)((turns + each - 1) / each) : 0;
+  const Rows r = backward_rows(S, C);
+  return (int)(r.groups * r.parts);
 }
 
 hipError_t launch_layer_norm_fwd(const LayerNormArgs& a, hipStream_t s) { return launch(a, false, s); }
