@@ -39,6 +39,9 @@ LARGE = [
     ([5000, 0, 4000], 264, {"gate": False, "wide": True, "params": BF}),
     ([1, 2300, 63, 700], 1032, {"low": 0.99, "high": 0.99999}),
     ([3100], 1089, {"low": 0.2, "high": 0.9999, "gate": False}),
+    # 32 tiles of tokens and fewer, whose sums of the decay's gradient are handed on
+    ([1200, 800], 1100, {}),
+    ([700], 3008, {"gate": False, "params": BF}),
 ]
 
 
