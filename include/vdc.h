@@ -450,8 +450,9 @@ int group_norm_silu_bwd(const void *x, int64_t x_stride, const void *weight, int
  * the normal FP32 numbers, and 2 scale softplus(decay) is at most 2^126.
  */
 typedef struct vdc_recurrence {
-    int64_t S;        /* tokens, at most 2^31 - 4096; for
-                         gated_recurrence_update rows, one token each        */
+    int64_t S;        /* tokens, at most 2^29 - 64, and as above for more
+                         than 64 channels; for gated_recurrence_update
+                         rows, one token each                                */
     int64_t C;        /* channels, 1 .. 2^20                                 */
     const void *x;    /* bf16 [S][C]                                         */
     const void *r;    /* bf16 [S][C], the decay's gate                       */
@@ -528,6 +529,8 @@ int gated_recurrence_update(const vdc_recurrence *args, void *y, hipStream_t str
  * x, residual bf16 [S][C] with row strides, C at most 16384; y bf16 [S][C];
  * stream_out bf16 [S][C], the sum s; NULL exactly where residual is.  2-byte
  * aligned.  weight, bias [C] of their dtypes; bias may be NULL.  eps >= 0.
+ * Squares are FP32's: differences from the mean are below 2^56 (16384 squares of
+ * them are below the largest number).
  */
 int layer_norm_fwd(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
                    const void *weight, int w_dtype, const void *bias, int b_dtype,

@@ -20,8 +20,8 @@
 //
 // Measured, with a residual: 16384 tokens, C = 4096 forward 92 us, 5.8 TB/s, backward 105,
 // 5.1 TB/s (a copy: 5.1), and the sum of its partial rows 5.8; 8192 tokens, C = 8192
-// forward 80 us, 6.7 TB/s, the last cache's part in it.  Few tokens are latency: 33 tokens,
-// C = 520 3.9 us; 1543 tokens of 1001 channels 5.0 forward, 8.3 and 4.7 backward.
+// forward 79 us, 6.8 TB/s, the last cache's part in it.  Few tokens are latency: 33 tokens,
+// C = 520 3.6 us; 1543 tokens of 1001 channels 5.0 forward, 8.6 and 4.6 backward.
 
 #include <algorithm>
 

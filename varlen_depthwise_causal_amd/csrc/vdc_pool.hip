@@ -25,8 +25,9 @@ __device__ __forceinline__ bool pool_row(const PoolArgs& a, int64_t row, int64_t
 
 // v / s rounded to odd: the quotient's 24 bits with the last one set where it is
 // not exact, so that rounding it once more to a code gives the code nearest to the
-// quotient itself.  Below 2^-20 every code is 0.  s is at least 2^-72, so that the
-// remainder has all its bits.
+// quotient itself.  Below 2^-20 every code is 0.  s is at least 2^-64 / 448, above 2^-73: the
+// remainder of a quotient from 2^-20 on is a multiple of 2^-139 (the last bits of t and s
+// are 2^-43 and 2^-96), which FP32 holds.
 __device__ __forceinline__ float odd_quotient(float v, float s) {
   const float t = v / s;
   const float rest = __builtin_fmaf(-t, s, v);

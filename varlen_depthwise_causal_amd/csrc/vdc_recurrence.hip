@@ -19,10 +19,10 @@
 // tiles behind it send), and finishes.  Two passes over a long row would read 14
 // bytes instead of 8.
 //
-// Measured: 65536 tokens, C = 4096 with a gate, forward 550 us, 4.9 TB/s (a copy: 5.1);
-// 16384 tokens 142 us, 4.7 TB/s, and backward 259, 4.7 TB/s, with VALU issue 68% and 64%
+// Measured: 65536 tokens, C = 4096 with a gate, forward 543 us, 4.9 TB/s (a copy: 5.1);
+// 16384 tokens 144 us, 4.7 TB/s, and backward 257, 4.7 TB/s, with VALU issue 67% and 64%
 // busy at 48 and 82 instructions a token and 64 channels.  A few tiles are latency: 1543
-// tokens, C = 520, 25 tiles in a row, 8.2 us forward and 11.3 backward.
+// tokens, C = 520, 25 tiles in a row, 7.9 us forward and 11.7 backward.
 //
 // What a tile hands on is one 64-bit word a channel: P and H, or, once the state
 // after the tile is known, that state and a mark in place of P.  A tile reads the
@@ -37,6 +37,9 @@
 //
 // Everything between documents is assigned, never multiplied by zero, so that
 // an infinity or a NaN stays in its document.
+//
+// The decay's gradient is a sum in FP32 over a tile's 64 tokens, whose terms are rounded
+// to FP32 already, and in FP64 over the tiles.
 
 #include <algorithm>
 #include <cfloat>
@@ -147,8 +150,8 @@ __device__ __forceinline__ void clear_starts(Starts<T, kState>& s) {
 // All threads of the workgroup, an entry of cu_seqlens each and all its loads at
 // once; the result is complete after the next barrier.  Where the tile's tokens have
 // more than sixteen entries a thread, nearly all of them are empty documents'; a search
-// for each token passes them, so that a tile has its word after some 50 us at most, while
-// others wait for it.
+// for each token, 62 loads one after another, passes them, so that a tile has its word
+// soon, while others wait for it.
 template <int W, int T, bool kState>
 __device__ __forceinline__ void find_starts(const RecurArgs& a, int32_t t0, Starts<T, kState>& s) {
   const int32_t entries = a.num_docs + 1;
