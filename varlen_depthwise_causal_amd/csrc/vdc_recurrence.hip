@@ -148,28 +148,17 @@ __device__ __forceinline__ void clear_starts(Starts<T, kState>& s) {
 }
 
 // All threads of the workgroup, an entry of cu_seqlens each and all its loads at
-// once; the result is complete after the next barrier.  Where the tile's tokens have
-// more than sixteen entries a thread, nearly all of them are empty documents'; a search
-// for each token, 62 loads one after another, passes them, so that a tile has its word
-// soon, while others wait for it.
+// once; the result is complete after the next barrier.  Where a wave has not come past
+// the tile's tokens after sixteen entries a thread, nearly all of these are empty
+// documents'; a search for each token, 62 loads one after another, passes the others, so
+// that a tile has its word soon, while others wait for it.
 template <int W, int T, bool kState>
 __device__ __forceinline__ void find_starts(const RecurArgs& a, int32_t t0, Starts<T, kState>& s) {
   const int32_t entries = a.num_docs + 1;
   int32_t e = entries > 64 * W ? first_at_least(a.cu, entries, t0) : 0;
-  constexpr int32_t kMany = 16 * 64 * W;
-  if (entries > kMany && e < entries - kMany && a.cu[e + kMany] <= t0 + T) {
-    const int32_t* const cu = a.cu;
-    for (int j = threadIdx.x; j <= T && t0 + j <= a.S; j += 64 * W) {
-      const TokenDocs d = token_docs([cu](int64_t i) { return cu[i]; }, entries, t0 + j);
-      if (!d.any) continue;
-      atomicOr(&s.mask[j / 32], 1u << (j % 32));
-      if (kState && d.starts >= 0 && a.resume && a.resume[d.starts]) s.from[j] = (int32_t)slot_of(a.index, d.starts, a.slots);
-      if (kState && d.ends >= 0) s.to[j] = (int32_t)slot_of(a.index, d.ends, a.slots);
-    }
-    return;
-  }
   e += threadIdx.x;
-  while (true) {
+#pragma unroll 1
+  for (int n = 0; n < 16; ++n, e += 64 * W) {
     int32_t v = INT_MAX, next = INT_MAX, past = INT_MAX, from = -1, to = -1;
     if (e < entries) v = a.cu[e];
     if (kState && e < a.num_docs) {
@@ -189,7 +178,19 @@ __device__ __forceinline__ void find_starts(const RecurArgs& a, int32_t t0, Star
       if (kState && past < v && to >= 0 && to < a.slots) s.to[j] = to;
     }
     if (__ballot(e < entries && j <= T) == 0) return;
-    e += 64 * W;
+  }
+  const int32_t* const cu = a.cu;
+#pragma unroll 1
+  for (int j = threadIdx.x & 63; j <= T && t0 + j <= a.S; j += 64) {
+    const TokenDocs d = token_docs([cu](int64_t i) { return cu[i]; }, entries, t0 + j);
+    if (!d.any) continue;
+    atomicOr(&s.mask[j / 32], 1u << (j % 32));
+    if (!kState) continue;
+    const int64_t from = d.starts >= 0 && a.resume && a.resume[d.starts] ? slot_of(a.index, d.starts, a.slots) : -1;
+    const int64_t to = d.ends >= 0 ? slot_of(a.index, d.ends, a.slots) : -1;
+    // other waves may write the same, and none another slot
+    if (from >= 0) s.from[j] = (int32_t)from;
+    if (to >= 0) s.to[j] = (int32_t)to;
   }
 }
 
